@@ -67,8 +67,9 @@ extern "C" {
 #define MERCURY_ETIMEOUT (-4)  /* a bounded device wait ran out                     */
 #define MERCURY_ENOMEM   (-5)  /* host-side allocation failed                       */
 #define MERCURY_EBUDGET  (-6)  /* no schedule fits the given device-memory budget   */
-#define MERCURY_EBOUNDS  (-7)  /* checked build only: an out-of-range index was
-                                  found in a kernel and its access skipped       */
+#define MERCURY_EBOUNDS  (-7)  /* an out-of-range index was found in a kernel and its
+                                  access skipped: a page, position or length of a paged
+                                  cache (any build), or any index (checked build) */
 
 /* Largest number of virtual ranks a compute call accepts. */
 #define MERCURY_MAX_R 128
@@ -272,10 +273,11 @@ MERCURY_API int mercury_attn_split_noalloc(const void *q, const void *k, const v
  * mercury_sync_status -- synchronise `stream`, then read and clear the device
  * error words of this process's kernels.  Returns MERCURY_OK,
  * MERCURY_ETIMEOUT (a bounded device wait ran out in some earlier kernel),
- * MERCURY_EBOUNDS (only in the checked build, libmercury_attn.so built with
- * -DMERCURY_CHECK: a kernel found an out-of-range TMA coordinate or output
- * index and skipped that access) or MERCURY_ECUDA (the synchronise itself
- * failed).
+ * MERCURY_EBOUNDS (a paged-cache kernel met a page, position or length out
+ * of range and skipped the access; or, only in the checked build,
+ * libmercury_attn.so built with -DMERCURY_CHECK, a kernel found an
+ * out-of-range TMA coordinate or output index and skipped that access) or
+ * MERCURY_ECUDA (the synchronise itself failed).
  */
 MERCURY_API int mercury_sync_status(void *stream);
 
@@ -479,6 +481,201 @@ MERCURY_API int mercury_tune_schedule(const void *q, const void *k, const void *
 
 /* Drop every cached tuning result of mercury_tune_schedule. */
 MERCURY_API void mercury_tune_cache_clear(void);
+
+/*
+ * Serving over a long context: rotary positions, a paged key-value cache and
+ * attention of new tokens over it.
+ *
+ * The pages take the shared KV buffer as a dense, sharded array; a serving
+ * loop grows it token by token for many sequences at once.  These calls keep
+ * it as pages: page p holds page_size consecutive tokens of one sequence for
+ * every KV head, and block_table[b][i] names the page of tokens
+ * [i * page_size, (i + 1) * page_size) of sequence b.  Pages may lie in any
+ * order, and two sequences may name the same page for a shared prefix.
+ *
+ * One decode step is mercury_kv_append (rotates the new tokens' queries and
+ * keys, stores keys and values) and mercury_attn_paged; a prompt is
+ * mercury_kv_append of all its tokens, with mercury_rope and
+ * mercury_attn_sharded for its own attention.  mercury_attn_paged's (O, LSE)
+ * is a partial like any other here: mercury_lse_merge joins it with attention
+ * over other shards of the context.
+ */
+
+/* Largest number of rotated elements of a head. */
+#define MERCURY_MAX_ROT 256
+
+/* Element types. */
+#define MERCURY_ELEM_BF16 0
+#define MERCURY_ELEM_E4M3 1
+#define MERCURY_ELEM_FP32 2
+
+/* Frequency scalings of mercury_rope_frequencies. */
+#define MERCURY_ROPE_NONE   0
+#define MERCURY_ROPE_LINEAR 1
+#define MERCURY_ROPE_NTK    2
+#define MERCURY_ROPE_YARN   3
+
+/* A rotation, from mercury_rope_init: plain host data, passed by value to the
+ * kernels, so it may be copied, reused and dropped at any time. */
+typedef struct mercury_rope_plan {
+    int rot_dim;       /* the first rot_dim elements of a head are rotated */
+    int interleaved;   /* 0: pair i is (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+    float magnitude;   /* factor on the rotated elements */
+    unsigned long long turns[MERCURY_MAX_ROT / 2];  /* per pair: turns a position, in units of 2^-64 */
+} mercury_rope_plan;
+
+/*
+ * mercury_rope_frequencies -- the angle (radians) of each pair per position
+ * (pure host code).
+ *
+ * With f_i = base^(-2i/rot_dim), i = 0 .. rot_dim/2 - 1:
+ *   MERCURY_ROPE_NONE    f_i;
+ *   MERCURY_ROPE_LINEAR  f_i / factor (positions interpolated);
+ *   MERCURY_ROPE_NTK     f_i for the base base * factor^(rot_dim/(rot_dim-2));
+ *   MERCURY_ROPE_YARN    with r_i = original_length f_i / (2 pi) turns over the
+ *       original context and g_i = (r_i - beta_slow) / (beta_fast - beta_slow)
+ *       held to [0, 1]: g_i f_i + (1 - g_i) f_i / factor, and the magnitude
+ *       0.1 ln(factor) + 1 (1 for every other scaling).
+ * freq: host array of rot_dim/2 doubles; magnitude: host double.
+ * Requirements: rot_dim even, 2..MERCURY_MAX_ROT (>= 4 for NTK); base > 1;
+ * factor >= 1; YARN: original_length > 0, beta_fast > beta_slow >= 0; all
+ * finite.  Errors: MERCURY_EINVAL.
+ */
+MERCURY_API int mercury_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                         double original_length, double beta_fast, double beta_slow,
+                                         double *freq, double *magnitude);
+
+/*
+ * mercury_rope_init -- a rotation plan from any frequencies (pure host code).
+ * freq: rot_dim/2 angles per position in radians, finite and in [0, 2^20];
+ * magnitude finite.  The plan holds each frequency as turns per position in
+ * 64-bit fixed point, so angles are exact modulo one turn up to the
+ * frequency's own rounding: 2^-53 turns a position at most for frequencies
+ * up to one turn, at any position.
+ * Errors: MERCURY_EINVAL.
+ */
+MERCURY_API int mercury_rope_init(int rot_dim, int interleaved, const double *freq, double magnitude,
+                                  mercury_rope_plan *plan);
+
+/*
+ * mercury_rope -- rotary positions on every head of x [B, H, S, d].
+ *
+ * Pair (a, b) of a head at position p, with t = p * freq of the pair, becomes
+ * magnitude * (a cos t - b sin t, b cos t + a sin t); elements from rot_dim
+ * on are copied.  inverse = 1 turns by -t: the transpose of the forward
+ * rotation (with the same magnitude), which is its gradient.
+ * x, out: elem MERCURY_ELEM_BF16 or MERCURY_ELEM_FP32; computed in fp32 and
+ * rounded once.  x_strides, out_strides: host arrays of the three element
+ * strides over batch, head and token (NULL: contiguous); the d elements of a
+ * head are contiguous.  out may be x with the same strides (in place);
+ * otherwise the two must not overlap, and out's elements must be distinct.
+ * positions: [B][S] int32 on the device, rows pos_stride apart (0: one row
+ * for all sequences); NULL: token s is at position start + s.
+ * Requirements: B, H, S >= 1; H <= 65535; B * S < 2^31; rot_dim <= d <= 512;
+ * pointers aligned to their element.  16-byte accesses are used where
+ * pointers and strides are multiples of 16 bytes and rot_dim is a multiple of
+ * 16 (bf16) or 8 (fp32); other shapes go element by element.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA.
+ */
+MERCURY_API int mercury_rope(const void *x, const long long *x_strides, const int *positions,
+                             long long pos_stride, long long start, int B, int H, int S, int d, int elem,
+                             const mercury_rope_plan *plan, int inverse, void *out,
+                             const long long *out_strides, void *stream);
+
+/* A paged cache of keys and values: the caller's device arrays and their
+ * sizes.  A plain host struct read during each call. */
+typedef struct mercury_paged_cache {
+    void *k;                  /* [num_pages][Hkv][page_size][d] */
+    void *v;                  /* the same */
+    const float *k_scale;     /* [Hkv] fp32, E4M3 only: an element is its byte's value times this */
+    const float *v_scale;
+    const int *block_table;   /* [B][max_pages] int32 */
+    long long page_stride;    /* elements from page to page, >= Hkv * page_size * d */
+    long long table_stride;   /* elements from row to row of block_table, >= max_pages */
+    int elem;                 /* MERCURY_ELEM_BF16 or MERCURY_ELEM_E4M3 */
+    int Hkv;
+    int d;
+    int page_size;
+    int num_pages;
+    int max_pages;
+    int B;                    /* sequences: rows of block_table */
+} mercury_paged_cache;
+
+/*
+ * mercury_kv_append -- new keys and values into a paged cache, the position
+ * rotation applied on the way.
+ *
+ * k, v [B, Hkv, S, d] bf16: token i of sequence b, for i < new_lens[b] (all S
+ * where new_lens is NULL), goes to position past_lens[b] + i.  With a rope
+ * plan the key is rotated by that position, in fp32, before its one rounding
+ * to the cache's type; a plan of NULL stores it as it is.  An E4M3 cache holds
+ * x / scale[head] rounded to nearest and saturated at +-448.
+ * q [B, Hq, S, d] bf16 (optional): the queries of the same tokens, rotated
+ * likewise into q_out (which may be q itself, with its strides); q NULL means
+ * q_out is not touched.
+ * Strides as in mercury_rope (k, v and q may be slices of one projection).
+ * past_lens, new_lens: [B] int32 on the device.  Rows i >= new_lens[b] of k, v
+ * and q are not read, those of q_out and every other row of the cache are
+ * left as they were.  No two tokens of a call may go to the same row of the
+ * same page.
+ * A position outside the block table, a page outside the cache or a new_lens
+ * outside [0, S] (taken to the nearer end) is skipped and reported as
+ * MERCURY_EBOUNDS by mercury_sync_status.
+ * Requirements: B = cache->B; S >= 1; B * S < 2^31; Hq >= 1 with q; the
+ * cache's fields as described, d in {64, 128}, max_pages * page_size <= 2^30,
+ * k and v of the cache 16-byte aligned and page_stride a multiple of 16
+ * bytes; rot_dim <= d.  Access width as in mercury_rope.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
+ * when MERCURY_SYNC_CHECK=1.
+ */
+MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, const void *v,
+                                  const long long *v_strides, int B, int S, const mercury_paged_cache *cache,
+                                  const int *past_lens, const int *new_lens, const mercury_rope_plan *rope,
+                                  const void *q, const long long *q_strides, int Hq, void *q_out,
+                                  const long long *q_out_strides, void *stream);
+
+/*
+ * mercury_attn_paged -- attention of the newest tokens of every sequence over
+ * a paged cache, split over the cache's length and joined.
+ *
+ * seq_lens [B] int32: tokens of sequence b in the cache, its new ones
+ * included.  Row i of q [B, Hq, Sq, d] bf16, for i < n = new_lens[b] (all Sq
+ * where new_lens is NULL), is the token at position seq_lens[b] - n + i; with
+ * causal it sees the keys up to its own position, without it all seq_lens[b]
+ * keys (drafted trees aside, attention to another sequence's states of any
+ * length).  Scale 1/sqrt(d), query head h uses KV head h / (Hq/Hkv).
+ * out [B, Hq, Sq, d] and lse [B, Hq, Sq] fp32, contiguous; a row without keys
+ * gets O = 0 and LSE = -inf, rows i >= n are left as they were.  Keys that a
+ * row does not see do not affect it, whatever they hold; cache rows at and
+ * after seq_lens[b] are not read.
+ * Scores, sums and products are kept in fp32, P as two 16-bit terms, so O
+ * carries fp32 accuracy (about 1e-6 relative) from the cache's values.
+ * The keys of all sequences are dealt to the SMs in equal shares on the
+ * device, so neither the lengths nor their spread need to be known on the
+ * host.  Parts of sequences cut between SMs go to scratch memory (2 * SMs *
+ * rows * (d + 2) * 4 bytes, rows 8 to 32) that comes stream-ordered from the
+ * library's pool; a captured graph owns its own.
+ * A page outside the cache counts as keys and values of zero, and it, a
+ * seq_lens outside the block table or a new_lens outside [0, Sq] (both taken
+ * to the nearer end) is reported as MERCURY_EBOUNDS by mercury_sync_status.
+ * q_strides as in mercury_rope, multiples of 8 elements, q 16-byte aligned.
+ * Requirements: as mercury_kv_append for the cache; Hq % Hkv == 0;
+ * 1 <= Sq <= 64 (longer prompts are mercury_attn_sharded's).  The first call
+ * for a shape class on a device prepares its kernel; make it before any
+ * stream capture.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
+ * when MERCURY_SYNC_CHECK=1.
+ */
+MERCURY_API int mercury_attn_paged(const void *q, const long long *q_strides, const mercury_paged_cache *cache,
+                                   const int *seq_lens, const int *new_lens, int B, int Hq, int Sq, int causal,
+                                   float *out, float *lse, void *stream);
+
+/* mercury_attn_paged_bf16 -- mercury_attn_paged with O rounded to bf16 (out
+ * [B, Hq, Sq, d] bf16, 16-byte aligned; lse stays fp32). */
+MERCURY_API int mercury_attn_paged_bf16(const void *q, const long long *q_strides,
+                                        const mercury_paged_cache *cache, const int *seq_lens,
+                                        const int *new_lens, int B, int Hq, int Sq, int causal, void *out,
+                                        float *lse, void *stream);
 
 #ifdef __cplusplus
 }

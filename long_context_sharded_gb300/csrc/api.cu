@@ -134,18 +134,27 @@ int check_attn_args(const void *q, const void *k, const void *v, int B, int Hq, 
 }
 
 // Synchronise `stream` and collect the error words of every kernel module
-// (bit 0: a bounded wait ran out; bit 1: the checked build skipped an
-// out-of-range access).
+// (bit 0: a bounded wait ran out; bit 1: an out-of-range access was skipped --
+// found by the checked build, or by the paged kernels in any build).
 int collect_device_errors(cudaStream_t stream)
 {
-    unsigned int w[3] = {0, 0, 0}, site[3] = {0, 0, 0};
+    constexpr int n = 5;
+    unsigned int w[n] = {}, site[n] = {};
     int rc = read_and_clear_device_error(stream, &w[0], &site[0], g_msg, sizeof g_msg);
     if (rc == MERCURY_OK)
         rc = read_and_clear_gemm_error(&w[1], &site[1], g_msg, sizeof g_msg);
     if (rc == MERCURY_OK)
         rc = read_and_clear_merge_error(&w[2], &site[2], g_msg, sizeof g_msg);
+    if (rc == MERCURY_OK)
+        rc = read_and_clear_append_error(&w[3], &site[3], g_msg, sizeof g_msg);
+    if (rc == MERCURY_OK)
+        rc = read_and_clear_paged_error(&w[4], &site[4], g_msg, sizeof g_msg);
     if (rc != MERCURY_OK)
         return rc;
+    for (int i = 3; i < n; ++i)
+        if (w[i] & 2u)
+            return fail(MERCURY_EBOUNDS, "paged cache: a length, position or page out of range was found and its "
+                        "access skipped (site 0x%x)", site[i]);
     for (int i = 0; i < 3; ++i)
         if (w[i] & 2u)
             return fail(MERCURY_EBOUNDS, "checked build: an out-of-range index was found and its access skipped "
@@ -363,6 +372,22 @@ int set_error(int code, const char *fmt, ...)
 int clear_error()
 {
     return ok();
+}
+
+char *error_buffer(size_t *len)
+{
+    *len = sizeof g_msg;
+    return g_msg;
+}
+
+int finish_call(int rc, cudaStream_t stream)
+{
+    return finish(rc, stream);
+}
+
+int device_scratch_pool(cudaMemPool_t *pool)
+{
+    return scratch_pool(pool);
 }
 
 int device_sm_count(int *n)

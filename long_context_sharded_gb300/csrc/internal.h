@@ -64,6 +64,38 @@ int read_and_clear_device_error(cudaStream_t stream, unsigned int *word, unsigne
 // Status and message of the calling thread, shared by the C-ABI files.
 int set_error(int code, const char *fmt, ...);
 int clear_error();
+char *error_buffer(size_t *len);
+
+// The end of every compute call: its status, or with MERCURY_SYNC_CHECK=1 the
+// device status after a synchronise.
+int finish_call(int rc, cudaStream_t stream);
+
+// The library's stream-ordered scratch pool of the current device.
+int device_scratch_pool(cudaMemPool_t *pool);
+
+// Element strides over (batch, head, token) of a [B, H, S, d] tensor whose
+// heads are contiguous.
+struct Strides;
+
+// Rotary positions (rope.cu): every argument validated by the C-ABI layer.
+int launch_rope(const void *x, const Strides &xs, const int *pos, long long pos_stride, long long start, int B, int H,
+                int S, int d, int elem, const mercury_rope_plan &plan, int inverse, void *out, const Strides &os,
+                int sms, cudaStream_t stream, char *msg, size_t msg_len);
+
+// New keys and values into a paged cache, q rotated beside them (kv_append.cu).
+int launch_kv_append(const void *k, const Strides &ks, const void *v, const Strides &vs, const void *q,
+                     const Strides &qs, void *q_out, const Strides &os, const mercury_paged_cache &cache,
+                     const int *past_lens, const int *new_lens, int B, int Hq, int S, const mercury_rope_plan *plan,
+                     int sms, cudaStream_t stream, char *msg, size_t msg_len);
+
+// Attention of new tokens over a paged cache (attn_paged.cu).
+int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
+                      const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
+                      cudaStream_t stream, char *msg, size_t msg_len);
+
+// Read and clear those kernels' device error words (no synchronisation).
+int read_and_clear_append_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
+int read_and_clear_paged_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
 
 // SMs of the current device (cached per device).
 int device_sm_count(int *n);

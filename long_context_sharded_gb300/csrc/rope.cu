@@ -1,0 +1,133 @@
+// rope.cu -- rotary positions: the plan's frequencies (host) and the rotation
+// of every head of a prompt or of single tokens.
+//
+// For pair i of a head at position p, with angle t = p * f_i and magnitude m,
+//     (a, b) -> m (a cos t - b sin t, b cos t + a sin t),
+// and with the angle negated for the transpose, which carries gradients back.
+// A pair is (i, i + rot/2) or (2i, 2i + 1); the elements from rot on pass
+// unchanged.
+//
+// Memory bound: every element is read and written once, three multiply-adds a
+// pair.  A thread owns one column unit of one token (two 16-byte chunks: the
+// two halves of the same pairs, or two chunks of whole pairs) and keeps the
+// unit's cosines and sines in registers while it walks over the token's
+// heads, so an angle is computed once per token and group of heads, not once
+// per head.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "rotate.cuh"
+
+namespace mercury {
+
+namespace {
+
+struct RopeArgs {
+    const void *x;
+    void *out;
+    const int *pos;
+    Strides xs, os;
+    long long start, pos_stride;
+    int H, S, d, heads_per_thread, units, tokens_per_block;
+    long long tokens;
+    int inverse, copy_rest;
+    mercury_rope_plan plan;
+};
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(kRotThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+{
+    const int lane_units = kRotThreads / a.tokens_per_block;
+    const long long token = (long long)blockIdx.x * a.tokens_per_block + threadIdx.x / lane_units;
+    if (token >= a.tokens)
+        return;
+    const int b = (int)(token / a.S), s = (int)(token % a.S);
+    const long long pos = a.pos ? a.pos[b * a.pos_stride + s] : a.start + s;
+    const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(a.H, h0 + a.heads_per_thread);
+    const T *src = (const T *)a.x + b * a.xs.b + s * a.xs.s;
+    T *dst = (T *)a.out + b * a.os.b + s * a.os.s;
+    for (int u = threadIdx.x % lane_units; u < a.units; u += lane_units) {
+        const RotUnit<VE> unit(a.plan, u, a.d, pos, a.inverse != 0);
+        if (!unit.rotated && !a.copy_rest)
+            continue;
+        // Four heads' loads first, then their stores: the output may be the
+        // input, so the compiler would keep each head's loads behind the last
+        // head's stores.
+        for (int hb = h0; hb < h1; hb += kRotBatch) {
+            Chunk<T, VE> x0[kRotBatch], x1[kRotBatch];
+#pragma unroll
+            for (int i = 0; i < kRotBatch; ++i)
+                if (hb + i < h1) {
+                    const T *p = src + (hb + i) * a.xs.h;
+                    x0[i].load(p + unit.at0);
+                    if (unit.two)
+                        x1[i].load(p + unit.at1);
+                }
+#pragma unroll
+            for (int i = 0; i < kRotBatch; ++i)
+                if (hb + i < h1) {
+                    float y0[VE], y1[VE];
+                    x0[i].widen(y0);
+                    x1[i].widen(y1);
+                    unit.turn(y0, y1);
+                    T *p = dst + (hb + i) * a.os.h;
+                    store_chunk<VE>(p + unit.at0, y0);
+                    if (unit.two)
+                        store_chunk<VE>(p + unit.at1, y1);
+                }
+        }
+    }
+}
+
+template <typename T, int VE>
+int launch(RopeArgs &a, int B, int sms, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    const RotShape g = rot_shape(a.tokens, a.H, a.d, a.plan.rot_dim, VE, sms);
+    a.units = g.units;
+    a.tokens_per_block = g.tokens_per_block;
+    a.heads_per_thread = g.heads_per_thread;
+    rope_kernel<T, VE><<<dim3((unsigned)g.blocks, (unsigned)g.head_groups), kRotThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "rope kernel launch: %s", cudaGetErrorString(e));
+        return MERCURY_ECUDA;
+    }
+    return MERCURY_OK;
+}
+
+}  // namespace
+
+int launch_rope(const void *x, const Strides &xs, const int *pos, long long pos_stride, long long start, int B, int H,
+                int S, int d, int elem, const mercury_rope_plan &plan, int inverse, void *out, const Strides &os,
+                int sms, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    RopeArgs a;
+    a.x = x;
+    a.out = out;
+    a.pos = pos;
+    a.xs = xs;
+    a.os = os;
+    a.start = start;
+    a.pos_stride = pos_stride;
+    a.H = H;
+    a.S = S;
+    a.d = d;
+    a.tokens = (long long)B * S;
+    a.inverse = inverse;
+    // in place, the elements behind the rotated ones are where they belong
+    a.copy_rest = !(x == out && xs.b == os.b && xs.h == os.h && xs.s == os.s);
+    a.plan = plan;
+    const int es = elem == MERCURY_ELEM_FP32 ? 4 : 2;
+    const bool wide = rot_vector_ok(x, xs, d, es) && rot_vector_ok(out, os, d, es);
+    if (elem == MERCURY_ELEM_FP32)
+        return wide && plan.rot_dim % 8 == 0 ? launch<float, 4>(a, B, sms, stream, msg, msg_len)
+                                             : launch<float, 1>(a, B, sms, stream, msg, msg_len);
+    return wide && plan.rot_dim % 16 == 0 ? launch<__nv_bfloat16, 8>(a, B, sms, stream, msg, msg_len)
+                                          : launch<__nv_bfloat16, 1>(a, B, sms, stream, msg, msg_len);
+}
+
+}  // namespace mercury

@@ -1,0 +1,182 @@
+// rotate.cuh -- the work split and the element arithmetic that the rotation
+// and the cache append share.
+//
+// A head of d elements is cut into column units of VE-element chunks (16
+// bytes; VE = 1 where sizes, strides or addresses allow no wide access).  The
+// first rot/(2 VE) units hold two chunks of the rotated part each, j and
+// j + rot/(2 VE): with half-split pairs these are the two sides of the same VE
+// pairs, with interleaved ones two times VE/2 whole pairs, so both layouts
+// read and write the same way and differ only in which registers meet.  The
+// rest of the head follows as units of two plain chunks.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "paged.cuh"
+
+namespace mercury {
+
+constexpr int kRotThreads = 256;
+constexpr int kRotBatch = 4;  // heads whose loads a thread has in flight
+
+template <typename T, int VE>
+struct Chunk;
+
+template <>
+struct Chunk<__nv_bfloat16, 8> {
+    uint4 w = {0, 0, 0, 0};
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void widen(float (&y)[8]) const
+    {
+        y[0] = bf16_lo(w.x), y[1] = bf16_hi(w.x), y[2] = bf16_lo(w.y), y[3] = bf16_hi(w.y);
+        y[4] = bf16_lo(w.z), y[5] = bf16_hi(w.z), y[6] = bf16_lo(w.w), y[7] = bf16_hi(w.w);
+    }
+};
+
+template <>
+struct Chunk<__nv_bfloat16, 1> {
+    __nv_bfloat16 w = __nv_bfloat16();
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *p; }
+    __device__ __forceinline__ void widen(float (&y)[1]) const { y[0] = __bfloat162float(w); }
+};
+
+template <>
+struct Chunk<float, 4> {
+    float4 w = {0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void widen(float (&y)[4]) const { y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w; }
+};
+
+template <>
+struct Chunk<float, 1> {
+    float w = 0.f;
+    __device__ __forceinline__ void load(const float *p) { w = *p; }
+    __device__ __forceinline__ void widen(float (&y)[1]) const { y[0] = w; }
+};
+
+// Each result is rounded once, from its 32-bit value, to the output's type.
+template <int VE>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, const float (&y)[VE])
+{
+    if constexpr (VE == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                   pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    else
+        *p = __float2bfloat16_rn(y[0]);
+}
+
+template <int VE>
+__device__ __forceinline__ void store_chunk(float *p, const float (&y)[VE])
+{
+    if constexpr (VE == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
+    else
+        *p = y[0];
+}
+
+template <int VE>
+__device__ __forceinline__ void store_chunk_e4m3(uint8_t *p, const float (&y)[VE])
+{
+    if constexpr (VE == 8)
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16, pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
+    else
+        *p = (uint8_t)pack_e4m3(y[0], 0.f);
+}
+
+// One column unit at one position: where its chunks lie, and its rotation.
+template <int VE>
+struct RotUnit {
+    int at0, at1;   // first element of each chunk
+    bool two;       // the second chunk exists
+    bool rotated;
+    bool interleaved;
+    float c[VE], s[VE];
+
+    __device__ __forceinline__ RotUnit(const mercury_rope_plan &plan, int u, int d, long long pos, bool inverse)
+    {
+        const int rot = plan.rot_dim, n = rot / (2 * VE);
+        interleaved = plan.interleaved != 0;
+        rotated = u < n;
+        two = true;
+        if (!rotated) {
+            at0 = rot + (u - n) * 2 * VE;
+            at1 = at0 + VE;
+            two = at1 < d;
+            return;
+        }
+        if (VE == 1 && interleaved) {
+            at0 = 2 * u;
+            at1 = at0 + 1;
+        } else {
+            at0 = u * VE;
+            at1 = at0 + rot / 2;
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            // pair of slot i: chunk element i, or for interleaved chunks
+            // pairs at0/2 + i (first chunk) and at1/2 + i - VE/2 (second)
+            int pair = at0 + i;
+            if (interleaved)
+                pair = VE == 1 ? u : (i < VE / 2 ? at0 / 2 + i : at1 / 2 + i - VE / 2);
+            rope_cos_sin(plan.turns[pair], inverse ? -pos : pos, plan.magnitude, c[i], s[i]);
+        }
+    }
+
+    __device__ __forceinline__ void turn(float (&y0)[VE], float (&y1)[VE]) const
+    {
+        if (!rotated)
+            return;
+        if (VE > 1 && interleaved) {
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+                const float a = y0[2 * i], b = y0[2 * i + 1], e = y1[2 * i], f = y1[2 * i + 1];
+                y0[2 * i] = a * c[i] - b * s[i];
+                y0[2 * i + 1] = b * c[i] + a * s[i];
+                y1[2 * i] = e * c[i + VE / 2] - f * s[i + VE / 2];
+                y1[2 * i + 1] = f * c[i + VE / 2] + e * s[i + VE / 2];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const float a = y0[i], b = y1[i];
+                y0[i] = a * c[i] - b * s[i];
+                y1[i] = b * c[i] + a * s[i];
+            }
+        }
+    }
+};
+
+// Grid of a launch over `tokens` tokens of H heads.
+struct RotShape {
+    int units, tokens_per_block, heads_per_thread, head_groups;
+    long long blocks;
+};
+
+inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int sms)
+{
+    RotShape g;
+    g.units = rot / (2 * VE) + (d - rot + 2 * VE - 1) / (2 * VE);
+    int lanes = 1;  // threads along a token's units: a power of two
+    while (lanes < g.units && lanes < kRotThreads)
+        lanes *= 2;
+    g.tokens_per_block = kRotThreads / lanes;
+    g.blocks = (tokens + g.tokens_per_block - 1) / g.tokens_per_block;
+    // Heads per thread: as many as leave eight blocks for each SM (an angle
+    // costs about as much as moving two heads), at most 16.
+    int hp = 16;
+    while (hp > 1 && g.blocks * ((H + hp - 1) / hp) < 8LL * sms)
+        hp /= 2;
+    g.heads_per_thread = hp;
+    g.head_groups = (H + hp - 1) / hp;
+    return g;
+}
+
+// Whether every chunk of a tensor with these strides starts on 16 bytes.
+inline bool rot_vector_ok(const void *p, const Strides &s, int d, int elem_size)
+{
+    const int n = 16 / elem_size;
+    return (uintptr_t)p % 16 == 0 && d % n == 0 && s.b % n == 0 && s.h % n == 0 && s.s % n == 0;
+}
+
+}  // namespace mercury

@@ -15,6 +15,12 @@ The functions keep the C names:
   mercury_choose_runs(B, Hq, Hkv, Sq, Skv, d, causal, R, shift, n_sms, scratch_cap=-1) -> int
   mercury_attn_run_schedule(q, k, v, causal, plan, out=None, lse=None, stream=None)
   mercury_tune_schedule(q, k, v, R, shift, causal, budget_bytes, top_k, ...)
+  mercury_rope_init(rot_dim, base, interleaved, scaling, factor, ...) -> RopePlan
+  mercury_rope(x, plan, positions=None, start=0, inverse=False, out=None, stream=None)
+  PagedCache(k_cache, v_cache, block_table, k_scale=None, v_scale=None)
+  mercury_kv_append(cache, k, v, past_lens, new_lens=None, rope=None, q=None, q_out=None, stream=None)
+  mercury_attn_paged(q, cache, seq_lens, new_lens=None, causal=True, out=None, lse=None, stream=None)
+  mercury_attn_paged_bf16(...) the same, O in bf16
 Tensors: q [B,Hq,Sq,d], k/v [B,Hkv,Skv,d] bf16 CUDA tensors, contiguous.
 """
 from __future__ import annotations
@@ -49,7 +55,13 @@ EXPORTED = ("mercury_plan_shift", "mercury_attn_sharded", "mercury_attn_partial"
             "mercury_gemm_shifted", "mercury_attn_decode", "mercury_attn_sharded_bf16",
             "mercury_default_cost_profile", "mercury_measure_cost_profile",
             "mercury_plan_schedules", "mercury_attn_run_schedule", "mercury_tune_schedule",
-            "mercury_tune_cache_clear", "mercury_choose_runs")
+            "mercury_tune_cache_clear", "mercury_choose_runs", "mercury_rope_frequencies",
+            "mercury_rope_init", "mercury_rope", "mercury_kv_append", "mercury_attn_paged",
+            "mercury_attn_paged_bf16")
+
+MERCURY_MAX_ROT = 256
+ELEM_BF16, ELEM_E4M3, ELEM_FP32 = 0, 1, 2
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class CostProfile(ctypes.Structure):
@@ -73,6 +85,22 @@ class Schedule(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class RopePlan(ctypes.Structure):
+    """mercury_rope_plan: a rotation (plain host data, from mercury_rope_init)."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_ulonglong * (MERCURY_MAX_ROT // 2))]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """mercury_paged_cache: the device arrays of a paged cache and their sizes."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("table_stride", ctypes.c_longlong),
+                ("elem", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("B", ctypes.c_int)]
 
 
 class MercuryError(RuntimeError):
@@ -118,6 +146,13 @@ def _load() -> ctypes.CDLL:
                                           i32, p, p, p, p, p]
     lib.mercury_tune_cache_clear.argtypes = []
     lib.mercury_choose_runs.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, i64, p]
+    lib.mercury_rope_frequencies.argtypes = [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double,
+                                             ctypes.c_double, ctypes.c_double, p, p]
+    lib.mercury_rope_init.argtypes = [i32, i32, p, ctypes.c_double, p]
+    lib.mercury_rope.argtypes = [p, p, p, i64, i64, i32, i32, i32, i32, i32, p, i32, p, p, p]
+    lib.mercury_kv_append.argtypes = [p, p, p, p, i32, i32, p, p, p, p, p, p, i32, p, p, p]
+    lib.mercury_attn_paged.argtypes = [p, p, p, p, p, i32, i32, i32, i32, p, p, p]
+    lib.mercury_attn_paged_bf16.argtypes = lib.mercury_attn_paged.argtypes
     for name in EXPORTED:
         if name not in ("mercury_last_error", "mercury_tune_cache_clear"):
             getattr(lib, name).restype = i32
@@ -454,3 +489,247 @@ def mercury_tune_schedule(q, k, v, R: int, shift: int, causal: bool, budget_byte
 
 def mercury_tune_cache_clear() -> None:
     lib.mercury_tune_cache_clear()
+
+
+_Strides = ctypes.c_longlong * 3
+
+
+def _strided_ptr(t, dtype, what, dev):
+    """(device pointer, stride array or None where contiguous) of a [B, H, S, d]
+    CUDA tensor whose heads are contiguous, on device `dev`."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % what)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s (got %s)" % (what, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s but the current device is cuda:%d" % (what, t.device, dev))
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] != 1:
+        raise ValueError("the heads (last axis) of %s must be contiguous" % what)
+    return t.data_ptr(), _Strides(st[0], st[1], st[2])
+
+
+def _lens_ptr(t, B, what):
+    """Device pointer of a contiguous [B] int32 CUDA tensor, or None."""
+    if t is None:
+        return None
+    p = _dev_ptr(t, "torch.int32", what)
+    if t.dim() != 1 or t.shape[0] != B:
+        raise ValueError("%s must have shape (%d,) (got %s)" % (what, B, tuple(t.shape)))
+    return p
+
+
+def mercury_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                             original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(radians per position of each pair as a float64 array, magnitude)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s (got %r)" % (sorted(ROPE_SCALINGS), scaling))
+    freq = np.zeros(MERCURY_MAX_ROT // 2, dtype=np.float64)
+    magnitude = ctypes.c_double(0.0)
+    _check(lib.mercury_rope_frequencies(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                        float(original_length), float(beta_fast), float(beta_slow),
+                                        freq.ctypes.data_as(ctypes.c_void_p), ctypes.byref(magnitude)))
+    return freq[:int(rot_dim) // 2].copy(), magnitude.value
+
+
+def mercury_rope_init(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                      factor: float = 1.0, original_length: float = 0.0, beta_fast: float = 32.0,
+                      beta_slow: float = 1.0, freq=None, magnitude=None) -> RopePlan:
+    """A rotation plan: the frequencies of mercury_rope_frequencies, or those
+    given as `freq` (rot_dim/2 radians per position); `magnitude` replaces the
+    scaling's own."""
+    if freq is None:
+        freq, own = mercury_rope_frequencies(rot_dim, base, scaling, factor, original_length, beta_fast, beta_slow)
+    else:
+        freq, own = np.ascontiguousarray(freq, dtype=np.float64), 1.0
+        if freq.shape != (int(rot_dim) // 2,):
+            raise ValueError("freq must hold rot_dim/2 = %d values (got shape %s)" % (int(rot_dim) // 2, freq.shape))
+    plan = RopePlan()
+    _check(lib.mercury_rope_init(int(rot_dim), int(bool(interleaved)), freq.ctypes.data_as(ctypes.c_void_p),
+                                 float(own if magnitude is None else magnitude), ctypes.byref(plan)))
+    return plan
+
+
+def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: bool = False, out=None, stream=None):
+    """Rotary positions on every head of x [B,H,S,d] (bf16 or fp32, any strides
+    with contiguous heads).  positions: int32 [B,S] or [S]; None: start + s.
+    inverse=True applies the transpose, the gradient of the forward call.
+    out: a tensor of x's shape and dtype, or x itself; a new one by default."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be a 4-D [B, H, S, d] tensor")
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan (mercury_rope_init)")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be torch.bfloat16 or torch.float32 (got %s)" % x.dtype)
+    B, H, S, d = x.shape
+    dev = torch.cuda.current_device() if x.is_cuda else -1
+    px, sx = _strided_ptr(x, x.dtype, "x", dev)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.shape != x.shape:
+        raise ValueError("out must have shape %s (got %s)" % (tuple(x.shape), tuple(out.shape)))
+    po, so = (px, sx) if out is x else _strided_ptr(out, x.dtype, "out", dev)
+    pp, row = None, 0
+    if positions is not None:
+        pp = _dev_ptr(positions, "torch.int32", "positions")
+        if positions.shape == (B, S):
+            row = S
+        elif positions.shape != (S,):
+            raise ValueError("positions must have shape %s or %s (got %s)" % ((B, S), (S,), tuple(positions.shape)))
+    _check(lib.mercury_rope(px, sx, pp, row, int(start), B, H, S, d,
+                            ELEM_FP32 if x.dtype is torch.float32 else ELEM_BF16, ctypes.byref(plan),
+                            int(bool(inverse)), po, so, _stream_ptr(stream)))
+    return out
+
+
+class PagedCache:
+    """A paged key-value cache over the caller's tensors, checked once.
+
+    k_cache, v_cache: [num_pages, Hkv, page_size, d], bf16 or float8_e4m3fn,
+    each page contiguous (pages may lie further apart, as slices of a larger
+    allocation do, equally far in both); block_table: int32 [B, max_pages];
+    k_scale, v_scale: fp32 [Hkv], for e4m3 only.  The object keeps the tensors
+    alive; their contents (the block table's too) may change between calls."""
+
+    def __init__(self, k_cache, v_cache, block_table, k_scale=None, v_scale=None):
+        import torch
+        for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_table, "block_table")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch tensor" % what)
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor" % what)
+            if t.get_device() != torch.cuda.current_device():
+                raise ValueError("%s is on %s but the current device is cuda:%d"
+                                 % (what, t.device, torch.cuda.current_device()))
+        if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError("k_cache must be torch.bfloat16 or torch.float8_e4m3fn (got %s)" % k_cache.dtype)
+        if v_cache.dtype is not k_cache.dtype:
+            raise TypeError("v_cache must be %s like k_cache (got %s)" % (k_cache.dtype, v_cache.dtype))
+        if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must both be [num_pages, Hkv, page_size, d] (got %s and %s)"
+                             % (tuple(k_cache.shape), tuple(v_cache.shape)))
+        n, Hkv, page_size, d = k_cache.shape
+        page = Hkv * page_size * d
+        for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if n and not t[0].is_contiguous():
+                raise ValueError("the pages of %s must be contiguous" % what)
+        stride = max(k_cache.stride(0), page) if n <= 1 else k_cache.stride(0)
+        if n > 1 and (v_cache.stride(0) != stride or stride < page):
+            raise ValueError("the pages of k_cache and v_cache must lie equally far apart, without overlap "
+                             "(strides %d and %d)" % (k_cache.stride(0), v_cache.stride(0)))
+        if block_table.dtype is not torch.int32:
+            raise TypeError("block_table must be torch.int32 (got %s)" % block_table.dtype)
+        if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or (
+                block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]):
+            raise ValueError("block_table must be [B, max_pages] with contiguous rows")
+        e4m3 = k_cache.dtype is torch.float8_e4m3fn
+        scales = []
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not e4m3 and t is not None:
+                raise ValueError("%s is for e4m3 caches only" % what)
+            if e4m3:
+                if t is None:
+                    raise ValueError("an e4m3 cache needs %s" % what)
+                _check_shape(t, (Hkv,), what)
+                scales.append(_dev_ptr(t, "torch.float32", what))
+            else:
+                scales.append(None)
+        self.k_cache, self.v_cache, self.block_table = k_cache, v_cache, block_table
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device_index = k_cache.get_device()
+        self.B, self.Hkv, self.d = block_table.shape[0], Hkv, d
+        self.struct = PagedCacheStruct(
+            k_cache.data_ptr(), v_cache.data_ptr(), scales[0], scales[1], block_table.data_ptr(), stride,
+            max(block_table.stride(0), block_table.shape[1]), ELEM_E4M3 if e4m3 else ELEM_BF16, Hkv, d, page_size, n,
+            block_table.shape[1], self.B)
+        self._ref = ctypes.byref(self.struct)
+
+    def _ptr(self):
+        """The struct's reference, for a call on the current device."""
+        import torch
+        if torch.cuda.current_device() != self.device_index:
+            raise ValueError("the cache is on cuda:%d but the current device is cuda:%d"
+                             % (self.device_index, torch.cuda.current_device()))
+        return self._ref
+
+
+def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=None, q=None, q_out=None, stream=None):
+    """New keys and values k, v [B,Hkv,S,d] bf16 into the cache at positions
+    past_lens[b] + i, keys rotated by `rope` (a RopePlan) on the way; q
+    [B,Hq,S,d], where given, is rotated into q_out (q itself is fine; a new
+    tensor by default), which is returned."""
+    import torch
+    ref = cache._ptr()
+    dev = cache.device_index
+    bf16 = torch.bfloat16
+    pk, sk = _strided_ptr(k, bf16, "k", dev)
+    pv, sv = _strided_ptr(v, bf16, "v", dev)
+    if k.dim() != 4 or v.shape != k.shape or k.shape[0] != cache.B or k.shape[1] != cache.Hkv or k.shape[3] != cache.d:
+        raise ValueError("k and v must be [B=%d, Hkv=%d, S, d=%d] (got %s and %s)"
+                         % (cache.B, cache.Hkv, cache.d, tuple(k.shape), tuple(v.shape)))
+    B, _, S, d = k.shape
+    if rope is not None and not isinstance(rope, RopePlan):
+        raise TypeError("rope must be a RopePlan (mercury_rope_init)")
+    pq, sq, po, so, Hq = None, None, None, None, 0
+    if q is not None:
+        if q.dim() != 4 or q.shape[0] != B or q.shape[2] != S or q.shape[3] != d:
+            raise ValueError("q must be [B=%d, Hq, S=%d, d=%d] (got %s)" % (B, S, d, tuple(q.shape)))
+        Hq = q.shape[1]
+        pq, sq = _strided_ptr(q, bf16, "q", dev)
+        if q_out is None:
+            # rows behind new_lens are not written: zeros rather than whatever was there
+            q_out = (torch.empty if new_lens is None else torch.zeros)(q.shape, dtype=bf16, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have shape %s (got %s)" % (tuple(q.shape), tuple(q_out.shape)))
+        po, so = (pq, sq) if q_out is q else _strided_ptr(q_out, bf16, "q_out", dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if past_lens is None:
+        raise TypeError("past_lens must be a torch tensor")
+    _check(lib.mercury_kv_append(pk, sk, pv, sv, B, S, ref, _lens_ptr(past_lens, B, "past_lens"),
+                                 _lens_ptr(new_lens, B, "new_lens"), ctypes.byref(rope) if rope is not None else None,
+                                 pq, sq, Hq, po, so, _stream_ptr(stream)))
+    return q_out
+
+
+def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, stream):
+    import torch
+    ref = cache._ptr()
+    pq, sq = _strided_ptr(q, torch.bfloat16, "q", cache.device_index)
+    if q.dim() != 4 or q.shape[0] != cache.B or q.shape[3] != cache.d:
+        raise ValueError("q must be [B=%d, Hq, Sq, d=%d] (got %s)" % (cache.B, cache.d, tuple(q.shape)))
+    B, Hq, Sq, d = q.shape
+    # rows behind new_lens are not written: zeros rather than whatever was there
+    make = torch.empty if new_lens is None else torch.zeros
+    if out is None:
+        out = make((B, Hq, Sq, d), dtype=_dtype(out_dtype), device=q.device)
+    if lse is None:
+        lse = make((B, Hq, Sq), dtype=torch.float32, device=q.device)
+    _check_shape(out, (B, Hq, Sq, d), "out")
+    _check_shape(lse, (B, Hq, Sq), "lse")
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch tensor")
+    _check(fn(pq, sq, ref, _lens_ptr(seq_lens, B, "seq_lens"), _lens_ptr(new_lens, B, "new_lens"), B, Hq, Sq,
+              int(bool(causal)), _dev_ptr(out, out_dtype, "out"), _dev_ptr(lse, "torch.float32", "lse"),
+              _stream_ptr(stream)))
+    return out, lse
+
+
+def mercury_attn_paged(q, cache: PagedCache, seq_lens, new_lens=None, causal: bool = True, out=None, lse=None,
+                       stream=None):
+    """Attention of the newest tokens q [B,Hq,Sq,d] bf16 of every sequence over
+    the cache's first seq_lens[b] tokens; returns (out fp32, lse fp32)."""
+    return _attn_paged(lib.mercury_attn_paged, "torch.float32", q, cache, seq_lens, new_lens, causal, out, lse, stream)
+
+
+def mercury_attn_paged_bf16(q, cache: PagedCache, seq_lens, new_lens=None, causal: bool = True, out=None, lse=None,
+                            stream=None):
+    """As mercury_attn_paged, with O returned in bf16 (lse fp32)."""
+    return _attn_paged(lib.mercury_attn_paged_bf16, "torch.bfloat16", q, cache, seq_lens, new_lens, causal, out, lse,
+                       stream)
