@@ -42,9 +42,7 @@ __device__ unsigned int g_paged_err_site = 0;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 
 struct PagedArgs {
     const __nv_bfloat16 *q;
@@ -53,25 +51,29 @@ struct PagedArgs {
     const int *seq_lens, *new_lens;
     void *out;
     float *lse;
-    float *ws_o;    // [2 * blocks][rows of a tile][d]
-    float2 *ws_ml;  // [2 * blocks][rows of a tile]: maximum (log2 units), sum
-    int4 *ws_rec;   // [blocks]: the split job whose first part the block holds, and its last block
+    float *ws_o;    // [2 * blocks][rows of a tile][d]: unnormalised sums of a part
+    float2 *ws_ml;  // [2 * blocks][rows of a tile]: maximum (log2 units), sum of exponentials
+    int4 *ws_rec;   // [blocks]: job cut behind its first part in the block, its new tokens, -, its last
+                    // block (-1: none)
     int B, Hq, Hkv, G, Sq, R, n_rt, causal, out_bf16;
+    int records;    // blocks of the first kernel, for the join kernel
+    int tiled;      // pages hold whole runs of 16 keys
     float scale_log2;
 };
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8, int MT, int W, int CPS>
 struct Cfg {
+    static constexpr int kWarps = W, kThreads = W * 32;
     static constexpr int kRowB = D * (FP8 ? 1 : 2);        // bytes of one key
     static constexpr int kKeys = kRowB == 256 ? 16 : 32;   // keys of a warp's tile
     static constexpr int kTile = kKeys * kWarps;           // keys of a block's tile
     static constexpr int kPart = kKeys * kRowB;            // bytes of a warp's K (or V) tile
     static constexpr int kStage = 2 * kPart;
-    static constexpr int kStages = 196608 / (kWarps * kStage);
+    static constexpr int kStages = (232448 / CPS - 1024 - kWarps * (MT == 0 ? 8 : 16 * MT) * 8) / (kWarps * kStage);
     static constexpr int kMt = MT == 0 ? 1 : MT;           // 16-row tiles
     static constexpr int kRows = MT == 0 ? 8 : 16 * MT;
     static constexpr int kPassRows = MT == 0 ? 8 : 16;     // rows reduced at a time
-    static constexpr int kSmem = kWarps * kStages * kStage + kWarps * kRows * 8 + 64;
+    static constexpr int kSmem = kWarps * kStages * kStage + kWarps * kRows * 8;
     static_assert(kPassRows * D * 4 <= kStage, "a warp's partial rows fit into one of its stages");
 };
 
@@ -91,6 +93,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid
 {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
                  : "memory");
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy_commit()
@@ -161,7 +168,9 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_
 }
 
 // 16-byte chunk c of key row r in a copied tile: permuted within 128 bytes so
-// that the eight rows of a matrix load hit eight different bank groups.
+// that the eight rows of a matrix load hit eight different bank groups.  The
+// permutation is an exclusive or with bits of the row, so from a chunk's
+// address those of others follow by an exclusive or with a constant.
 template <int ROWB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c)
 {
@@ -182,10 +191,17 @@ __device__ __forceinline__ int new_of(const PagedArgs &a, int b)
     return a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.Sq) : a.Sq;
 }
 
-// A place in the list of all tiles of all jobs.
+// Positions.  All tiles of all jobs lie on one line, on which a job takes
+// kJobCost positions without a tile before its tiles: what beginning and
+// ending a job costs a block, in tiles, so that a share with many short jobs
+// is not longer than one with a few long ones.
+constexpr int kJobCost = 1;
+
+// A tile on that line.
 struct Place {
-    int b, h, rt, j;       // sequence, KV head, row tile, tile of the job
-    int tiles, keys, n;    // of sequence b: tiles of a job, keys, new tokens
+    int pos;          // its position
+    int b, hr, j;     // sequence, job (KV head * row tiles + row tile), tile of the job
+    int tiles, keys;  // of sequence b: tiles of a job, keys
 };
 
 template <int TILE>
@@ -198,87 +214,88 @@ template <int TILE>
 __device__ __forceinline__ void enter(const PagedArgs &a, Place &p)
 {
     p.keys = keys_of(a, p.b);
-    p.n = new_of(a, p.b);
-    p.tiles = tiles_of<TILE>(p.keys, p.n);
+    p.tiles = tiles_of<TILE>(p.keys, new_of(a, p.b));
 }
 
-// The next tile (the caller knows that there is one).
+// Whether the share that ends at `end` has another tile behind p.
+__device__ __forceinline__ bool has_next(const Place &p, int end)
+{
+    return p.pos + 1 + (p.j + 1 < p.tiles ? 0 : kJobCost) < end;
+}
+
+// That tile.
 template <int TILE>
 __device__ __forceinline__ void advance(const PagedArgs &a, Place &p)
 {
+    ++p.pos;
     if (++p.j < p.tiles)
         return;
+    p.pos += kJobCost;
     p.j = 0;
-    if (++p.rt < a.n_rt)
+    if (++p.hr < a.Hkv * a.n_rt)
         return;
-    p.rt = 0;
-    if (++p.h < a.Hkv)
-        return;
-    p.h = 0;
+    p.hr = 0;
     do {
-        ++p.b;
+        ++p.b;  // there is one: the position lies before the end
         enter<TILE>(a, p);
     } while (p.tiles == 0);
 }
 
-// Number of tiles of sequences c*kThreads + [0, kThreads) and this thread's
-// inclusive prefix of it.
+// The line in equal shares: block c has [first(c), first(c + 1)).
+struct Shares {
+    int each, more;  // positions of every share, and shares with one more
+    __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int pos) const
+    {
+        const int longer = more * (each + 1);
+        return pos < longer ? pos / (each + 1) : more + (pos - longer) / each;
+    }
+};
+
+// Positions of all jobs of sequence b (0 behind the last).
 template <int TILE>
-__device__ __forceinline__ int scan_tiles(const PagedArgs &a, int c, int &incl, int *warp_sums)
+__device__ __forceinline__ int length_of(const PagedArgs &a, int b)
 {
-    const int b = c * kThreads + threadIdx.x;
-    int w = 0;
-    if (b < a.B)
-        w = tiles_of<TILE>(keys_of(a, b), new_of(a, b)) * a.Hkv * a.n_rt;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += x;
-    }
-    __syncthreads();
-    if (lane == 31)
-        warp_sums[warp] = incl;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i == warp)
-            incl += total;
-        total += warp_sums[i];
-    }
-    return total;
+    if (b >= a.B)
+        return 0;
+    const int tiles = tiles_of<TILE>(keys_of(a, b), new_of(a, b));
+    return tiles == 0 ? 0 : (tiles + kJobCost) * a.Hkv * a.n_rt;
 }
 
-template <int D, bool FP8, int MT>
-__global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_constant__ PagedArgs a)
+__device__ __forceinline__ int warp_scan(int x, int lane)
 {
-    using C = Cfg<D, FP8, MT>;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    return x;
+}
+
+template <int D, bool FP8, int MT, int W, int CPS>
+__global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_constant__ PagedArgs a)
+{
+    using C = Cfg<D, FP8, MT, W, CPS>;
+    constexpr int kWarps = W, kThreads = W * 32;
     constexpr int ROWB = C::kRowB, KEYS = C::kKeys, TILE = C::kTile, NS = C::kStages, NT = KEYS / 8;
     constexpr int KK = D / 16, DN = D / 8;  // k-steps of Q.K, 8-column tiles of O
     extern __shared__ __align__(1024) char smem[];
     float *red_m = reinterpret_cast<float *>(smem + kWarps * NS * C::kStage);
     float *red_l = red_m + kWarps * C::kRows;
-    int *sums = reinterpret_cast<int *>(red_l + kWarps * C::kRows);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_wait();
 
-    // ---- this block's share of the tiles
-    const int chunks = (a.B + kThreads - 1) / kThreads;
-    int incl = 0, total = 0, first_total = 0;
-    for (int c = 0; c < chunks; ++c) {
-        int x;
-        const int s = scan_tiles<TILE>(a, c, x, sums);
-        if (c == 0) {
-            incl = x;
-            first_total = s;
-        }
-        total += s;
-    }
+    // ---- this block's share.  Every warp counts for itself, each lane a run of
+    // sequences, which costs no barrier.
+    const int per_lane = (a.B + 31) / 32;
+    int mine = 0;
+    for (int k = 0; k < per_lane; ++k)
+        mine += length_of<TILE>(a, lane * per_lane + k);
+    const int incl = warp_scan(mine, lane);
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
     if (blockIdx.x == 0)
         for (int b = tid; b < a.B; b += kThreads) {
             if (__ldg(a.seq_lens + b) != keys_of(a, b))
@@ -286,44 +303,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             if (a.new_lens && __ldg(a.new_lens + b) != new_of(a, b))
                 record_bounds(0x902);
         }
-    // every working block gets a tile at least, so that the blocks that share a
-    // job are neighbours
+    // every working block gets a position at least, so that the blocks that
+    // share a job are neighbours
     const int blocks = min((int)gridDim.x, total);
-    if ((int)blockIdx.x >= blocks) {
-        if (tid == 0 && a.ws_rec)
-            a.ws_rec[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (a.ws_rec && tid == 0)
+        a.ws_rec[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if ((int)blockIdx.x >= blocks)
         return;
-    }
-    const int start = (int)((long long)blockIdx.x * total / blocks);
-    const int end = (int)((long long)(blockIdx.x + 1) * total / blocks);
-    {
-        int base = 0;
-        for (int c = 0; c < chunks; ++c) {
-            int s = first_total;
-            if (c > 0)
-                s = scan_tiles<TILE>(a, c, incl, sums);
-            if (start >= base && start < base + s) {
-                const int b = c * kThreads + tid;
-                const int w = b < a.B ? tiles_of<TILE>(keys_of(a, b), new_of(a, b)) * a.Hkv * a.n_rt : 0;
-                const int off = start - (base + incl - w);
-                __syncthreads();
-                if (off >= 0 && off < w) {
-                    sums[8] = b;
-                    sums[9] = off;
-                }
-            }
-            base += s;
-        }
-    }
-    __syncthreads();
+    const Shares shares = {total / blocks, total % blocks};
+    const int end = shares.first(blockIdx.x + 1);
     Place at;
-    at.b = sums[8];
-    enter<TILE>(a, at);
+    at.pos = shares.first(blockIdx.x);
     {
-        const int off = sums[9], job = off / at.tiles;
-        at.j = off - job * at.tiles;
-        at.h = job / a.n_rt;
-        at.rt = job - at.h * a.n_rt;
+        // the lane whose run holds the position, the sequence in its run, the job
+        const int o = __ffs(__ballot_sync(0xffffffffu, incl > at.pos)) - 1;
+        int base = __shfl_sync(0xffffffffu, incl - mine, o);
+        at.b = o * per_lane;
+        for (int k = 0; per_lane > 1 && k < per_lane; k += 32) {
+            const int w = k + lane < per_lane ? length_of<TILE>(a, o * per_lane + k + lane) : 0;
+            const int x = warp_scan(w, lane);
+            const unsigned in = __ballot_sync(0xffffffffu, base + x > at.pos);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                at.b = o * per_lane + k + l;
+                base += __shfl_sync(0xffffffffu, x - w, l);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+        enter<TILE>(a, at);
+        const int off = at.pos - base, job = off / (at.tiles + kJobCost);
+        at.j = off - job * (at.tiles + kJobCost) - kJobCost;
+        at.hr = job;
+        if (at.j < 0) {  // the share begins between two jobs
+            at.pos -= at.j;
+            at.j = 0;
+        }
+        if (at.pos >= end)
+            return;
     }
 
     // ---- the ring of copied tiles: this warp's part of each block tile
@@ -332,109 +349,190 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     constexpr int CPR = ROWB / 16, RPP = 32 / CPR;  // chunks of a row, rows copied at a time
     const int my_row = lane / CPR, my_chunk = lane % CPR;
     Place ahead = at;
-    int ahead_t = start;
-    // the key row looked up by this lane for the next copy: page, row in it
-    int look_page = -1, look_row = 0, look_h = 0;
-    bool look_live = false;
-    auto look_up = [&]() {
-        look_live = ahead_t < end;
-        if (!look_live)
+    bool more = true;  // `ahead` is a tile of this share
+    // What was looked up for a copy: how many of the warp's keys exist, their
+    // head, and the page and row in it of each run of 16 keys, or where pages
+    // do not hold whole runs of 16, of this lane's key.  Two tiles are looked
+    // up ahead of the copies: an entry may come from memory, behind the copies
+    // in flight.
+    constexpr int RUNS = KEYS / 16;
+    struct Look {
+        int n, h, page[RUNS], row[RUNS];
+    };
+    Look look = {}, look2 = {};
+    auto look_up = [&](Look &l) {
+        l.n = 0;
+        if (!more)
             return;
-        const int key = (ahead.j * kWarps + warp) * KEYS + lane % KEYS;
-        look_page = -1;
-        look_h = ahead.h;
-        look_row = -1;
-        if (key < ahead.keys) {
-            const int pg = (int)((unsigned int)key / (unsigned int)a.cache.page_size);
-            look_row = key - pg * a.cache.page_size;
-            look_page = __ldg(a.cache.table + ahead.b * a.cache.table_stride + pg);
+        const int key0 = (ahead.j * kWarps + warp) * KEYS;
+        l.n = min(ahead.keys - key0, KEYS);
+        l.h = a.n_rt == 1 ? ahead.hr : ahead.hr / a.n_rt;
+        const int *entries = a.cache.table + ahead.b * a.cache.table_stride;
+#pragma unroll
+        for (int u = 0; u < RUNS; ++u) {
+            const int key = key0 + (a.tiled ? u * 16 : lane % KEYS);
+            l.row[u] = -1;
+            if (key < ahead.keys) {
+                const int pg = page_of(a.cache, key);
+                l.row[u] = key - pg * a.cache.page_size;
+                l.page[u] = __ldg(entries + pg);
+            }
         }
-        if (++ahead_t < end)
+        more = has_next(ahead, end);
+        if (more)
             advance<TILE>(a, ahead);
     };
+    // byte offset of a row of a page; -1, and a report, for a page that is none
+    auto offset_of = [&](int page, int row) {
+        if (page >= 0 && page < a.cache.num_pages)
+            return (page * a.cache.page_stride + ((long long)look.h * a.cache.page_size + row) * D) * (FP8 ? 1 : 2);
+        record_bounds(0x903);
+        return -1LL;
+    };
+    const uint32_t copy_to = ring_u + chunk_at<ROWB>(my_row, my_chunk);
     auto copy_tile = [&](int stage) {
-        if (look_live) {
-            long long off = -1;
-            if (look_row >= 0) {
-                if (look_page >= 0 && look_page < a.cache.num_pages)
-                    off = (look_page * a.cache.page_stride +
-                           ((long long)look_h * a.cache.page_size + look_row) * D) * (FP8 ? 1 : 2);
-                else
-                    record_bounds(0x903);
-            }
-            const uint32_t dst = ring_u + stage * C::kStage;
+        if (look.n > 0) {
+            const uint32_t base = copy_to + stage * C::kStage;
+            // row i * RPP + my_row: the same permutation but for these bits
+            auto to = [&](int i) { return (base ^ (ROWB >= 128 ? ((i * RPP) & 7) << 4 : 0)) + i * 512; };
+            if (a.tiled) {
 #pragma unroll
-            for (int i = 0; i < KEYS / RPP; ++i) {
-                const int r = i * RPP + my_row;
-                const long long o = __shfl_sync(0xffffffffu, off, r);
-                const long long src = max(o, 0LL) + my_chunk * 16;
-                const uint32_t to = dst + chunk_at<ROWB>(r, my_chunk);
-                copy16(to, a.cache.k + src, o >= 0);
-                copy16(to + C::kPart, a.cache.v + src, o >= 0);
+                for (int u = 0; u < RUNS; ++u) {
+                    const long long off = look.row[u] >= 0 ? offset_of(look.page[u], look.row[u]) : -1;
+                    const long long from = max(off, 0LL) + lane * 16;
+                    const char *ks = a.cache.k + from, *vs = a.cache.v + from;
+                    constexpr int N = 16 / RPP;
+                    if (off >= 0 && look.n >= u * 16 + 16) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            copy16(to(u * N + i), ks + i * 512);
+                            copy16(to(u * N + i) + C::kPart, vs + i * 512);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const bool ok = off >= 0 && u * 16 + i * RPP + my_row < look.n;
+                            copy16(to(u * N + i), ks + i * 512, ok);
+                            copy16(to(u * N + i) + C::kPart, vs + i * 512, ok);
+                        }
+                    }
+                }
+            } else {
+                const long long off = look.row[0] >= 0 ? offset_of(look.page[0], look.row[0]) : -1;
+#pragma unroll
+                for (int i = 0; i < KEYS / RPP; ++i) {
+                    const long long o = __shfl_sync(0xffffffffu, off, i * RPP + my_row);
+                    const long long from = max(o, 0LL) + my_chunk * 16;
+                    copy16(to(i), a.cache.k + from, o >= 0);
+                    copy16(to(i) + C::kPart, a.cache.v + from, o >= 0);
+                }
             }
         }
         copy_commit();
+        look = look2;
+        look_up(look2);
     };
+    uint32_t qf[C::kMt][KK][MT == 0 ? 2 : 4];
+    int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
+    auto load_q = [&]() {
+        h_kv = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
+        row0 = (at.hr - h_kv * a.n_rt) * C::kRows;
+        n_new = new_of(a, at.b);
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) {
-        look_up();
+        for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
+                const int r = row0 + mt * 16 + g + hf * 8;
+                const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
+                const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h_kv * a.G + head) * a.qs.h + s * a.qs.s;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint32_t x = 0, y = 0;
+                    if (r < a.R) {
+                        if (FP8) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * t);
+                            x = w.x;
+                            y = w.y;
+                        } else {
+                            x = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * t);
+                            y = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * t);
+                        }
+                    }
+                    qf[mt][kk][hf] = x;
+                    qf[mt][kk][MT == 0 ? 1 : 2 + hf] = y;
+                }
+            }
+    };
+    load_q();
+    look_up(look);
+    look_up(look2);
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i)
         copy_tile(i);
-    }
-    look_up();
 
     // ---- the tiles
-    uint32_t qf[C::kMt][KK][MT == 0 ? 2 : 4];
     float acc[C::kMt][DN][4];
     float m_run[C::kMt][2], l_run[C::kMt][2], s_mul[C::kMt][2];
     int lim[C::kMt][2];  // keys that each of this thread's rows sees
-    int rec_last = -1;
-    Place rec = at;
-    bool fresh = true;
+    bool fresh = true;  // the tile is the first of its job in this share
     int first_j = at.j;
 
-    for (int i = start; i < end; ++i) {
-        const int stage = (i - start) % NS;
+    constexpr int TPR = (kThreads >= 256 ? 256 : kThreads >= 128 ? 128 : kThreads >= 64 ? 64 : 32) / C::kPassRows;
+    constexpr int CP = D / TPR;  // columns of a thread, TPR threads a row, when rows are joined and written
+    const int my_line = tid / TPR, col0 = (tid % TPR) * CP;
+    // The finished row r of the current job from its maximum, sum and sums.
+    auto write_row = [&](int r, float top, float sum, const float (&o)[CP]) {
+        if (a.Sq > 1 && r % a.Sq >= n_new)
+            return;
+        const float f = sum == 0.f ? 0.f : (FP8 ? __ldg(a.cache.v_scale + h_kv) : 1.f) / sum;
+        const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
+#pragma unroll
+        for (int e = 0; e < CP; e += 2) {
+            if (a.out_bf16)
+                *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e) =
+                    pack_bf16(o[e] * f, o[e + 1] * f);
+            else
+                *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e) = make_float2(o[e] * f, o[e + 1] * f);
+        }
+        if (col0 == 0)
+            a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    };
+    // where the matrix loads of this lane begin in a tile (see the loops)
+    const uint32_t k_lane = ring_u + (FP8 ? chunk_at<ROWB>(lane, 0)
+                                          : chunk_at<ROWB>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+    const uint32_t v_lane = ring_u + C::kPart + (FP8 ? chunk_at<ROWB>(lane, 0)
+                                                     : chunk_at<ROWB>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4));
+    int stage = NS - 1;
+    for (;;) {
+        const int refill = stage;  // the stage that the last tile left
+        stage = stage == NS - 1 ? 0 : stage + 1;
         copy_wait<NS - 2>();
         __syncwarp();
-        copy_tile((i - start + NS - 1) % NS);
-        look_up();
+        copy_tile(refill);
 
         if (fresh) {
             fresh = false;
             first_j = at.j;
+            // a factor of at least 2^-120, so that a masked score stays -inf
+            // under it; a scale's sign goes to the queries
             float kmul = a.scale_log2;
-            if (FP8)
-                kmul *= __ldg(a.cache.k_scale + at.h);
+            uint32_t flip = 0;
+            if (FP8) {
+                kmul *= __ldg(a.cache.k_scale + h_kv);
+                flip = kmul < 0.f ? 0x80008000u : 0u;
+                kmul = fabsf(kmul);
+            }
 #pragma unroll
             for (int mt = 0; mt < C::kMt; ++mt)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int r = at.rt * C::kRows + mt * 16 + g + hf * 8;
-                    const bool live = r < a.R && (MT > 0 || hf == 0);
-                    const int head = at.h * a.G + r / a.Sq, s = r % a.Sq;
                     m_run[mt][hf] = -INFINITY;
                     l_run[mt][hf] = 0.f;
-                    lim[mt][hf] = a.causal ? at.keys - at.n + min(s, at.n - 1) + 1 : at.keys;
+                    const int s = (row0 + mt * 16 + g + hf * 8) % a.Sq;
+                    lim[mt][hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
                     s_mul[mt][hf] = kmul;
                     if (MT == 0 && hf == 1)
                         continue;
-                    const __nv_bfloat16 *src = a.q + at.b * a.qs.b + head * a.qs.h + s * a.qs.s;
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        uint32_t x = 0, y = 0;
-                        if (live) {
-                            if (FP8) {
-                                const uint2 w = *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * t);
-                                x = w.x;
-                                y = w.y;
-                            } else {
-                                x = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * t);
-                                y = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * t);
-                            }
-                        }
-                        qf[mt][kk][hf] = x;
-                        qf[mt][kk][MT == 0 ? 1 : 2 + hf] = y;
-                    }
                     if (FP8) {
                         // e4m3 keys widen exactly to fp16, so the queries are
                         // taken to fp16 too: scaled by a power of two that
@@ -453,12 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
                         up = min(max(up, -110), 110);
                         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                        s_mul[mt][hf] = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
+                        const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
+                        s_mul[mt][hf] = mul < 7.5e-37f ? 7.5e-37f : mul;
 #pragma unroll
                         for (int kk = 0; kk < KK; ++kk) {
                             uint32_t &x = qf[mt][kk][hf], &y = qf[mt][kk][MT == 0 ? 1 : 2 + hf];
-                            x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
-                            y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f);
+                            x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
+                            y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f) ^ flip;
                         }
                     }
                 }
@@ -473,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 
         const int kb = (at.j * kWarps + warp) * KEYS;
         if (kb < at.keys) {
-            const uint32_t k_u = ring_u + stage * C::kStage, v_u = k_u + C::kPart;
+            const uint32_t k_u = k_lane + stage * C::kStage, v_u = v_lane + stage * C::kStage;
             // ---- S = Q K^T
             float sc[C::kMt][NT][4];
 #pragma unroll
@@ -488,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
                     for (int n = 0; n < NT; n += 2) {
+                        // keys n*8 .. +15, elements kk*16 .. +15
                         uint32_t f[4];
-                        const int r = n * 8 + (lane >> 4) * 8 + (lane & 7);
-                        ldsm_x4(f, k_u + chunk_at<ROWB>(r, 2 * kk + ((lane >> 3) & 1)));
+                        ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * 128 + n * 8 * ROWB);
 #pragma unroll
                         for (int mt = 0; mt < C::kMt; ++mt) {
                             const uint32_t a1 = MT == 0 ? 0u : qf[mt][kk][1], a3 = MT == 0 ? 0u : qf[mt][kk][MT == 0 ? 1 : 3];
@@ -507,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     uint32_t f[4];
-                    ldsm_x4(f, k_u + chunk_at<ROWB>(lane, kk));
+                    ldsm_x4(f, k_u ^ (kk << 4));
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const uint32_t b0 = e4m3_to_f16(f[n]), b1 = e4m3_to_f16(f[n] >> 16);
@@ -520,30 +619,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 }
             }
             // ---- running maximum and sum; the masked keys of a row count as -inf
-            const int seen_by_all = a.causal ? at.keys - at.n + 1 : at.keys;
+            const int seen_by_all = a.causal ? at.keys - n_new + 1 : at.keys;
             const bool edge = kb + KEYS > seen_by_all;
-            uint32_t p_hi[C::kMt][NT][2], p_lo[C::kMt][NT][2];
+            if (edge) {
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt) {
-#pragma unroll
-                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                    float top = -INFINITY;
+                for (int mt = 0; mt < C::kMt; ++mt)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &x = sc[mt][n][hf * 2 + e];
-                            x *= s_mul[mt][hf];
-                            if (edge && kb + n * 8 + t * 2 + e >= lim[mt][hf])
-                                x = -INFINITY;
-                            top = fmaxf(top, x);
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float m_old = m_run[mt][hf], m_new = fmaxf(m_old, top);
-                    const float m_ref = m_new == -INFINITY ? 0.f : m_new;
-                    if (__any_sync(0xffffffffu, m_new != m_old)) {
-                        const float f = ex2(m_old - m_ref);
+                        for (int e = 0; e < 4; ++e)
+                            if (kb + n * 8 + t * 2 + (e & 1) >= lim[mt][e >> 1])
+                                sc[mt][n][e] = -INFINITY;
+            }
+            // The maximum moves only when a score exceeds it by 2^8: sum and O
+            // share whatever reference the terms were taken with, and the
+            // reduction and the rescaling stay off the common path.
+            bool grow = false;
+            float top[C::kMt][2];
+#pragma unroll
+            for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
+                    float x = fmaxf(sc[mt][0][hf * 2], sc[mt][0][hf * 2 + 1]);
+#pragma unroll
+                    for (int n = 1; n < NT; ++n)
+                        x = fmaxf(x, fmaxf(sc[mt][n][hf * 2], sc[mt][n][hf * 2 + 1]));
+                    top[mt][hf] = x * s_mul[mt][hf];
+                    grow |= top[mt][hf] > m_run[mt][hf] + 8.f;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
+                        float x = top[mt][hf];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        x = fmaxf(x, m_run[mt][hf]);
+                        const float f = x == -INFINITY ? 1.f : ex2(m_run[mt][hf] - x);
+                        m_run[mt][hf] = x;
                         l_run[mt][hf] *= f;
 #pragma unroll
                         for (int n = 0; n < DN; ++n)
@@ -554,17 +668,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                                     acc[mt][n][2 + e] *= f;
                             }
                     }
-                    m_run[mt][hf] = m_new;
+            }
+            uint32_t p_hi[C::kMt][NT][2], p_lo[C::kMt][NT][2];
+#pragma unroll
+            for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
+                    const float ref = m_run[mt][hf] == -INFINITY ? 0.f : -m_run[mt][hf];
                     float sum = 0.f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const float p0 = ex2(sc[mt][n][hf * 2] - m_ref), p1 = ex2(sc[mt][n][hf * 2 + 1] - m_ref);
+                        const float p0 = ex2(fmaf(sc[mt][n][hf * 2], s_mul[mt][hf], ref));
+                        const float p1 = ex2(fmaf(sc[mt][n][hf * 2 + 1], s_mul[mt][hf], ref));
                         sum += p0 + p1;
                         split2<FP8>(p0, p1, p_hi[mt][n][hf], p_lo[mt][n][hf]);
                     }
                     l_run[mt][hf] += sum;
                 }
-            }
             // ---- O += P V
             auto add_pv = [&](float (&d)[4], int mt, int n, uint32_t b0, uint32_t b1) {
                 if constexpr (MT == 0) {
@@ -583,8 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 #pragma unroll
                         for (int c = 0; c < DN; c += 2) {
                             uint32_t f[4];
-                            const int r = n * 8 + ((lane >> 3) & 1) * 8 + (lane & 7);
-                            ldsm_x4_t(f, v_u + chunk_at<ROWB>(r, c + (lane >> 4)));
+                            ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * 128 + n * 8 * ROWB);
                             use(c, n, f[0], f[1]);
                             use(c + 1, n, f[2], f[3]);
                         }
@@ -595,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 #pragma unroll
                     for (int c = 0; c < DN; c += 2) {
                         uint32_t f[4];
-                        ldsm_x4_t(f, v_u + chunk_at<ROWB>(lane, c >> 1));
+                        ldsm_x4_t(f, v_u ^ ((c >> 1) << 4));
 #pragma unroll
                         for (int n = 0; n < 4; n += 2) {
                             const uint32_t x = __byte_perm(f[n], 0, 0x3120), y = __byte_perm(f[n + 1], 0, 0x3120);
@@ -608,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             // A key that only some rows see still meets the others' products,
             // as 0 * v: harmless unless v is infinite or NaN.
             bool poison = false;
-            if (edge && a.causal && at.n > 1) {
+            if (edge && a.causal && n_new > 1) {
                 const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
                 for (int r = r0; r < r1; ++r)
                     for (int w = lane; w < ROWB / 4; w += 32) {
@@ -628,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             } else {
                 // token by token, the last first: the keys that token s does
                 // not see are zeroed, and only its rows take the product
-                for (int s = at.n - 1; s >= 0; --s) {
-                    const int seen = at.keys - at.n + s + 1;
+                for (int s = n_new - 1; s >= 0; --s) {
+                    const int seen = at.keys - n_new + s + 1;
                     __syncwarp();
                     for (int r = max(seen - kb, 0); r < KEYS; ++r)
                         for (int w = lane; w < ROWB / 4; w += 32)
@@ -640,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         for (int mt = 0; mt < C::kMt; ++mt) {
                             float d[4] = {0.f, 0.f, 0.f, 0.f};
                             add_pv(d, mt, n, b0, b1);
-                            const int r = at.rt * C::kRows + mt * 16 + g;
+                            const int r = row0 + mt * 16 + g;
                             const bool own0 = r % a.Sq == s, own1 = MT == 0 ? own0 : (r + 8) % a.Sq == s;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -654,16 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 
         // ---- the job's or the share's end: join the warps
         const bool last_tile = at.j == at.tiles - 1;
-        if (last_tile || i == end - 1) {
+        const bool on = has_next(at, end);
+        if (last_tile || !on) {
             const bool whole = first_j == 0 && last_tile;
             const int slot = 2 * blockIdx.x + (first_j == 0 ? 1 : 0);
-            if (first_j == 0 && !last_tile) {
-                // the block that holds the job's last tile
-                const long long x = (long long)i + (at.tiles - 1 - at.j);
-                rec = at;
-                rec_last = (int)(((x + 1) * blocks - 1) / total);
-            }
-            constexpr int TPR = kThreads / C::kPassRows, CP = D / TPR;  // threads of a row, columns of a thread
 #pragma unroll
             for (int mt = 0; mt < C::kMt; ++mt) {
                 if (mt > 0)
@@ -700,162 +813,190 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     }
                 }
                 __syncthreads();
-                const int row = tid / TPR, col0 = (tid % TPR) * CP;
-                float top = -INFINITY;
+                const int row = my_line, r = row0 + mt * 16 + row;
+                if (row < C::kPassRows && r < a.R) {
+                    float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    top = fmaxf(top, red_m[w * C::kRows + mt * 16 + row]);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float sum = 0.f, o[CP];
+                    for (int w = 0; w < kWarps; ++w)
+                        top = fmaxf(top, red_m[w * C::kRows + mt * 16 + row]);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f, o[CP];
 #pragma unroll
-                for (int e = 0; e < CP; ++e)
-                    o[e] = 0.f;
+                    for (int e = 0; e < CP; ++e)
+                        o[e] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ex2(red_m[w * C::kRows + mt * 16 + row] - ref);
-                    sum += f * red_l[w * C::kRows + mt * 16 + row];
-                    const float *src = reinterpret_cast<const float *>(smem + w * (NS * C::kStage) + stage * C::kStage) + row * D;
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = ex2(red_m[w * C::kRows + mt * 16 + row] - ref);
+                        sum += f * red_l[w * C::kRows + mt * 16 + row];
+                        const float *src =
+                            reinterpret_cast<const float *>(smem + w * (NS * C::kStage) + stage * C::kStage) + row * D;
 #pragma unroll
-                    for (int e = 0; e < CP; e += 2) {
-                        const int col = col0 + e;
-                        const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
-                        o[e] += f * x.x;
-                        o[e + 1] += f * x.y;
+                        for (int e = 0; e < CP; e += 2) {
+                            const int col = col0 + e;
+                            const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
+                            o[e] += f * x.x;
+                            o[e + 1] += f * x.y;
+                        }
                     }
-                }
-                const int r = at.rt * C::kRows + mt * 16 + row;
-                if (!whole) {
-                    const long long at_ws = (long long)slot * C::kRows + mt * 16 + row;
+                    if (whole) {
+                        write_row(r, top, sum, o);
+                    } else {
+                        const long long at_ws = (long long)slot * C::kRows + mt * 16 + row;
 #pragma unroll
-                    for (int e = 0; e < CP; e += 2)
-                        *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e) = make_float2(o[e], o[e + 1]);
-                    if (col0 == 0)
-                        a.ws_ml[at_ws] = make_float2(top, sum);
-                } else if (r < a.R && r % a.Sq < at.n) {
-                    const float f = sum == 0.f ? 0.f : (FP8 ? __ldg(a.cache.v_scale + at.h) : 1.f) / sum;
-                    const long long at_row = ((long long)at.b * a.Hq + at.h * a.G) * a.Sq + r;
-#pragma unroll
-                    for (int e = 0; e < CP; e += 2) {
-                        if (a.out_bf16)
-                            *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e) =
-                                pack_bf16(o[e] * f, o[e + 1] * f);
-                        else
-                            *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e) =
-                                make_float2(o[e] * f, o[e + 1] * f);
+                        for (int e = 0; e < CP; e += 2)
+                            *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e) = make_float2(o[e], o[e + 1]);
+                        if (col0 == 0)
+                            a.ws_ml[at_ws] = make_float2(top, sum);
                     }
-                    if (col0 == 0)
-                        a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                 }
             }
+            if (first_j == 0 && !last_tile && tid == 0)  // the first part of a cut job: where is its last?
+                a.ws_rec[blockIdx.x] = make_int4(at.b * a.Hkv * a.n_rt + at.hr, n_new, 0,
+                                                 shares.owner(at.pos - at.j + at.tiles - 1));
             __syncthreads();
             fresh = true;
         }
-        if (i + 1 < end)
-            advance<TILE>(a, at);
+        if (!on)
+            break;
+        advance<TILE>(a, at);
+        if (fresh)
+            load_q();
     }
     copy_wait<0>();
-    if (tid == 0 && a.ws_rec)
-        a.ws_rec[blockIdx.x] = make_int4(rec.b, rec.h, rec.rt, rec_last);
 }
 
-// Joins the parts of a job that was cut between blocks: one thread block per
-// (block that holds a first part, row of the tile).
+// Joins the parts of the jobs that were cut between blocks: blockIdx.y is a row
+// of the tile, and each block takes the records of every gridDim.x-th block of
+// the first kernel, 32 in one look.  Each warp joins every eighth part of the
+// row, then the warps join through shared memory.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __grid_constant__ PagedArgs a)
 {
     constexpr int W = kJoinThreads / 32, PER = D / 32;
-    __shared__ float part[W][D], red[W], sums[W];
-    // every block waits, also those with nothing to do: the call is over only
-    // when the first kernel is
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int first = blockIdx.x, row = blockIdx.y;
-    const int4 rec = a.ws_rec[first];
-    const int r = rec.z * ROWS + row;
-    if (rec.w < 0 || r >= a.R || r % a.Sq >= new_of(a, rec.x))
-        return;
-    const int n = rec.w - first + 1;
+    __shared__ float part[W][D], tops[W], sums[W];
+    chain_wait();
+    const int row = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto slot_of = [&](int i) { return (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * ROWS + row; };
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += kJoinThreads)
-        top = fmaxf(top, a.ws_ml[slot_of(i)].x);
+    for (int from = blockIdx.x; from < a.records; from += 32 * gridDim.x) {
+        const int mine = from + lane * gridDim.x;
+        int4 rec = make_int4(0, 0, 0, -1);
+        if (mine < a.records)
+            rec = __ldcg(a.ws_rec + mine);
+        unsigned todo = __ballot_sync(0xffffffffu, rec.w >= 0);
+        while (todo) {
+            const int l = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int first = from + l * gridDim.x, last = __shfl_sync(0xffffffffu, rec.w, l);
+            const int job = __shfl_sync(0xffffffffu, rec.x, l), n_new = __shfl_sync(0xffffffffu, rec.y, l);
+            const int bh = job / a.n_rt, r = (job - bh * a.n_rt) * ROWS + row;
+            if (r >= a.R || (a.Sq > 1 && r % a.Sq >= n_new))
+                continue;
+            const int n = last - first + 1;
+            float top = -INFINITY, sum = 0.f, o[PER];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0)
-        red[warp] = top;
-    __syncthreads();
+            for (int e = 0; e < PER; ++e)
+                o[e] = 0.f;
+            constexpr int U = 8;  // parts in flight
+            for (int i0 = warp; i0 < n; i0 += W * U) {
+                float2 ml[U];
+                float x[U][PER];
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-        top = fmaxf(top, red[w]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o[PER];
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * W;
+                    ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int e = 0; e < PER; ++e)
-        o[e] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += W) {
-        const long long s = slot_of(i);
-        const float2 ml = a.ws_ml[s];
-        const float f = ex2(ml.x - ref);
-        sum += f * ml.y;
-        const float *src = a.ws_o + s * D + lane * PER;
-        float x[PER];
-        if constexpr (PER == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            x[0] = v.x, x[1] = v.y;
+                    for (int e = 0; e < PER; ++e)
+                        x[u][e] = 0.f;
+                    if (i < n) {
+                        const long long s = (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * ROWS + row;
+                        ml[u] = __ldcg(a.ws_ml + s);
+                        const float *src = a.ws_o + s * D + lane * PER;
+                        if constexpr (PER == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                            x[u][0] = v.x, x[u][1] = v.y;
+                        }
+                    }
+                }
+                float m = top;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    m = fmaxf(m, ml[u].x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                const float f0 = ex2(top - ref);
+                top = m;
+                sum *= f0;
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    o[e] *= f0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float f = ex2(ml[u].x - ref);
+                    sum += f * ml[u].y;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e)
+                        o[e] += f * x[u][e];
+                }
+            }
+            __syncthreads();  // the last job's sums have been read
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                part[warp][lane * PER + e] = o[e];
+            if (lane == 0) {
+                tops[warp] = top;
+                sums[warp] = sum;
+            }
+            __syncthreads();
+            if (tid >= D)
+                continue;
+            top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                top = fmaxf(top, tops[w]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float x = 0.f;
+            sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f = ex2(tops[w] - ref);
+                sum += f * sums[w];
+                x += f * part[w][tid];
+            }
+            const long long at_row = (long long)bh * a.R + r;
+            x *= sum == 0.f ? 0.f : (a.cache.v_scale ? __ldg(a.cache.v_scale + bh % a.Hkv) : 1.f) / sum;
+            if (a.out_bf16)
+                ((__nv_bfloat16 *)a.out)[at_row * D + tid] = __float2bfloat16_rn(x);
+            else
+                ((float *)a.out)[at_row * D + tid] = x;
+            if (tid == 0)
+                a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-            o[e] += f * x[e];
     }
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-        part[warp][lane * PER + e] = o[e];
-    if (lane == 0)
-        sums[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-        sum += sums[w];
-    const long long at_row = ((long long)rec.x * a.Hq + rec.y * a.G) * a.Sq + r;
-    const float f = sum == 0.f ? 0.f : (a.cache.v_scale ? __ldg(a.cache.v_scale + rec.y) : 1.f) / sum;
-    for (int c = tid; c < D; c += kJoinThreads) {
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            x += part[w][c];
-        if (a.out_bf16)
-            ((__nv_bfloat16 *)a.out)[at_row * D + c] = __float2bfloat16_rn(x * f);
-        else
-            ((float *)a.out)[at_row * D + c] = x * f;
-    }
-    if (tid == 0)
-        a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8, int MT, int W, int CPS>
 int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    using C = Cfg<D, FP8, MT>;
+    using C = Cfg<D, FP8, MT, W, CPS>;
     a.n_rt = (a.R + C::kRows - 1) / C::kRows;
+    a.tiled = a.cache.page_size % 16 == 0;
     const long long keys = (long long)a.cache.max_pages * a.cache.page_size;
-    const long long most = (keys + C::kTile - 1) / C::kTile * a.B * a.Hkv * a.n_rt;
+    const long long jobs = (long long)a.B * a.Hkv * a.n_rt;
+    const long long most = ((keys + C::kTile - 1) / C::kTile + kJobCost) * jobs;
     if (most > 0x7fffffffLL) {
         snprintf(msg, msg_len, "too many key tiles for one call (%lld)", most);
         return MERCURY_EINVAL;
     }
-    auto *kernel = attn_paged_kernel<D, FP8, MT>;
+    auto *kernel = attn_paged_kernel<D, FP8, MT, W, CPS>;
     KernelInfo ki;
     int rc = prepare_kernel((const void *)kernel, C::kSmem, &ki, msg, msg_len);
     if (rc != MERCURY_OK)
         return rc;
-    // one block per SM, and none that could not get a tile
-    const unsigned grid = (unsigned)(most < ki.sms ? most : ki.sms);
+    // as many blocks as the SMs hold at once, and none that could not get a tile
+    const unsigned grid = (unsigned)(most < ki.sms * CPS ? most : ki.sms * CPS);
+    a.records = (int)grid;
     // a job that fits into one tile is never cut: no parts, nothing to join
     const bool split = keys > C::kTile;
     void *ws = nullptr;
@@ -875,20 +1016,10 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         a.ws_ml = (float2 *)((char *)ws + o_bytes);
         a.ws_rec = (int4 *)((char *)ws + o_bytes + ml_bytes);
     }
-    kernel<<<grid, kThreads, C::kSmem, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && split) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(grid, C::kRows);
-        cfg.blockDim = dim3(kJoinThreads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D, C::kRows>, a);
-    }
+    cudaError_t e = launch_chained(kernel, dim3(grid), C::kThreads, C::kSmem, stream, a);
+    if (e == cudaSuccess && split)
+        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid < (unsigned)ki.sms ? grid : ki.sms, C::kRows < a.R ? C::kRows : a.R),
+                           kJoinThreads, 0, stream, a);
     rc = MERCURY_OK;
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "paged attention launch: %s", cudaGetErrorString(e));
@@ -905,13 +1036,24 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 }
 
 template <int D, bool FP8>
-int launch_rows(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
+int launch_rows(PagedArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    if (a.R <= 8)
-        return launch<D, FP8, 0>(a, stream, msg, msg_len);
+    // Warps a block and blocks an SM, measured at the sizes named.  Eight warps
+    // in one block leave the fewest parts to join (one 4K sequence of 8 KV
+    // heads: 8.5 us against 9.4 with three blocks of four).  Many short jobs
+    // want several blocks, one of which streams while another changes jobs (64
+    // sequences of 1 to 2047 tokens, 16 heads of 64: 53 us in one block, 48 in
+    // three), and so do 8-bit keys, whose conversions one block does not hide
+    // (8 sequences of 20K to 32K: 79 against 75 us).
+    const long long jobs = (long long)a.B * a.Hkv;
+    if (a.R <= 8) {
+        if (jobs >= 2 * sms)
+            return launch<D, FP8, 0, 4, 3>(a, stream, msg, msg_len);
+        return FP8 ? launch<D, FP8, 0, 4, 2>(a, stream, msg, msg_len) : launch<D, FP8, 0, 8, 1>(a, stream, msg, msg_len);
+    }
     if (a.R <= 16)
-        return launch<D, FP8, 1>(a, stream, msg, msg_len);
-    return launch<D, FP8, 2>(a, stream, msg, msg_len);
+        return FP8 ? launch<D, FP8, 1, 4, 2>(a, stream, msg, msg_len) : launch<D, FP8, 1, 8, 1>(a, stream, msg, msg_len);
+    return launch<D, FP8, 2, 4, 2>(a, stream, msg, msg_len);
 }
 
 }  // namespace
@@ -937,12 +1079,16 @@ int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cach
     a.causal = causal;
     a.out_bf16 = out_bf16;
     a.scale_log2 = kLog2e / sqrtf((float)cache.d);
+    int sms = 0;
+    int rc = device_sm_count(&sms);
+    if (rc != MERCURY_OK)
+        return rc;
     const bool fp8 = cache.elem == MERCURY_ELEM_E4M3;
     if (!fp8)
         a.cache.v_scale = nullptr;
     if (cache.d == 128)
-        return fp8 ? launch_rows<128, true>(a, stream, msg, msg_len) : launch_rows<128, false>(a, stream, msg, msg_len);
-    return fp8 ? launch_rows<64, true>(a, stream, msg, msg_len) : launch_rows<64, false>(a, stream, msg, msg_len);
+        return fp8 ? launch_rows<128, true>(a, sms, stream, msg, msg_len) : launch_rows<128, false>(a, sms, stream, msg, msg_len);
+    return fp8 ? launch_rows<64, true>(a, sms, stream, msg, msg_len) : launch_rows<64, false>(a, sms, stream, msg, msg_len);
 }
 
 int read_and_clear_paged_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)

@@ -50,6 +50,7 @@ template <bool FP8, int VE>
 __global__ void __launch_bounds__(kRotThreads) append_kernel(const __grid_constant__ AppendArgs a)
 {
     using T = __nv_bfloat16;
+    chain_wait();
     const int lane_units = kRotThreads / a.tokens_per_block;
     const long long token = (long long)blockIdx.x * a.tokens_per_block + threadIdx.x / lane_units;
     if (token >= a.tokens)
@@ -73,12 +74,12 @@ __global__ void __launch_bounds__(kRotThreads) append_kernel(const __grid_consta
     if (pos < 0 || pos >= (long long)c.max_pages * c.page_size) {
         record_bounds(0x802);
     } else {
-        const unsigned int at = (unsigned int)pos / (unsigned int)c.page_size;
+        const int at = page_of(c, (int)pos);
         const int page = c.table[b * c.table_stride + at];
         if (page < 0 || page >= c.num_pages)
             record_bounds(0x803);
         else
-            row = page * c.page_stride + ((long long)((unsigned int)pos - at * c.page_size)) * a.d;
+            row = page * c.page_stride + (pos - (long long)at * c.page_size) * a.d;
     }
     const long long head_stride = (long long)c.page_size * a.d;
 
@@ -154,8 +155,8 @@ int launch(AppendArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_le
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
-    append_kernel<FP8, VE><<<dim3((unsigned)g.blocks, (unsigned)g.head_groups), kRotThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(append_kernel<FP8, VE>, dim3((unsigned)g.blocks, (unsigned)g.head_groups),
+                                         kRotThreads, 0, stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cache append kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -17,6 +17,34 @@ constexpr unsigned int kPagedErrBounds = 2u;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Launch chaining.  The serving kernels run a few microseconds each, one after
+// another on a stream, so each may be brought onto the GPU while the kernel
+// before it still runs (launch_chained) and waits for that kernel's end, and
+// with it for everything earlier on the stream, before it touches memory.
+// Every thread calls chain_wait first thing: a block that returned without it
+// would let the grid end, and its successor begin, before the predecessor did.
+__device__ __forceinline__ void chain_wait()
+{
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+
+template <typename Args>
+cudaError_t launch_chained(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                           const Args &args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // A tensor's element strides over (batch, head, token); the head dimension is
 // contiguous.
 struct Strides {
@@ -30,7 +58,13 @@ struct PagedView {
     const int *table;        // [B][max_pages], rows table_stride apart
     long long page_stride, table_stride;
     int Hkv, page_size, num_pages, max_pages;
+    int page_shift;          // log2 of page_size, or -1 where it is no power of two
 };
+
+__device__ __forceinline__ int page_of(const PagedView &c, int pos)
+{
+    return c.page_shift >= 0 ? pos >> c.page_shift : (int)((unsigned int)pos / (unsigned int)c.page_size);
+}
 
 inline PagedView make_view(const mercury_paged_cache &c)
 {
@@ -46,6 +80,10 @@ inline PagedView make_view(const mercury_paged_cache &c)
     v.page_size = c.page_size;
     v.num_pages = c.num_pages;
     v.max_pages = c.max_pages;
+    v.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (c.page_size == 1 << i)
+            v.page_shift = i;
     return v;
 }
 

@@ -41,6 +41,7 @@ struct RopeArgs {
 template <typename T, int VE>
 __global__ void __launch_bounds__(kRotThreads) rope_kernel(const __grid_constant__ RopeArgs a)
 {
+    chain_wait();
     const int lane_units = kRotThreads / a.tokens_per_block;
     const long long token = (long long)blockIdx.x * a.tokens_per_block + threadIdx.x / lane_units;
     if (token >= a.tokens)
@@ -90,8 +91,8 @@ int launch(RopeArgs &a, int B, int sms, cudaStream_t stream, char *msg, size_t m
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
-    rope_kernel<T, VE><<<dim3((unsigned)g.blocks, (unsigned)g.head_groups), kRotThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_chained(rope_kernel<T, VE>, dim3((unsigned)g.blocks, (unsigned)g.head_groups), kRotThreads, 0, stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "rope kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -162,10 +162,10 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
         lanes *= 2;
     g.tokens_per_block = kRotThreads / lanes;
     g.blocks = (tokens + g.tokens_per_block - 1) / g.tokens_per_block;
-    // Heads per thread: as many as leave eight blocks for each SM (an angle
+    // Heads per thread: as many as leave two blocks for each SM (an angle
     // costs about as much as moving two heads), at most 16.
     int hp = 16;
-    while (hp > 1 && g.blocks * ((H + hp - 1) / hp) < 8LL * sms)
+    while (hp > 1 && g.blocks * ((H + hp - 1) / hp) < 2LL * sms)
         hp /= 2;
     g.heads_per_thread = hp;
     g.head_groups = (H + hp - 1) / hp;

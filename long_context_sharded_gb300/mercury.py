@@ -494,18 +494,57 @@ def mercury_tune_cache_clear() -> None:
 _Strides = ctypes.c_longlong * 3
 
 
-def _strided_ptr(t, dtype, what, dev):
-    """(device pointer, stride array or None where contiguous) of a [B, H, S, d]
-    CUDA tensor whose heads are contiguous, on device `dev`."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+class _Torch:
+    """The torch names that the serving calls use, looked up once: those calls
+    are bound by their marshalling (a decode step's kernels take a few
+    microseconds), so they query each tensor as little as their checks need."""
+
+    def __init__(self):
+        import torch
+        self.Tensor, self.empty, self.zeros = torch.Tensor, torch.empty, torch.zeros
+        self.bf16, self.fp32, self.int32 = torch.bfloat16, torch.float32, torch.int32
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_torch_names = None
+
+
+def _names():
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _refuse(t, dtype, dev, what):
+    """Says what is wrong with a tensor that a call cannot take."""
+    if not isinstance(t, _names().Tensor):
         raise TypeError("%s must be a torch tensor" % what)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s (got %s)" % (what, dtype, t.dtype))
     if t.get_device() != dev:
-        raise ValueError("%s is on %s but the current device is cuda:%d" % (what, t.device, dev))
+        raise ValueError("%s is on %s but the call runs on cuda:%d" % (what, t.device, dev))
+    raise ValueError("%s must be contiguous" % what)
+
+
+def _flat(t, dtype, dev, shape, what):
+    """Device pointer of a contiguous tensor of this dtype and shape on device `dev`."""
+    if not (isinstance(t, _torch_names.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _refuse(t, dtype, dev, what)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s (got %s)" % (what, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _heads(t, dtype, dev, what):
+    """(device pointer, stride array or None where contiguous) of a 4-D tensor
+    on device `dev` whose heads (last axis) are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, dev, what)
     if t.is_contiguous():
         return t.data_ptr(), None
     st = t.stride()
@@ -514,14 +553,15 @@ def _strided_ptr(t, dtype, what, dev):
     return t.data_ptr(), _Strides(st[0], st[1], st[2])
 
 
-def _lens_ptr(t, B, what):
-    """Device pointer of a contiguous [B] int32 CUDA tensor, or None."""
-    if t is None:
-        return None
-    p = _dev_ptr(t, "torch.int32", what)
-    if t.dim() != 1 or t.shape[0] != B:
-        raise ValueError("%s must have shape (%d,) (got %s)" % (what, B, tuple(t.shape)))
-    return p
+def _on_current(dev, what):
+    cur = _torch_names.current_device()
+    if cur != dev:
+        raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (what, dev, cur))
+
+
+def _is_4d(t, what):
+    if not isinstance(t, _names().Tensor) or t.dim() != 4:
+        raise ValueError("%s must be a 4-D tensor" % what)
 
 
 def mercury_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -560,31 +600,41 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
     with contiguous heads).  positions: int32 [B,S] or [S]; None: start + s.
     inverse=True applies the transpose, the gradient of the forward call.
     out: a tensor of x's shape and dtype, or x itself; a new one by default."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dim() != 4:
-        raise ValueError("x must be a 4-D [B, H, S, d] tensor")
+    T = _names()
+    _is_4d(x, "x")
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (mercury_rope_init)")
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("x must be torch.bfloat16 or torch.float32 (got %s)" % x.dtype)
-    B, H, S, d = x.shape
-    dev = torch.cuda.current_device() if x.is_cuda else -1
-    px, sx = _strided_ptr(x, x.dtype, "x", dev)
+    dtype = x.dtype
+    if dtype is not T.bf16 and dtype is not T.fp32:
+        raise TypeError("x must be torch.bfloat16 or torch.float32 (got %s)" % dtype)
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
+    _on_current(dev, "x")
+    shape = x.shape
+    B, H, S, d = shape
+    px, sx = _heads(x, dtype, dev, "x")
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif out.shape != x.shape:
-        raise ValueError("out must have shape %s (got %s)" % (tuple(x.shape), tuple(out.shape)))
-    po, so = (px, sx) if out is x else _strided_ptr(out, x.dtype, "out", dev)
+        out = T.empty(shape, dtype=dtype, device=x.device)
+        po, so = out.data_ptr(), None
+    elif out is x:
+        po, so = px, sx
+    else:
+        _is_4d(out, "out")
+        if out.shape != shape:
+            raise ValueError("out must have shape %s (got %s)" % (tuple(shape), tuple(out.shape)))
+        po, so = _heads(out, dtype, dev, "out")
     pp, row = None, 0
     if positions is not None:
-        pp = _dev_ptr(positions, "torch.int32", "positions")
-        if positions.shape == (B, S):
-            row = S
-        elif positions.shape != (S,):
-            raise ValueError("positions must have shape %s or %s (got %s)" % ((B, S), (S,), tuple(positions.shape)))
-    _check(lib.mercury_rope(px, sx, pp, row, int(start), B, H, S, d,
-                            ELEM_FP32 if x.dtype is torch.float32 else ELEM_BF16, ctypes.byref(plan),
-                            int(bool(inverse)), po, so, _stream_ptr(stream)))
+        if not isinstance(positions, T.Tensor):
+            raise TypeError("positions must be a torch tensor")
+        row = S if positions.dim() == 2 else 0
+        pp = _flat(positions, T.int32, dev, (B, S) if row else (S,), "positions")
+    rc = lib.mercury_rope(px, sx, pp, row, start, B, H, S, d, ELEM_BF16 if dtype is T.bf16 else ELEM_FP32,
+                          ctypes.byref(plan), 1 if inverse else 0, po, so,
+                          T.raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -640,6 +690,7 @@ class PagedCache:
                 scales.append(_dev_ptr(t, "torch.float32", what))
             else:
                 scales.append(None)
+        _names()
         self.k_cache, self.v_cache, self.block_table = k_cache, v_cache, block_table
         self.k_scale, self.v_scale = k_scale, v_scale
         self.device_index = k_cache.get_device()
@@ -650,74 +701,85 @@ class PagedCache:
             block_table.shape[1], self.B)
         self._ref = ctypes.byref(self.struct)
 
-    def _ptr(self):
-        """The struct's reference, for a call on the current device."""
-        import torch
-        if torch.cuda.current_device() != self.device_index:
-            raise ValueError("the cache is on cuda:%d but the current device is cuda:%d"
-                             % (self.device_index, torch.cuda.current_device()))
-        return self._ref
-
 
 def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=None, q=None, q_out=None, stream=None):
     """New keys and values k, v [B,Hkv,S,d] bf16 into the cache at positions
     past_lens[b] + i, keys rotated by `rope` (a RopePlan) on the way; q
     [B,Hq,S,d], where given, is rotated into q_out (q itself is fine; a new
     tensor by default), which is returned."""
-    import torch
-    ref = cache._ptr()
+    T = _names()
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
     dev = cache.device_index
-    bf16 = torch.bfloat16
-    pk, sk = _strided_ptr(k, bf16, "k", dev)
-    pv, sv = _strided_ptr(v, bf16, "v", dev)
-    if k.dim() != 4 or v.shape != k.shape or k.shape[0] != cache.B or k.shape[1] != cache.Hkv or k.shape[3] != cache.d:
+    _on_current(dev, "the cache")
+    _is_4d(k, "k")
+    _is_4d(v, "v")
+    shape = k.shape
+    B, Hkv, S, d = shape
+    if v.shape != shape or B != cache.B or Hkv != cache.Hkv or d != cache.d:
         raise ValueError("k and v must be [B=%d, Hkv=%d, S, d=%d] (got %s and %s)"
-                         % (cache.B, cache.Hkv, cache.d, tuple(k.shape), tuple(v.shape)))
-    B, _, S, d = k.shape
-    if rope is not None and not isinstance(rope, RopePlan):
-        raise TypeError("rope must be a RopePlan (mercury_rope_init)")
-    pq, sq, po, so, Hq = None, None, None, None, 0
+                         % (cache.B, cache.Hkv, cache.d, tuple(shape), tuple(v.shape)))
+    pk, sk = _heads(k, T.bf16, dev, "k")
+    pv, sv = _heads(v, T.bf16, dev, "v")
+    plan = None
+    if rope is not None:
+        if not isinstance(rope, RopePlan):
+            raise TypeError("rope must be a RopePlan (mercury_rope_init)")
+        plan = ctypes.byref(rope)
+    pq = sq = po = so = None
+    Hq = 0
     if q is not None:
-        if q.dim() != 4 or q.shape[0] != B or q.shape[2] != S or q.shape[3] != d:
-            raise ValueError("q must be [B=%d, Hq, S=%d, d=%d] (got %s)" % (B, S, d, tuple(q.shape)))
-        Hq = q.shape[1]
-        pq, sq = _strided_ptr(q, bf16, "q", dev)
+        _is_4d(q, "q")
+        qshape = q.shape
+        Hq = qshape[1]
+        if qshape[0] != B or qshape[2] != S or qshape[3] != d:
+            raise ValueError("q must be [B=%d, Hq, S=%d, d=%d] (got %s)" % (B, S, d, tuple(qshape)))
+        pq, sq = _heads(q, T.bf16, dev, "q")
         if q_out is None:
             # rows behind new_lens are not written: zeros rather than whatever was there
-            q_out = (torch.empty if new_lens is None else torch.zeros)(q.shape, dtype=bf16, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have shape %s (got %s)" % (tuple(q.shape), tuple(q_out.shape)))
-        po, so = (pq, sq) if q_out is q else _strided_ptr(q_out, bf16, "q_out", dev)
+            q_out = (T.empty if new_lens is None else T.zeros)(qshape, dtype=T.bf16, device=q.device)
+            po = q_out.data_ptr()
+        elif q_out is q:
+            po, so = pq, sq
+        else:
+            _is_4d(q_out, "q_out")
+            if q_out.shape != qshape:
+                raise ValueError("q_out must have shape %s (got %s)" % (tuple(qshape), tuple(q_out.shape)))
+            po, so = _heads(q_out, T.bf16, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if past_lens is None:
-        raise TypeError("past_lens must be a torch tensor")
-    _check(lib.mercury_kv_append(pk, sk, pv, sv, B, S, ref, _lens_ptr(past_lens, B, "past_lens"),
-                                 _lens_ptr(new_lens, B, "new_lens"), ctypes.byref(rope) if rope is not None else None,
-                                 pq, sq, Hq, po, so, _stream_ptr(stream)))
+    rc = lib.mercury_kv_append(pk, sk, pv, sv, B, S, cache._ref, _flat(past_lens, T.int32, dev, (B,), "past_lens"),
+                               None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), plan,
+                               pq, sq, Hq, po, so, T.raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return q_out
 
 
 def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, stream):
-    import torch
-    ref = cache._ptr()
-    pq, sq = _strided_ptr(q, torch.bfloat16, "q", cache.device_index)
-    if q.dim() != 4 or q.shape[0] != cache.B or q.shape[3] != cache.d:
-        raise ValueError("q must be [B=%d, Hq, Sq, d=%d] (got %s)" % (cache.B, cache.d, tuple(q.shape)))
-    B, Hq, Sq, d = q.shape
+    T = _torch_names
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    dev = cache.device_index
+    _on_current(dev, "the cache")
+    _is_4d(q, "q")
+    shape = q.shape
+    B, Hq, Sq, d = shape
+    if B != cache.B or d != cache.d:
+        raise ValueError("q must be [B=%d, Hq, Sq, d=%d] (got %s)" % (cache.B, cache.d, tuple(shape)))
+    pq, sq = _heads(q, T.bf16, dev, "q")
     # rows behind new_lens are not written: zeros rather than whatever was there
-    make = torch.empty if new_lens is None else torch.zeros
+    make = T.empty if new_lens is None else T.zeros
     if out is None:
-        out = make((B, Hq, Sq, d), dtype=_dtype(out_dtype), device=q.device)
+        out = make(shape, dtype=out_dtype, device=q.device)
     if lse is None:
-        lse = make((B, Hq, Sq), dtype=torch.float32, device=q.device)
-    _check_shape(out, (B, Hq, Sq, d), "out")
-    _check_shape(lse, (B, Hq, Sq), "lse")
-    if seq_lens is None:
-        raise TypeError("seq_lens must be a torch tensor")
-    _check(fn(pq, sq, ref, _lens_ptr(seq_lens, B, "seq_lens"), _lens_ptr(new_lens, B, "new_lens"), B, Hq, Sq,
-              int(bool(causal)), _dev_ptr(out, out_dtype, "out"), _dev_ptr(lse, "torch.float32", "lse"),
-              _stream_ptr(stream)))
+        lse = make((B, Hq, Sq), dtype=T.fp32, device=q.device)
+    rc = fn(pq, sq, cache._ref, _flat(seq_lens, T.int32, dev, (B,), "seq_lens"),
+            None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), B, Hq, Sq,
+            1 if causal else 0, _flat(out, out_dtype, dev, shape, "out"), _flat(lse, T.fp32, dev, (B, Hq, Sq), "lse"),
+            T.raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out, lse
 
 
@@ -725,11 +787,11 @@ def mercury_attn_paged(q, cache: PagedCache, seq_lens, new_lens=None, causal: bo
                        stream=None):
     """Attention of the newest tokens q [B,Hq,Sq,d] bf16 of every sequence over
     the cache's first seq_lens[b] tokens; returns (out fp32, lse fp32)."""
-    return _attn_paged(lib.mercury_attn_paged, "torch.float32", q, cache, seq_lens, new_lens, causal, out, lse, stream)
+    return _attn_paged(lib.mercury_attn_paged, _names().fp32, q, cache, seq_lens, new_lens, causal, out, lse, stream)
 
 
 def mercury_attn_paged_bf16(q, cache: PagedCache, seq_lens, new_lens=None, causal: bool = True, out=None, lse=None,
                             stream=None):
     """As mercury_attn_paged, with O returned in bf16 (lse fp32)."""
-    return _attn_paged(lib.mercury_attn_paged_bf16, "torch.bfloat16", q, cache, seq_lens, new_lens, causal, out, lse,
+    return _attn_paged(lib.mercury_attn_paged_bf16, _names().bf16, q, cache, seq_lens, new_lens, causal, out, lse,
                        stream)
