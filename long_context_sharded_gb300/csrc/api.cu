@@ -159,7 +159,7 @@ int collect_device_errors(cudaStream_t stream)
         if (w[i] & 2u)
             return fail(MERCURY_EBOUNDS, "checked build: an out-of-range index was found and its access skipped "
                         "(site 0x%x)", site[i]);
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < n; ++i)
         if (w[i] & 1u)
             return fail(MERCURY_ETIMEOUT, "a bounded device wait ran out (site 0x%x)", site[i]);
     return MERCURY_OK;
@@ -383,6 +383,17 @@ char *error_buffer(size_t *len)
 int finish_call(int rc, cudaStream_t stream)
 {
     return finish(rc, stream);
+}
+
+unsigned long long device_wait_ns()
+{
+    return wait_budget_ns();
+}
+
+int paged_fault()
+{
+    const char *e = getenv("MERCURY_FAULT");
+    return e && strcmp(e, "drop_page_copy") == 0;
 }
 
 int device_scratch_pool(cudaMemPool_t *pool)

@@ -16,12 +16,13 @@
 //     share's end it leaves the unnormalised partial sums, maximum and sum
 //     (at most two per block), which a second kernel joins by the exact
 //     log-sum-exp rule.  That kernel is resident before the first one ends.
-//   * within a block every warp takes its own keys of the tile through its own
-//     ring of asynchronous copies and never waits for another warp before the
-//     end of a job; rows are looked up in the block table key by key, one tile
-//     ahead, so any page size will do and no page has to end with a tile.
+//   * in a block four warps do nothing but look up pages and send tensor
+//     copies of whole tiles into a ring of stages, across the ends of jobs, so
+//     the memory is kept busy while the other eight change jobs; with copies
+//     and look-ups spread over the computing warps these took more of a tile's
+//     time (1000 cycles of 2800) than its products.
 //   * both products run on warp-level matrix instructions: the rows of one KV
-//     head fill at most 8 to 32 rows of a tile, and the operands come straight
+//     head fill at most 8 to 64 rows of a tile, and the operands come straight
 //     from the copied tile.  P goes in as two 16-bit terms (value and
 //     remainder), which holds O to 32-bit outputs; with at most 8 rows the
 //     remainder rides in the tile's idle half and costs nothing.
@@ -31,20 +32,30 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace mercury {
 
 // Error word of this file's kernels: kPagedErrBounds = a length or page
-// outside the table or the cache; the first site (0x901 seq_lens, 0x902
-// new_lens, 0x903 page).
+// outside the table or the cache, kErrTimeout = a bounded wait ran out; the
+// first site (0x901 seq_lens, 0x902 new_lens, 0x903 page, 0x904 wait).
 __device__ unsigned int g_paged_err_word = 0;
 __device__ unsigned int g_paged_err_site = 0;
 
 namespace {
 
+constexpr int kWarps = 8;                    // computing warps of a block
+constexpr int kCopyWarps = 4;                // and those that copy
+constexpr int kThreads = (kWarps + kCopyWarps) * 32;
+// Registers a thread after the split (setmaxnreg): the copying warpgroup's go
+// to the computing ones.  Their sum may not exceed what the launch provides.
+constexpr uint32_t kRegsCopy = 72;
+constexpr uint32_t kRegsCompute = 216;
+constexpr int kMinLaunchRegs = (int)(kRegsCopy * 128 + kRegsCompute * kWarps * 32 + kThreads - 1) / kThreads;
 constexpr int kJoinThreads = 256;
 
 struct PagedArgs {
+    CUtensorMap map_k, map_v;  // the cache in boxes of box_rows keys, where box_rows > 0
     const __nv_bfloat16 *q;
     Strides qs;
     PagedView cache;
@@ -57,35 +68,61 @@ struct PagedArgs {
                     // block (-1: none)
     int B, Hq, Hkv, G, Sq, R, n_rt, causal, out_bf16;
     int records;    // blocks of the first kernel, for the join kernel
-    int tiled;      // pages hold whole runs of 16 keys
+    int box_rows;   // keys of a tensor copy: the largest power of two that divides page_size, at most a
+                    // tile; 0 below 16, where keys are copied one by one
     float scale_log2;
+    int fault;      // test hook: withhold one copy
+    unsigned long long wait_ns;
 };
 
-template <int D, bool FP8, int MT, int W, int CPS>
+// RG: 16-row groups of a row tile; 0 for a tile of 8 rows.  The computing
+// warps are RG row groups times 8 / RG key groups, each with kKeys keys at a
+// time; a tile's keys are the same for every RG.
+template <int D, bool FP8, int RG>
 struct Cfg {
-    static constexpr int kWarps = W, kThreads = W * 32;
-    static constexpr int kRowB = D * (FP8 ? 1 : 2);        // bytes of one key
-    static constexpr int kKeys = kRowB == 256 ? 16 : 32;   // keys of a warp's tile
-    static constexpr int kTile = kKeys * kWarps;           // keys of a block's tile
-    static constexpr int kPart = kKeys * kRowB;            // bytes of a warp's K (or V) tile
+    static constexpr int kRowB = D * (FP8 ? 1 : 2);            // bytes of one key
+    static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;    // bytes of a key in one box
+    static constexpr int kKeys = kRowB == 256 ? 16 : 32;       // keys of a warp's step
+    static constexpr int kTile = kKeys * kWarps;               // keys of a block's tile
+    static constexpr int kRg = RG == 0 ? 1 : RG;
+    static constexpr int kKg = kWarps / kRg;
+    static constexpr int kPart = kTile * kRowB;                // bytes of a tile's keys (or values)
     static constexpr int kStage = 2 * kPart;
-    static constexpr int kStages = (232448 / CPS - 1024 - kWarps * (MT == 0 ? 8 : 16 * MT) * 8) / (kWarps * kStage);
-    static constexpr int kMt = MT == 0 ? 1 : MT;           // 16-row tiles
-    static constexpr int kRows = MT == 0 ? 8 : 16 * MT;
-    static constexpr int kPassRows = MT == 0 ? 8 : 16;     // rows reduced at a time
-    static constexpr int kSmem = kWarps * kStages * kStage + kWarps * kRows * 8;
-    static_assert(kPassRows * D * 4 <= kStage, "a warp's partial rows fit into one of its stages");
+    static constexpr int kStages = 196608 / kStage;
+    static constexpr int kRows = RG == 0 ? 8 : 16 * RG;
+    static constexpr int kWarpRows = RG == 0 ? 8 : 16;
+    static constexpr int kRed = kWarps * kWarpRows * 8;        // each warp's maxima and sums
+    static constexpr int kSmem = kStages * kStage + kRed + kStages * 16;
+    static_assert(kTile % (32 * kCopyWarps) == 0, "whole runs for each copying warp");
+    static_assert(kWarps * kWarpRows * D * 4 <= kStage, "the warps' partial rows fit into a stage");
 };
 
-__device__ __noinline__ void record_bounds(unsigned int site)
+__device__ __forceinline__ void record_bounds(unsigned int site)
 {
     atomicOr(&g_paged_err_word, kPagedErrBounds);
     atomicCAS(&g_paged_err_site, 0u, site);
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p)
+// Waits for a phase of `bar`, at most `budget` ns.  A wait that runs out is
+// recorded and leaves later ones a millisecond each; the caller goes on with
+// whatever data there is, since which tiles, rows and barriers it touches does
+// not depend on them.
+__device__ __forceinline__ unsigned long long wait_long(uint64_t *bar, uint32_t parity, unsigned long long budget)
 {
-    return (uint32_t)__cvta_generic_to_shared(p);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > budget) {
+            atomicOr(&g_paged_err_word, kErrTimeout);
+            atomicCAS(&g_paged_err_site, 0u, 0x904u);
+            return 1000000;
+        }
+    return budget;
+}
+
+__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, unsigned long long &budget)
+{
+    if (!mbar_try_wait(bar, parity))
+        budget = wait_long(bar, parity, budget);
 }
 
 // 16 bytes global -> shared; zeros where !valid (the source is not read).
@@ -95,20 +132,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid
                  : "memory");
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+// One arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t *bar)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy_commit()
-{
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
@@ -145,39 +172,49 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ex2(float x)
+// 4-D tiled bulk tensor load global -> shared, completion counted in bytes on
+// `bar`; c0 (elements) is a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3)
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
 
 // p as the sum of two 16-bit terms: the nearest, and the nearest to what it
-// leaves (2^-18 of p at most in bf16, far less in fp16).
+// leaves (2^-18 of p at most in bf16, 2^-22 in fp16).  Returns the sum of what
+// the terms stand for: the rows are normalised by the weights that they were
+// taken with, so that what the terms lose cancels where one key dominates.
 template <bool F16>
-__device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ float split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
 {
     if constexpr (F16) {
         hi = pack_f16(p0, p1);
         const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
         lo = pack_f16(p0 - h.x, p1 - h.y);
+        return p0 + p1;
     } else {
         hi = pack_bf16(p0, p1);
         lo = pack_bf16(p0 - bf16_lo(hi), p1 - bf16_hi(hi));
+        return (bf16_lo(hi) + bf16_lo(lo)) + (bf16_hi(hi) + bf16_hi(lo));
     }
 }
 
-// 16-byte chunk c of key row r in a copied tile: permuted within 128 bytes so
-// that the eight rows of a matrix load hit eight different bank groups.  The
-// permutation is an exclusive or with bits of the row, so from a chunk's
-// address those of others follow by an exclusive or with a constant.
-template <int ROWB>
+// A copied tile's keys (or values): boxes of all its keys x kBoxB bytes (128,
+// or 64 for heads of 64 bytes), the 16-byte chunks of a row permuted so that
+// the eight rows of a matrix load hit eight different bank groups -- the
+// layout of a tensor copy with 128- (64-) byte swizzle.  The permutation is an
+// exclusive or with bits of the row, so from a chunk's address those of others
+// follow by an exclusive or with a constant.
+template <int ROWB, int TILE>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c)
 {
-    if constexpr (ROWB >= 128)
-        return r * ROWB + ((c ^ (r & 7)) << 4);
-    else
-        return r * ROWB + ((c ^ ((r >> 1) & 3)) << 4);
+    constexpr int B = ROWB < 128 ? ROWB : 128, CB = B / 16;
+    const int x = ROWB >= 128 ? r & 7 : (r >> 1) & 3;
+    return c / CB * TILE * B + r * B + (((c % CB) ^ x) << 4);
 }
 
 __device__ __forceinline__ int keys_of(const PagedArgs &a, int b)
@@ -191,15 +228,18 @@ __device__ __forceinline__ int new_of(const PagedArgs &a, int b)
     return a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.Sq) : a.Sq;
 }
 
-// Positions.  All tiles of all jobs lie on one line, on which a job takes
-// kJobCost positions without a tile before its tiles: what beginning and
-// ending a job costs a block, in tiles, so that a share with many short jobs
-// is not longer than one with a few long ones.
-constexpr int kJobCost = 1;
+// Positions.  All jobs lie on one line, in units of an eighth of a tile, the
+// time that its keys take: a full tile is eight, a job's last one as many as
+// it has eighths, and a job takes kJobCost more before its first tile, what
+// changing jobs costs a block (64 sequences of 1 to 2047 tokens, 16 heads of
+// 64: 58 us with 2 units, 52.5 with 4, 47.7 with 12, 48.9 with 24).  A tile
+// belongs to the share that holds its first unit.
+constexpr int kUnits = 8;
+constexpr int kJobCost = 14;
 
 // A tile on that line.
 struct Place {
-    int pos;          // its position
+    int pos;          // its first unit
     int b, hr, j;     // sequence, job (KV head * row tiles + row tile), tile of the job
     int tiles, keys;  // of sequence b: tiles of a job, keys
 };
@@ -217,26 +257,33 @@ __device__ __forceinline__ void enter(const PagedArgs &a, Place &p)
     p.tiles = tiles_of<TILE>(p.keys, new_of(a, p.b));
 }
 
-// Whether the share that ends at `end` has another tile behind p.
-__device__ __forceinline__ bool has_next(const Place &p, int end)
+// Units of a job's last tile.
+template <int TILE>
+__device__ __forceinline__ int last_units(int keys, int tiles)
 {
-    return p.pos + 1 + (p.j + 1 < p.tiles ? 0 : kJobCost) < end;
+    return max(1, (keys - (tiles - 1) * TILE + TILE / kUnits - 1) / (TILE / kUnits));
 }
 
-// That tile.
+// First unit of the tile behind p (of the next job's first one, if there is one).
 template <int TILE>
-__device__ __forceinline__ void advance(const PagedArgs &a, Place &p)
+__device__ __forceinline__ int next_pos(const Place &p)
 {
-    ++p.pos;
+    return p.pos + (p.j + 1 < p.tiles ? kUnits : last_units<TILE>(p.keys, p.tiles) + kJobCost);
+}
+
+// The tile at `pos`, the one behind p.
+template <int TILE>
+__device__ __forceinline__ void advance(const PagedArgs &a, Place &p, int pos)
+{
+    p.pos = pos;
     if (++p.j < p.tiles)
         return;
-    p.pos += kJobCost;
     p.j = 0;
     if (++p.hr < a.Hkv * a.n_rt)
         return;
     p.hr = 0;
     do {
-        ++p.b;  // there is one: the position lies before the end
+        ++p.b;  // there is one: the position lies before the share's end
         enter<TILE>(a, p);
     } while (p.tiles == 0);
 }
@@ -258,8 +305,8 @@ __device__ __forceinline__ int length_of(const PagedArgs &a, int b)
 {
     if (b >= a.B)
         return 0;
-    const int tiles = tiles_of<TILE>(keys_of(a, b), new_of(a, b));
-    return tiles == 0 ? 0 : (tiles + kJobCost) * a.Hkv * a.n_rt;
+    const int keys = keys_of(a, b), tiles = tiles_of<TILE>(keys, new_of(a, b));
+    return tiles == 0 ? 0 : (kJobCost + (tiles - 1) * kUnits + last_units<TILE>(keys, tiles)) * a.Hkv * a.n_rt;
 }
 
 __device__ __forceinline__ int warp_scan(int x, int lane)
@@ -273,29 +320,205 @@ __device__ __forceinline__ int warp_scan(int x, int lane)
     return x;
 }
 
-template <int D, bool FP8, int MT, int W, int CPS>
-__global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_constant__ PagedArgs a)
+// This block's share: its first tile and the position behind its last; false
+// where it has none.  Called by whole warps: each counts for itself, a lane a
+// run of sequences, which costs no barrier.
+template <int TILE>
+__device__ __forceinline__ bool find_share(const PagedArgs &a, int lane, Shares &shares, Place &at, int &end)
 {
-    using C = Cfg<D, FP8, MT, W, CPS>;
-    constexpr int kWarps = W, kThreads = W * 32;
-    constexpr int ROWB = C::kRowB, KEYS = C::kKeys, TILE = C::kTile, NS = C::kStages, NT = KEYS / 8;
-    constexpr int KK = D / 16, DN = D / 8;  // k-steps of Q.K, 8-column tiles of O
-    extern __shared__ __align__(1024) char smem[];
-    float *red_m = reinterpret_cast<float *>(smem + kWarps * NS * C::kStage);
-    float *red_l = red_m + kWarps * C::kRows;
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    chain_wait();
-
-    // ---- this block's share.  Every warp counts for itself, each lane a run of
-    // sequences, which costs no barrier.
     const int per_lane = (a.B + 31) / 32;
     int mine = 0;
     for (int k = 0; k < per_lane; ++k)
         mine += length_of<TILE>(a, lane * per_lane + k);
-    const int incl = warp_scan(mine, lane);
+    const int incl = a.B == 1 ? __shfl_sync(0xffffffffu, mine, 0) : warp_scan(mine, lane);
     const int total = __shfl_sync(0xffffffffu, incl, 31);
+    // every share is a tile long at least, so that each of those that a job is
+    // cut into holds one of its tiles
+    const int blocks = total > 0 ? min((int)gridDim.x, max(total / kUnits, 1)) : 0;
+    if ((int)blockIdx.x >= blocks)
+        return false;
+    shares.each = total / blocks;
+    shares.more = total - shares.each * blocks;
+    end = shares.first(blockIdx.x + 1);
+    at.pos = shares.first(blockIdx.x);
+    // the lane whose run holds the position, the sequence in its run, the job
+    const int o = __ffs(__ballot_sync(0xffffffffu, incl > at.pos)) - 1;
+    int base = __shfl_sync(0xffffffffu, incl - mine, o);
+    at.b = o * per_lane;
+    for (int k = 0; per_lane > 1 && k < per_lane; k += 32) {
+        const int w = k + lane < per_lane ? length_of<TILE>(a, o * per_lane + k + lane) : 0;
+        const int x = warp_scan(w, lane);
+        const unsigned in = __ballot_sync(0xffffffffu, base + x > at.pos);
+        if (in) {
+            const int l = __ffs(in) - 1;
+            at.b = o * per_lane + k + l;
+            base += __shfl_sync(0xffffffffu, x - w, l);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    enter<TILE>(a, at);
+    const int length = kJobCost + (at.tiles - 1) * kUnits + last_units<TILE>(at.keys, at.tiles);
+    at.hr = (at.pos - base) / length;
+    // the first tile whose first unit lies in the share
+    const int job = base + at.hr * length + kJobCost;
+    at.j = max(at.pos - job + kUnits - 1, 0) / kUnits;
+    at.pos = job + at.j * kUnits;
+    if (at.j == at.tiles) {
+        at.j = at.tiles - 1;
+        at.pos -= kUnits;
+        const int pos = next_pos<TILE>(at);
+        if (pos >= end)
+            return false;
+        advance<TILE>(a, at, pos);
+    }
+    return at.pos < end;
+}
+
+// The copying warps: every tile of the share into the ring, a stage as soon as
+// the computing warps have left it.  A tile's boxes (or runs of 32 keys) are
+// dealt to the four warps in turn: with pages of 16 keys a tile is 32 tensor
+// copies, which took one warp 2200 cycles.
+template <int D, bool FP8, int RG>
+__device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end, char *smem, uint64_t *full,
+                                           uint64_t *empty, int warp, int lane)
+{
+    using C = Cfg<D, FP8, RG>;
+    constexpr int ROWB = C::kRowB, TILE = C::kTile, NS = C::kStages, N = TILE / 32 / kCopyWarps;
+    constexpr int ES = FP8 ? 1 : 2, CPR = ROWB / 16, RPP = 32 / CPR;  // chunks of a row, rows copied at a time
+    unsigned long long budget = a.wait_ns;
+    // Page entries of the next tile, asked for a tile ahead: with tensor
+    // copies lane l's is that of box l * kCopyWarps + warp, else those of key l
+    // of this warp's runs.
+    int entry[N];
+    const int first = (lane * kCopyWarps + warp) * a.box_rows;  // this lane's box
+    auto run = [&](int i) { return (i * kCopyWarps + warp) * 32; };
+    auto key_of = [&](int i) { return at.j * TILE + (a.box_rows ? first : run(i) + lane); };
+    auto look_up = [&]() {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i == 0 || !a.box_rows) && key_of(i) < at.keys)
+                entry[i] = __ldg(a.cache.table + at.b * a.cache.table_stride + page_of(a.cache, key_of(i)));
+    };
+    look_up();
+    int stage = 0;
+    uint32_t phase = 1;  // a fresh ring's stages count as left
+    for (int tile = 0;; ++tile) {
+        const int next = next_pos<TILE>(at);
+        const bool on = next < end;
+        const int h = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
+        char *const part = smem + stage * C::kStage;
+        wait_phase(empty + stage, phase, budget);
+        if (a.box_rows) {
+            const int key = key_of(0);
+            const int page = entry[0], row = key - page_of(a.cache, key) * a.cache.page_size;
+            const bool live = first < TILE && key < at.keys;
+            const bool good = live && page >= 0 && page < a.cache.num_pages;
+            if (live && !good) {  // such keys count as zeros
+                record_bounds(0x903);
+                for (int r = first; r < first + a.box_rows; ++r)
+                    for (int c = 0; c < CPR; ++c) {
+                        const uint32_t to = smem_u32(part) + chunk_at<ROWB, TILE>(r, c);
+                        st_shared_v4(to, 0, 0, 0, 0);
+                        st_shared_v4(to + C::kPart, 0, 0, 0, 0);
+                    }
+                fence_proxy_async_smem();
+            }
+            const int boxes = __popc(__ballot_sync(0xffffffffu, good));
+            const bool withheld = a.fault && tile == 0 && warp == 0;
+            if (lane == 0 && !withheld)
+                mbar_arrive_expect_tx(full + stage, boxes * a.box_rows * 2 * ROWB);
+            __syncwarp();
+            if (good && !withheld) {
+#pragma unroll
+                for (int x = 0; x < ROWB / C::kBoxB; ++x) {
+                    const uint32_t to = smem_u32(part) + x * TILE * C::kBoxB + first * C::kBoxB;
+                    tma_load_4d(to, &a.map_k, smem_u32(full + stage), x * (C::kBoxB / ES), row, h, page);
+                    tma_load_4d(to + C::kPart, &a.map_v, smem_u32(full + stage), x * (C::kBoxB / ES), row, h, page);
+                }
+            }
+        } else {
+            const int my_row = lane / CPR, my_chunk = lane % CPR;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int key = key_of(i);
+                long long off = -1;  // byte offset of this lane's key
+                if (key < at.keys) {
+                    if (entry[i] >= 0 && entry[i] < a.cache.num_pages)
+                        off = (entry[i] * a.cache.page_stride +
+                               ((long long)h * a.cache.page_size + key - page_of(a.cache, key) * a.cache.page_size) * D) * ES;
+                    else
+                        record_bounds(0x903);
+                }
+#pragma unroll 4
+                for (int p = 0; p < CPR; ++p) {
+                    const int r = p * RPP + my_row;
+                    const long long o = __shfl_sync(0xffffffffu, off, r), from = max(o, 0LL) + my_chunk * 16;
+                    const uint32_t to = smem_u32(part) + chunk_at<ROWB, TILE>(run(i) + r, my_chunk);
+                    copy16(to, a.cache.k + from, o >= 0);
+                    copy16(to + C::kPart, a.cache.v + from, o >= 0);
+                }
+            }
+            copy_arrive(full + stage);
+        }
+        if (!on)
+            break;
+        advance<TILE>(a, at, next);
+        look_up();
+        if (at.j == 0 && warp == 0) {
+            // a new job: its queries into L2 by the time the computing warps
+            // get there
+            const int h1 = a.n_rt == 1 ? at.hr : at.hr / a.n_rt, row0 = (at.hr - h1 * a.n_rt) * C::kRows;
+            for (int r = row0 + lane; r < min(row0 + C::kRows, a.R); r += 32) {
+                const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
+                const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h1 * a.G + head) * a.qs.h + s * a.qs.s;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                if (D == 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+            }
+        }
+        if (++stage == NS) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+template <int D, bool FP8, int RG>
+__global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_constant__ PagedArgs a)
+{
+    using C = Cfg<D, FP8, RG>;
+    constexpr int ROWB = C::kRowB, KEYS = C::kKeys, TILE = C::kTile, NS = C::kStages, NT = KEYS / 8;
+    constexpr int KK = D / 16, DN = D / 8;  // k-steps of Q.K, 8-column tiles of O
+    constexpr int BOX = C::kBoxB, BOXES = TILE * BOX;  // bytes from a row to the next, from a box to the next
+    extern __shared__ __align__(1024) char smem[];
+    float *const red_m = reinterpret_cast<float *>(smem + NS * C::kStage);
+    float *const red_l = red_m + kWarps * C::kWarpRows;
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + NS * C::kStage + C::kRed);
+    uint64_t *const empty = full + NS;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            // a tile has landed: an arrival of each copying warp and the bytes
+            // of its tensor copies, or an arrival of each copying lane
+            mbar_init(full + i, a.box_rows ? kCopyWarps : kCopyWarps * 32);
+            mbar_init(empty + i, kWarps);
+        }
+        fence_mbar_init();
+    }
+    // The parameters that the share is found with: fetched while the kernel
+    // before this one still runs, where their latency costs nothing.
+    asm volatile("" ::"l"(a.seq_lens), "l"(a.new_lens), "r"(a.B), "r"(a.Hkv), "r"(a.n_rt), "r"(a.cache.max_pages),
+                 "r"(a.cache.page_size), "l"(a.cache.table), "l"(a.q), "r"(a.Sq), "l"(a.ws_rec), "l"(a.wait_ns));
+    if (warp == kWarps && a.box_rows) {
+        tma_prefetch_desc(&a.map_k);
+        tma_prefetch_desc(&a.map_v);
+    }
+    chain_wait();
+    __syncthreads();
+    if (tid == 0 && a.ws_rec)
+        a.ws_rec[blockIdx.x] = make_int4(0, 0, 0, -1);
     if (blockIdx.x == 0)
         for (int b = tid; b < a.B; b += kThreads) {
             if (__ldg(a.seq_lens + b) != keys_of(a, b))
@@ -303,213 +526,72 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
             if (a.new_lens && __ldg(a.new_lens + b) != new_of(a, b))
                 record_bounds(0x902);
         }
-    // every working block gets a position at least, so that the blocks that
-    // share a job are neighbours
-    const int blocks = min((int)gridDim.x, total);
-    if (a.ws_rec && tid == 0)
-        a.ws_rec[blockIdx.x] = make_int4(0, 0, 0, -1);
-    if ((int)blockIdx.x >= blocks)
-        return;
-    const Shares shares = {total / blocks, total % blocks};
-    const int end = shares.first(blockIdx.x + 1);
+    Shares shares;
     Place at;
-    at.pos = shares.first(blockIdx.x);
-    {
-        // the lane whose run holds the position, the sequence in its run, the job
-        const int o = __ffs(__ballot_sync(0xffffffffu, incl > at.pos)) - 1;
-        int base = __shfl_sync(0xffffffffu, incl - mine, o);
-        at.b = o * per_lane;
-        for (int k = 0; per_lane > 1 && k < per_lane; k += 32) {
-            const int w = k + lane < per_lane ? length_of<TILE>(a, o * per_lane + k + lane) : 0;
-            const int x = warp_scan(w, lane);
-            const unsigned in = __ballot_sync(0xffffffffu, base + x > at.pos);
-            if (in) {
-                const int l = __ffs(in) - 1;
-                at.b = o * per_lane + k + l;
-                base += __shfl_sync(0xffffffffu, x - w, l);
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, x, 31);
-        }
-        enter<TILE>(a, at);
-        const int off = at.pos - base, job = off / (at.tiles + kJobCost);
-        at.j = off - job * (at.tiles + kJobCost) - kJobCost;
-        at.hr = job;
-        if (at.j < 0) {  // the share begins between two jobs
-            at.pos -= at.j;
-            at.j = 0;
-        }
-        if (at.pos >= end)
-            return;
+    int end;
+    if (!find_share<TILE>(a, lane, shares, at, end))
+        return;
+    if (warp >= kWarps) {
+        regs_dec<kRegsCopy>();
+        copy_tiles<D, FP8, RG>(a, at, end, smem, full, empty, warp - kWarps, lane);
+        return;
     }
 
-    // ---- the ring of copied tiles: this warp's part of each block tile
-    char *const ring = smem + warp * (NS * C::kStage);
-    const uint32_t ring_u = smem_addr(ring);
-    constexpr int CPR = ROWB / 16, RPP = 32 / CPR;  // chunks of a row, rows copied at a time
-    const int my_row = lane / CPR, my_chunk = lane % CPR;
-    Place ahead = at;
-    bool more = true;  // `ahead` is a tile of this share
-    // What was looked up for a copy: how many of the warp's keys exist, their
-    // head, and the page and row in it of each run of 16 keys, or where pages
-    // do not hold whole runs of 16, of this lane's key.  Two tiles are looked
-    // up ahead of the copies: an entry may come from memory, behind the copies
-    // in flight.
-    constexpr int RUNS = KEYS / 16;
-    struct Look {
-        int n, h, page[RUNS], row[RUNS];
-    };
-    Look look = {}, look2 = {};
-    auto look_up = [&](Look &l) {
-        l.n = 0;
-        if (!more)
-            return;
-        const int key0 = (ahead.j * kWarps + warp) * KEYS;
-        l.n = min(ahead.keys - key0, KEYS);
-        l.h = a.n_rt == 1 ? ahead.hr : ahead.hr / a.n_rt;
-        const int *entries = a.cache.table + ahead.b * a.cache.table_stride;
-#pragma unroll
-        for (int u = 0; u < RUNS; ++u) {
-            const int key = key0 + (a.tiled ? u * 16 : lane % KEYS);
-            l.row[u] = -1;
-            if (key < ahead.keys) {
-                const int pg = page_of(a.cache, key);
-                l.row[u] = key - pg * a.cache.page_size;
-                l.page[u] = __ldg(entries + pg);
-            }
-        }
-        more = has_next(ahead, end);
-        if (more)
-            advance<TILE>(a, ahead);
-    };
-    // byte offset of a row of a page; -1, and a report, for a page that is none
-    auto offset_of = [&](int page, int row) {
-        if (page >= 0 && page < a.cache.num_pages)
-            return (page * a.cache.page_stride + ((long long)look.h * a.cache.page_size + row) * D) * (FP8 ? 1 : 2);
-        record_bounds(0x903);
-        return -1LL;
-    };
-    const uint32_t copy_to = ring_u + chunk_at<ROWB>(my_row, my_chunk);
-    auto copy_tile = [&](int stage) {
-        if (look.n > 0) {
-            const uint32_t base = copy_to + stage * C::kStage;
-            // row i * RPP + my_row: the same permutation but for these bits
-            auto to = [&](int i) { return (base ^ (ROWB >= 128 ? ((i * RPP) & 7) << 4 : 0)) + i * 512; };
-            if (a.tiled) {
-#pragma unroll
-                for (int u = 0; u < RUNS; ++u) {
-                    const long long off = look.row[u] >= 0 ? offset_of(look.page[u], look.row[u]) : -1;
-                    const long long from = max(off, 0LL) + lane * 16;
-                    const char *ks = a.cache.k + from, *vs = a.cache.v + from;
-                    constexpr int N = 16 / RPP;
-                    if (off >= 0 && look.n >= u * 16 + 16) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            copy16(to(u * N + i), ks + i * 512);
-                            copy16(to(u * N + i) + C::kPart, vs + i * 512);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const bool ok = off >= 0 && u * 16 + i * RPP + my_row < look.n;
-                            copy16(to(u * N + i), ks + i * 512, ok);
-                            copy16(to(u * N + i) + C::kPart, vs + i * 512, ok);
-                        }
-                    }
-                }
-            } else {
-                const long long off = look.row[0] >= 0 ? offset_of(look.page[0], look.row[0]) : -1;
-#pragma unroll
-                for (int i = 0; i < KEYS / RPP; ++i) {
-                    const long long o = __shfl_sync(0xffffffffu, off, i * RPP + my_row);
-                    const long long from = max(o, 0LL) + my_chunk * 16;
-                    copy16(to(i), a.cache.k + from, o >= 0);
-                    copy16(to(i) + C::kPart, a.cache.v + from, o >= 0);
-                }
-            }
-        }
-        copy_commit();
-        look = look2;
-        look_up(look2);
-    };
-    uint32_t qf[C::kMt][KK][MT == 0 ? 2 : 4];
+    // ---- the computing warps
+    regs_inc<kRegsCompute>();
+    const int g = lane >> 2, t = lane & 3;
+    const int kg = warp % C::kKg, rg = warp / C::kKg;  // this warp's keys of a tile, and rows
+    unsigned long long budget = a.wait_ns;
+    uint32_t qf[KK][RG == 0 ? 2 : 4];
     int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
     auto load_q = [&]() {
         h_kv = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
         row0 = (at.hr - h_kv * a.n_rt) * C::kRows;
         n_new = new_of(a, at.b);
 #pragma unroll
-        for (int mt = 0; mt < C::kMt; ++mt)
+        for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+            const int r = row0 + rg * 16 + g + hf * 8;
+            const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
+            const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h_kv * a.G + head) * a.qs.h + s * a.qs.s;
 #pragma unroll
-            for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                const int r = row0 + mt * 16 + g + hf * 8;
-                const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
-                const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h_kv * a.G + head) * a.qs.h + s * a.qs.s;
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    uint32_t x = 0, y = 0;
-                    if (r < a.R) {
-                        if (FP8) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * t);
-                            x = w.x;
-                            y = w.y;
-                        } else {
-                            x = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * t);
-                            y = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * t);
-                        }
+            for (int kk = 0; kk < KK; ++kk) {
+                uint32_t x = 0, y = 0;
+                if (r < a.R) {
+                    if (FP8) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * t);
+                        x = w.x;
+                        y = w.y;
+                    } else {
+                        x = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * t);
+                        y = *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * t);
                     }
-                    qf[mt][kk][hf] = x;
-                    qf[mt][kk][MT == 0 ? 1 : 2 + hf] = y;
                 }
+                qf[kk][hf] = x;
+                qf[kk][RG == 0 ? 1 : 2 + hf] = y;
             }
+        }
     };
     load_q();
-    look_up(look);
-    look_up(look2);
-#pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i)
-        copy_tile(i);
 
-    // ---- the tiles
-    float acc[C::kMt][DN][4];
-    float m_run[C::kMt][2], l_run[C::kMt][2], s_mul[C::kMt][2];
-    int lim[C::kMt][2];  // keys that each of this thread's rows sees
+    float acc[DN][4];
+    float m_run[2], l_run[2], s_mul[2];
+    int lim[2];         // keys that each of this thread's rows sees
     bool fresh = true;  // the tile is the first of its job in this share
     int first_j = at.j;
-
-    constexpr int TPR = (kThreads >= 256 ? 256 : kThreads >= 128 ? 128 : kThreads >= 64 ? 64 : 32) / C::kPassRows;
-    constexpr int CP = D / TPR;  // columns of a thread, TPR threads a row, when rows are joined and written
-    const int my_line = tid / TPR, col0 = (tid % TPR) * CP;
-    // The finished row r of the current job from its maximum, sum and sums.
-    auto write_row = [&](int r, float top, float sum, const float (&o)[CP]) {
-        if (a.Sq > 1 && r % a.Sq >= n_new)
-            return;
-        const float f = sum == 0.f ? 0.f : (FP8 ? __ldg(a.cache.v_scale + h_kv) : 1.f) / sum;
-        const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
-#pragma unroll
-        for (int e = 0; e < CP; e += 2) {
-            if (a.out_bf16)
-                *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e) =
-                    pack_bf16(o[e] * f, o[e + 1] * f);
-            else
-                *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e) = make_float2(o[e] * f, o[e + 1] * f);
-        }
-        if (col0 == 0)
-            a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    };
+    // A row of the joined tile belongs to TPR threads, which take its columns
+    // in turn, two at a time.
+    constexpr int TPR = kWarps * 32 / C::kRows, CP = D / TPR;
+    const int my_line = tid / TPR, col0 = tid % TPR * 2;
     // where the matrix loads of this lane begin in a tile (see the loops)
-    const uint32_t k_lane = ring_u + (FP8 ? chunk_at<ROWB>(lane, 0)
-                                          : chunk_at<ROWB>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
-    const uint32_t v_lane = ring_u + C::kPart + (FP8 ? chunk_at<ROWB>(lane, 0)
-                                                     : chunk_at<ROWB>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4));
-    int stage = NS - 1;
+    const uint32_t k_lane = smem_u32(smem) + (FP8 ? chunk_at<ROWB, TILE>(lane, 0)
+                                                  : chunk_at<ROWB, TILE>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+    const uint32_t v_lane = smem_u32(smem) + C::kPart +
+                            (FP8 ? chunk_at<ROWB, TILE>(lane, 0)
+                                 : chunk_at<ROWB, TILE>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4));
+    int stage = 0;
+    uint32_t phase = 0;
     for (;;) {
-        const int refill = stage;  // the stage that the last tile left
-        stage = stage == NS - 1 ? 0 : stage + 1;
-        copy_wait<NS - 2>();
-        __syncwarp();
-        copy_tile(refill);
-
+        wait_phase(full + stage, phase, budget);
         if (fresh) {
             fresh = false;
             first_j = at.j;
@@ -523,65 +605,78 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
                 kmul = fabsf(kmul);
             }
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
+            for (int hf = 0; hf < 2; ++hf) {
+                m_run[hf] = -INFINITY;
+                l_run[hf] = 0.f;
+                const int s = (row0 + rg * 16 + g + hf * 8) % a.Sq;
+                lim[hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
+                s_mul[hf] = kmul;
+                if (RG == 0 && hf == 1)
+                    continue;
+                if (FP8) {
+                    // e4m3 keys widen exactly to fp16, so the queries are
+                    // taken to fp16 too: scaled by a power of two that brings
+                    // the row's largest element to [2^14, 2^15), their 8 bits
+                    // fit exactly down to 2^-28 of it
+                    float top = 0.f;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    m_run[mt][hf] = -INFINITY;
-                    l_run[mt][hf] = 0.f;
-                    const int s = (row0 + mt * 16 + g + hf * 8) % a.Sq;
-                    lim[mt][hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
-                    s_mul[mt][hf] = kmul;
-                    if (MT == 0 && hf == 1)
-                        continue;
-                    if (FP8) {
-                        // e4m3 keys widen exactly to fp16, so the queries are
-                        // taken to fp16 too: scaled by a power of two that
-                        // brings the row's largest element to [2^14, 2^15),
-                        // their 8 bits fit exactly down to 2^-28 of it
-                        float top = 0.f;
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const uint32_t x = qf[kk][hf], y = qf[kk][RG == 0 ? 1 : 2 + hf];
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))),
+                                               fmaxf(fabsf(bf16_lo(y)), fabsf(bf16_hi(y)))));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // exponent of 2^(14 - e), kept where both it and its inverse are normal
+                    int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+                    up = min(max(up, -110), 110);
+                    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                    const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
+                    s_mul[hf] = mul < 7.5e-37f ? 7.5e-37f : mul;
 #pragma unroll
-                        for (int kk = 0; kk < KK; ++kk) {
-                            const uint32_t x = qf[mt][kk][hf], y = qf[mt][kk][MT == 0 ? 1 : 2 + hf];
-                            top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))),
-                                                   fmaxf(fabsf(bf16_lo(y)), fabsf(bf16_hi(y)))));
-                        }
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        // exponent of 2^(14 - e), kept where both it and its inverse are normal
-                        int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
-                        up = min(max(up, -110), 110);
-                        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                        const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
-                        s_mul[mt][hf] = mul < 7.5e-37f ? 7.5e-37f : mul;
-#pragma unroll
-                        for (int kk = 0; kk < KK; ++kk) {
-                            uint32_t &x = qf[mt][kk][hf], &y = qf[mt][kk][MT == 0 ? 1 : 2 + hf];
-                            x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
-                            y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f) ^ flip;
-                        }
+                    for (int kk = 0; kk < KK; ++kk) {
+                        uint32_t &x = qf[kk][hf], &y = qf[kk][RG == 0 ? 1 : 2 + hf];
+                        x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
+                        y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f) ^ flip;
                     }
                 }
+            }
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
+            for (int n = 0; n < DN; ++n)
 #pragma unroll
-                for (int n = 0; n < DN; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[mt][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e)
+                    acc[n][e] = 0.f;
         }
 
-        const int kb = (at.j * kWarps + warp) * KEYS;
-        if (kb < at.keys) {
-            const uint32_t k_u = k_lane + stage * C::kStage, v_u = v_lane + stage * C::kStage;
+#pragma unroll 1
+        for (int step = kg; step < kWarps; step += C::kKg) {
+            const int kb = at.j * TILE + step * KEYS;
+            if (kb >= at.keys)
+                break;
+            const uint32_t k_u = k_lane + stage * C::kStage + step * KEYS * BOX;
+            const uint32_t v_u = v_lane + stage * C::kStage + step * KEYS * BOX;
+            // Word w of row r of this step's values.
+            auto v_word = [&](int r, int w) {
+                return reinterpret_cast<uint32_t *>(smem + stage * C::kStage + C::kPart + (step * KEYS + r) * BOX +
+                                                    w / (BOX / 4) * BOXES) + w % (BOX / 4);
+            };
+            // A copied box's rows behind the last key may hold anything: their
+            // scores are masked, their values must not be infinite or NaN.
+            // (Warps of several row groups write the same zeros.)
+            // This is the job's last tile, so the fence at the job's end stands
+            // between these zeros and the next tensor copy.
+            if (kb + KEYS > at.keys) {
+                for (int i = (at.keys - kb) * (ROWB / 16) + lane; i < KEYS * (ROWB / 16); i += 32)
+                    st_shared_v4(smem_u32(v_word(i / (ROWB / 16), i % (ROWB / 16) * 4)), 0, 0, 0, 0);
+                __syncwarp();
+            }
             // ---- S = Q K^T
-            float sc[C::kMt][NT][4];
+            float sc[NT][4];
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[mt][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e)
+                    sc[n][e] = 0.f;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk)
@@ -589,14 +684,11 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
                     for (int n = 0; n < NT; n += 2) {
                         // keys n*8 .. +15, elements kk*16 .. +15
                         uint32_t f[4];
-                        ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * 128 + n * 8 * ROWB);
-#pragma unroll
-                        for (int mt = 0; mt < C::kMt; ++mt) {
-                            const uint32_t a1 = MT == 0 ? 0u : qf[mt][kk][1], a3 = MT == 0 ? 0u : qf[mt][kk][MT == 0 ? 1 : 3];
-                            const uint32_t a2 = qf[mt][kk][MT == 0 ? 1 : 2];
-                            mma<false>(sc[mt][n], qf[mt][kk][0], a1, a2, a3, f[0], f[1]);
-                            mma<false>(sc[mt][n + 1], qf[mt][kk][0], a1, a2, a3, f[2], f[3]);
-                        }
+                        ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * BOXES + n * 8 * BOX);
+                        const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
+                        const uint32_t a2 = qf[kk][RG == 0 ? 1 : 2];
+                        mma<false>(sc[n], qf[kk][0], a1, a2, a3, f[0], f[1]);
+                        mma<false>(sc[n + 1], qf[kk][0], a1, a2, a3, f[2], f[3]);
                     }
             } else {
                 // A matrix load gives each thread four neighbouring elements of
@@ -607,15 +699,11 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
                 for (int kk = 0; kk < KK; ++kk) {
                     uint32_t f[4];
                     ldsm_x4(f, k_u ^ (kk << 4));
+                    const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint32_t b0 = e4m3_to_f16(f[n]), b1 = e4m3_to_f16(f[n] >> 16);
-#pragma unroll
-                        for (int mt = 0; mt < C::kMt; ++mt) {
-                            const uint32_t a1 = MT == 0 ? 0u : qf[mt][kk][1], a3 = MT == 0 ? 0u : qf[mt][kk][MT == 0 ? 1 : 3];
-                            mma<true>(sc[mt][n], qf[mt][kk][0], a1, qf[mt][kk][MT == 0 ? 1 : 2], a3, b0, b1);
-                        }
-                    }
+                    for (int n = 0; n < 4; ++n)
+                        mma<true>(sc[n], qf[kk][0], a1, qf[kk][RG == 0 ? 1 : 2], a3, e4m3_to_f16(f[n]),
+                                  e4m3_to_f16(f[n] >> 16));
                 }
             }
             // ---- running maximum and sum; the masked keys of a row count as -inf
@@ -623,79 +711,70 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
             const bool edge = kb + KEYS > seen_by_all;
             if (edge) {
 #pragma unroll
-                for (int mt = 0; mt < C::kMt; ++mt)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (kb + n * 8 + t * 2 + (e & 1) >= lim[mt][e >> 1])
-                                sc[mt][n][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e)
+                        if (kb + n * 8 + t * 2 + (e & 1) >= lim[e >> 1])
+                            sc[n][e] = -INFINITY;
             }
             // The maximum moves only when a score exceeds it by 2^8: sum and O
             // share whatever reference the terms were taken with, and the
             // reduction and the rescaling stay off the common path.
             bool grow = false;
-            float top[C::kMt][2];
+            float top[2];
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
+            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                float x = fmaxf(sc[0][hf * 2], sc[0][hf * 2 + 1]);
 #pragma unroll
-                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                    float x = fmaxf(sc[mt][0][hf * 2], sc[mt][0][hf * 2 + 1]);
-#pragma unroll
-                    for (int n = 1; n < NT; ++n)
-                        x = fmaxf(x, fmaxf(sc[mt][n][hf * 2], sc[mt][n][hf * 2 + 1]));
-                    top[mt][hf] = x * s_mul[mt][hf];
-                    grow |= top[mt][hf] > m_run[mt][hf] + 8.f;
-                }
+                for (int n = 1; n < NT; ++n)
+                    x = fmaxf(x, fmaxf(sc[n][hf * 2], sc[n][hf * 2 + 1]));
+                top[hf] = x * s_mul[hf];
+                grow |= top[hf] > m_run[hf] + 8.f;
+            }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int mt = 0; mt < C::kMt; ++mt)
+                for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                    float x = top[hf];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    x = fmaxf(x, m_run[hf]);
+                    const float f = x == -INFINITY ? 1.f : ex2_approx(m_run[hf] - x);
+                    m_run[hf] = x;
+                    l_run[hf] *= f;
 #pragma unroll
-                    for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                        float x = top[mt][hf];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        x = fmaxf(x, m_run[mt][hf]);
-                        const float f = x == -INFINITY ? 1.f : ex2(m_run[mt][hf] - x);
-                        m_run[mt][hf] = x;
-                        l_run[mt][hf] *= f;
+                    for (int n = 0; n < DN; ++n)
 #pragma unroll
-                        for (int n = 0; n < DN; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                acc[mt][n][hf * 2 + e] *= f;
-                                if (MT == 0)
-                                    acc[mt][n][2 + e] *= f;
-                            }
-                    }
-            }
-            uint32_t p_hi[C::kMt][NT][2], p_lo[C::kMt][NT][2];
-#pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
-#pragma unroll
-                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                    const float ref = m_run[mt][hf] == -INFINITY ? 0.f : -m_run[mt][hf];
-                    float sum = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float p0 = ex2(fmaf(sc[mt][n][hf * 2], s_mul[mt][hf], ref));
-                        const float p1 = ex2(fmaf(sc[mt][n][hf * 2 + 1], s_mul[mt][hf], ref));
-                        sum += p0 + p1;
-                        split2<FP8>(p0, p1, p_hi[mt][n][hf], p_lo[mt][n][hf]);
-                    }
-                    l_run[mt][hf] += sum;
+                        for (int e = 0; e < 2; ++e) {
+                            acc[n][hf * 2 + e] *= f;
+                            if (RG == 0)
+                                acc[n][2 + e] *= f;
+                        }
                 }
+            }
+            uint32_t p_hi[NT][2], p_lo[NT][2];
+#pragma unroll
+            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                const float ref = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float p0 = ex2_approx(fmaf(sc[n][hf * 2], s_mul[hf], ref));
+                    const float p1 = ex2_approx(fmaf(sc[n][hf * 2 + 1], s_mul[hf], ref));
+                    sum += split2<FP8>(p0, p1, p_hi[n][hf], p_lo[n][hf]);
+                }
+                l_run[hf] += sum;
+            }
             // ---- O += P V
-            auto add_pv = [&](float (&d)[4], int mt, int n, uint32_t b0, uint32_t b1) {
-                if constexpr (MT == 0) {
-                    mma<FP8>(d, p_hi[mt][n][0], p_lo[mt][n][0], p_hi[mt][n + 1][0], p_lo[mt][n + 1][0], b0, b1);
+            auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
+                if constexpr (RG == 0) {
+                    mma<FP8>(d, p_hi[n][0], p_lo[n][0], p_hi[n + 1][0], p_lo[n + 1][0], b0, b1);
                 } else {
-                    mma<FP8>(d, p_hi[mt][n][0], p_hi[mt][n][1], p_hi[mt][n + 1][0], p_hi[mt][n + 1][1], b0, b1);
-                    mma<FP8>(d, p_lo[mt][n][0], p_lo[mt][n][1], p_lo[mt][n + 1][0], p_lo[mt][n + 1][1], b0, b1);
+                    mma<FP8>(d, p_hi[n][0], p_hi[n][1], p_hi[n + 1][0], p_hi[n + 1][1], b0, b1);
+                    mma<FP8>(d, p_lo[n][0], p_lo[n][1], p_lo[n + 1][0], p_lo[n + 1][1], b0, b1);
                 }
             };
-            // every (two 8-column tiles of O, 16 keys) once: `use` gets the
-            // m tile, the column tile, the key tile and the operand
+            // every (8-column tile of O, 16 keys) once: `use` gets the column
+            // tile, the key tile and the operand
             auto each_v = [&](auto &&use) {
                 if constexpr (!FP8) {
 #pragma unroll
@@ -703,14 +782,14 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
 #pragma unroll
                         for (int c = 0; c < DN; c += 2) {
                             uint32_t f[4];
-                            ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * 128 + n * 8 * ROWB);
+                            ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * BOXES + n * 8 * BOX);
                             use(c, n, f[0], f[1]);
                             use(c + 1, n, f[2], f[3]);
                         }
                 } else {
                     // the transposed load pairs neighbouring elements of a key
-                    // in each half: the low bytes of both halves make the
-                    // even columns' operand, the high bytes the odd ones'
+                    // in each half: the low bytes of both halves make the even
+                    // columns' operand, the high bytes the odd ones'
 #pragma unroll
                     for (int c = 0; c < DN; c += 2) {
                         uint32_t f[4];
@@ -731,7 +810,7 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
                 const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
                 for (int r = r0; r < r1; ++r)
                     for (int w = lane; w < ROWB / 4; w += 32) {
-                        const uint32_t x = *reinterpret_cast<const uint32_t *>(ring + stage * C::kStage + C::kPart + r * ROWB + w * 4);
+                        const uint32_t x = *v_word(r, w);
                         poison |= FP8 ? ((x & 0x7fu) == 0x7fu || (x & 0x7f00u) == 0x7f00u ||
                                          (x & 0x7f0000u) == 0x7f0000u || (x & 0x7f000000u) == 0x7f000000u)
                                       : ((x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u);
@@ -739,130 +818,135 @@ __global__ void __launch_bounds__(W * 32, CPS) attn_paged_kernel(const __grid_co
                 poison = __any_sync(0xffffffffu, poison);
             }
             if (!poison) {
-                each_v([&](int c, int n, uint32_t b0, uint32_t b1) {
-#pragma unroll
-                    for (int mt = 0; mt < C::kMt; ++mt)
-                        add_pv(acc[mt][c], mt, n, b0, b1);
-                });
+                each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
             } else {
-                // token by token, the last first: the keys that token s does
-                // not see are zeroed, and only its rows take the product
+                // token by token: the values that token s does not see are
+                // taken as zero, and only its rows take the product
                 for (int s = n_new - 1; s >= 0; --s) {
                     const int seen = at.keys - n_new + s + 1;
-                    __syncwarp();
-                    for (int r = max(seen - kb, 0); r < KEYS; ++r)
-                        for (int w = lane; w < ROWB / 4; w += 32)
-                            *reinterpret_cast<uint32_t *>(ring + stage * C::kStage + C::kPart + r * ROWB + w * 4) = 0u;
-                    __syncwarp();
+                    auto keep = [&](int key, uint32_t w) {
+                        return (key < seen ? w & 0xffffu : 0u) | (key + 1 < seen ? w & 0xffff0000u : 0u);
+                    };
+                    const int r = row0 + rg * 16 + g;
+                    const bool own0 = r % a.Sq == s, own1 = RG == 0 ? own0 : (r + 8) % a.Sq == s;
                     each_v([&](int c, int n, uint32_t b0, uint32_t b1) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        add_pv(d, n, keep(kb + n * 8 + 2 * t, b0), keep(kb + n * 8 + 8 + 2 * t, b1));
 #pragma unroll
-                        for (int mt = 0; mt < C::kMt; ++mt) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            add_pv(d, mt, n, b0, b1);
-                            const int r = row0 + mt * 16 + g;
-                            const bool own0 = r % a.Sq == s, own1 = MT == 0 ? own0 : (r + 8) % a.Sq == s;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (e < 2 ? own0 : own1)
-                                    acc[mt][c][e] += d[e];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (e < 2 ? own0 : own1)
+                                acc[c][e] += d[e];
                     });
                 }
             }
         }
 
-        // ---- the job's or the share's end: join the warps
+        // ---- the job's or the share's end: join the key groups' warps
         const bool last_tile = at.j == at.tiles - 1;
-        const bool on = has_next(at, end);
+        const int next = next_pos<TILE>(at);
+        const bool on = next < end;
         if (last_tile || !on) {
             const bool whole = first_j == 0 && last_tile;
-            const int slot = 2 * blockIdx.x + (first_j == 0 ? 1 : 0);
+            // through the stage, once no warp reads the tile any more
+            char *const rows = smem + stage * C::kStage;
+            named_barrier_sync(1, kWarps * 32);
+            float *mine = reinterpret_cast<float *>(rows) + warp * C::kWarpRows * D;
 #pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt) {
-                if (mt > 0)
-                    __syncthreads();
-                float *mine = reinterpret_cast<float *>(ring + stage * C::kStage);
-                __syncwarp();
+            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                float l = l_run[hf];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int row = g + hf * 8;
+                if (t == 0) {
+                    red_m[warp * C::kWarpRows + row] = m_run[hf];
+                    red_l[warp * C::kWarpRows + row] = l;
+                }
 #pragma unroll
-                for (int hf = 0; hf < (MT == 0 ? 1 : 2); ++hf) {
-                    float l = l_run[mt][hf];
-                    l += __shfl_xor_sync(0xffffffffu, l, 1);
-                    l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    const int row = g + hf * 8;
-                    if (t == 0) {
-                        red_m[warp * C::kRows + mt * 16 + row] = m_run[mt][hf];
-                        red_l[warp * C::kRows + mt * 16 + row] = l;
+                for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = acc[n][hf * 2 + e] + (RG == 0 ? acc[n][2 + e] : 0.f);
+                        if (FP8)
+                            x[2 + e] = acc[n + 1][hf * 2 + e] + (RG == 0 ? acc[n + 1][2 + e] : 0.f);
                     }
-#pragma unroll
-                    for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
-                        float x[4];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            x[e] = acc[mt][n][hf * 2 + e] + (MT == 0 ? acc[mt][n][2 + e] : 0.f);
-                            if (FP8)
-                                x[2 + e] = acc[mt][n + 1][hf * 2 + e] + (MT == 0 ? acc[mt][n + 1][2 + e] : 0.f);
-                        }
-                        if (FP8) {
-                            const int col = n * 8 + t * 4;
-                            *reinterpret_cast<float4 *>(mine + row * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7)) =
-                                make_float4(x[0], x[2], x[1], x[3]);
-                        } else {
-                            *reinterpret_cast<float2 *>(mine + row * D + ((n ^ (row & 7)) << 3) + t * 2) =
-                                make_float2(x[0], x[1]);
-                        }
+                    if (FP8) {
+                        const int col = n * 8 + t * 4;
+                        *reinterpret_cast<float4 *>(mine + row * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7)) =
+                            make_float4(x[0], x[2], x[1], x[3]);
+                    } else {
+                        *reinterpret_cast<float2 *>(mine + row * D + ((n ^ (row & 7)) << 3) + t * 2) = make_float2(x[0], x[1]);
                     }
                 }
-                __syncthreads();
-                const int row = my_line, r = row0 + mt * 16 + row;
-                if (row < C::kPassRows && r < a.R) {
-                    float top = -INFINITY;
+            }
+            fence_proxy_async_smem();  // before a tensor copy lands there
+            named_barrier_sync(1, kWarps * 32);
+            const int r = row0 + my_line;
+            if (r < a.R) {
+                const int row = my_line % C::kWarpRows, w0 = my_line / C::kWarpRows * C::kKg;
+                float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w)
-                        top = fmaxf(top, red_m[w * C::kRows + mt * 16 + row]);
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f, o[CP];
+                for (int w = 0; w < C::kKg; ++w)
+                    top = fmaxf(top, red_m[(w0 + w) * C::kWarpRows + row]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float sum = 0.f, o[CP];
 #pragma unroll
-                    for (int e = 0; e < CP; ++e)
-                        o[e] = 0.f;
+                for (int e = 0; e < CP; ++e)
+                    o[e] = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float f = ex2(red_m[w * C::kRows + mt * 16 + row] - ref);
-                        sum += f * red_l[w * C::kRows + mt * 16 + row];
-                        const float *src =
-                            reinterpret_cast<const float *>(smem + w * (NS * C::kStage) + stage * C::kStage) + row * D;
+                for (int w = 0; w < C::kKg; ++w) {
+                    const float f = ex2_approx(red_m[(w0 + w) * C::kWarpRows + row] - ref);
+                    sum += f * red_l[(w0 + w) * C::kWarpRows + row];
+                    const float *src = reinterpret_cast<const float *>(rows) + ((w0 + w) * C::kWarpRows + row) * D;
 #pragma unroll
-                        for (int e = 0; e < CP; e += 2) {
-                            const int col = col0 + e;
-                            const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
-                            o[e] += f * x.x;
-                            o[e + 1] += f * x.y;
-                        }
+                    for (int e = 0; e < CP; e += 2) {
+                        const int col = col0 + e * TPR;
+                        const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
+                        o[e] += f * x.x;
+                        o[e + 1] += f * x.y;
                     }
-                    if (whole) {
-                        write_row(r, top, sum, o);
-                    } else {
-                        const long long at_ws = (long long)slot * C::kRows + mt * 16 + row;
+                }
+                if (!whole) {
+                    const long long at_ws = (long long)(2 * blockIdx.x + (first_j == 0 ? 1 : 0)) * C::kRows + my_line;
 #pragma unroll
-                        for (int e = 0; e < CP; e += 2)
-                            *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e) = make_float2(o[e], o[e + 1]);
-                        if (col0 == 0)
-                            a.ws_ml[at_ws] = make_float2(top, sum);
+                    for (int e = 0; e < CP; e += 2)
+                        *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e * TPR) = make_float2(o[e], o[e + 1]);
+                    if (col0 == 0)
+                        a.ws_ml[at_ws] = make_float2(top, sum);
+                } else if (a.Sq == 1 || r % a.Sq < n_new) {
+                    const float f = sum == 0.f ? 0.f : (FP8 ? __ldg(a.cache.v_scale + h_kv) : 1.f) / sum;
+                    const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
+#pragma unroll
+                    for (int e = 0; e < CP; e += 2) {
+                        if (a.out_bf16)
+                            *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e * TPR) =
+                                pack_bf16(o[e] * f, o[e + 1] * f);
+                        else
+                            *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e * TPR) =
+                                make_float2(o[e] * f, o[e + 1] * f);
                     }
+                    if (col0 == 0)
+                        a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                 }
             }
             if (first_j == 0 && !last_tile && tid == 0)  // the first part of a cut job: where is its last?
                 a.ws_rec[blockIdx.x] = make_int4(at.b * a.Hkv * a.n_rt + at.hr, n_new, 0,
-                                                 shares.owner(at.pos - at.j + at.tiles - 1));
-            __syncthreads();
+                                                 shares.owner(at.pos + (at.tiles - 1 - at.j) * kUnits));
             fresh = true;
         }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(empty + stage);
         if (!on)
             break;
-        advance<TILE>(a, at);
+        advance<TILE>(a, at, next);
         if (fresh)
             load_q();
+        if (++stage == NS) {
+            stage = 0;
+            phase ^= 1;
+        }
     }
-    copy_wait<0>();
 }
 
 // Joins the parts of the jobs that were cut between blocks: blockIdx.y is a row
@@ -874,6 +958,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
 {
     constexpr int W = kJoinThreads / 32, PER = D / 32;
     __shared__ float part[W][D], tops[W], sums[W];
+    asm volatile("" ::"l"(a.ws_rec), "l"(a.ws_ml), "l"(a.ws_o), "r"(a.records), "r"(a.n_rt), "r"(a.R), "r"(a.Sq), "l"(a.out),
+                 "l"(a.lse), "l"(a.cache.v_scale), "r"(a.out_bf16));
     chain_wait();
     const int row = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -925,7 +1011,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
                 for (int u = 0; u < U; ++u)
                     m = fmaxf(m, ml[u].x);
                 const float ref = m == -INFINITY ? 0.f : m;
-                const float f0 = ex2(top - ref);
+                const float f0 = ex2_approx(top - ref);
                 top = m;
                 sum *= f0;
 #pragma unroll
@@ -933,7 +1019,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
                     o[e] *= f0;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float f = ex2(ml[u].x - ref);
+                    const float f = ex2_approx(ml[u].x - ref);
                     sum += f * ml[u].y;
 #pragma unroll
                     for (int e = 0; e < PER; ++e)
@@ -960,7 +1046,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
             sum = 0.f;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float f = ex2(tops[w] - ref);
+                const float f = ex2_approx(tops[w] - ref);
                 sum += f * sums[w];
                 x += f * part[w][tid];
             }
@@ -976,26 +1062,79 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
     }
 }
 
-template <int D, bool FP8, int MT, int W, int CPS>
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn get_encode_fn()
+{
+    static EncodeFn fn = []() -> EncodeFn {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? (EncodeFn)ptr : nullptr;
+    }();
+    return fn;
+}
+
+// The cache as [page][head][row][element], read in boxes of `rows` rows.
+int encode_cache(CUtensorMap *m, const PagedView &c, void *base, int d, bool fp8, int rows, char *msg, size_t msg_len)
+{
+    const EncodeFn fn = get_encode_fn();
+    if (!fn) {
+        snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
+        return MERCURY_ECUDA;
+    }
+    const uint64_t es = fp8 ? 1 : 2, row = d * es;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {row, row * c.page_size, (cuuint64_t)c.page_stride * es};
+    const cuuint32_t box[4] = {(cuuint32_t)((row < 128 ? row : 128) / es), (cuuint32_t)rows, 1, 1}, unit[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
+                          box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(msg, msg_len, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", (int)r);
+        return MERCURY_ECUDA;
+    }
+    return MERCURY_OK;
+}
+
+template <int D, bool FP8, int RG>
 int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    using C = Cfg<D, FP8, MT, W, CPS>;
+    using C = Cfg<D, FP8, RG>;
     a.n_rt = (a.R + C::kRows - 1) / C::kRows;
-    a.tiled = a.cache.page_size % 16 == 0;
     const long long keys = (long long)a.cache.max_pages * a.cache.page_size;
     const long long jobs = (long long)a.B * a.Hkv * a.n_rt;
-    const long long most = ((keys + C::kTile - 1) / C::kTile + kJobCost) * jobs;
-    if (most > 0x7fffffffLL) {
+    const long long most = ((keys + C::kTile - 1) / C::kTile + 1) * jobs;  // tiles
+    if (most > 0x7fffffffLL / kUnits) {
         snprintf(msg, msg_len, "too many key tiles for one call (%lld)", most);
         return MERCURY_EINVAL;
     }
-    auto *kernel = attn_paged_kernel<D, FP8, MT, W, CPS>;
+    a.box_rows = 0;
+    if (a.cache.page_size % 16 == 0) {
+        for (a.box_rows = 16; a.box_rows < C::kTile && a.cache.page_size % (2 * a.box_rows) == 0;)
+            a.box_rows *= 2;
+        int rc = encode_cache(&a.map_k, a.cache, a.cache.k, D, FP8, a.box_rows, msg, msg_len);
+        if (rc == MERCURY_OK)
+            rc = encode_cache(&a.map_v, a.cache, a.cache.v, D, FP8, a.box_rows, msg, msg_len);
+        if (rc != MERCURY_OK)
+            return rc;
+    }
+    auto *kernel = attn_paged_kernel<D, FP8, RG>;
     KernelInfo ki;
     int rc = prepare_kernel((const void *)kernel, C::kSmem, &ki, msg, msg_len);
     if (rc != MERCURY_OK)
         return rc;
-    // as many blocks as the SMs hold at once, and none that could not get a tile
-    const unsigned grid = (unsigned)(most < ki.sms * CPS ? most : ki.sms * CPS);
+    if (ki.regs < kMinLaunchRegs) {
+        // the register increase would wait for registers that do not exist
+        snprintf(msg, msg_len, "paged attention kernel built with %d registers a thread, needs %d", ki.regs, kMinLaunchRegs);
+        return MERCURY_ECUDA;
+    }
+    // a block per SM, and none that could not get a tile (a job's cost included)
+    const unsigned grid = (unsigned)(most < ki.sms ? most : ki.sms);
     a.records = (int)grid;
     // a job that fits into one tile is never cut: no parts, nothing to join
     const bool split = keys > C::kTile;
@@ -1016,9 +1155,9 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         a.ws_ml = (float2 *)((char *)ws + o_bytes);
         a.ws_rec = (int4 *)((char *)ws + o_bytes + ml_bytes);
     }
-    cudaError_t e = launch_chained(kernel, dim3(grid), C::kThreads, C::kSmem, stream, a);
+    cudaError_t e = launch_chained(kernel, dim3(grid), kThreads, C::kSmem, stream, a);
     if (e == cudaSuccess && split)
-        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid < (unsigned)ki.sms ? grid : ki.sms, C::kRows < a.R ? C::kRows : a.R),
+        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid, C::kRows < a.R ? C::kRows : a.R),
                            kJoinThreads, 0, stream, a);
     rc = MERCURY_OK;
     if (e != cudaSuccess) {
@@ -1036,33 +1175,26 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 }
 
 template <int D, bool FP8>
-int launch_rows(PagedArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_len)
+int launch_rows(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    // Warps a block and blocks an SM, measured at the sizes named.  Eight warps
-    // in one block leave the fewest parts to join (one 4K sequence of 8 KV
-    // heads: 8.5 us against 9.4 with three blocks of four).  Many short jobs
-    // want several blocks, one of which streams while another changes jobs (64
-    // sequences of 1 to 2047 tokens, 16 heads of 64: 53 us in one block, 48 in
-    // three), and so do 8-bit keys, whose conversions one block does not hide
-    // (8 sequences of 20K to 32K: 79 against 75 us).
-    const long long jobs = (long long)a.B * a.Hkv;
-    if (a.R <= 8) {
-        if (jobs >= 2 * sms)
-            return launch<D, FP8, 0, 4, 3>(a, stream, msg, msg_len);
-        return FP8 ? launch<D, FP8, 0, 4, 2>(a, stream, msg, msg_len) : launch<D, FP8, 0, 8, 1>(a, stream, msg, msg_len);
-    }
+    if (a.R <= 8)
+        return launch<D, FP8, 0>(a, stream, msg, msg_len);
     if (a.R <= 16)
-        return FP8 ? launch<D, FP8, 1, 4, 2>(a, stream, msg, msg_len) : launch<D, FP8, 1, 8, 1>(a, stream, msg, msg_len);
-    return launch<D, FP8, 2, 4, 2>(a, stream, msg, msg_len);
+        return launch<D, FP8, 1>(a, stream, msg, msg_len);
+    if (a.R <= 32)
+        return launch<D, FP8, 2>(a, stream, msg, msg_len);
+    return launch<D, FP8, 4>(a, stream, msg, msg_len);
 }
 
 }  // namespace
 
 int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
                       const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
-                      cudaStream_t stream, char *msg, size_t msg_len)
+                      unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg, size_t msg_len)
 {
     PagedArgs a = {};
+    a.wait_ns = wait_ns;
+    a.fault = fault;
     a.q = (const __nv_bfloat16 *)q;
     a.qs = qs;
     a.cache = make_view(cache);
@@ -1079,16 +1211,12 @@ int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cach
     a.causal = causal;
     a.out_bf16 = out_bf16;
     a.scale_log2 = kLog2e / sqrtf((float)cache.d);
-    int sms = 0;
-    int rc = device_sm_count(&sms);
-    if (rc != MERCURY_OK)
-        return rc;
     const bool fp8 = cache.elem == MERCURY_ELEM_E4M3;
     if (!fp8)
         a.cache.v_scale = nullptr;
     if (cache.d == 128)
-        return fp8 ? launch_rows<128, true>(a, sms, stream, msg, msg_len) : launch_rows<128, false>(a, sms, stream, msg, msg_len);
-    return fp8 ? launch_rows<64, true>(a, sms, stream, msg, msg_len) : launch_rows<64, false>(a, sms, stream, msg, msg_len);
+        return fp8 ? launch_rows<128, true>(a, stream, msg, msg_len) : launch_rows<128, false>(a, stream, msg, msg_len);
+    return fp8 ? launch_rows<64, true>(a, stream, msg, msg_len) : launch_rows<64, false>(a, stream, msg, msg_len);
 }
 
 int read_and_clear_paged_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)

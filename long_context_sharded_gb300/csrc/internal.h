@@ -70,6 +70,11 @@ char *error_buffer(size_t *len);
 // device status after a synchronise.
 int finish_call(int rc, cudaStream_t stream);
 
+// Device wait budget (MERCURY_WAIT_NS) and the tests' fault hook of the paged
+// attention kernel (MERCURY_FAULT=drop_page_copy).
+unsigned long long device_wait_ns();
+int paged_fault();
+
 // The library's stream-ordered scratch pool of the current device.
 int device_scratch_pool(cudaMemPool_t *pool);
 
@@ -91,7 +96,7 @@ int launch_kv_append(const void *k, const Strides &ks, const void *v, const Stri
 // Attention of new tokens over a paged cache (attn_paged.cu).
 int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
                       const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
-                      cudaStream_t stream, char *msg, size_t msg_len);
+                      unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg, size_t msg_len);
 
 // Read and clear those kernels' device error words (no synchronisation).
 int read_and_clear_append_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);

@@ -11,7 +11,8 @@
 
 namespace mercury {
 
-// Error bits of the paged kernels' device error words (as in ptx.cuh).
+// Error bit of the paged kernels' device error words: a length, position or
+// page out of range (kErrBounds of ptx.cuh, here set in every build).
 constexpr unsigned int kPagedErrBounds = 2u;
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -147,8 +147,8 @@ int attn_paged(const void *q, const long long *q_strides, const mercury_paged_ca
     size_t len;
     char *msg = error_buffer(&len);
     cudaStream_t s = (cudaStream_t)stream;
-    rc = launch_attn_paged(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, out, lse, out_bf16, s, msg,
-                           len);
+    rc = launch_attn_paged(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, out, lse, out_bf16,
+                           device_wait_ns(), paged_fault(), s, msg, len);
     return finish_call(rc, s);
 }
 

@@ -872,3 +872,21 @@ def test_pages_and_lengths_out_of_range_are_reported(gm):
     expect(lambda: gm.mercury_kv_append(cache, k, k, zero, new_lens=torch.tensor([2, 3, -1], dtype=torch.int32, device="cuda")))
     cache.block_table[1, 0] = kc.shape[0]
     expect(lambda: gm.mercury_kv_append(cache, k, k, zero))
+
+
+@pytest.mark.gpu
+def test_a_copy_that_never_comes_ends_in_a_timeout(gm, monkeypatch):
+    """With one copy withheld (the test hook) its wait runs out, the status says so, and the next call is right."""
+    lens = [700, 20]
+    r = run_attention(gm, 2, 8, 2, 1, 128, 16, lens, seed=61)
+    monkeypatch.setenv("MERCURY_FAULT", "drop_page_copy")
+    monkeypatch.setenv("MERCURY_WAIT_NS", "20000000")
+    gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    with pytest.raises(gm.MercuryError) as e:
+        gm.mercury_sync_status()
+    assert e.value.status == gm.MERCURY_ETIMEOUT
+    monkeypatch.delenv("MERCURY_FAULT")
+    monkeypatch.delenv("MERCURY_WAIT_NS")
+    out, lse = gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    gm.mercury_sync_status()
+    assert torch.equal(out, r["out"]) and torch.equal(lse, r["lse"])
