@@ -40,111 +40,111 @@ struct AppendArgs {
     Strides qs, ks, vs, os;
     const int *past, *new_lens;
     PagedView cache;
-    int Hq, S, d, heads_per_thread, units, tokens_per_block;
+    int Hq, S, d, head_groups, heads_per_thread, units, tokens_per_block;
     long long tokens;
     int copy_rest;  // q_out is not q itself
     mercury_rope_plan plan;
 };
 
 template <bool FP8, int VE>
-__global__ void __launch_bounds__(kRotThreads) append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(kRotThreads, 2) append_kernel(const __grid_constant__ AppendArgs a)
 {
     using T = __nv_bfloat16;
+    __shared__ unsigned long long turns[MERCURY_MAX_ROT / 2];
+    stage_turns(a.plan, turns);
     chain_wait();
+    __syncthreads();
     const int lane_units = kRotThreads / a.tokens_per_block;
-    const long long token = (long long)blockIdx.x * a.tokens_per_block + threadIdx.x / lane_units;
+    const int group = blockIdx.x % a.head_groups;  // neighbours take the same tokens: their rows adjoin
+    const long long token = (long long)(blockIdx.x / (unsigned int)a.head_groups) * a.tokens_per_block + threadIdx.x / lane_units;
     if (token >= a.tokens)
         return;
-    const int b = (int)(token / a.S), i = (int)(token % a.S);
-    int n_new = a.S;
-    if (a.new_lens) {
-        n_new = a.new_lens[b];
-        if ((n_new < 0 || n_new > a.S) && i == 0)
-            record_bounds(0x801);
-    }
-    if (i >= n_new)
-        return;
+    const int b = (unsigned int)token / (unsigned int)a.S, i = (int)token - b * a.S;
     const PagedView &c = a.cache;
     const int Hkv = c.Hkv, Hq = a.Hq;
-    const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(Hq + 2 * Hkv, h0 + a.heads_per_thread);
-
+    const int h0 = group * a.heads_per_thread, h1 = min(Hq + 2 * Hkv, h0 + a.heads_per_thread);
+    const long long past = a.past[b];
+    const int n_new = a.new_lens ? a.new_lens[b] : a.S;
+    if ((n_new < 0 || n_new > a.S) && i == 0)
+        record_bounds(0x801);
+    if (i >= n_new)
+        return;
     // the cache row, or none where the position or its page does not exist
-    const long long pos = (long long)a.past[b] + i;
-    long long row = -1;  // element offset of head 0's row
-    if (pos < 0 || pos >= (long long)c.max_pages * c.page_size) {
-        record_bounds(0x802);
+    const long long pos = past + i;
+    const bool in_table = pos >= 0 && pos < (long long)c.max_pages * c.page_size;
+    int page = -1, at = 0;
+    if (in_table) {
+        at = page_of(c, (int)pos);
+        page = c.table[b * c.table_stride + at];
     } else {
-        const int at = page_of(c, (int)pos);
-        const int page = c.table[b * c.table_stride + at];
-        if (page < 0 || page >= c.num_pages)
-            record_bounds(0x803);
-        else
-            row = page * c.page_stride + (pos - (long long)at * c.page_size) * a.d;
+        record_bounds(0x802);
     }
     const long long head_stride = (long long)c.page_size * a.d;
 
     for (int u = threadIdx.x % lane_units; u < a.units; u += lane_units) {
-        const RotUnit<VE> unit(a.plan, u, a.d, pos, false);
-        for (int hb = h0; hb < h1; hb += kRotBatch) {
-            Chunk<T, VE> x0[kRotBatch], x1[kRotBatch];
+        RotUnit<VE> unit(a.plan, u, a.d);
+        long long row = -1;  // element offset of head 0's row
+        bool known = false;
+        auto ready = [&] {
+            if (known)
+                return;
+            known = true;
+            if (h0 < Hq + Hkv)
+                unit.set_angles(turns, a.plan.magnitude, pos);
+            if (page >= 0 && page < c.num_pages)
+                row = page * c.page_stride + (pos - (long long)at * c.page_size) * a.d;
+            else if (in_table)
+                record_bounds(0x803);
+        };
+        // one head's unit into the cache
+        auto keep = [&](char *cache, const float *scale, int h, const float (&y0)[VE], const float (&y1)[VE]) {
+            if (row < 0)
+                return;
+            const long long to = row + h * head_stride;
+            if constexpr (FP8) {
+                // divided, not multiplied by a reciprocal: the stored byte is
+                // the nearest one to the exact quotient's 32-bit rounding
+                const float sc = scale[h];
+                float z0[VE], z1[VE];
 #pragma unroll
-            for (int j = 0; j < kRotBatch; ++j) {
-                const int h = hb + j;
-                if (h < h1) {
-                    const T *p = h < Hq         ? a.q + b * a.qs.b + i * a.qs.s + h * a.qs.h
-                                 : h < Hq + Hkv ? a.k + b * a.ks.b + i * a.ks.s + (h - Hq) * a.ks.h
-                                                : a.v + b * a.vs.b + i * a.vs.s + (h - Hq - Hkv) * a.vs.h;
-                    x0[j].load(p + unit.at0);
-                    if (unit.two)
-                        x1[j].load(p + unit.at1);
+                for (int e = 0; e < VE; ++e) {
+                    z0[e] = y0[e] / sc;
+                    z1[e] = y1[e] / sc;
                 }
+                store_chunk_e4m3<VE>((uint8_t *)cache + to + unit.at0, z0);
+                if (unit.two)
+                    store_chunk_e4m3<VE>((uint8_t *)cache + to + unit.at1, z1);
+            } else {
+                store_chunk<VE>((T *)cache + to + unit.at0, y0);
+                if (unit.two)
+                    store_chunk<VE>((T *)cache + to + unit.at1, y1);
             }
-#pragma unroll
-            for (int j = 0; j < kRotBatch; ++j) {
-                const int h = hb + j;
-                if (h >= h1)
-                    continue;
-                float y0[VE], y1[VE];
-                x0[j].widen(y0);
-                x1[j].widen(y1);
-                if (h < Hq + Hkv)
-                    unit.turn(y0, y1);
-                if (h < Hq) {
-                    T *p = a.q_out + b * a.os.b + i * a.os.s + h * a.os.h;
-                    if (unit.rotated || a.copy_rest) {
-                        store_chunk<VE>(p + unit.at0, y0);
-                        if (unit.two)
-                            store_chunk<VE>(p + unit.at1, y1);
-                    }
-                    continue;
-                }
-                if (row < 0)
-                    continue;
-                const bool is_k = h < Hq + Hkv;
-                const int hk = is_k ? h - Hq : h - Hq - Hkv;
-                const long long at = row + hk * head_stride;
-                if constexpr (FP8) {
-                    // divided, not multiplied by a reciprocal: the stored
-                    // byte is the nearest one to the exact quotient's 32-bit
-                    // rounding
-                    const float sc = (is_k ? c.k_scale : c.v_scale)[hk];
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        y0[e] = y0[e] / sc;
-                        y1[e] = y1[e] / sc;
-                    }
-                    uint8_t *p = (uint8_t *)(is_k ? c.k : c.v) + at;
-                    store_chunk_e4m3<VE>(p + unit.at0, y0);
-                    if (unit.two)
-                        store_chunk_e4m3<VE>(p + unit.at1, y1);
-                } else {
-                    T *p = (T *)(is_k ? c.k : c.v) + at;
-                    store_chunk<VE>(p + unit.at0, y0);
-                    if (unit.two)
-                        store_chunk<VE>(p + unit.at1, y1);
-                }
-            }
+        };
+        // this block's part of the queries, the keys and the values
+        const int q1 = min(h1, Hq), k0 = max(h0 - Hq, 0), k1 = min(h1 - Hq, Hkv), v0 = max(h0 - Hq - Hkv, 0),
+                  v1 = h1 - Hq - Hkv;
+        if (h0 < q1) {
+            T *const dst = a.q_out + b * a.os.b + i * a.os.s;
+            walk_heads<T, VE, true>(a.q + b * a.qs.b + i * a.qs.s + h0 * a.qs.h, a.qs.h, q1 - h0, unit, ready,
+                                    [&](int h, const float (&y0)[VE], const float (&y1)[VE]) {
+                                        if (!unit.rotated && !a.copy_rest)
+                                            return;
+                                        T *p = dst + (h0 + h) * a.os.h;
+                                        store_chunk<VE>(p + unit.at0, y0);
+                                        if (unit.two)
+                                            store_chunk<VE>(p + unit.at1, y1);
+                                    });
         }
+        if (k0 < k1)
+            walk_heads<T, VE, true>(a.k + b * a.ks.b + i * a.ks.s + k0 * a.ks.h, a.ks.h, k1 - k0, unit, ready,
+                                    [&](int h, const float (&y0)[VE], const float (&y1)[VE]) {
+                                        keep(c.k, c.k_scale, k0 + h, y0, y1);
+                                    });
+        if (v0 < v1)
+            walk_heads<T, VE, false>(a.v + b * a.vs.b + i * a.vs.s + v0 * a.vs.h, a.vs.h, v1 - v0, unit, ready,
+                                     [&](int h, const float (&y0)[VE], const float (&y1)[VE]) {
+                                         keep(c.v, c.v_scale, v0 + h, y0, y1);
+                                     });
     }
 }
 
@@ -152,11 +152,16 @@ template <bool FP8, int VE>
 int launch(AppendArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_len)
 {
     const RotShape g = rot_shape(a.tokens, a.Hq + 2 * a.cache.Hkv, a.d, a.plan.rot_dim, VE, sms);
+    if (g.blocks * g.head_groups > 0x7fffffffLL) {
+        snprintf(msg, msg_len, "too many tokens for one call (%lld)", (long long)a.tokens);
+        return MERCURY_EINVAL;
+    }
+    a.head_groups = g.head_groups;
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
-    const cudaError_t e = launch_chained(append_kernel<FP8, VE>, dim3((unsigned)g.blocks, (unsigned)g.head_groups),
-                                         kRotThreads, 0, stream, a);
+    const cudaError_t e = launch_chained(append_kernel<FP8, VE>, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0,
+                                         stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cache append kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -32,55 +32,48 @@ struct RopeArgs {
     const int *pos;
     Strides xs, os;
     long long start, pos_stride;
-    int H, S, d, heads_per_thread, units, tokens_per_block;
+    int heads_adjoin, blocks, H, S, d, head_groups, heads_per_thread, units, tokens_per_block;
     long long tokens;
     int inverse, copy_rest;
     mercury_rope_plan plan;
 };
 
 template <typename T, int VE>
-__global__ void __launch_bounds__(kRotThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+__global__ void __launch_bounds__(kRotThreads, 2) rope_kernel(const __grid_constant__ RopeArgs a)
 {
+    __shared__ unsigned long long turns[MERCURY_MAX_ROT / 2];
+    stage_turns(a.plan, turns);
     chain_wait();
+    __syncthreads();
     const int lane_units = kRotThreads / a.tokens_per_block;
-    const long long token = (long long)blockIdx.x * a.tokens_per_block + threadIdx.x / lane_units;
+    // neighbouring blocks take what adjoins in memory: the next heads of the
+    // same tokens, or the next tokens of the same heads
+    const int group = a.heads_adjoin ? blockIdx.x % (unsigned int)a.head_groups : blockIdx.x / (unsigned int)a.blocks;
+    const long long token = (long long)(a.heads_adjoin ? blockIdx.x / (unsigned int)a.head_groups
+                                                       : blockIdx.x - (unsigned int)group * a.blocks) * a.tokens_per_block +
+                            threadIdx.x / lane_units;
     if (token >= a.tokens)
         return;
-    const int b = (int)(token / a.S), s = (int)(token % a.S);
-    const long long pos = a.pos ? a.pos[b * a.pos_stride + s] : a.start + s;
-    const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(a.H, h0 + a.heads_per_thread);
+    const int b = (unsigned int)token / (unsigned int)a.S, s = (int)token - b * a.S;
+    const int h0 = group * a.heads_per_thread, h1 = min(a.H, h0 + a.heads_per_thread);
     const T *src = (const T *)a.x + b * a.xs.b + s * a.xs.s;
     T *dst = (T *)a.out + b * a.os.b + s * a.os.s;
     for (int u = threadIdx.x % lane_units; u < a.units; u += lane_units) {
-        const RotUnit<VE> unit(a.plan, u, a.d, pos, a.inverse != 0);
+        RotUnit<VE> unit(a.plan, u, a.d);
         if (!unit.rotated && !a.copy_rest)
             continue;
-        // Four heads' loads first, then their stores: the output may be the
-        // input, so the compiler would keep each head's loads behind the last
-        // head's stores.
-        for (int hb = h0; hb < h1; hb += kRotBatch) {
-            Chunk<T, VE> x0[kRotBatch], x1[kRotBatch];
-#pragma unroll
-            for (int i = 0; i < kRotBatch; ++i)
-                if (hb + i < h1) {
-                    const T *p = src + (hb + i) * a.xs.h;
-                    x0[i].load(p + unit.at0);
-                    if (unit.two)
-                        x1[i].load(p + unit.at1);
-                }
-#pragma unroll
-            for (int i = 0; i < kRotBatch; ++i)
-                if (hb + i < h1) {
-                    float y0[VE], y1[VE];
-                    x0[i].widen(y0);
-                    x1[i].widen(y1);
-                    unit.turn(y0, y1);
-                    T *p = dst + (hb + i) * a.os.h;
-                    store_chunk<VE>(p + unit.at0, y0);
-                    if (unit.two)
-                        store_chunk<VE>(p + unit.at1, y1);
-                }
-        }
+        walk_heads<T, VE, true>(
+            src + h0 * a.xs.h, a.xs.h, h1 - h0, unit,
+            [&] {
+                const long long pos = a.pos ? a.pos[b * a.pos_stride + s] : a.start + s;
+                unit.set_angles(turns, a.plan.magnitude, a.inverse ? -pos : pos);
+            },
+            [&](int h, const float (&y0)[VE], const float (&y1)[VE]) {
+                T *p = dst + (h0 + h) * a.os.h;
+                store_chunk<VE>(p + unit.at0, y0);
+                if (unit.two)
+                    store_chunk<VE>(p + unit.at1, y1);
+            });
     }
 }
 
@@ -88,11 +81,18 @@ template <typename T, int VE>
 int launch(RopeArgs &a, int B, int sms, cudaStream_t stream, char *msg, size_t msg_len)
 {
     const RotShape g = rot_shape(a.tokens, a.H, a.d, a.plan.rot_dim, VE, sms);
+    if (g.blocks * g.head_groups > 0x7fffffffLL) {
+        snprintf(msg, msg_len, "too many tokens for one call (%lld)", (long long)a.tokens);
+        return MERCURY_EINVAL;
+    }
+    a.head_groups = g.head_groups;
+    a.blocks = (int)g.blocks;
+    a.heads_adjoin = a.xs.h < a.xs.s;
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
     const cudaError_t e =
-        launch_chained(rope_kernel<T, VE>, dim3((unsigned)g.blocks, (unsigned)g.head_groups), kRotThreads, 0, stream, a);
+        launch_chained(rope_kernel<T, VE>, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0, stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "rope kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -17,7 +17,7 @@
 namespace mercury {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotBatch = 4;  // heads whose loads a thread has in flight
+constexpr int kRotBatch = 4;  // heads that a thread loads at a time
 
 template <typename T, int VE>
 struct Chunk;
@@ -84,6 +84,15 @@ __device__ __forceinline__ void store_chunk_e4m3(uint8_t *p, const float (&y)[VE
         *p = (uint8_t)pack_e4m3(y[0], 0.f);
 }
 
+// The plan's frequencies into shared memory: lanes want different ones, which
+// the parameter bank would serve one after the other, for every warp anew.
+// They are no other kernel's work, so this goes before chain_wait.
+__device__ __forceinline__ void stage_turns(const mercury_rope_plan &plan, unsigned long long *turns)
+{
+    for (int i = threadIdx.x; i < plan.rot_dim / 2; i += kRotThreads)
+        turns[i] = plan.turns[i];
+}
+
 // One column unit at one position: where its chunks lie, and its rotation.
 template <int VE>
 struct RotUnit {
@@ -93,7 +102,7 @@ struct RotUnit {
     bool interleaved;
     float c[VE], s[VE];
 
-    __device__ __forceinline__ RotUnit(const mercury_rope_plan &plan, int u, int d, long long pos, bool inverse)
+    __device__ __forceinline__ RotUnit(const mercury_rope_plan &plan, int u, int d)
     {
         const int rot = plan.rot_dim, n = rot / (2 * VE);
         interleaved = plan.interleaved != 0;
@@ -103,23 +112,28 @@ struct RotUnit {
             at0 = rot + (u - n) * 2 * VE;
             at1 = at0 + VE;
             two = at1 < d;
-            return;
-        }
-        if (VE == 1 && interleaved) {
+        } else if (VE == 1 && interleaved) {
             at0 = 2 * u;
             at1 = at0 + 1;
         } else {
             at0 = u * VE;
             at1 = at0 + rot / 2;
         }
+    }
+
+    // turns: the plan's, in shared memory
+    __device__ __forceinline__ void set_angles(const unsigned long long *turns, float magnitude, long long pos)
+    {
+        if (!rotated)
+            return;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
             // pair of slot i: chunk element i, or for interleaved chunks
             // pairs at0/2 + i (first chunk) and at1/2 + i - VE/2 (second)
             int pair = at0 + i;
             if (interleaved)
-                pair = VE == 1 ? u : (i < VE / 2 ? at0 / 2 + i : at1 / 2 + i - VE / 2);
-            rope_cos_sin(plan.turns[pair], inverse ? -pos : pos, plan.magnitude, c[i], s[i]);
+                pair = VE == 1 ? at0 / 2 : (i < VE / 2 ? at0 / 2 + i : at1 / 2 + i - VE / 2);
+            rope_cos_sin(turns[pair], pos, magnitude, c[i], s[i]);
         }
     }
 
@@ -147,6 +161,58 @@ struct RotUnit {
     }
 };
 
+// One unit of n heads, `stride` elements apart from `src` on: turned if TURN,
+// and given to store(head, chunk 0, chunk 1).  kRotBatch heads are loaded at a
+// time, the first ones while ready(), which has the angles and whatever a
+// store needs found, runs.  16-bit heads are double buffered, the next batch on
+// its way while one is turned and stored (32K prompt of 40 heads: 109 to 99
+// us); 32-bit ones are not: with twice the bytes in flight a head the registers
+// cost more than the overlap gains (12.0 against 10.9 us at 2 x 12 heads x
+// 4099 tokens).  (Written out, because the output may be the input: the
+// compiler would keep each load behind the stores before it.)
+template <typename T, int VE, bool TURN, typename Ready, typename Store>
+__device__ __forceinline__ void walk_heads(const T *src, long long stride, int n, RotUnit<VE> &unit, Ready ready,
+                                           Store store)
+{
+    constexpr bool kAhead = sizeof(T) == 2;
+    Chunk<T, VE> x0[2][kRotBatch], x1[2][kRotBatch];
+    auto load = [&](int slot, int h0) {
+#pragma unroll
+        for (int i = 0; i < kRotBatch; ++i)
+            if (h0 + i < n) {
+                const T *p = src + (h0 + i) * stride;
+                x0[slot][i].load(p + unit.at0);
+                if (unit.two)
+                    x1[slot][i].load(p + unit.at1);
+            }
+    };
+    load(0, 0);
+    ready();
+    for (int h0 = 0; h0 < n; h0 += kRotBatch) {
+        if (kAhead)
+            load(1, h0 + kRotBatch);
+        else if (h0 > 0)
+            load(0, h0);
+#pragma unroll
+        for (int i = 0; i < kRotBatch; ++i)
+            if (h0 + i < n) {
+                float y0[VE], y1[VE];
+                x0[0][i].widen(y0);
+                x1[0][i].widen(y1);
+                if (TURN)
+                    unit.turn(y0, y1);
+                store(h0 + i, y0, y1);
+            }
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < kRotBatch; ++i) {
+                x0[0][i] = x0[1][i];
+                x1[0][i] = x1[1][i];
+            }
+        }
+    }
+}
+
 // Grid of a launch over `tokens` tokens of H heads.
 struct RotShape {
     int units, tokens_per_block, heads_per_thread, head_groups;
@@ -162,10 +228,13 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
         lanes *= 2;
     g.tokens_per_block = kRotThreads / lanes;
     g.blocks = (tokens + g.tokens_per_block - 1) / g.tokens_per_block;
-    // Heads per thread: as many as leave two blocks for each SM (an angle
-    // costs about as much as moving two heads), at most 16.
+    // Heads per thread: as many as leave three blocks for two SMs, at most 16.
+    // An angle costs about as much as moving two heads, so a thread of many
+    // heads is cheap (a 32K prompt of 40 heads: 138 us with 4, 113 with 8, 99
+    // with 16, 102 with 32), but a short call needs its blocks (6 x 1000
+    // tokens of 24 heads into an 8-bit cache: 12.8 us with 16, 11.7 with 2).
     int hp = 16;
-    while (hp > 1 && g.blocks * ((H + hp - 1) / hp) < 2LL * sms)
+    while (hp > 1 && 2 * g.blocks * ((H + hp - 1) / hp) < 3LL * sms)
         hp /= 2;
     g.heads_per_thread = hp;
     g.head_groups = (H + hp - 1) / hp;
