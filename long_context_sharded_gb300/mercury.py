@@ -533,35 +533,45 @@ def _refuse(t, dtype, dev, what):
 
 def _flat(t, dtype, dev, shape, what):
     """Device pointer of a contiguous tensor of this dtype and shape on device `dev`."""
-    if not (isinstance(t, _torch_names.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+    try:
+        ok = t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    except AttributeError:
+        ok = False
+    if not ok:
         _refuse(t, dtype, dev, what)
     if t.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (what, tuple(shape), tuple(t.shape)))
     return t.data_ptr()
 
 
-def _heads(t, dtype, dev, what):
-    """(device pointer, stride array or None where contiguous) of a 4-D tensor
-    on device `dev` whose heads (last axis) are contiguous."""
+def _strides(t, dtype, dev, what):
+    """Element strides of a 4-D tensor on device `dev` whose heads (last axis)
+    are contiguous; None where all of it is."""
     if t.dtype is not dtype or t.get_device() != dev:
         _refuse(t, dtype, dev, what)
     if t.is_contiguous():
-        return t.data_ptr(), None
+        return None
     st = t.stride()
     if st[3] != 1 and t.shape[3] != 1:
         raise ValueError("the heads (last axis) of %s must be contiguous" % what)
-    return t.data_ptr(), _Strides(st[0], st[1], st[2])
+    return st
+
+
+def _shape4(t, what):
+    """The shape of a 4-D tensor."""
+    try:
+        shape = t.shape
+        if len(shape) == 4:
+            return shape
+    except AttributeError:
+        pass
+    raise ValueError("%s must be a 4-D tensor" % what)
 
 
 def _on_current(dev, what):
     cur = _torch_names.current_device()
     if cur != dev:
         raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (what, dev, cur))
-
-
-def _is_4d(t, what):
-    if not isinstance(t, _names().Tensor) or t.dim() != 4:
-        raise ValueError("%s must be a 4-D tensor" % what)
 
 
 def mercury_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -601,7 +611,7 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
     inverse=True applies the transpose, the gradient of the forward call.
     out: a tensor of x's shape and dtype, or x itself; a new one by default."""
     T = _names()
-    _is_4d(x, "x")
+    shape = _shape4(x, "x")
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (mercury_rope_init)")
     dtype = x.dtype
@@ -611,19 +621,23 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
     if dev < 0:
         raise ValueError("x must be a CUDA tensor")
     _on_current(dev, "x")
-    shape = x.shape
     B, H, S, d = shape
-    px, sx = _heads(x, dtype, dev, "x")
+    sx = _strides(x, dtype, dev, "x")
+    if sx is not None:
+        sx = _Strides(sx[0], sx[1], sx[2])
+    px = x.data_ptr()
     if out is None:
         out = T.empty(shape, dtype=dtype, device=x.device)
         po, so = out.data_ptr(), None
     elif out is x:
         po, so = px, sx
     else:
-        _is_4d(out, "out")
-        if out.shape != shape:
+        if _shape4(out, "out") != shape:
             raise ValueError("out must have shape %s (got %s)" % (tuple(shape), tuple(out.shape)))
-        po, so = _heads(out, dtype, dev, "out")
+        so = _strides(out, dtype, dev, "out")
+        if so is not None:
+            so = _Strides(so[0], so[1], so[2])
+        po = out.data_ptr()
     pp, row = None, 0
     if positions is not None:
         if not isinstance(positions, T.Tensor):
@@ -712,15 +726,17 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
         raise TypeError("cache must be a PagedCache")
     dev = cache.device_index
     _on_current(dev, "the cache")
-    _is_4d(k, "k")
-    _is_4d(v, "v")
-    shape = k.shape
+    shape = _shape4(k, "k")
     B, Hkv, S, d = shape
-    if v.shape != shape or B != cache.B or Hkv != cache.Hkv or d != cache.d:
+    if _shape4(v, "v") != shape or B != cache.B or Hkv != cache.Hkv or d != cache.d:
         raise ValueError("k and v must be [B=%d, Hkv=%d, S, d=%d] (got %s and %s)"
                          % (cache.B, cache.Hkv, cache.d, tuple(shape), tuple(v.shape)))
-    pk, sk = _heads(k, T.bf16, dev, "k")
-    pv, sv = _heads(v, T.bf16, dev, "v")
+    bf16 = T.bf16
+    sk, sv = _strides(k, bf16, dev, "k"), _strides(v, bf16, dev, "v")
+    if sk is not None:
+        sk = _Strides(sk[0], sk[1], sk[2])
+    if sv is not None:
+        sv = _Strides(sv[0], sv[1], sv[2])
     plan = None
     if rope is not None:
         if not isinstance(rope, RopePlan):
@@ -729,26 +745,30 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
     pq = sq = po = so = None
     Hq = 0
     if q is not None:
-        _is_4d(q, "q")
-        qshape = q.shape
-        Hq = qshape[1]
-        if qshape[0] != B or qshape[2] != S or qshape[3] != d:
+        qshape = _shape4(q, "q")
+        Bq, Hq, Sq, dq = qshape
+        if Bq != B or Sq != S or dq != d:
             raise ValueError("q must be [B=%d, Hq, S=%d, d=%d] (got %s)" % (B, S, d, tuple(qshape)))
-        pq, sq = _heads(q, T.bf16, dev, "q")
+        sq = _strides(q, bf16, dev, "q")
+        if sq is not None:
+            sq = _Strides(sq[0], sq[1], sq[2])
+        pq = q.data_ptr()
         if q_out is None:
             # rows behind new_lens are not written: zeros rather than whatever was there
-            q_out = (T.empty if new_lens is None else T.zeros)(qshape, dtype=T.bf16, device=q.device)
+            q_out = (T.empty if new_lens is None else T.zeros)(qshape, dtype=bf16, device=q.device)
             po = q_out.data_ptr()
         elif q_out is q:
             po, so = pq, sq
         else:
-            _is_4d(q_out, "q_out")
-            if q_out.shape != qshape:
+            if _shape4(q_out, "q_out") != qshape:
                 raise ValueError("q_out must have shape %s (got %s)" % (tuple(qshape), tuple(q_out.shape)))
-            po, so = _heads(q_out, T.bf16, dev, "q_out")
+            so = _strides(q_out, bf16, dev, "q_out")
+            if so is not None:
+                so = _Strides(so[0], so[1], so[2])
+            po = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rc = lib.mercury_kv_append(pk, sk, pv, sv, B, S, cache._ref, _flat(past_lens, T.int32, dev, (B,), "past_lens"),
+    rc = lib.mercury_kv_append(k.data_ptr(), sk, v.data_ptr(), sv, B, S, cache._ref, _flat(past_lens, T.int32, dev, (B,), "past_lens"),
                                None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), plan,
                                pq, sq, Hq, po, so, T.raw_stream(dev) if stream is None else _stream_ptr(stream))
     if rc:
@@ -762,19 +782,20 @@ def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, s
         raise TypeError("cache must be a PagedCache")
     dev = cache.device_index
     _on_current(dev, "the cache")
-    _is_4d(q, "q")
-    shape = q.shape
+    shape = _shape4(q, "q")
     B, Hq, Sq, d = shape
     if B != cache.B or d != cache.d:
         raise ValueError("q must be [B=%d, Hq, Sq, d=%d] (got %s)" % (cache.B, cache.d, tuple(shape)))
-    pq, sq = _heads(q, T.bf16, dev, "q")
+    sq = _strides(q, T.bf16, dev, "q")
+    if sq is not None:
+        sq = _Strides(sq[0], sq[1], sq[2])
     # rows behind new_lens are not written: zeros rather than whatever was there
     make = T.empty if new_lens is None else T.zeros
     if out is None:
         out = make(shape, dtype=out_dtype, device=q.device)
     if lse is None:
         lse = make((B, Hq, Sq), dtype=T.fp32, device=q.device)
-    rc = fn(pq, sq, cache._ref, _flat(seq_lens, T.int32, dev, (B,), "seq_lens"),
+    rc = fn(q.data_ptr(), sq, cache._ref, _flat(seq_lens, T.int32, dev, (B,), "seq_lens"),
             None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), B, Hq, Sq,
             1 if causal else 0, _flat(out, out_dtype, dev, shape, "out"), _flat(lse, T.fp32, dev, (B, Hq, Sq), "lse"),
             T.raw_stream(dev) if stream is None else _stream_ptr(stream))
