@@ -46,6 +46,8 @@
  *     drop_kv_free makes the attention kernel withhold one internal arrive,
  *     so the MMA issuer's or the TMA producer's bounded wait runs out and the
  *     call ends with MERCURY_ETIMEOUT -- a timeout, never a GPU fault.
+ *     drop_page_copy withholds one copy of the paged attention kernel, with
+ *     the same end.
  */
 #ifndef MERCURY_ATTN_H
 #define MERCURY_ATTN_H
@@ -646,15 +648,21 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * length).  Scale 1/sqrt(d), query head h uses KV head h / (Hq/Hkv).
  * out [B, Hq, Sq, d] and lse [B, Hq, Sq] fp32, contiguous; a row without keys
  * gets O = 0 and LSE = -inf, rows i >= n are left as they were.  Keys that a
- * row does not see do not affect it, whatever they hold; cache rows at and
- * after seq_lens[b] are not read.
- * Scores, sums and products are kept in fp32, P as two 16-bit terms, so O
- * carries fp32 accuracy (about 1e-6 relative) from the cache's values.
+ * row does not see do not affect it, whatever they hold; of the cache rows at
+ * and after seq_lens[b] nothing is used (the rest of the last page may be
+ * read).
+ * Scores, sums and products are kept in fp32 and P as a sum of 16-bit terms
+ * (24 bits or more), so O carries fp32 accuracy (about 1e-6 relative) from the
+ * cache's values.
  * The keys of all sequences are dealt to the SMs in equal shares on the
  * device, so neither the lengths nor their spread need to be known on the
  * host.  Parts of sequences cut between SMs go to scratch memory (2 * SMs *
- * rows * (d + 2) * 4 bytes, rows 8 to 32) that comes stream-ordered from the
- * library's pool; a captured graph owns its own.
+ * rows * (d + 2) * 4 bytes, rows 8 to 64) that comes stream-ordered from the
+ * library's pool; a captured graph owns its own.  Pages of a multiple of 16
+ * tokens are copied whole by the copy engine; other sizes go token by token
+ * (about a tenth slower at 32K tokens).
+ * Device waits are bounded as in every call (MERCURY_WAIT_NS): one that runs
+ * out is reported as MERCURY_ETIMEOUT.
  * A page outside the cache counts as keys and values of zero, and it, a
  * seq_lens outside the block table or a new_lens outside [0, Sq] (both taken
  * to the nearer end) is reported as MERCURY_EBOUNDS by mercury_sync_status.
@@ -664,7 +672,7 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * for a shape class on a device prepares its kernel; make it before any
  * stream capture.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
- * when MERCURY_SYNC_CHECK=1.
+ * or MERCURY_ETIMEOUT when MERCURY_SYNC_CHECK=1.
  */
 MERCURY_API int mercury_attn_paged(const void *q, const long long *q_strides, const mercury_paged_cache *cache,
                                    const int *seq_lens, const int *new_lens, int B, int Hq, int Sq, int causal,

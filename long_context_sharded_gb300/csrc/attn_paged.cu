@@ -22,10 +22,19 @@
 //     and look-ups spread over the computing warps these took more of a tile's
 //     time (1000 cycles of 2800) than its products.
 //   * both products run on warp-level matrix instructions: the rows of one KV
-//     head fill at most 8 to 64 rows of a tile, and the operands come straight
-//     from the copied tile.  P goes in as two 16-bit terms (value and
-//     remainder), which holds O to 32-bit outputs; with at most 8 rows the
-//     remainder rides in the tile's idle half and costs nothing.
+//     head fill 8 to 64 rows of a tile, and the operands come straight from
+//     the copied tile.  P goes in as three bf16 terms (two fp16 ones with 8-bit
+//     keys), which keeps O as near to 64 bits as a 32-bit softmax; with at most
+//     8 rows two of them share an instruction, whose lower half would idle.
+//
+// Measured on a GB300, of the measured copy bandwidth (6770 GB/s): 16 sequences
+// of 700 to 32K tokens, 64 query and 8 KV heads of 128: 165 us, 98 %; one
+// sequence of 128K: 83 us, 96 %; 8 x 32K tokens, 16 rows a KV head: 163 us,
+// 95 %, and with 28 rows, where the matrix instructions begin to bound it, 208
+// us.  8-bit, 8 sequences of 20K to 32K: 73 us, 87 %, bound by the conversions
+// (64 of a warp's 450 instructions a step of 32 keys for each product).  One
+// 4K sequence takes 9.1 us, of which the start (lengths, pages, the first tile)
+// is 3.5 and the second kernel 2.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -184,22 +193,22 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// p as the sum of two 16-bit terms: the nearest, and the nearest to what it
-// leaves (2^-18 of p at most in bf16, 2^-22 in fp16).  Returns the sum of what
-// the terms stand for: the rows are normalised by the weights that they were
-// taken with, so that what the terms lose cancels where one key dominates.
+// p as a sum of 16-bit terms, each the nearest to what those before it leave:
+// two fp16 ones hold it to 2^-22, three bf16 ones to 2^-26.  (Two bf16 terms,
+// 2^-18, left O four times further from 64 bits than a 32-bit softmax does.)
 template <bool F16>
-__device__ __forceinline__ float split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ void split(float p0, float p1, uint32_t (&term)[F16 ? 2 : 3])
 {
     if constexpr (F16) {
-        hi = pack_f16(p0, p1);
-        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        lo = pack_f16(p0 - h.x, p1 - h.y);
-        return p0 + p1;
+        term[0] = pack_f16(p0, p1);
+        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&term[0]));
+        term[1] = pack_f16(p0 - h.x, p1 - h.y);
     } else {
-        hi = pack_bf16(p0, p1);
-        lo = pack_bf16(p0 - bf16_lo(hi), p1 - bf16_hi(hi));
-        return (bf16_lo(hi) + bf16_lo(lo)) + (bf16_hi(hi) + bf16_hi(lo));
+        term[0] = pack_bf16(p0, p1);
+        p0 -= bf16_lo(term[0]);
+        p1 -= bf16_hi(term[0]);
+        term[1] = pack_bf16(p0, p1);
+        term[2] = pack_bf16(p0 - bf16_lo(term[1]), p1 - bf16_hi(term[1]));
     }
 }
 
@@ -220,12 +229,12 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c)
 __device__ __forceinline__ int keys_of(const PagedArgs &a, int b)
 {
     const int most = a.cache.max_pages * a.cache.page_size;
-    return min(max(__ldg(a.seq_lens + b), 0), most);
+    return min(max(a.seq_lens[b], 0), most);
 }
 
 __device__ __forceinline__ int new_of(const PagedArgs &a, int b)
 {
-    return a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.Sq) : a.Sq;
+    return a.new_lens ? min(max(a.new_lens[b], 0), a.Sq) : a.Sq;
 }
 
 // Positions.  All jobs lie on one line, in units of an eighth of a tile, the
@@ -287,6 +296,10 @@ __device__ __forceinline__ void advance(const PagedArgs &a, Place &p, int pos)
         enter<TILE>(a, p);
     } while (p.tiles == 0);
 }
+
+// (Loads of what an earlier kernel may have written are plain ones: the
+// read-only path promises nothing about data that was written after this
+// kernel came up.)
 
 // The line in equal shares: block c has [first(c), first(c + 1)).
 struct Shares {
@@ -398,7 +411,7 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if ((i == 0 || !a.box_rows) && key_of(i) < at.keys)
-                entry[i] = __ldg(a.cache.table + at.b * a.cache.table_stride + page_of(a.cache, key_of(i)));
+                entry[i] = a.cache.table[at.b * a.cache.table_stride + page_of(a.cache, key_of(i))];
     };
     look_up();
     int stage = 0;
@@ -521,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         a.ws_rec[blockIdx.x] = make_int4(0, 0, 0, -1);
     if (blockIdx.x == 0)
         for (int b = tid; b < a.B; b += kThreads) {
-            if (__ldg(a.seq_lens + b) != keys_of(a, b))
+            if (a.seq_lens[b] != keys_of(a, b))
                 record_bounds(0x901);
-            if (a.new_lens && __ldg(a.new_lens + b) != new_of(a, b))
+            if (a.new_lens && a.new_lens[b] != new_of(a, b))
                 record_bounds(0x902);
         }
     Shares shares;
@@ -600,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             float kmul = a.scale_log2;
             uint32_t flip = 0;
             if (FP8) {
-                kmul *= __ldg(a.cache.k_scale + h_kv);
+                kmul *= a.cache.k_scale[h_kv];
                 flip = kmul < 0.f ? 0x80008000u : 0u;
                 kmul = fabsf(kmul);
             }
@@ -678,6 +691,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 for (int e = 0; e < 4; ++e)
                     sc[n][e] = 0.f;
             if constexpr (!FP8) {
+                // in 2 sums of d/2 products each, added at the end
+                float part[2][NT][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            part[i][n][e] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -687,9 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * BOXES + n * 8 * BOX);
                         const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
                         const uint32_t a2 = qf[kk][RG == 0 ? 1 : 2];
-                        mma<false>(sc[n], qf[kk][0], a1, a2, a3, f[0], f[1]);
-                        mma<false>(sc[n + 1], qf[kk][0], a1, a2, a3, f[2], f[3]);
+                        mma<false>(part[kk % 2][n], qf[kk][0], a1, a2, a3, f[0], f[1]);
+                        mma<false>(part[kk % 2][n + 1], qf[kk][0], a1, a2, a3, f[2], f[3]);
                     }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < (RG == 0 ? 2 : 4); ++e)
+                        sc[n][e] = part[0][n][e] + part[1][n][e];
             } else {
                 // A matrix load gives each thread four neighbouring elements of
                 // a key; the first two stand for columns 2t, 2t+1 of the
@@ -751,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         }
                 }
             }
-            uint32_t p_hi[NT][2], p_lo[NT][2];
+            constexpr int TERMS = FP8 ? 2 : 3;
+            uint32_t p[NT][2][TERMS];
 #pragma unroll
             for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
                 const float ref = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
@@ -760,17 +788,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 for (int n = 0; n < NT; ++n) {
                     const float p0 = ex2_approx(fmaf(sc[n][hf * 2], s_mul[hf], ref));
                     const float p1 = ex2_approx(fmaf(sc[n][hf * 2 + 1], s_mul[hf], ref));
-                    sum += split2<FP8>(p0, p1, p_hi[n][hf], p_lo[n][hf]);
+                    sum += p0 + p1;
+                    split<FP8>(p0, p1, p[n][hf]);
                 }
                 l_run[hf] += sum;
             }
             // ---- O += P V
             auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
+                // eight rows take two terms at once, the second in the tile's
+                // lower half, whose sums join the upper half's at the end; the
+                // third goes there too (the unit truncates its sums, and the
+                // upper one is the one that matters)
                 if constexpr (RG == 0) {
-                    mma<FP8>(d, p_hi[n][0], p_lo[n][0], p_hi[n + 1][0], p_lo[n + 1][0], b0, b1);
+                    mma<FP8>(d, p[n][0][0], p[n][0][1], p[n + 1][0][0], p[n + 1][0][1], b0, b1);
+                    if constexpr (TERMS == 3)
+                        mma<FP8>(d, 0u, p[n][0][2], 0u, p[n + 1][0][2], b0, b1);
                 } else {
-                    mma<FP8>(d, p_hi[n][0], p_hi[n][1], p_hi[n + 1][0], p_hi[n + 1][1], b0, b1);
-                    mma<FP8>(d, p_lo[n][0], p_lo[n][1], p_lo[n + 1][0], p_lo[n + 1][1], b0, b1);
+#pragma unroll
+                    for (int i = 0; i < TERMS; ++i)
+                        mma<FP8>(d, p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
                 }
             };
             // every (8-column tile of O, 16 keys) once: `use` gets the column
@@ -914,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     if (col0 == 0)
                         a.ws_ml[at_ws] = make_float2(top, sum);
                 } else if (a.Sq == 1 || r % a.Sq < n_new) {
-                    const float f = sum == 0.f ? 0.f : (FP8 ? __ldg(a.cache.v_scale + h_kv) : 1.f) / sum;
+                    const float f = sum == 0.f ? 0.f : (FP8 ? a.cache.v_scale[h_kv] : 1.f) / sum;
                     const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
 #pragma unroll
                     for (int e = 0; e < CP; e += 2) {
@@ -1051,7 +1087,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
                 x += f * part[w][tid];
             }
             const long long at_row = (long long)bh * a.R + r;
-            x *= sum == 0.f ? 0.f : (a.cache.v_scale ? __ldg(a.cache.v_scale + bh % a.Hkv) : 1.f) / sum;
+            x *= sum == 0.f ? 0.f : (a.cache.v_scale ? a.cache.v_scale[bh % a.Hkv] : 1.f) / sum;
             if (a.out_bf16)
                 ((__nv_bfloat16 *)a.out)[at_row * D + tid] = __float2bfloat16_rn(x);
             else
@@ -1108,7 +1144,8 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     a.n_rt = (a.R + C::kRows - 1) / C::kRows;
     const long long keys = (long long)a.cache.max_pages * a.cache.page_size;
     const long long jobs = (long long)a.B * a.Hkv * a.n_rt;
-    const long long most = ((keys + C::kTile - 1) / C::kTile + 1) * jobs;  // tiles
+    static_assert(kJobCost <= 2 * kUnits, "a job's cost counts as two tiles below");
+    const long long most = ((keys + C::kTile - 1) / C::kTile + 2) * jobs;  // tiles, a job's cost included
     if (most > 0x7fffffffLL / kUnits) {
         snprintf(msg, msg_len, "too many key tiles for one call (%lld)", most);
         return MERCURY_EINVAL;
@@ -1133,7 +1170,7 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         snprintf(msg, msg_len, "paged attention kernel built with %d registers a thread, needs %d", ki.regs, kMinLaunchRegs);
         return MERCURY_ECUDA;
     }
-    // a block per SM, and none that could not get a tile (a job's cost included)
+    // a block per SM, and none that could not get a tile
     const unsigned grid = (unsigned)(most < ki.sms ? most : ki.sms);
     a.records = (int)grid;
     // a job that fits into one tile is never cut: no parts, nothing to join
