@@ -18,11 +18,13 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmercury_attn.so")
+BINDING_PATH = os.path.join(LIB_DIR, "mercury_binding.so")  # the serving calls' CPython extension
 CHECK_LIB_DIR = os.path.join(HERE, "_lib_check")
 CHECK_LIB_PATH = os.path.join(CHECK_LIB_DIR, "libmercury_attn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "lse_merge.cu", "noalloc.cu", "gemm_shifted.cu", "schedule.cu",
@@ -52,8 +54,26 @@ def up_to_date(path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    """The CPython extension of the serving calls (plain C, the host compiler)."""
+    srcs = [os.path.join(CSRC, "binding.c"), os.path.join(HERE, "..", "include", "mercury_attn.h")]
+    if not force and os.path.exists(BINDING_PATH) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING_PATH) for f in srcs):
+        return BINDING_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"], srcs[0],
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("gcc failed on binding.c:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, check: bool = False) -> str:
     lib_dir, lib_path = (CHECK_LIB_DIR, CHECK_LIB_PATH) if check else (LIB_DIR, LIB_PATH)
+    build_binding(force)
     if not force and up_to_date(lib_path):
         return lib_path
     nvcc = _nvcc()

@@ -163,6 +163,22 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+def _load_binding():
+    """The C side of the serving calls' marshalling (csrc/binding.c)."""
+    import importlib.machinery
+    import importlib.util
+    path = _build.BINDING_PATH
+    if not os.path.exists(path):
+        raise ImportError("mercury_binding.so is not built (%s); run long_context_sharded_gb300.build.build() first" % path)
+    loader = importlib.machinery.ExtensionFileLoader("mercury_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("mercury_binding", path, loader=loader))
+    loader.exec_module(module)
+    return module
+
+
+_fast = _load_binding()
+
+
 def _check(rc: int) -> None:
     if rc != MERCURY_OK:
         raise MercuryError(rc, lib.mercury_last_error().decode(errors="replace"))
@@ -495,9 +511,11 @@ _Strides = ctypes.c_longlong * 3
 
 
 class _Torch:
-    """The torch names that the serving calls use, looked up once: those calls
+    """The torch names that the serving calls use, looked up once.  Those calls
     are bound by their marshalling (a decode step's kernels take a few
-    microseconds), so they query each tensor as little as their checks need."""
+    microseconds), so a call whose tensors are all as they should be goes
+    through the C extension; the Python side allocates outputs, takes a given
+    stream, and says what is wrong where something is."""
 
     def __init__(self):
         import torch
@@ -514,7 +532,11 @@ _torch_names = None
 def _names():
     global _torch_names
     if _torch_names is None:
-        _torch_names = _Torch()
+        T = _Torch()
+        _fast.init(T.bf16, T.fp32, T.int32, T.current_device, T.raw_stream,
+                   *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                       lib.mercury_rope, lib.mercury_kv_append, lib.mercury_attn_paged, lib.mercury_attn_paged_bf16)))
+        _torch_names = T
     return _torch_names
 
 
@@ -610,10 +632,16 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
     with contiguous heads).  positions: int32 [B,S] or [S]; None: start + s.
     inverse=True applies the transpose, the gradient of the forward call.
     out: a tensor of x's shape and dtype, or x itself; a new one by default."""
-    T = _names()
-    shape = _shape4(x, "x")
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (mercury_rope_init)")
+    T = _torch_names or _names()
+    if out is not None and stream is None:
+        rc = _fast.rope(x, ctypes.addressof(plan), positions, start, inverse, out)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return out
+    shape = _shape4(x, "x")
     dtype = x.dtype
     if dtype is not T.bf16 and dtype is not T.fp32:
         raise TypeError("x must be torch.bfloat16 or torch.float32 (got %s)" % dtype)
@@ -714,6 +742,7 @@ class PagedCache:
             max(block_table.stride(0), block_table.shape[1]), ELEM_E4M3 if e4m3 else ELEM_BF16, Hkv, d, page_size, n,
             block_table.shape[1], self.B)
         self._ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=None, q=None, q_out=None, stream=None):
@@ -721,10 +750,19 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
     past_lens[b] + i, keys rotated by `rope` (a RopePlan) on the way; q
     [B,Hq,S,d], where given, is rotated into q_out (q itself is fine; a new
     tensor by default), which is returned."""
-    T = _names()
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
+    if rope is not None and not isinstance(rope, RopePlan):
+        raise TypeError("rope must be a RopePlan (mercury_rope_init)")
     dev = cache.device_index
+    if stream is None and (q is None or q_out is not None):
+        rc = _fast.append(cache.address, dev, k, v, past_lens, new_lens, 0 if rope is None else ctypes.addressof(rope), q,
+                          q_out)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return q_out
+    T = _names()
     _on_current(dev, "the cache")
     shape = _shape4(k, "k")
     B, Hkv, S, d = shape
@@ -737,11 +775,7 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
         sk = _Strides(sk[0], sk[1], sk[2])
     if sv is not None:
         sv = _Strides(sv[0], sv[1], sv[2])
-    plan = None
-    if rope is not None:
-        if not isinstance(rope, RopePlan):
-            raise TypeError("rope must be a RopePlan (mercury_rope_init)")
-        plan = ctypes.byref(rope)
+    plan = None if rope is None else ctypes.byref(rope)
     pq = sq = po = so = None
     Hq = 0
     if q is not None:
@@ -777,10 +811,16 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
 
 
 def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, stream):
-    T = _torch_names
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
+    T = _torch_names
     dev = cache.device_index
+    if out is not None and lse is not None and stream is None:
+        rc = _fast.attn(out_dtype is T.bf16, q, cache.address, dev, seq_lens, new_lens, causal, out, lse)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return out, lse
     _on_current(dev, "the cache")
     shape = _shape4(q, "q")
     B, Hq, Sq, d = shape

@@ -7,11 +7,12 @@ Bounds.  A rounding is off by at most half a step: 2^-8 of the value for bf16,
 32-bit sine and cosine and two products round a few times more: 6e-7 of
 |a| + |b| covers them.  Attention: a score is a sum of d products in a 32-bit
 accumulator (2^-21 of the sum of their magnitudes, over sqrt(d), allows for
-its truncation), P is kept to 2^-17 and an accumulator that takes the keys in
+its truncation), P is kept to 2^-17 or better and an accumulator that takes the keys in
 steps of 16 to 128 loses 2^-23 a step; each is relative to sum p |v|.
 """
 import ctypes
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -278,6 +279,34 @@ def test_binding_refuses_cpu_tensors(m):
 
 
 # ------------------------------------------------------------------------------------ rope
+
+def test_extension_leaves_what_it_cannot_take(m):
+    """The C side of the binding calls nothing for arguments that are not as a call wants them: it returns None,
+    leaves no exception, and keeps no reference."""
+    m._names()
+    plan = ctypes.addressof(m.mercury_rope_init(64))
+    struct = cache_struct(m)
+    cache = ctypes.addressof(struct)
+    x = torch.zeros(1, 2, 3, 64, dtype=BF16)
+    lens = torch.zeros(struct.B, dtype=torch.int32)
+
+    class Odd:
+        dtype, shape = BF16, (1, 2, 3, 64)
+
+        def get_device(self):
+            raise RuntimeError("no")
+
+    for bad in (x, x.float(), x[0], None, 3, "x", Odd(), torch.zeros(0, dtype=BF16)):
+        before = sys.getrefcount(bad)
+        assert m._fast.rope(bad, plan, None, 0, False, bad) is None
+        assert m._fast.rope(bad, plan, bad, 2 ** 70, False, x) is None
+        assert m._fast.append(cache, 0, bad, bad, lens, None, plan, bad, bad) is None
+        assert m._fast.append(cache, 0, bad, bad, bad, bad, 0, None, None) is None
+        assert m._fast.attn(False, bad, cache, 0, lens, None, True, bad, bad) is None
+        assert m._fast.attn(True, bad, cache, -1, lens, bad, True, bad, bad) is None
+        assert sys.getrefcount(bad) == before
+    assert m._fast.rope() is None and m._fast.append(cache) is None and m._fast.attn() is None
+
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, FP32])
@@ -633,6 +662,44 @@ def test_strided_queries(gm):
 
 
 # --------------------------------------------------------------------- streams, graphs, runs
+
+@pytest.mark.gpu
+def test_both_ways_into_a_call(gm):
+    """A call goes through the C extension or, with a stream given, through the Python checks: the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen)
+    here = torch.cuda.current_stream()
+    plan = gm.mercury_rope_init(64)
+    pos = torch.randint(-9, 9000, (2, 5), device="cuda", generator=gen, dtype=torch.int32)
+    for x in (rand(2, 3, 5, 64), rand(2, 3, 5, 64).to(BF16), rand(2, 5, 3, 64).to(BF16).transpose(1, 2)):
+        for p, start, inverse in ((None, 7, False), (pos, 0, True), (pos[0], 0, False)):
+            a, b = torch.zeros_like(x), torch.zeros_like(x)
+            assert gm.mercury_rope(x, plan, positions=p, start=start, inverse=inverse, out=a) is a
+            gm.mercury_rope(x, plan, positions=p, start=start, inverse=inverse, out=b, stream=here)
+            assert torch.equal(a, b) and not torch.equal(a, x)
+    table = torch.randperm(8, device="cuda", generator=gen).to(torch.int32).reshape(2, 4)
+    past = torch.tensor([3, 20], dtype=torch.int32, device="cuda")
+    new = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    k, v = rand(2, 5, 2, 64).to(BF16).transpose(1, 2), rand(2, 2, 5, 64).to(BF16)
+    q = rand(2, 4, 5, 64).to(BF16)
+    for fresh in (None, new):
+        for rope in (None, plan):
+            got = []
+            for stream in (None, here):
+                cache = gm.PagedCache(torch.zeros(8, 2, 16, 64, dtype=BF16, device="cuda"),
+                                      torch.zeros(8, 2, 16, 64, dtype=BF16, device="cuda"), table)
+                qo = torch.zeros_like(q)
+                assert gm.mercury_kv_append(cache, k, v, past, new_lens=fresh, rope=rope, q=q, q_out=qo, stream=stream) is qo
+                assert gm.mercury_kv_append(cache, k, v, past, new_lens=fresh, rope=rope, stream=stream) is None
+                res = [cache.k_cache, cache.v_cache, qo]
+                for call, dtype in ((gm.mercury_attn_paged, FP32), (gm.mercury_attn_paged_bf16, BF16)):
+                    out, lse = torch.zeros(q.shape, dtype=dtype, device="cuda"), torch.zeros(q.shape[:3], device="cuda")
+                    res += call(qo, cache, past + 5, new_lens=fresh, causal=rope is None, out=out, lse=lse, stream=stream)
+                    assert res[-1] is lse and res[-2] is out
+                got.append(res)
+            gm.mercury_sync_status()
+            assert all(torch.equal(a, b) for a, b in zip(*got)) and all(a.abs().sum() > 0 for a in got[0])
+
 
 @pytest.mark.gpu
 def test_streams_and_graphs(gm):
