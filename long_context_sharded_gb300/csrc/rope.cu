@@ -67,13 +67,13 @@ __global__ void __launch_bounds__(kRotThreads, 2) rope_kernel(const __grid_const
         RotUnit<VE> unit(a.plan, u, a.d);
         if (!unit.rotated && !a.copy_rest)
             continue;
-        walk_heads<T, VE, true>(
-            src + h0 * a.xs.h, a.xs.h, h1 - h0, unit,
+        walk_heads<T, VE, true, false>(
+            src + h0 * a.xs.h, a.xs.h, nullptr, h1 - h0, unit,
             [&] {
                 const long long pos = a.pos ? a.pos[b * a.pos_stride + s] : a.start + s;
                 unit.set_angles(turns, a.plan.magnitude, a.inverse ? -pos : pos);
             },
-            [&](int h, const float (&y0)[VE], const float (&y1)[VE]) {
+            [&](int h, const float (&y0)[VE], const float (&y1)[VE], float) {
                 T *p = dst + (h0 + h) * a.os.h;
                 store_chunk<VE>(p + unit.at0, y0);
                 if (unit.two)

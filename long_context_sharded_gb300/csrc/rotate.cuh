@@ -74,15 +74,48 @@ __device__ __forceinline__ void store_chunk(float *p, const float (&y)[VE])
         *p = y[0];
 }
 
-template <int VE>
-__device__ __forceinline__ void store_chunk_e4m3(uint8_t *p, const float (&y)[VE])
-{
-    if constexpr (VE == 8)
-        *reinterpret_cast<uint2 *>(p) =
-            make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16, pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
-    else
-        *p = (uint8_t)pack_e4m3(y[0], 0.f);
-}
+// y / scale[head] to the nearest e4m3 and saturated.  The stored byte is the one
+// nearest to the quotient's 32-bit rounding, as a division gives it, mostly
+// without dividing: with r the rounded reciprocal, y r (1 -+ 2^-21) lie on the
+// two sides of that quotient (four roundings of 2^-24 each do not reach 2^-21),
+// so where both round to the same byte it is the quotient's.  Where they do not
+// (next to a tie), or r is zero, infinite or near either, the elements are
+// divided.  (6 x 1000 tokens of 24 heads of 64: 10.5 us with divisions
+// throughout, 8.9 so; 6 x 8000 of 48 heads of 128: 132 and 121.)
+struct Quotient {
+    float scale, lo, hi;
+    bool divide;
+
+    __device__ __forceinline__ explicit Quotient(float s) : scale(s)
+    {
+        const float r = 1.f / s;
+        lo = r * (1.f - 0x1p-21f);
+        hi = r * (1.f + 0x1p-21f);
+        divide = !(fabsf(r) > 0x1p-100f && fabsf(r) < 0x1p100f);
+    }
+
+    template <int VE>
+    __device__ __forceinline__ void store(uint8_t *p, const float (&y)[VE]) const
+    {
+        constexpr int N = VE == 1 ? 1 : VE / 2;
+        uint32_t w[N], differ = divide;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float a = y[2 * i], b = VE == 1 ? 0.f : y[2 * i + (VE > 1)];
+            w[i] = pack_e4m3(a * lo, b * lo);
+            differ |= w[i] ^ pack_e4m3(a * hi, b * hi);
+        }
+        if (differ) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[i] = pack_e4m3(y[2 * i] / scale, VE == 1 ? 0.f : y[2 * i + (VE > 1)] / scale);
+        }
+        if constexpr (VE == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        else
+            *p = (uint8_t)w[0];
+    }
+};
 
 // The plan's frequencies into shared memory: lanes want different ones, which
 // the parameter bank would serve one after the other, for every warp anew.
@@ -162,52 +195,64 @@ struct RotUnit {
 };
 
 // One unit of n heads, `stride` elements apart from `src` on: turned if TURN,
-// and given to store(head, chunk 0, chunk 1).  kRotBatch heads are loaded at a
-// time, the first ones while ready(), which has the angles and whatever a
-// store needs found, runs.  16-bit heads are double buffered, the next batch on
+// and given to store(head, chunk 0, chunk 1, scale).  kRotBatch heads are
+// loaded at a time, the first ones while ready(), which has the angles and
+// whatever a store needs found, runs.  16-bit heads are double buffered, the next batch on
 // its way while one is turned and stored (32K prompt of 40 heads: 109 to 99
 // us); 32-bit ones are not: with twice the bytes in flight a head the registers
 // cost more than the overlap gains (12.0 against 10.9 us at 2 x 12 heads x
 // 4099 tokens).  (Written out, because the output may be the input: the
-// compiler would keep each load behind the stores before it.)
-template <typename T, int VE, bool TURN, typename Ready, typename Store>
-__device__ __forceinline__ void walk_heads(const T *src, long long stride, int n, RotUnit<VE> &unit, Ready ready,
-                                           Store store)
+// compiler would keep each load behind the stores before it.)  With SCALED,
+// scales[head] goes the same way; two heads at a time then, since with the
+// quantisation's registers four spill (6 x 1000 tokens of 24 heads of 64: 8.2
+// us instead of 10.7; 6 x 8000 of 48 of 128: 122 and 150).
+template <typename T, int VE, bool TURN, bool SCALED, typename Ready, typename Store>
+__device__ __forceinline__ void walk_heads(const T *src, long long stride, const float *scales, int n,
+                                           RotUnit<VE> &unit, Ready ready, Store store)
 {
     constexpr bool kAhead = sizeof(T) == 2;
-    Chunk<T, VE> x0[2][kRotBatch], x1[2][kRotBatch];
+    constexpr int kBatch = SCALED ? kRotBatch / 2 : kRotBatch;
+    Chunk<T, VE> x0[2][kBatch], x1[2][kBatch];
+    float sc[2][kBatch];
     auto load = [&](int slot, int h0) {
 #pragma unroll
-        for (int i = 0; i < kRotBatch; ++i)
+        for (int i = 0; i < kBatch; ++i)
             if (h0 + i < n) {
                 const T *p = src + (h0 + i) * stride;
                 x0[slot][i].load(p + unit.at0);
                 if (unit.two)
                     x1[slot][i].load(p + unit.at1);
+                if constexpr (SCALED)
+                    sc[slot][i] = scales[h0 + i];
             }
     };
     load(0, 0);
     ready();
-    for (int h0 = 0; h0 < n; h0 += kRotBatch) {
+    for (int h0 = 0; h0 < n; h0 += kBatch) {
         if (kAhead)
-            load(1, h0 + kRotBatch);
+            load(1, h0 + kBatch);
         else if (h0 > 0)
             load(0, h0);
 #pragma unroll
-        for (int i = 0; i < kRotBatch; ++i)
+        for (int i = 0; i < kBatch; ++i)
             if (h0 + i < n) {
                 float y0[VE], y1[VE];
                 x0[0][i].widen(y0);
                 x1[0][i].widen(y1);
                 if (TURN)
                     unit.turn(y0, y1);
-                store(h0 + i, y0, y1);
+                if constexpr (SCALED)
+                    store(h0 + i, y0, y1, sc[0][i]);
+                else
+                    store(h0 + i, y0, y1, 1.f);
             }
         if (kAhead) {
 #pragma unroll
-            for (int i = 0; i < kRotBatch; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
                 x0[0][i] = x0[1][i];
                 x1[0][i] = x1[1][i];
+                if constexpr (SCALED)
+                    sc[0][i] = sc[1][i];
             }
         }
     }
@@ -232,7 +277,8 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
     // An angle costs about as much as moving two heads, so a thread of many
     // heads is cheap (a 32K prompt of 40 heads: 138 us with 4, 113 with 8, 99
     // with 16, 102 with 32), but a short call needs its blocks (6 x 1000
-    // tokens of 24 heads into an 8-bit cache: 12.8 us with 16, 11.7 with 2).
+    // tokens of 24 heads into an 8-bit cache, with a division for every element: 12.8 us with 16,
+    // 11.7 with 2).
     int hp = 16;
     while (hp > 1 && 2 * g.blocks * ((H + hp - 1) / hp) < 3LL * sms)
         hp /= 2;

@@ -501,6 +501,32 @@ def test_append_saturates_and_keeps_nan(gm):
     assert row[:4].tolist() == [448.0, -448.0, 448.0, -448.0] and math.isnan(row[4]) and row[5] == 448.0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 0.5, 3.0, 1 / 3, 0.7, -5.0, 1.1e-3, 2.0 ** -120, 1e-40, 2.0 ** 120, 0.0, math.inf, math.nan])
+def test_append_stores_the_quotient(gm, scale, aligned):
+    """Every bf16 value over a scale: the e4m3 nearest to the quotient's 32-bit rounding (ties to even), saturated;
+    bit for bit, ties and their neighbours among them."""
+    x = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.int16).view(BF16).reshape(1, 1, 1024, 64)
+    if not aligned:  # one element at a time
+        y = torch.empty(1, 1, 1024, 65, dtype=BF16, device="cuda")[..., 1:]
+        x = y.copy_(x)
+    kc, vc = (torch.zeros(16, 1, 64, 64, device="cuda").to(E4M3) for _ in range(2))
+    sc = torch.tensor([scale], device="cuda")
+    table = torch.arange(16, dtype=torch.int32, device="cuda").reshape(1, 16)
+    gm.mercury_kv_append(gm.PagedCache(kc, vc, table, k_scale=sc, v_scale=sc), x, x,
+                         torch.zeros(1, dtype=torch.int32, device="cuda"))
+    gm.mercury_sync_status()
+    # the quotient in 64 bits, rounded to 32 (twice rounded, which is exact here: 8 by 24 bits), then by steps
+    z = (x.double().cpu() / float(np.float32(scale)) if scale else x.double().cpu() / 0.0).float().double().reshape(-1)
+    step = torch.exp2(torch.floor(torch.log2(z.abs().clamp(2.0 ** -6, 448.0))) - 3)
+    want = (torch.round(z.abs().clamp(max=512.0) / step) * step).clamp(max=448.0) * torch.sign(z)
+    for cache in (kc, vc):
+        got = cache.cpu().float().double().reshape(-1)
+        nan = z.isnan()
+        assert torch.equal(got.isnan(), nan) and torch.equal(got[~nan], want[~nan])
+
+
 # ------------------------------------------------------------------------------- attention
 
 def run_attention(gm, B, Hq, Hkv, Sq, d, page, lens, dtype=BF16, new=None, causal=True, bf16_out=False, scale=1.5,
