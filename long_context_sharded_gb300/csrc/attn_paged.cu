@@ -557,10 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     unsigned long long budget = a.wait_ns;
     uint32_t qf[KK][RG == 0 ? 2 : 4];
     int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
+    float k_scale = 1.f;
     auto load_q = [&]() {
         h_kv = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
         row0 = (at.hr - h_kv * a.n_rt) * C::kRows;
         n_new = new_of(a, at.b);
+        if (FP8)
+            k_scale = a.cache.k_scale[h_kv];
 #pragma unroll
         for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
             const int r = row0 + rg * 16 + g + hf * 8;
@@ -589,8 +592,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     float acc[DN][4];
     float m_run[2], l_run[2], s_mul[2];
     int lim[2];         // keys that each of this thread's rows sees
-    bool fresh = true;  // the tile is the first of its job in this share
-    int first_j = at.j;
     // A row of the joined tile belongs to TPR threads, which take its columns
     // in turn, two at a time.
     constexpr int TPR = kWarps * 32 / C::kRows, CP = D / TPR;
@@ -603,385 +604,392 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                                  : chunk_at<ROWB, TILE>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4));
     int stage = 0;
     uint32_t phase = 0;
-    for (;;) {
-        wait_phase(full + stage, phase, budget);
-        if (fresh) {
-            fresh = false;
-            first_j = at.j;
-            // a factor of at least 2^-120, so that a masked score stays -inf
-            // under it; a scale's sign goes to the queries
-            float kmul = a.scale_log2;
-            uint32_t flip = 0;
-            if (FP8) {
-                kmul *= a.cache.k_scale[h_kv];
-                flip = kmul < 0.f ? 0x80008000u : 0u;
-                kmul = fabsf(kmul);
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                m_run[hf] = -INFINITY;
-                l_run[hf] = 0.f;
-                const int s = (row0 + rg * 16 + g + hf * 8) % a.Sq;
-                lim[hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
-                s_mul[hf] = kmul;
-                if (RG == 0 && hf == 1)
-                    continue;
-                if (FP8) {
-                    // e4m3 keys widen exactly to fp16, so the queries are
-                    // taken to fp16 too: scaled by a power of two that brings
-                    // the row's largest element to [2^14, 2^15), their 8 bits
-                    // fit exactly down to 2^-28 of it
-                    float top = 0.f;
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        const uint32_t x = qf[kk][hf], y = qf[kk][RG == 0 ? 1 : 2 + hf];
-                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))),
-                                               fmaxf(fabsf(bf16_lo(y)), fabsf(bf16_hi(y)))));
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // exponent of 2^(14 - e), kept where both it and its inverse are normal
-                    int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
-                    up = min(max(up, -110), 110);
-                    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                    const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
-                    s_mul[hf] = mul < 7.5e-37f ? 7.5e-37f : mul;
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        uint32_t &x = qf[kk][hf], &y = qf[kk][RG == 0 ? 1 : 2 + hf];
-                        x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
-                        y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f) ^ flip;
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < DN; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[n][e] = 0.f;
+    // this warp is done with the stage
+    auto release = [&] {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(empty + stage);
+        if (++stage == NS) {
+            stage = 0;
+            phase ^= 1;
         }
-
-#pragma unroll 1
-        for (int step = kg; step < kWarps; step += C::kKg) {
-            const int kb = at.j * TILE + step * KEYS;
-            if (kb >= at.keys)
-                break;
-            const uint32_t k_u = k_lane + stage * C::kStage + step * KEYS * BOX;
-            const uint32_t v_u = v_lane + stage * C::kStage + step * KEYS * BOX;
-            // Word w of row r of this step's values.
-            auto v_word = [&](int r, int w) {
-                return reinterpret_cast<uint32_t *>(smem + stage * C::kStage + C::kPart + (step * KEYS + r) * BOX +
-                                                    w / (BOX / 4) * BOXES) + w % (BOX / 4);
-            };
-            // A copied box's rows behind the last key may hold anything: their
-            // scores are masked, their values must not be infinite or NaN.
-            // (Warps of several row groups write the same zeros.)
-            // This is the job's last tile, so the fence at the job's end stands
-            // between these zeros and the next tensor copy.
-            if (kb + KEYS > at.keys) {
-                for (int i = (at.keys - kb) * (ROWB / 16) + lane; i < KEYS * (ROWB / 16); i += 32)
-                    st_shared_v4(smem_u32(v_word(i / (ROWB / 16), i % (ROWB / 16) * 4)), 0, 0, 0, 0);
-                __syncwarp();
-            }
-            // ---- S = Q K^T
-            float sc[NT][4];
+    };
+    for (;;) {
+        // ---- a job, or its part in this share: everything that does not need
+        // a tile goes before the first wait
+        const int first_j = at.j;
+        int left = min(at.tiles - at.j, (end - at.pos + kUnits - 1) / kUnits);  // its tiles here
+        at.pos += (left - 1) * kUnits;                                          // of the last of them
+        // a factor of at least 2^-120, so that a masked score stays -inf
+        // under it; a scale's sign goes to the queries
+        float kmul = a.scale_log2;
+        uint32_t flip = 0;
+        if (FP8) {
+            kmul *= k_scale;
+            flip = kmul < 0.f ? 0x80008000u : 0u;
+            kmul = fabsf(kmul);
+        }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sc[n][e] = 0.f;
-            if constexpr (!FP8) {
-                // in 2 sums of d/2 products each, added at the end
-                float part[2][NT][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            part[i][n][e] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        // keys n*8 .. +15, elements kk*16 .. +15
-                        uint32_t f[4];
-                        ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * BOXES + n * 8 * BOX);
-                        const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
-                        const uint32_t a2 = qf[kk][RG == 0 ? 1 : 2];
-                        mma<false>(part[kk % 2][n], qf[kk][0], a1, a2, a3, f[0], f[1]);
-                        mma<false>(part[kk % 2][n + 1], qf[kk][0], a1, a2, a3, f[2], f[3]);
-                    }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < (RG == 0 ? 2 : 4); ++e)
-                        sc[n][e] = part[0][n][e] + part[1][n][e];
-            } else {
-                // A matrix load gives each thread four neighbouring elements of
-                // a key; the first two stand for columns 2t, 2t+1 of the
-                // product's inner axis and the last two for 2t+8, 2t+9, and
-                // the queries were loaded in the same order.
+        for (int hf = 0; hf < 2; ++hf) {
+            m_run[hf] = -INFINITY;
+            l_run[hf] = 0.f;
+            const int s = (row0 + rg * 16 + g + hf * 8) % a.Sq;
+            lim[hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
+            s_mul[hf] = kmul;
+            if (RG == 0 && hf == 1)
+                continue;
+            if (FP8) {
+                // e4m3 keys widen exactly to fp16, so the queries are
+                // taken to fp16 too: scaled by a power of two that brings
+                // the row's largest element to [2^14, 2^15), their 8 bits
+                // fit exactly down to 2^-28 of it
+                float top = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
-                    uint32_t f[4];
-                    ldsm_x4(f, k_u ^ (kk << 4));
-                    const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
+                    const uint32_t x = qf[kk][hf], y = qf[kk][RG == 0 ? 1 : 2 + hf];
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))),
+                                           fmaxf(fabsf(bf16_lo(y)), fabsf(bf16_hi(y)))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // exponent of 2^(14 - e), kept where both it and its inverse are normal
+                int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+                up = min(max(up, -110), 110);
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
+                s_mul[hf] = mul < 7.5e-37f ? 7.5e-37f : mul;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        mma<true>(sc[n], qf[kk][0], a1, qf[kk][RG == 0 ? 1 : 2], a3, e4m3_to_f16(f[n]),
-                                  e4m3_to_f16(f[n] >> 16));
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint32_t &x = qf[kk][hf], &y = qf[kk][RG == 0 ? 1 : 2 + hf];
+                    x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
+                    y = pack_f16(bf16_lo(y) * f, bf16_hi(y) * f) ^ flip;
                 }
             }
-            // ---- running maximum and sum; the masked keys of a row count as -inf
-            const int seen_by_all = a.causal ? at.keys - n_new + 1 : at.keys;
-            const bool edge = kb + KEYS > seen_by_all;
-            if (edge) {
+        }
+#pragma unroll
+        for (int n = 0; n < DN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[n][e] = 0.f;
+
+        for (;;) {
+            wait_phase(full + stage, phase, budget);
+#pragma unroll 1
+            for (int step = kg; step < kWarps; step += C::kKg) {
+                const int kb = at.j * TILE + step * KEYS;
+                if (kb >= at.keys)
+                    break;
+                const uint32_t k_u = k_lane + stage * C::kStage + step * KEYS * BOX;
+                const uint32_t v_u = v_lane + stage * C::kStage + step * KEYS * BOX;
+                // Word w of row r of this step's values.
+                auto v_word = [&](int r, int w) {
+                    return reinterpret_cast<uint32_t *>(smem + stage * C::kStage + C::kPart + (step * KEYS + r) * BOX +
+                                                        w / (BOX / 4) * BOXES) + w % (BOX / 4);
+                };
+                // A copied box's rows behind the last key may hold anything: their
+                // scores are masked, their values must not be infinite or NaN.
+                // (Warps of several row groups write the same zeros.)
+                // This is the job's last tile, so the fence at the job's end stands
+                // between these zeros and the next tensor copy.
+                if (kb + KEYS > at.keys) {
+                    for (int i = (at.keys - kb) * (ROWB / 16) + lane; i < KEYS * (ROWB / 16); i += 32)
+                        st_shared_v4(smem_u32(v_word(i / (ROWB / 16), i % (ROWB / 16) * 4)), 0, 0, 0, 0);
+                    __syncwarp();
+                }
+                // ---- S = Q K^T
+                float sc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (kb + n * 8 + t * 2 + (e & 1) >= lim[e >> 1])
-                            sc[n][e] = -INFINITY;
-            }
-            // The maximum moves only when a score exceeds it by 2^8: sum and O
-            // share whatever reference the terms were taken with, and the
-            // reduction and the rescaling stay off the common path.
-            bool grow = false;
-            float top[2];
+                        sc[n][e] = 0.f;
+                if constexpr (!FP8) {
+                    // in 2 sums of d/2 products each, added at the end
+                    float part[2][NT][4];
 #pragma unroll
-            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                float x = fmaxf(sc[0][hf * 2], sc[0][hf * 2 + 1]);
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int n = 1; n < NT; ++n)
-                    x = fmaxf(x, fmaxf(sc[n][hf * 2], sc[n][hf * 2 + 1]));
-                top[hf] = x * s_mul[hf];
-                grow |= top[hf] > m_run[hf] + 8.f;
-            }
-            if (__any_sync(0xffffffffu, grow)) {
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                part[i][n][e] = 0.f;
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                        for (int n = 0; n < NT; n += 2) {
+                            // keys n*8 .. +15, elements kk*16 .. +15
+                            uint32_t f[4];
+                            ldsm_x4(f, (k_u ^ ((kk & 3) << 5)) + (kk >> 2) * BOXES + n * 8 * BOX);
+                            const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
+                            const uint32_t a2 = qf[kk][RG == 0 ? 1 : 2];
+                            mma<false>(part[kk % 2][n], qf[kk][0], a1, a2, a3, f[0], f[1]);
+                            mma<false>(part[kk % 2][n + 1], qf[kk][0], a1, a2, a3, f[2], f[3]);
+                        }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < (RG == 0 ? 2 : 4); ++e)
+                            sc[n][e] = part[0][n][e] + part[1][n][e];
+                } else {
+                    // A matrix load gives each thread four neighbouring elements of
+                    // a key; the first two stand for columns 2t, 2t+1 of the
+                    // product's inner axis and the last two for 2t+8, 2t+9, and
+                    // the queries were loaded in the same order.
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        uint32_t f[4];
+                        ldsm_x4(f, k_u ^ (kk << 4));
+                        const uint32_t a1 = RG == 0 ? 0u : qf[kk][1], a3 = RG == 0 ? 0u : qf[kk][RG == 0 ? 1 : 3];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            mma<true>(sc[n], qf[kk][0], a1, qf[kk][RG == 0 ? 1 : 2], a3, e4m3_to_f16(f[n]),
+                                      e4m3_to_f16(f[n] >> 16));
+                    }
+                }
+                // ---- running maximum and sum; the masked keys of a row count as -inf
+                const int seen_by_all = a.causal ? at.keys - n_new + 1 : at.keys;
+                const bool edge = kb + KEYS > seen_by_all;
+                if (edge) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (kb + n * 8 + t * 2 + (e & 1) >= lim[e >> 1])
+                                sc[n][e] = -INFINITY;
+                }
+                // The maximum moves only when a score exceeds it by 2^8: sum and O
+                // share whatever reference the terms were taken with, and the
+                // reduction and the rescaling stay off the common path.
+                bool grow = false;
+                float top[2];
 #pragma unroll
                 for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                    float x = top[hf];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    x = fmaxf(x, m_run[hf]);
-                    const float f = x == -INFINITY ? 1.f : ex2_approx(m_run[hf] - x);
-                    m_run[hf] = x;
-                    l_run[hf] *= f;
+                    float x = fmaxf(sc[0][hf * 2], sc[0][hf * 2 + 1]);
 #pragma unroll
-                    for (int n = 0; n < DN; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            acc[n][hf * 2 + e] *= f;
-                            if (RG == 0)
-                                acc[n][2 + e] *= f;
-                        }
+                    for (int n = 1; n < NT; ++n)
+                        x = fmaxf(x, fmaxf(sc[n][hf * 2], sc[n][hf * 2 + 1]));
+                    top[hf] = x * s_mul[hf];
+                    grow |= top[hf] > m_run[hf] + 8.f;
                 }
-            }
-            constexpr int TERMS = FP8 ? 2 : 3;
-            uint32_t p[NT][2][TERMS];
+                if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                const float ref = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
-                float sum = 0.f;
+                    for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                        float x = top[hf];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        x = fmaxf(x, m_run[hf]);
+                        const float f = x == -INFINITY ? 1.f : ex2_approx(m_run[hf] - x);
+                        m_run[hf] = x;
+                        l_run[hf] *= f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float p0 = ex2_approx(fmaf(sc[n][hf * 2], s_mul[hf], ref));
-                    const float p1 = ex2_approx(fmaf(sc[n][hf * 2 + 1], s_mul[hf], ref));
-                    sum += p0 + p1;
-                    split<FP8>(p0, p1, p[n][hf]);
+                        for (int n = 0; n < DN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                acc[n][hf * 2 + e] *= f;
+                                if (RG == 0)
+                                    acc[n][2 + e] *= f;
+                            }
+                    }
                 }
-                l_run[hf] += sum;
-            }
-            // ---- O += P V
-            auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
-                // eight rows take two terms at once, the second in the tile's
-                // lower half, whose sums join the upper half's at the end; the
-                // third goes there too (the unit truncates its sums, and the
-                // upper one is the one that matters)
-                if constexpr (RG == 0) {
-                    mma<FP8>(d, p[n][0][0], p[n][0][1], p[n + 1][0][0], p[n + 1][0][1], b0, b1);
-                    if constexpr (TERMS == 3)
-                        mma<FP8>(d, 0u, p[n][0][2], 0u, p[n + 1][0][2], b0, b1);
-                } else {
+                constexpr int TERMS = FP8 ? 2 : 3;
+                uint32_t p[NT][2][TERMS];
 #pragma unroll
-                    for (int i = 0; i < TERMS; ++i)
-                        mma<FP8>(d, p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
+                for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                    const float ref = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float p0 = ex2_approx(fmaf(sc[n][hf * 2], s_mul[hf], ref));
+                        const float p1 = ex2_approx(fmaf(sc[n][hf * 2 + 1], s_mul[hf], ref));
+                        sum += p0 + p1;
+                        split<FP8>(p0, p1, p[n][hf]);
+                    }
+                    l_run[hf] += sum;
                 }
-            };
-            // every (8-column tile of O, 16 keys) once: `use` gets the column
-            // tile, the key tile and the operand
-            auto each_v = [&](auto &&use) {
-                if constexpr (!FP8) {
+                // ---- O += P V
+                auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
+                    // eight rows take two terms at once, the second in the tile's
+                    // lower half, whose sums join the upper half's at the end; the
+                    // third goes there too (the unit truncates its sums, and the
+                    // upper one is the one that matters)
+                    if constexpr (RG == 0) {
+                        mma<FP8>(d, p[n][0][0], p[n][0][1], p[n + 1][0][0], p[n + 1][0][1], b0, b1);
+                        if constexpr (TERMS == 3)
+                            mma<FP8>(d, 0u, p[n][0][2], 0u, p[n + 1][0][2], b0, b1);
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2)
+                        for (int i = 0; i < TERMS; ++i)
+                            mma<FP8>(d, p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
+                    }
+                };
+                // every (8-column tile of O, 16 keys) once: `use` gets the column
+                // tile, the key tile and the operand
+                auto each_v = [&](auto &&use) {
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int n = 0; n < NT; n += 2)
+#pragma unroll
+                            for (int c = 0; c < DN; c += 2) {
+                                uint32_t f[4];
+                                ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * BOXES + n * 8 * BOX);
+                                use(c, n, f[0], f[1]);
+                                use(c + 1, n, f[2], f[3]);
+                            }
+                    } else {
+                        // the transposed load pairs neighbouring elements of a key
+                        // in each half: the low bytes of both halves make the even
+                        // columns' operand, the high bytes the odd ones'
 #pragma unroll
                         for (int c = 0; c < DN; c += 2) {
                             uint32_t f[4];
-                            ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * BOXES + n * 8 * BOX);
-                            use(c, n, f[0], f[1]);
-                            use(c + 1, n, f[2], f[3]);
+                            ldsm_x4_t(f, v_u ^ ((c >> 1) << 4));
+#pragma unroll
+                            for (int n = 0; n < 4; n += 2) {
+                                const uint32_t x = __byte_perm(f[n], 0, 0x3120), y = __byte_perm(f[n + 1], 0, 0x3120);
+                                use(c, n, e4m3_to_f16(x), e4m3_to_f16(y));
+                                use(c + 1, n, e4m3_to_f16(x >> 16), e4m3_to_f16(y >> 16));
+                            }
                         }
+                    }
+                };
+                // A key that only some rows see still meets the others' products,
+                // as 0 * v: harmless unless v is infinite or NaN.
+                bool poison = false;
+                if (edge && a.causal && n_new > 1) {
+                    const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
+                    for (int r = r0; r < r1; ++r)
+                        for (int w = lane; w < ROWB / 4; w += 32) {
+                            const uint32_t x = *v_word(r, w);
+                            poison |= FP8 ? ((x & 0x7fu) == 0x7fu || (x & 0x7f00u) == 0x7f00u ||
+                                             (x & 0x7f0000u) == 0x7f0000u || (x & 0x7f000000u) == 0x7f000000u)
+                                          : ((x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u);
+                        }
+                    poison = __any_sync(0xffffffffu, poison);
+                }
+                if (!poison) {
+                    each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
                 } else {
-                    // the transposed load pairs neighbouring elements of a key
-                    // in each half: the low bytes of both halves make the even
-                    // columns' operand, the high bytes the odd ones'
+                    // token by token: the values that token s does not see are
+                    // taken as zero, and only its rows take the product
+                    for (int s = n_new - 1; s >= 0; --s) {
+                        const int seen = at.keys - n_new + s + 1;
+                        auto keep = [&](int key, uint32_t w) {
+                            return (key < seen ? w & 0xffffu : 0u) | (key + 1 < seen ? w & 0xffff0000u : 0u);
+                        };
+                        const int r = row0 + rg * 16 + g;
+                        const bool own0 = r % a.Sq == s, own1 = RG == 0 ? own0 : (r + 8) % a.Sq == s;
+                        each_v([&](int c, int n, uint32_t b0, uint32_t b1) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            add_pv(d, n, keep(kb + n * 8 + 2 * t, b0), keep(kb + n * 8 + 8 + 2 * t, b1));
 #pragma unroll
-                    for (int c = 0; c < DN; c += 2) {
-                        uint32_t f[4];
-                        ldsm_x4_t(f, v_u ^ ((c >> 1) << 4));
-#pragma unroll
-                        for (int n = 0; n < 4; n += 2) {
-                            const uint32_t x = __byte_perm(f[n], 0, 0x3120), y = __byte_perm(f[n + 1], 0, 0x3120);
-                            use(c, n, e4m3_to_f16(x), e4m3_to_f16(y));
-                            use(c + 1, n, e4m3_to_f16(x >> 16), e4m3_to_f16(y >> 16));
-                        }
+                            for (int e = 0; e < 4; ++e)
+                                if (e < 2 ? own0 : own1)
+                                    acc[c][e] += d[e];
+                        });
                     }
                 }
-            };
-            // A key that only some rows see still meets the others' products,
-            // as 0 * v: harmless unless v is infinite or NaN.
-            bool poison = false;
-            if (edge && a.causal && n_new > 1) {
-                const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
-                for (int r = r0; r < r1; ++r)
-                    for (int w = lane; w < ROWB / 4; w += 32) {
-                        const uint32_t x = *v_word(r, w);
-                        poison |= FP8 ? ((x & 0x7fu) == 0x7fu || (x & 0x7f00u) == 0x7f00u ||
-                                         (x & 0x7f0000u) == 0x7f0000u || (x & 0x7f000000u) == 0x7f000000u)
-                                      : ((x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u);
-                    }
-                poison = __any_sync(0xffffffffu, poison);
             }
-            if (!poison) {
-                each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
-            } else {
-                // token by token: the values that token s does not see are
-                // taken as zero, and only its rows take the product
-                for (int s = n_new - 1; s >= 0; --s) {
-                    const int seen = at.keys - n_new + s + 1;
-                    auto keep = [&](int key, uint32_t w) {
-                        return (key < seen ? w & 0xffffu : 0u) | (key + 1 < seen ? w & 0xffff0000u : 0u);
-                    };
-                    const int r = row0 + rg * 16 + g;
-                    const bool own0 = r % a.Sq == s, own1 = RG == 0 ? own0 : (r + 8) % a.Sq == s;
-                    each_v([&](int c, int n, uint32_t b0, uint32_t b1) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        add_pv(d, n, keep(kb + n * 8 + 2 * t, b0), keep(kb + n * 8 + 8 + 2 * t, b1));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (e < 2 ? own0 : own1)
-                                acc[c][e] += d[e];
-                    });
-                }
-            }
+            if (--left == 0)
+                break;
+            release();
+            ++at.j;
         }
 
         // ---- the job's or the share's end: join the key groups' warps
         const bool last_tile = at.j == at.tiles - 1;
         const int next = next_pos<TILE>(at);
         const bool on = next < end;
-        if (last_tile || !on) {
-            const bool whole = first_j == 0 && last_tile;
-            // through the stage, once no warp reads the tile any more
-            char *const rows = smem + stage * C::kStage;
-            named_barrier_sync(1, kWarps * 32);
-            float *mine = reinterpret_cast<float *>(rows) + warp * C::kWarpRows * D;
+        const bool whole = first_j == 0 && last_tile;
+        // through the stage, once no warp reads the tile any more
+        char *const rows = smem + stage * C::kStage;
+        named_barrier_sync(1, kWarps * 32);
+        float *mine = reinterpret_cast<float *>(rows) + warp * C::kWarpRows * D;
 #pragma unroll
-            for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                float l = l_run[hf];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int row = g + hf * 8;
-                if (t == 0) {
-                    red_m[warp * C::kWarpRows + row] = m_run[hf];
-                    red_l[warp * C::kWarpRows + row] = l;
+        for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+            float l = l_run[hf];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int row = g + hf * 8;
+            if (t == 0) {
+                red_m[warp * C::kWarpRows + row] = m_run[hf];
+                red_l[warp * C::kWarpRows + row] = l;
+            }
+#pragma unroll
+            for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = acc[n][hf * 2 + e] + (RG == 0 ? acc[n][2 + e] : 0.f);
+                    if (FP8)
+                        x[2 + e] = acc[n + 1][hf * 2 + e] + (RG == 0 ? acc[n + 1][2 + e] : 0.f);
                 }
-#pragma unroll
-                for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = acc[n][hf * 2 + e] + (RG == 0 ? acc[n][2 + e] : 0.f);
-                        if (FP8)
-                            x[2 + e] = acc[n + 1][hf * 2 + e] + (RG == 0 ? acc[n + 1][2 + e] : 0.f);
-                    }
-                    if (FP8) {
-                        const int col = n * 8 + t * 4;
-                        *reinterpret_cast<float4 *>(mine + row * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7)) =
-                            make_float4(x[0], x[2], x[1], x[3]);
-                    } else {
-                        *reinterpret_cast<float2 *>(mine + row * D + ((n ^ (row & 7)) << 3) + t * 2) = make_float2(x[0], x[1]);
-                    }
+                if (FP8) {
+                    const int col = n * 8 + t * 4;
+                    *reinterpret_cast<float4 *>(mine + row * D + (((col >> 3) ^ (row & 7)) << 3) + (col & 7)) =
+                        make_float4(x[0], x[2], x[1], x[3]);
+                } else {
+                    *reinterpret_cast<float2 *>(mine + row * D + ((n ^ (row & 7)) << 3) + t * 2) = make_float2(x[0], x[1]);
                 }
             }
-            fence_proxy_async_smem();  // before a tensor copy lands there
-            named_barrier_sync(1, kWarps * 32);
-            const int r = row0 + my_line;
-            if (r < a.R) {
-                const int row = my_line % C::kWarpRows, w0 = my_line / C::kWarpRows * C::kKg;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < C::kKg; ++w)
-                    top = fmaxf(top, red_m[(w0 + w) * C::kWarpRows + row]);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float sum = 0.f, o[CP];
-#pragma unroll
-                for (int e = 0; e < CP; ++e)
-                    o[e] = 0.f;
-#pragma unroll
-                for (int w = 0; w < C::kKg; ++w) {
-                    const float f = ex2_approx(red_m[(w0 + w) * C::kWarpRows + row] - ref);
-                    sum += f * red_l[(w0 + w) * C::kWarpRows + row];
-                    const float *src = reinterpret_cast<const float *>(rows) + ((w0 + w) * C::kWarpRows + row) * D;
-#pragma unroll
-                    for (int e = 0; e < CP; e += 2) {
-                        const int col = col0 + e * TPR;
-                        const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
-                        o[e] += f * x.x;
-                        o[e + 1] += f * x.y;
-                    }
-                }
-                if (!whole) {
-                    const long long at_ws = (long long)(2 * blockIdx.x + (first_j == 0 ? 1 : 0)) * C::kRows + my_line;
-#pragma unroll
-                    for (int e = 0; e < CP; e += 2)
-                        *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e * TPR) = make_float2(o[e], o[e + 1]);
-                    if (col0 == 0)
-                        a.ws_ml[at_ws] = make_float2(top, sum);
-                } else if (a.Sq == 1 || r % a.Sq < n_new) {
-                    const float f = sum == 0.f ? 0.f : (FP8 ? a.cache.v_scale[h_kv] : 1.f) / sum;
-                    const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
-#pragma unroll
-                    for (int e = 0; e < CP; e += 2) {
-                        if (a.out_bf16)
-                            *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e * TPR) =
-                                pack_bf16(o[e] * f, o[e + 1] * f);
-                        else
-                            *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e * TPR) =
-                                make_float2(o[e] * f, o[e + 1] * f);
-                    }
-                    if (col0 == 0)
-                        a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-                }
-            }
-            if (first_j == 0 && !last_tile && tid == 0)  // the first part of a cut job: where is its last?
-                a.ws_rec[blockIdx.x] = make_int4(at.b * a.Hkv * a.n_rt + at.hr, n_new, 0,
-                                                 shares.owner(at.pos + (at.tiles - 1 - at.j) * kUnits));
-            fresh = true;
         }
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(empty + stage);
+        fence_proxy_async_smem();  // before a tensor copy lands there
+        named_barrier_sync(1, kWarps * 32);
+        const int r = row0 + my_line;
+        if (r < a.R) {
+            const int row = my_line % C::kWarpRows, w0 = my_line / C::kWarpRows * C::kKg;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < C::kKg; ++w)
+                top = fmaxf(top, red_m[(w0 + w) * C::kWarpRows + row]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f, o[CP];
+#pragma unroll
+            for (int e = 0; e < CP; ++e)
+                o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < C::kKg; ++w) {
+                const float f = ex2_approx(red_m[(w0 + w) * C::kWarpRows + row] - ref);
+                sum += f * red_l[(w0 + w) * C::kWarpRows + row];
+                const float *src = reinterpret_cast<const float *>(rows) + ((w0 + w) * C::kWarpRows + row) * D;
+#pragma unroll
+                for (int e = 0; e < CP; e += 2) {
+                    const int col = col0 + e * TPR;
+                    const float2 x = *reinterpret_cast<const float2 *>(src + (((col >> 3) ^ (row & 7)) << 3) + (col & 7));
+                    o[e] += f * x.x;
+                    o[e + 1] += f * x.y;
+                }
+            }
+            if (!whole) {
+                const long long at_ws = (long long)(2 * blockIdx.x + (first_j == 0 ? 1 : 0)) * C::kRows + my_line;
+#pragma unroll
+                for (int e = 0; e < CP; e += 2)
+                    *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e * TPR) = make_float2(o[e], o[e + 1]);
+                if (col0 == 0)
+                    a.ws_ml[at_ws] = make_float2(top, sum);
+            } else if (a.Sq == 1 || r % a.Sq < n_new) {
+                const float f = sum == 0.f ? 0.f : (FP8 ? a.cache.v_scale[h_kv] : 1.f) / sum;
+                const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
+#pragma unroll
+                for (int e = 0; e < CP; e += 2) {
+                    if (a.out_bf16)
+                        *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.out + at_row * D + col0 + e * TPR) =
+                            pack_bf16(o[e] * f, o[e + 1] * f);
+                    else
+                        *reinterpret_cast<float2 *>((float *)a.out + at_row * D + col0 + e * TPR) =
+                            make_float2(o[e] * f, o[e + 1] * f);
+                }
+                if (col0 == 0)
+                    a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            }
+        }
+        if (first_j == 0 && !last_tile && tid == 0)  // the first part of a cut job: where is its last?
+            a.ws_rec[blockIdx.x] = make_int4(at.b * a.Hkv * a.n_rt + at.hr, n_new, 0,
+                                             shares.owner(at.pos + (at.tiles - 1 - at.j) * kUnits));
+        release();
         if (!on)
             break;
         advance<TILE>(a, at, next);
-        if (fresh)
-            load_q();
-        if (++stage == NS) {
-            stage = 0;
-            phase ^= 1;
-        }
+        load_q();
     }
 }
 
