@@ -33,7 +33,7 @@
 // 95 %, and with 28 rows, where the matrix instructions begin to bound it, 208
 // us.  8-bit, 8 sequences of 20K to 32K: 73 us, 87 %, bound by the conversions
 // (64 of a warp's 450 instructions a step of 32 keys for each product).  One
-// 4K sequence takes 9.1 us, of which the start (lengths, pages, the first tile)
+// 4K sequence takes 8.8 us, of which the start (lengths, pages, the first tile)
 // is 3.5 and the second kernel 2.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -61,7 +61,8 @@ constexpr int kThreads = (kWarps + kCopyWarps) * 32;
 constexpr uint32_t kRegsCopy = 72;
 constexpr uint32_t kRegsCompute = 216;
 constexpr int kMinLaunchRegs = (int)(kRegsCopy * 128 + kRegsCompute * kWarps * 32 + kThreads - 1) / kThreads;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8;                // of a block of the second kernel
+constexpr int kJoinAhead = 4;                // parts that each has on the way
 
 struct PagedArgs {
     CUtensorMap map_k, map_v;  // the cache in boxes of box_rows keys, where box_rows > 0
@@ -77,6 +78,7 @@ struct PagedArgs {
                     // block (-1: none)
     int B, Hq, Hkv, G, Sq, R, n_rt, causal, out_bf16;
     int records;    // blocks of the first kernel, for the join kernel
+    int join_warps; // warps for a row there
     int box_rows;   // keys of a tensor copy: the largest power of two that divides page_size, at most a
                     // tile; 0 below 16, where keys are copied one by one
     float scale_log2;
@@ -993,20 +995,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     }
 }
 
-// Joins the parts of the jobs that were cut between blocks: blockIdx.y is a row
-// of the tile, and each block takes the records of every gridDim.x-th block of
-// the first kernel, 32 in one look.  Each warp joins every eighth part of the
-// row, then the warps join through shared memory.
+// Joins the parts of the jobs that were cut between blocks.  Each block takes
+// the records of every gridDim.x-th block of the first kernel, 32 in one look,
+// and of each job kJoinWarps / join_warps rows, beginning at blockIdx.y times
+// that: join_warps warps join every join_warps-th part of a row, then through
+// shared memory.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) attn_paged_join_kernel(const __grid_constant__ PagedArgs a)
 {
-    constexpr int W = kJoinThreads / 32, PER = D / 32;
+    constexpr int W = kJoinWarps, PER = D / 32;
     __shared__ float part[W][D], tops[W], sums[W];
     asm volatile("" ::"l"(a.ws_rec), "l"(a.ws_ml), "l"(a.ws_o), "r"(a.records), "r"(a.n_rt), "r"(a.R), "r"(a.Sq), "l"(a.out),
-                 "l"(a.lse), "l"(a.cache.v_scale), "r"(a.out_bf16));
+                 "l"(a.lse), "l"(a.cache.v_scale), "r"(a.out_bf16), "r"(a.join_warps));
     chain_wait();
-    const int row = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pw = a.join_warps, rows = W / pw;
+    const int row0 = blockIdx.y * rows, row = row0 + warp / pw;
     for (int from = blockIdx.x; from < a.records; from += 32 * gridDim.x) {
         const int mine = from + lane * gridDim.x;
         int4 rec = make_int4(0, 0, 0, -1);
@@ -1018,21 +1022,23 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
             todo &= todo - 1;
             const int first = from + l * gridDim.x, last = __shfl_sync(0xffffffffu, rec.w, l);
             const int job = __shfl_sync(0xffffffffu, rec.x, l), n_new = __shfl_sync(0xffffffffu, rec.y, l);
-            const int bh = job / a.n_rt, r = (job - bh * a.n_rt) * ROWS + row;
-            if (r >= a.R || (a.Sq > 1 && r % a.Sq >= n_new))
-                continue;
-            const int n = last - first + 1;
+            const int bh = job / a.n_rt, job_row = (job - bh * a.n_rt) * ROWS;
+            // a row of the tile that is a row of the output
+            auto there = [&](int i) {
+                return i < ROWS && job_row + i < a.R && (a.Sq == 1 || (job_row + i) % a.Sq < n_new);
+            };
+            const int n = there(row) ? last - first + 1 : 0;
             float top = -INFINITY, sum = 0.f, o[PER];
 #pragma unroll
             for (int e = 0; e < PER; ++e)
                 o[e] = 0.f;
-            constexpr int U = 8;  // parts in flight
-            for (int i0 = warp; i0 < n; i0 += W * U) {
+            constexpr int U = kJoinAhead;
+            for (int i0 = warp % pw; i0 < n; i0 += pw * U) {
                 float2 ml[U];
                 float x[U][PER];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * W;
+                    const int i = i0 + u * pw;
                     ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
                     for (int e = 0; e < PER; ++e)
@@ -1079,29 +1085,30 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
                 sums[warp] = sum;
             }
             __syncthreads();
-            if (tid >= D)
-                continue;
-            top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                top = fmaxf(top, tops[w]);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float x = 0.f;
-            sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f = ex2_approx(tops[w] - ref);
-                sum += f * sums[w];
-                x += f * part[w][tid];
+            for (int at = tid; at < rows * D; at += W * 32) {
+                const int i = at / D, col = at % D, w0 = i * pw;
+                if (!there(row0 + i))
+                    continue;
+                top = -INFINITY;
+                for (int w = 0; w < pw; ++w)
+                    top = fmaxf(top, tops[w0 + w]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float x = 0.f;
+                sum = 0.f;
+                for (int w = 0; w < pw; ++w) {
+                    const float f = ex2_approx(tops[w0 + w] - ref);
+                    sum += f * sums[w0 + w];
+                    x += f * part[w0 + w][col];
+                }
+                const long long at_row = (long long)bh * a.R + job_row + row0 + i;
+                x *= sum == 0.f ? 0.f : (a.cache.v_scale ? a.cache.v_scale[bh % a.Hkv] : 1.f) / sum;
+                if (a.out_bf16)
+                    ((__nv_bfloat16 *)a.out)[at_row * D + col] = __float2bfloat16_rn(x);
+                else
+                    ((float *)a.out)[at_row * D + col] = x;
+                if (col == 0)
+                    a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
-            const long long at_row = (long long)bh * a.R + r;
-            x *= sum == 0.f ? 0.f : (a.cache.v_scale ? a.cache.v_scale[bh % a.Hkv] : 1.f) / sum;
-            if (a.out_bf16)
-                ((__nv_bfloat16 *)a.out)[at_row * D + tid] = __float2bfloat16_rn(x);
-            else
-                ((float *)a.out)[at_row * D + tid] = x;
-            if (tid == 0)
-                a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
     }
 }
@@ -1201,9 +1208,19 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         a.ws_rec = (int4 *)((char *)ws + o_bytes + ml_bytes);
     }
     cudaError_t e = launch_chained(kernel, dim3(grid), kThreads, C::kSmem, stream, a);
-    if (e == cudaSuccess && split)
-        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid, C::kRows < a.R ? C::kRows : a.R),
-                           kJoinThreads, 0, stream, a);
+    if (e == cudaSuccess && split) {
+        // As many warps for a row as take its parts in one look, where the
+        // jobs are alike; four at least, for jobs that are much longer than
+        // the others.  (8 sequences of 16 rows, 64 jobs: 33.4 us, with all
+        // eight warps 35.0, since twice the blocks take turns; with two 33.1,
+        // but 73.7 instead of 73.0 in the 8-bit case above.)
+        const long long parts = grid / jobs + 1;
+        for (a.join_warps = 4; a.join_warps < kJoinWarps && a.join_warps * kJoinAhead < parts;)
+            a.join_warps *= 2;
+        const int rows = kJoinWarps / a.join_warps, used = C::kRows < a.R ? C::kRows : a.R;
+        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid, (used + rows - 1) / rows), kJoinWarps * 32, 0,
+                           stream, a);
+    }
     rc = MERCURY_OK;
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "paged attention launch: %s", cudaGetErrorString(e));
