@@ -576,7 +576,8 @@ MERCURY_API int mercury_rope_init(int rot_dim, int interleaved, const double *fr
  * Requirements: B, H, S >= 1; H <= 65535; B * S < 2^31; rot_dim <= d <= 512;
  * pointers aligned to their element.  16-byte accesses are used where
  * pointers and strides are multiples of 16 bytes and rot_dim is a multiple of
- * 16 (bf16) or 8 (fp32); other shapes go element by element.
+ * 16 (bf16) or 8 (fp32), 8-byte ones where they are multiples of 8 bytes and
+ * rot_dim of 8 (bf16); other shapes go element by element.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA.
  */
 MERCURY_API int mercury_rope(const void *x, const long long *x_strides, const int *positions,

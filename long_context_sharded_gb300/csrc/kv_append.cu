@@ -203,11 +203,18 @@ int launch_kv_append(const void *k, const Strides &ks, const void *v, const Stri
         a.plan.interleaved = 0;
         a.plan.magnitude = 1.f;
     }
-    const bool wide = rot_vector_ok(k, ks, a.d, 2) && rot_vector_ok(v, vs, a.d, 2) && a.plan.rot_dim % 16 == 0 &&
-                      (!q || (rot_vector_ok(q, qs, a.d, 2) && rot_vector_ok(q_out, os, a.d, 2)));
+    auto fits = [&](int VE) {
+        return rot_vector_ok(k, ks, a.d, 2, VE) && rot_vector_ok(v, vs, a.d, 2, VE) && a.plan.rot_dim % (2 * VE) == 0 &&
+               (!q || (rot_vector_ok(q, qs, a.d, 2, VE) && rot_vector_ok(q_out, os, a.d, 2, VE)));
+    };
+    const int VE = fits(8) ? 8 : fits(4) ? 4 : 1;
     if (cache.elem == MERCURY_ELEM_E4M3)
-        return wide ? launch<true, 8>(a, sms, stream, msg, msg_len) : launch<true, 1>(a, sms, stream, msg, msg_len);
-    return wide ? launch<false, 8>(a, sms, stream, msg, msg_len) : launch<false, 1>(a, sms, stream, msg, msg_len);
+        return VE == 8   ? launch<true, 8>(a, sms, stream, msg, msg_len)
+               : VE == 4 ? launch<true, 4>(a, sms, stream, msg, msg_len)
+                         : launch<true, 1>(a, sms, stream, msg, msg_len);
+    return VE == 8   ? launch<false, 8>(a, sms, stream, msg, msg_len)
+           : VE == 4 ? launch<false, 4>(a, sms, stream, msg, msg_len)
+                     : launch<false, 1>(a, sms, stream, msg, msg_len);
 }
 
 int read_and_clear_append_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)

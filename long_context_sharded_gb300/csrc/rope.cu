@@ -128,12 +128,15 @@ int launch_rope(const void *x, const Strides &xs, const int *pos, long long pos_
     a.copy_rest = !(x == out && xs.b == os.b && xs.h == os.h && xs.s == os.s);
     a.plan = plan;
     const int es = elem == MERCURY_ELEM_FP32 ? 4 : 2;
-    const bool wide = rot_vector_ok(x, xs, d, es) && rot_vector_ok(out, os, d, es);
+    auto fits = [&](int VE) {
+        return rot_vector_ok(x, xs, d, es, VE) && rot_vector_ok(out, os, d, es, VE) && plan.rot_dim % (2 * VE) == 0;
+    };
     if (elem == MERCURY_ELEM_FP32)
-        return wide && plan.rot_dim % 8 == 0 ? launch<float, 4>(a, B, sms, stream, msg, msg_len)
-                                             : launch<float, 1>(a, B, sms, stream, msg, msg_len);
-    return wide && plan.rot_dim % 16 == 0 ? launch<__nv_bfloat16, 8>(a, B, sms, stream, msg, msg_len)
-                                          : launch<__nv_bfloat16, 1>(a, B, sms, stream, msg, msg_len);
+        return fits(4) ? launch<float, 4>(a, B, sms, stream, msg, msg_len)
+                       : launch<float, 1>(a, B, sms, stream, msg, msg_len);
+    return fits(8)   ? launch<__nv_bfloat16, 8>(a, B, sms, stream, msg, msg_len)
+           : fits(4) ? launch<__nv_bfloat16, 4>(a, B, sms, stream, msg, msg_len)
+                     : launch<__nv_bfloat16, 1>(a, B, sms, stream, msg, msg_len);
 }
 
 }  // namespace mercury

@@ -1,8 +1,9 @@
 // rotate.cuh -- the work split and the element arithmetic that the rotation
 // and the cache append share.
 //
-// A head of d elements is cut into column units of VE-element chunks (16
-// bytes; VE = 1 where sizes, strides or addresses allow no wide access).  The
+// A head of d elements is cut into column units of VE-element chunks (16 bytes;
+// 8 bytes for 16-bit elements whose rotated part is a multiple of 8 but not of
+// 16, or whose strides are of 8 bytes; else VE = 1).  The
 // first rot/(2 VE) units hold two chunks of the rotated part each, j and
 // j + rot/(2 VE): with half-split pairs these are the two sides of the same VE
 // pairs, with interleaved ones two times VE/2 whole pairs, so both layouts
@@ -34,6 +35,16 @@ struct Chunk<__nv_bfloat16, 8> {
 };
 
 template <>
+struct Chunk<__nv_bfloat16, 4> {
+    uint2 w = {0, 0};
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void widen(float (&y)[4]) const
+    {
+        y[0] = bf16_lo(w.x), y[1] = bf16_hi(w.x), y[2] = bf16_lo(w.y), y[3] = bf16_hi(w.y);
+    }
+};
+
+template <>
 struct Chunk<__nv_bfloat16, 1> {
     __nv_bfloat16 w = __nv_bfloat16();
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *p; }
@@ -61,6 +72,8 @@ __device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, const float (&y)[V
     if constexpr (VE == 8)
         *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
                                                    pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    else if constexpr (VE == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
     else
         *p = __float2bfloat16_rn(y[0]);
 }
@@ -112,6 +125,8 @@ struct Quotient {
         }
         if constexpr (VE == 8)
             *reinterpret_cast<uint2 *>(p) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        else if constexpr (VE == 4)
+            *reinterpret_cast<uint32_t *>(p) = w[0] | w[1] << 16;
         else
             *p = (uint8_t)w[0];
     }
@@ -287,11 +302,11 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
     return g;
 }
 
-// Whether every chunk of a tensor with these strides starts on 16 bytes.
-inline bool rot_vector_ok(const void *p, const Strides &s, int d, int elem_size)
+// Whether every chunk of VE elements of a tensor with these strides starts on
+// a multiple of its bytes.
+inline bool rot_vector_ok(const void *p, const Strides &s, int d, int elem_size, int VE)
 {
-    const int n = 16 / elem_size;
-    return (uintptr_t)p % 16 == 0 && d % n == 0 && s.b % n == 0 && s.h % n == 0 && s.s % n == 0;
+    return (uintptr_t)p % (VE * elem_size) == 0 && d % VE == 0 && s.b % VE == 0 && s.h % VE == 0 && s.s % VE == 0;
 }
 
 }  // namespace mercury

@@ -502,6 +502,46 @@ def test_append_saturates_and_keeps_nan(gm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot,d", [(8, 64), (24, 64), (24, 128), (40, 64), (64, 128), (2, 64)])
+def test_access_widths_agree(gm, interleaved, rot, d):
+    """Tensors on 16, 8 and 2 bytes (and rotated parts of a multiple of 16, 8 and 2) take different accesses: the same
+    bits, and the formula's."""
+    B, Hq, Hkv, S = 2, 6, 3, 21
+    gen = torch.Generator("cuda").manual_seed(rot + d)
+    heads = Hq + 2 * Hkv
+    src = torch.randn(B, S, heads, d, generator=gen, device="cuda").to(BF16)
+    plan = gm.mercury_rope_init(rot, interleaved=interleaved)
+    past = torch.tensor([5, 900], dtype=torch.int32, device="cuda")
+    table = torch.randperm(2 * 60, generator=gen, device="cuda").to(torch.int32).reshape(2, 60)
+    scale = torch.rand(Hkv, generator=gen, device="cuda") * 0.02 + 0.001
+    got = []
+    for off in (0, 4, 1):
+        flat = torch.empty(src.numel() + 8, dtype=BF16, device="cuda")[off:off + src.numel()]
+        x = flat.copy_(src.reshape(-1)).view(src.shape).transpose(1, 2)
+        q, k, v = x.split([Hq, Hkv, Hkv], 1)
+        res = [gm.mercury_rope(x, plan, start=40), gm.mercury_rope(x, plan, start=40, inverse=True)]
+        for dtype, sc in ((BF16, None), (E4M3, scale)):
+            kc, vc = (torch.zeros(120, Hkv, 16, d, device="cuda").to(dtype) for _ in range(2))
+            qo = torch.empty(flat.numel() + 8, dtype=BF16, device="cuda")[off:off + B * S * Hq * d].view(B, S, Hq, d).transpose(1, 2)
+            gm.mercury_kv_append(gm.PagedCache(kc, vc, table, k_scale=sc, v_scale=sc), k, v, past, rope=plan, q=q, q_out=qo)
+            res += [bits(kc), bits(vc), qo]
+        got.append(res)
+    gm.mercury_sync_status()
+    for res in got[1:]:
+        for a, b in zip(got[0], res):
+            assert torch.equal(a, b)
+    x = src.transpose(1, 2)
+    pos = (40 + torch.arange(S, device="cuda")).expand(B, S)
+    ref = rotate(x, pos, frequencies(rot), interleaved)
+    bound = rotation_bound(x, rot // 2, interleaved)
+    assert_within(got[0][0], ref, bound + half_step(ref.abs() + bound, BF16), "rope")
+    ref = rotate(x[:, :Hq], past[:, None].long() + torch.arange(S, device="cuda"), frequencies(rot), interleaved)
+    bound = rotation_bound(x[:, :Hq], rot // 2, interleaved)
+    assert_within(got[0][4], ref, bound + half_step(ref.abs() + bound, BF16), "q")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("scale", [1.0, 0.5, 3.0, 1 / 3, 0.7, -5.0, 1.1e-3, 2.0 ** -120, 1e-40, 2.0 ** 120, 0.0, math.inf, math.nan])
 def test_append_stores_the_quotient(gm, scale, aligned):
