@@ -28,13 +28,14 @@
 //     8 rows two of them share an instruction, whose lower half would idle.
 //
 // Measured on a GB300, of the measured copy bandwidth (6770 GB/s): 16 sequences
-// of 700 to 32K tokens, 64 query and 8 KV heads of 128: 165 us, 98 %; one
-// sequence of 128K: 83 us, 96 %; 8 x 32K tokens, 16 rows a KV head: 163 us,
-// 95 %, and with 28 rows, where the matrix instructions begin to bound it, 208
-// us.  8-bit, 8 sequences of 20K to 32K: 73 us, 87 %, bound by the conversions
-// (64 of a warp's 450 instructions a step of 32 keys for each product).  One
-// 4K sequence takes 8.8 us, of which the start (lengths, pages, the first tile)
-// is 3.5 and the second kernel 2.
+// of 700 to 32K tokens, 64 query and 8 KV heads of 128: 162 us, 100 %; one
+// sequence of 128K: 82 us, 97 %; 8 sequences of 20K to 32K with 16 rows a KV
+// head: 135 us, 95 %; with 28 rows, where the matrix instructions begin to
+// bound it, 161 us, 79 %.  8-bit keys and values, 4 rows: 72 us, 88 %, with 16
+// rows 78 us, bound by the conversions (64 of a warp's 450 instructions a step
+// of 32 keys for each product) and the latency of two warps a quarter of an
+// SM.  One 4K sequence takes 8.3 us, of which the start (lengths, pages, the
+// first tile) is 3.5 and the second kernel 2.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -103,7 +104,10 @@ struct Cfg {
     static constexpr int kRows = RG == 0 ? 8 : 16 * RG;
     static constexpr int kWarpRows = RG == 0 ? 8 : 16;
     static constexpr int kRed = kWarps * kWarpRows * 8;        // each warp's maxima and sums
-    static constexpr int kSmem = kStages * kStage + kRed + kStages * 16;
+    static constexpr int kRowBytes = kWarps * kWarpRows * D * 4;  // the warps' partial rows
+    static constexpr int kRowsAt = kStages * kStage + kRed + kStages * 16;
+    static constexpr bool kOwnRows = kRowsAt + kRowBytes <= 232448;
+    static constexpr int kSmem = kRowsAt + (kOwnRows ? kRowBytes : 0);
     static_assert(kTile % (32 * kCopyWarps) == 0, "whole runs for each copying warp");
     static_assert(kWarps * kWarpRows * D * 4 <= kStage, "the warps' partial rows fit into a stage");
 };
@@ -855,41 +859,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     }
                 };
                 // A key that only some rows see still meets the others' products,
-                // as 0 * v: harmless unless v is infinite or NaN.
-                bool poison = false;
+                // as 0 * v: harmless unless v is infinite or NaN.  Such an
+                // element is taken as zero, and made NaN in its column of O in
+                // the rows that see it (their sum of p's terms times an
+                // infinity is one anyway).  In here, not in a second version of
+                // the products, whose registers slowed the first (128K keys:
+                // 83.3 us instead of 81.5; 8-bit, 64 rows: 263 instead of 245).
                 if (edge && a.causal && n_new > 1) {
                     const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
-                    for (int r = r0; r < r1; ++r)
-                        for (int w = lane; w < ROWB / 4; w += 32) {
-                            const uint32_t x = *v_word(r, w);
-                            poison |= FP8 ? ((x & 0x7fu) == 0x7fu || (x & 0x7f00u) == 0x7f00u ||
-                                             (x & 0x7f0000u) == 0x7f0000u || (x & 0x7f000000u) == 0x7f000000u)
-                                          : ((x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u);
-                        }
-                    poison = __any_sync(0xffffffffu, poison);
-                }
-                if (!poison) {
-                    each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
-                } else {
-                    // token by token: the values that token s does not see are
-                    // taken as zero, and only its rows take the product
-                    for (int s = n_new - 1; s >= 0; --s) {
-                        const int seen = at.keys - n_new + s + 1;
-                        auto keep = [&](int key, uint32_t w) {
-                            return (key < seen ? w & 0xffffu : 0u) | (key + 1 < seen ? w & 0xffff0000u : 0u);
-                        };
-                        const int r = row0 + rg * 16 + g;
-                        const bool own0 = r % a.Sq == s, own1 = RG == 0 ? own0 : (r + 8) % a.Sq == s;
-                        each_v([&](int c, int n, uint32_t b0, uint32_t b1) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            add_pv(d, n, keep(kb + n * 8 + 2 * t, b0), keep(kb + n * 8 + 8 + 2 * t, b1));
+                    constexpr int WORDS = ROWB / 4, EACH = FP8 ? 4 : 2, BITS = 32 / EACH;
+                    constexpr uint32_t NOT_FINITE = FP8 ? 0x7fu : 0x7f80u, ELEM = FP8 ? 0xffu : 0xffffu;
+                    auto word = [&](int r, int w) {
+                        return reinterpret_cast<uint32_t *>(smem + stage * C::kStage + C::kPart +
+                                                            chunk_at<ROWB, TILE>(step * KEYS + r, w >> 2)) + (w & 3);
+                    };
+                    // the first such key of this lane's columns, a byte each
+                    uint32_t bad = 0xffffffffu;
+                    for (int r = r1 - 1; r >= r0; --r)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (e < 2 ? own0 : own1)
-                                    acc[c][e] += d[e];
-                        });
+                        for (int w = lane; w < WORDS; w += 32)
+#pragma unroll
+                            for (int i = 0; i < EACH; ++i)
+                                if ((*word(r, w) >> (i * BITS) & NOT_FINITE) == NOT_FINITE) {
+                                    const int at_bit = (w / 32 * EACH + i) * 8;
+                                    bad = (bad & ~(0xffu << at_bit)) | (uint32_t)r << at_bit;
+                                }
+                    if (__any_sync(0xffffffffu, bad != 0xffffffffu)) {
+                        if (C::kRg > 1)  // the other row groups' warps have looked too
+                            named_barrier_sync(2 + kg, C::kRg * 32);
+                        for (int r = r0; r < r1; ++r)
+                            for (int w = lane; w < WORDS; w += 32)
+#pragma unroll
+                                for (int i = 0; i < EACH; ++i)
+                                    if ((*word(r, w) >> (i * BITS) & NOT_FINITE) == NOT_FINITE)
+                                        *word(r, w) &= ~(ELEM << (i * BITS));
+                        fence_proxy_async_smem();  // before a tensor copy lands there
+                        __syncwarp();
+#pragma unroll
+                        for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
+                            const int w = FP8 ? n * 2 + t : n * 4 + t;
+                            const uint32_t x = __shfl_sync(0xffffffffu, bad, w & 31) >> (FP8 ? 0 : w / 32 * 16);
+#pragma unroll
+                            for (int i = 0; i < EACH; ++i)
+#pragma unroll
+                                for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
+                                    float &o = acc[FP8 ? n + i % 2 : n][hf * 2 + (FP8 ? i / 2 : i)];
+                                    const int r = (int)(x >> (i * 8) & 0xffu);
+                                    if (r != 0xff && kb + r < lim[hf])
+                                        o = __int_as_float(0x7fffffff);
+                                }
+                        }
                     }
                 }
+                each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
             }
             if (--left == 0)
                 break;
@@ -902,8 +924,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         const int next = next_pos<TILE>(at);
         const bool on = next < end;
         const bool whole = first_j == 0 && last_tile;
-        // through the stage, once no warp reads the tile any more
-        char *const rows = smem + stage * C::kStage;
+        // the next job's queries are asked for now, and arrive meanwhile
+        const Place done = at;
+        const int done_h = h_kv, done_row0 = row0, done_new = n_new;
+        if (on) {
+            advance<TILE>(a, at, next);
+            load_q();
+        }
+        // through memory of their own where it fits, else through the stage,
+        // once no warp reads the tile any more
+        char *const rows = C::kOwnRows ? smem + C::kRowsAt : smem + stage * C::kStage;
+        fence_proxy_async_smem();  // zeros in the stage, before a tensor copy lands there
+        if (C::kOwnRows)
+            release();
         named_barrier_sync(1, kWarps * 32);
         float *mine = reinterpret_cast<float *>(rows) + warp * C::kWarpRows * D;
 #pragma unroll
@@ -934,9 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 }
             }
         }
-        fence_proxy_async_smem();  // before a tensor copy lands there
+        if (!C::kOwnRows)
+            fence_proxy_async_smem();
         named_barrier_sync(1, kWarps * 32);
-        const int r = row0 + my_line;
+        const int r = done_row0 + my_line;
         if (r < a.R) {
             const int row = my_line % C::kWarpRows, w0 = my_line / C::kWarpRows * C::kKg;
             float top = -INFINITY;
@@ -968,9 +1002,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col0 + e * TPR) = make_float2(o[e], o[e + 1]);
                 if (col0 == 0)
                     a.ws_ml[at_ws] = make_float2(top, sum);
-            } else if (a.Sq == 1 || r % a.Sq < n_new) {
-                const float f = sum == 0.f ? 0.f : (FP8 ? a.cache.v_scale[h_kv] : 1.f) / sum;
-                const long long at_row = ((long long)at.b * a.Hkv + h_kv) * a.R + r;
+            } else if (a.Sq == 1 || r % a.Sq < done_new) {
+                const float f = sum == 0.f ? 0.f : (FP8 ? a.cache.v_scale[done_h] : 1.f) / sum;
+                const long long at_row = ((long long)done.b * a.Hkv + done_h) * a.R + r;
 #pragma unroll
                 for (int e = 0; e < CP; e += 2) {
                     if (a.out_bf16)
@@ -985,13 +1019,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             }
         }
         if (first_j == 0 && !last_tile && tid == 0)  // the first part of a cut job: where is its last?
-            a.ws_rec[blockIdx.x] = make_int4(at.b * a.Hkv * a.n_rt + at.hr, n_new, 0,
-                                             shares.owner(at.pos + (at.tiles - 1 - at.j) * kUnits));
-        release();
+            a.ws_rec[blockIdx.x] = make_int4(done.b * a.Hkv * a.n_rt + done.hr, done_new, 0,
+                                             shares.owner(done.pos + (done.tiles - 1 - done.j) * kUnits));
+        if (!C::kOwnRows)
+            release();
         if (!on)
             break;
-        advance<TILE>(a, at, next);
-        load_q();
     }
 }
 

@@ -699,6 +699,41 @@ def test_hidden_rows_do_not_matter(gm, dtype, value):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(2, 2, 5), (8, 2, 4), (8, 1, 4), (16, 2, 7), (16, 1, 64)])
+def test_values_that_some_rows_see(gm, dtype, d, Hq, Hkv, Sq):
+    """Single NaN (and infinite) elements among the new tokens' values: not finite in their column of the rows that
+    see them, and nowhere else.  The new tokens lie across the ends of pages, of a warp's keys and of tiles."""
+    lens, page = [Sq, 133, 257, 515, 1026], 16
+    gen = torch.Generator("cpu").manual_seed(d + Hq)
+    spots = []  # (sequence, key, head, column)
+
+    def spoil(k, v, table):
+        b8 = v.view(torch.uint8) if dtype is E4M3 else v
+        for b, n in enumerate(lens):
+            for i in range(0 if Sq < 64 else 3, Sq, 1 if Sq < 64 else 9):
+                at, h, col = n - Sq + i, i % Hkv, int(torch.randint(0, d, (1,), generator=gen))
+                spots.append((b, at, h, col))
+                b8[table[b, at // page].long(), h, at % page, col] = 0x7f if dtype is E4M3 else (math.nan, math.inf)[i % 2]
+
+    r = run_attention(gm, len(lens), Hq, Hkv, Sq, d, page, lens, dtype, spoil=spoil, seed=13)
+    gm.mercury_sync_status()
+    G = Hq // Hkv
+    hit = torch.zeros_like(r["out"], dtype=torch.bool)
+    for b, at, h, col in spots:
+        hit[b, h * G:(h + 1) * G, max(at - (lens[b] - Sq), 0):, col] = True
+    assert torch.equal(~torch.isfinite(r["out"]), hit)
+    for b, n in enumerate(lens):
+        k, v = gather_states(r["k"], r["ks"], r["table"][b], n), gather_states(r["v"], r["vs"], r["table"][b], n)
+        v = torch.where(torch.isfinite(v), v, 0.0)
+        o, l, eo, el = attention(r["q"][b], k, v, [n - Sq + i + 1 for i in range(Sq)])
+        fine = ~hit[b]
+        assert_within(r["out"][b][fine], o[fine], eo[fine], "O")
+        assert_within(r["lse"][b], l, el, "LSE")
+
+
+@pytest.mark.gpu
 def test_extreme_scores(gm):
     """Scores far apart: one key takes everything, earlier and later than its rivals; tiny and huge queries."""
     for at, scale in ((0, 40.0), (999, 40.0), (500, 1e-30), (3, 0.0)):
