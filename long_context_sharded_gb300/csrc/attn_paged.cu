@@ -29,9 +29,9 @@
 //
 // Measured on a GB300, of the measured copy bandwidth (6770 GB/s): 16 sequences
 // of 700 to 32K tokens, 64 query and 8 KV heads of 128: 162 us, 100 %; one
-// sequence of 128K: 82 us, 97 %; 8 sequences of 20K to 32K with 16 rows a KV
+// sequence of 128K: 81.5 us, 97 %; 8 sequences of 20K to 32K with 16 rows a KV
 // head: 135 us, 95 %; with 28 rows, where the matrix instructions begin to
-// bound it, 161 us, 79 %.  8-bit keys and values, 4 rows: 72 us, 88 %, with 16
+// bound it, 161 us, 79 %.  8-bit keys and values, 4 rows: 72 us, 89 %, with 16
 // rows 78 us, bound by the conversions (64 of a warp's 450 instructions a step
 // of 32 keys for each product) and the latency of two warps a quarter of an
 // SM.  One 4K sequence takes 8.3 us, of which the start (lengths, pages, the
