@@ -659,9 +659,9 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * device, so neither the lengths nor their spread need to be known on the
  * host.  Parts of sequences cut between SMs go to scratch memory (2 * SMs *
  * rows * (d + 2) * 4 bytes, rows 8 to 64) that comes stream-ordered from the
- * library's pool; a captured graph owns its own.  Pages of a multiple of 16
- * tokens are copied whole by the copy engine; other sizes go token by token
- * (about a tenth slower at 32K tokens).
+ * library's pool; a captured graph owns its own.  Pages of a multiple of 8
+ * tokens are copied by the copy engine; other sizes go token by token (about a
+ * tenth slower at 32K tokens).
  * Device waits are bounded as in every call (MERCURY_WAIT_NS): one that runs
  * out is reported as MERCURY_ETIMEOUT.
  * A page outside the cache counts as keys and values of zero, and it, a

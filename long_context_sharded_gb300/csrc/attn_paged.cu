@@ -81,7 +81,9 @@ struct PagedArgs {
     int records;    // blocks of the first kernel, for the join kernel
     int join_warps; // warps for a row there
     int box_rows;   // keys of a tensor copy: the largest power of two that divides page_size, at most a
-                    // tile; 0 below 16, where keys are copied one by one
+                    // tile; 0 below 8 (the rows of a swizzle), where keys are copied one by one, which
+                    // takes longer (pages of 8, one by one: 16 of 700 to 32K 174 us instead of 170, 8-bit
+                    // 84 instead of 78, 64 short ones 55.7 instead of 50.5)
     float scale_log2;
     int fault;      // test hook: withhold one copy
     unsigned long long wait_ns;
@@ -247,7 +249,8 @@ __device__ __forceinline__ int new_of(const PagedArgs &a, int b)
 // time that its keys take: a full tile is eight, a job's last one as many as
 // it has eighths, and a job takes kJobCost more before its first tile, what
 // changing jobs costs a block (64 sequences of 1 to 2047 tokens, 16 heads of
-// 64: 58 us with 2 units, 52.5 with 4, 47.7 with 12, 48.9 with 24).  A tile
+// 64: 53.5 us with 4 units, 50.8 with 7, 49.4 with 10 and 14; of 1 to 600
+// tokens 36.7, 30.3, 27.9 and 26.1).  A tile
 // belongs to the share that holds its first unit.
 constexpr int kUnits = 8;
 constexpr int kJobCost = 14;
@@ -1199,8 +1202,8 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         return MERCURY_EINVAL;
     }
     a.box_rows = 0;
-    if (a.cache.page_size % 16 == 0) {
-        for (a.box_rows = 16; a.box_rows < C::kTile && a.cache.page_size % (2 * a.box_rows) == 0;)
+    if (a.cache.page_size % 8 == 0) {
+        for (a.box_rows = 8; a.box_rows < C::kTile && a.cache.page_size % (2 * a.box_rows) == 0;)
             a.box_rows *= 2;
         int rc = encode_cache(&a.map_k, a.cache, a.cache.k, D, FP8, a.box_rows, msg, msg_len);
         if (rc == MERCURY_OK)
