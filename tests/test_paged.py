@@ -10,6 +10,7 @@ accumulator (2^-21 of the sum of their magnitudes, over sqrt(d), allows for
 its truncation), P is kept to 2^-17 or better and an accumulator that takes the keys in
 steps of 16 to 128 loses 2^-23 a step; each is relative to sum p |v|.
 """
+import concurrent.futures
 import ctypes
 import math
 import sys
@@ -839,6 +840,45 @@ def test_streams_and_graphs(gm):
         assert torch.equal(o, out) and torch.equal(l, lse)
     r.update(out=out, lse=lse)
     check_attention(r, [77, 5000, 4, 0], None, True, 16)
+
+
+@pytest.mark.gpu
+def test_two_threads_at_once(gm):
+    """Two host threads with a stream and a cache each, calling at the same time (a call leaves the interpreter while it
+    launches): the results of one after the other."""
+    plan = gm.mercury_rope_init(128)
+
+    def inputs(seed):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        B, Hq, Hkv, page = 3, 8, 2, 16
+        k_cache, v_cache, table, _ = make_cache(B, Hkv, 128, page, 40, BF16, gen)
+        rand = lambda h: torch.randn(B, h, 1, 128, generator=gen, device="cuda").to(BF16)
+        past = torch.randint(1, 600, (B,), generator=gen, device="cuda").to(torch.int32)
+        return gm.PagedCache(k_cache, v_cache, table), rand(Hq), rand(Hkv), rand(Hkv), past
+
+    def steps(data, stream, n=40):
+        cache, q, k, v, past = data
+        with torch.cuda.stream(stream):
+            past, res = past.clone(), []
+            for _ in range(n):
+                qo, out, lse = torch.empty_like(q), torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:3], device="cuda")
+                gm.mercury_kv_append(cache, k, v, past, rope=plan, q=q, q_out=qo)
+                past += 1
+                gm.mercury_attn_paged(qo, cache, past, out=out, lse=lse)
+                res.append((gm.mercury_rope(qo, plan, inverse=True, out=qo), out, lse))
+            return res
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want = [steps(inputs(s), streams[0]) for s in (1, 2)]
+    data = [inputs(s) for s in (1, 2)]
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        got = list(pool.map(steps, data, streams))
+    torch.cuda.synchronize()
+    gm.mercury_sync_status()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert all(torch.equal(i, j) for i, j in zip(x, y))
 
 
 @pytest.mark.gpu
