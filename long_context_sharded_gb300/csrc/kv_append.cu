@@ -55,8 +55,8 @@ struct AppendArgs {
     mercury_rope_plan plan;
 };
 
-template <bool FP8, int VE>
-__global__ void __launch_bounds__(kRotThreads, 2) append_kernel(const __grid_constant__ AppendArgs a)
+template <bool FP8, int VE, bool FEW>
+__global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) append_kernel(const __grid_constant__ AppendArgs a)
 {
     using T = __nv_bfloat16;
     __shared__ unsigned long long turns[MERCURY_MAX_ROT / 2];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) append_kernel(const __grid_con
                   v1 = h1 - Hq - Hkv;
         if (h0 < q1) {
             T *const dst = a.q_out + b * a.os.b + i * a.os.s;
-            walk_heads<T, VE, true, false>(a.q + b * a.qs.b + i * a.qs.s + h0 * a.qs.h, a.qs.h, nullptr, q1 - h0, unit, ready,
+            walk_heads<T, VE, true, false, FEW>(a.q + b * a.qs.b + i * a.qs.s + h0 * a.qs.h, a.qs.h, nullptr, q1 - h0, unit, ready,
                                     [&](int h, const float (&y0)[VE], const float (&y1)[VE], float) {
                                         if (!unit.rotated && !a.copy_rest)
                                             return;
@@ -137,13 +137,13 @@ __global__ void __launch_bounds__(kRotThreads, 2) append_kernel(const __grid_con
                                     });
         }
         if (k0 < k1)
-            walk_heads<T, VE, true, FP8>(a.k + b * a.ks.b + i * a.ks.s + k0 * a.ks.h, a.ks.h,
+            walk_heads<T, VE, true, FP8, FEW>(a.k + b * a.ks.b + i * a.ks.s + k0 * a.ks.h, a.ks.h,
                                     FP8 ? c.k_scale + k0 : nullptr, k1 - k0, unit, ready,
                                     [&](int h, const float (&y0)[VE], const float (&y1)[VE], float scale) {
                                         keep(c.k, scale, k0 + h, y0, y1);
                                     });
         if (v0 < v1)
-            walk_heads<T, VE, false, FP8>(a.v + b * a.vs.b + i * a.vs.s + v0 * a.vs.h, a.vs.h,
+            walk_heads<T, VE, false, FP8, FEW>(a.v + b * a.vs.b + i * a.vs.s + v0 * a.vs.h, a.vs.h,
                                      FP8 ? c.v_scale + v0 : nullptr, v1 - v0, unit, ready,
                                      [&](int h, const float (&y0)[VE], const float (&y1)[VE], float scale) {
                                          keep(c.v, scale, v0 + h, y0, y1);
@@ -163,8 +163,12 @@ int launch(AppendArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_le
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
-    const cudaError_t e = launch_chained(append_kernel<FP8, VE>, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0,
-                                         stream, a);
+    void (*kernel)(AppendArgs) = append_kernel<FP8, VE, false>;
+    if constexpr (VE == 4)
+        if (rot_few(g, a.Hq + 2 * a.cache.Hkv, VE, 2, sms))
+            kernel = append_kernel<FP8, VE, true>;
+    const cudaError_t e =
+        launch_chained(kernel, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0, stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cache append kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -43,8 +43,8 @@ struct RopeArgs {
     mercury_rope_plan plan;
 };
 
-template <typename T, int VE>
-__global__ void __launch_bounds__(kRotThreads, 2) rope_kernel(const __grid_constant__ RopeArgs a)
+template <typename T, int VE, bool FEW>
+__global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     __shared__ unsigned long long turns[MERCURY_MAX_ROT / 2];
     stage_turns(a.plan, turns);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) rope_kernel(const __grid_const
         RotUnit<VE> unit(a.plan, u, a.d);
         if (!unit.rotated && !a.copy_rest)
             continue;
-        walk_heads<T, VE, true, false>(
+        walk_heads<T, VE, true, false, FEW>(
             src + h0 * a.xs.h, a.xs.h, nullptr, h1 - h0, unit,
             [&] {
                 const long long pos = a.pos ? a.pos[b * a.pos_stride + s] : a.start + s;
@@ -96,8 +96,12 @@ int launch(RopeArgs &a, int B, int sms, cudaStream_t stream, char *msg, size_t m
     a.units = g.units;
     a.tokens_per_block = g.tokens_per_block;
     a.heads_per_thread = g.heads_per_thread;
+    void (*kernel)(RopeArgs) = rope_kernel<T, VE, false>;
+    if constexpr (VE * sizeof(T) == 8)
+        if (rot_few(g, a.H, VE, sizeof(T), sms))
+            kernel = rope_kernel<T, VE, true>;
     const cudaError_t e =
-        launch_chained(rope_kernel<T, VE>, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0, stream, a);
+        launch_chained(kernel, dim3((unsigned)(g.blocks * g.head_groups)), kRotThreads, 0, stream, a);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "rope kernel launch: %s", cudaGetErrorString(e));
         return MERCURY_ECUDA;

@@ -222,13 +222,13 @@ struct RotUnit {
 // quantisation's registers four spill (6 x 1000 tokens of 24 heads of 64: 8.2
 // us instead of 10.7; 6 x 8000 of 48 of 128: 122 and 150).  Twice as many of
 // 8-byte chunks, for as many bytes on the way (32K prompt of 40 heads, 24
-// elements rotated: 118 us instead of 134).
-template <typename T, int VE, bool TURN, bool SCALED, typename Ready, typename Store>
+// elements rotated: 118 us instead of 134).  FEW: see rot_few.
+template <typename T, int VE, bool TURN, bool SCALED, bool FEW, typename Ready, typename Store>
 __device__ __forceinline__ void walk_heads(const T *src, long long stride, const float *scales, int n,
                                            RotUnit<VE> &unit, Ready ready, Store store)
 {
-    constexpr bool kAhead = sizeof(T) == 2;
-    constexpr int kBatch = (SCALED ? kRotBatch / 2 : kRotBatch) * (VE * sizeof(T) == 8 ? 2 : 1);
+    constexpr bool kAhead = sizeof(T) == 2 && !FEW;
+    constexpr int kBatch = (SCALED ? kRotBatch / 2 : kRotBatch) * (VE * sizeof(T) == 8 && !FEW ? 2 : 1);
     Chunk<T, VE> x0[2][kBatch], x1[2][kBatch];
     float sc[2][kBatch];
     auto load = [&](int slot, int h0) {
@@ -302,6 +302,17 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
     g.heads_per_thread = hp;
     g.head_groups = (H + hp - 1) / hp;
     return g;
+}
+
+// Whether a call takes the variant for a token's few heads, where a thread's
+// life is one batch: nothing loaded ahead, and the registers that frees spent
+// on a third block an SM.  (8-byte chunks, 24 elements rotated: 10 x 15475
+// tokens of 3 heads of 128 into a cache 61 us instead of 96, 32K of 2 heads
+// rotated 13.4 instead of 19.5; up to two blocks an SM there is no third, and
+// with 16-byte chunks it would spill: 3 heads 15.9 instead of 15.5.)
+inline bool rot_few(const RotShape &g, int H, int VE, int elem_size, int sms)
+{
+    return VE * elem_size == 8 && H <= kRotBatch && g.blocks * g.head_groups > 2LL * sms;
 }
 
 // Whether every chunk of VE elements of a tensor with these strides starts on

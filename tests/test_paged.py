@@ -543,6 +543,37 @@ def test_access_widths_agree(gm, interleaved, rot, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rot,interleaved", [(24, False), (24, True), (40, True)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (0, 2), (3, 1)])
+def test_few_heads_of_many_tokens(gm, Hq, Hkv, rot, interleaved):
+    """A long prompt of few heads: the same bits as in short calls."""
+    B, S, d = 2, 5003, 64
+    gen = torch.Generator("cuda").manual_seed(rot + Hq)
+    x = torch.randn(B, S, Hq + 2 * Hkv, d, generator=gen, device="cuda").to(BF16).transpose(1, 2)
+    q, k, v = x.split([Hq, Hkv, Hkv], 1)
+    plan = gm.mercury_rope_init(rot, interleaved=interleaved)
+    whole = gm.mercury_rope(x, plan, start=9)
+    for s in range(0, S, 500):
+        assert torch.equal(whole[:, :, s:s + 500], gm.mercury_rope(x[:, :, s:s + 500], plan, start=9 + s))
+    table = torch.randperm(2 * 320, generator=gen, device="cuda").to(torch.int32).reshape(2, 320)
+    past = torch.tensor([3, 77], dtype=torch.int32, device="cuda")
+    for dtype in (BF16, E4M3):
+        sc = torch.rand(Hkv, generator=gen, device="cuda") * 0.02 + 0.001 if dtype is E4M3 else None
+        got = []
+        for step in (S, 500):
+            kc, vc = (torch.zeros(640, Hkv, 16, d, device="cuda").to(dtype) for _ in range(2))
+            cache, qo = gm.PagedCache(kc, vc, table, k_scale=sc, v_scale=sc), torch.zeros_like(q) if Hq else None
+            for s in range(0, S, step):
+                part = slice(s, s + step)
+                kw = dict(q=q[:, :, part], q_out=qo[:, :, part]) if Hq else {}
+                gm.mercury_kv_append(cache, k[:, :, part], v[:, :, part], past + s, rope=plan, **kw)
+            got.append([bits(kc), bits(vc)] + ([qo] if Hq else []))
+        gm.mercury_sync_status()
+        for a, b in zip(*got):
+            assert torch.equal(a, b) and (a != 0).any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("scale", [1.0, 0.5, 3.0, 1 / 3, 0.7, -5.0, 1.1e-3, 2.0 ** -120, 1e-40, 2.0 ** 120, 0.0, math.inf, math.nan])
 def test_append_stores_the_quotient(gm, scale, aligned):
