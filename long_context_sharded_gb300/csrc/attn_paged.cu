@@ -201,6 +201,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// o += d, rounded to nearest, two elements an instruction (28 rows of 128 at 20K
+// to 32K keys: 184 us instead of 189 one by one).
+__device__ __forceinline__ void add_to(float (&o)[4], const float (&d)[4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+        asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+            "mov.b64 {%0, %1}, x;\n\t}"
+            : "+f"(o[e]), "+f"(o[e + 1])
+            : "f"(d[e]), "f"(d[e + 1]));
+}
+
 // p as a sum of 16-bit terms, each the nearest to what those before it leave:
 // two fp16 ones hold it to 2^-22, three bf16 ones to 2^-26.  (Two bf16 terms,
 // 2^-18, left O four times further from 64 bits than a 32-bit softmax does.)
@@ -598,8 +610,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     };
     load_q();
 
-    float acc[DN][4];
-    float m_run[2], l_run[2], s_mul[2];
+    // O's sums.  The matrix unit truncates: with O as its accumulator for a
+    // whole job, each product lost up to a unit in O's last place, always
+    // towards zero (32K keys, 64 rows: 6e-5 of O).  So its own sums, acc, are
+    // short, kWindow products from zero, and are added to O's by an ordinary
+    // addition.  Heads of 128 with more than 8 rows have no registers for both
+    // and take a step's products at a time (28 rows at 20K to 32K keys: 161 us
+    // as it was, 184 so, 201 with windows; 56 rows of 64: 315, 359 and 337).
+    constexpr int TERMS = FP8 ? 2 : 3;
+    constexpr int AW = RG == 0 ? 2 : 4;  // sums of this thread in each 8-column tile of O: one row's, or two
+    constexpr bool kByStep = D == 128 && RG > 0;
+    constexpr int kWindow = 24, kTileProducts = C::kRg * (NT / 2) * (RG == 0 ? 1 : TERMS);
+    constexpr int kFlush = kWindow > kTileProducts ? kWindow / kTileProducts : 1;  // tiles of a window
+    float sums[DN][AW];
+    float acc[kByStep ? 1 : DN][4];  // of eight rows the tile's lower half holds small terms
+    int fresh;                       // tiles in acc
+    float m_run[2], l_run[2], l_rest[2], s_mul[2];  // l_rest: what the roundings of l_run left out
+    auto clear_acc = [&] {
+        fresh = 0;
+        if constexpr (!kByStep) {
+#pragma unroll
+            for (int n = 0; n < DN; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[n][e] = 0.f;
+        }
+    };
+    auto flush = [&] {
+        if constexpr (RG == 0) {
+#pragma unroll
+            for (int n = 0; n < DN; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    sums[n][e] += acc[n][e] + acc[n][2 + e];
+        } else if constexpr (!kByStep) {
+#pragma unroll
+            for (int n = 0; n < DN; ++n)
+                add_to(sums[n], acc[n]);
+        }
+        clear_acc();
+    };
     int lim[2];         // keys that each of this thread's rows sees
     // A row of the joined tile belongs to TPR threads, which take its columns
     // in turn, two at a time.
@@ -642,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         for (int hf = 0; hf < 2; ++hf) {
             m_run[hf] = -INFINITY;
             l_run[hf] = 0.f;
+            l_rest[hf] = 0.f;
             const int s = (row0 + rg * 16 + g + hf * 8) % a.Sq;
             lim[hf] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
             s_mul[hf] = kmul;
@@ -678,8 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
 #pragma unroll
         for (int n = 0; n < DN; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[n][e] = 0.f;
+            for (int e = 0; e < AW; ++e)
+                sums[n][e] = 0.f;
+        clear_acc();
 
         for (;;) {
             wait_phase(full + stage, phase, budget);
@@ -790,17 +842,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         const float f = x == -INFINITY ? 1.f : ex2_approx(m_run[hf] - x);
                         m_run[hf] = x;
                         l_run[hf] *= f;
+                        l_rest[hf] *= f;
 #pragma unroll
                         for (int n = 0; n < DN; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                acc[n][hf * 2 + e] *= f;
-                                if (RG == 0)
+                                sums[n][hf * 2 + e] *= f;
+                                if constexpr (!kByStep)
+                                    acc[n][hf * 2 + e] *= f;
+                                if constexpr (RG == 0)
                                     acc[n][2 + e] *= f;
                             }
                     }
                 }
-                constexpr int TERMS = FP8 ? 2 : 3;
                 uint32_t p[NT][2][TERMS];
 #pragma unroll
                 for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
@@ -813,52 +867,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         sum += p0 + p1;
                         split<FP8>(p0, p1, p[n][hf]);
                     }
-                    l_run[hf] += sum;
+                    // with what is left of earlier roundings: equal weights,
+                    // small beside the sum, all round the same way (16K of
+                    // them: 2e-5 of the sum)
+                    sum += l_rest[hf];
+                    const float l = l_run[hf] + sum;
+                    l_rest[hf] = sum - (l - l_run[hf]);
+                    l_run[hf] = l;
                 }
                 // ---- O += P V
                 auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
                     // eight rows take two terms at once, the second in the tile's
-                    // lower half, whose sums join the upper half's at the end; the
-                    // third goes there too (the unit truncates its sums, and the
-                    // upper one is the one that matters)
+                    // lower half, and the third goes there too; else small ones first
                     if constexpr (RG == 0) {
                         mma<FP8>(d, p[n][0][0], p[n][0][1], p[n + 1][0][0], p[n + 1][0][1], b0, b1);
                         if constexpr (TERMS == 3)
                             mma<FP8>(d, 0u, p[n][0][2], 0u, p[n + 1][0][2], b0, b1);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < TERMS; ++i)
+                        for (int i = TERMS - 1; i >= 0; --i)
                             mma<FP8>(d, p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
-                    }
-                };
-                // every (8-column tile of O, 16 keys) once: `use` gets the column
-                // tile, the key tile and the operand
-                auto each_v = [&](auto &&use) {
-                    if constexpr (!FP8) {
-#pragma unroll
-                        for (int n = 0; n < NT; n += 2)
-#pragma unroll
-                            for (int c = 0; c < DN; c += 2) {
-                                uint32_t f[4];
-                                ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * BOXES + n * 8 * BOX);
-                                use(c, n, f[0], f[1]);
-                                use(c + 1, n, f[2], f[3]);
-                            }
-                    } else {
-                        // the transposed load pairs neighbouring elements of a key
-                        // in each half: the low bytes of both halves make the even
-                        // columns' operand, the high bytes the odd ones'
-#pragma unroll
-                        for (int c = 0; c < DN; c += 2) {
-                            uint32_t f[4];
-                            ldsm_x4_t(f, v_u ^ ((c >> 1) << 4));
-#pragma unroll
-                            for (int n = 0; n < 4; n += 2) {
-                                const uint32_t x = __byte_perm(f[n], 0, 0x3120), y = __byte_perm(f[n + 1], 0, 0x3120);
-                                use(c, n, e4m3_to_f16(x), e4m3_to_f16(y));
-                                use(c + 1, n, e4m3_to_f16(x >> 16), e4m3_to_f16(y >> 16));
-                            }
-                        }
                     }
                 };
                 // A key that only some rows see still meets the others' products,
@@ -906,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                             for (int i = 0; i < EACH; ++i)
 #pragma unroll
                                 for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                                    float &o = acc[FP8 ? n + i % 2 : n][hf * 2 + (FP8 ? i / 2 : i)];
+                                    float &o = sums[FP8 ? n + i % 2 : n][hf * 2 + (FP8 ? i / 2 : i)];
                                     const int r = (int)(x >> (i * 8) & 0xffu);
                                     if (r != 0xff && kb + r < lim[hf])
                                         o = __int_as_float(0x7fffffff);
@@ -914,13 +942,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                         }
                     }
                 }
-                each_v([&](int c, int n, uint32_t b0, uint32_t b1) { add_pv(acc[c], n, b0, b1); });
+                // values of 16 keys n*8 .. +15, columns c*8 .. +15
+                auto load_v = [&](uint32_t (&f)[4], int c, int n) {
+                    ldsm_x4_t(f, (v_u ^ (((c >> 1) & 3) << 5)) + (c >> 3) * BOXES + n * 8 * BOX);
+                };
+                if constexpr (FP8 || kByStep) {
+#pragma unroll
+                    for (int c = 0; c < DN; c += 2) {
+                        float step_sums[2][4] = {};
+                        float (&even)[4] = kByStep ? step_sums[0] : acc[kByStep ? 0 : c];
+                        float (&odd)[4] = kByStep ? step_sums[1] : acc[kByStep ? 0 : c + 1];
+                        if constexpr (FP8) {
+                            // the transposed load pairs neighbouring elements of
+                            // a key in each half: the low bytes of both halves
+                            // make the even columns' operand, the high bytes the
+                            // odd ones'
+                            uint32_t f[4];
+                            ldsm_x4_t(f, v_u ^ ((c >> 1) << 4));
+#pragma unroll
+                            for (int n = 0; n < 4; n += 2) {
+                                const uint32_t x = __byte_perm(f[n], 0, 0x3120), y = __byte_perm(f[n + 1], 0, 0x3120);
+                                add_pv(even, n, e4m3_to_f16(x), e4m3_to_f16(y));
+                                add_pv(odd, n, e4m3_to_f16(x >> 16), e4m3_to_f16(y >> 16));
+                            }
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < NT; n += 2) {
+                                uint32_t f[4];
+                                load_v(f, c, n);
+                                add_pv(even, n, f[0], f[1]);
+                                add_pv(odd, n, f[2], f[3]);
+                            }
+                        }
+                        if constexpr (kByStep) {
+                            add_to(sums[c], even);
+                            add_to(sums[c + 1], odd);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2)
+#pragma unroll
+                        for (int c = 0; c < DN; c += 2) {
+                            uint32_t f[4];
+                            load_v(f, c, n);
+                            add_pv(acc[c], n, f[0], f[1]);
+                            add_pv(acc[c + 1], n, f[2], f[3]);
+                        }
+                }
             }
             if (--left == 0)
                 break;
             release();
             ++at.j;
+            if (!kByStep && ++fresh == kFlush)
+                flush();
         }
+        flush();
 
         // ---- the job's or the share's end: join the key groups' warps
         const bool last_tile = at.j == at.tiles - 1;
@@ -957,9 +1035,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[e] = acc[n][hf * 2 + e] + (RG == 0 ? acc[n][2 + e] : 0.f);
+                    x[e] = sums[n][hf * 2 + e];
                     if (FP8)
-                        x[2 + e] = acc[n + 1][hf * 2 + e] + (RG == 0 ? acc[n + 1][2 + e] : 0.f);
+                        x[2 + e] = sums[n + 1][hf * 2 + e];
                 }
                 if (FP8) {
                     const int col = n * 8 + t * 4;

@@ -6,12 +6,14 @@ Bounds are derived where they are used; a rounding is off by at most half a step
 definitions these tests share.
 """
 import contextlib
+import math
 import types
 
 import pytest
 import torch
 
-from tests.test_paged import BF16, FP32, cache_struct, gm, m, make_cache  # noqa: F401  (gm, m: fixtures)
+from tests.test_paged import (BF16, E4M3, FP32, attention, cache_struct, gather_states, gm, m,  # noqa: F401  (gm, m: fixtures)
+                              make_cache)
 
 
 # --------------------------------------------------------- outputs that a call makes itself
@@ -111,3 +113,86 @@ def test_padded_calls_on_a_given_stream_keep_their_rows(gm, as_int):
     gm.mercury_sync_status()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ sums over long contexts
+
+def shared_cache(gm, n, d, dtype, gen, B):
+    """One sequence of n tokens whose pages B sequences name: jobs for every SM in little memory."""
+    page = 64
+    k_cache, v_cache, table, (ks, vs) = make_cache(1, 1, d, page, -(-n // page), dtype, gen)
+    return gm.PagedCache(k_cache, v_cache, table.expand(B, -1).contiguous(), k_scale=ks, v_scale=vs)
+
+
+def states(cache, n):
+    return (gather_states(c, s, cache.block_table[0], n)
+            for c, s in ((cache.k_cache, cache.k_scale), (cache.v_cache, cache.v_scale)))
+
+
+def sum_bound(n):
+    """Relative bound of a sum of n weighted values that do not cancel, kept in 32 bits and rounded to nearest.
+
+    Sixteen keys at a time, n/16 additions, each off by at most 2^-24 of the sum, independently and either way: beyond
+    7 (n/16)^(1/2) 2^-24 the chance is 2 exp(-98) (Hoeffding).  A weight's exponent, at most 16 in powers of two, is
+    off by 2^-21 and by 3 roundings of a factor, its exponential by 2^-22, its terms by 2^-23: 30 * 2^-24 in all, once
+    above and once below the line, and a dozen joins and the quotient."""
+    return (7 * math.sqrt(n) / 4 + 72) * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [1, 16, 28, 64])
+def test_sums_over_a_long_context(gm, dtype, d, rows):
+    """32K keys whose values are all positive: the rounding of the sums shows, and nothing cancels."""
+    n, B = 32768, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator("cuda").manual_seed(rows + d)
+    cache = shared_cache(gm, n, d, dtype, gen, B)
+    # scores of one product each, exact in 32 bits: multiples of 1/8 in [-2, 2] times multiples of 1/16 in [8, 12)
+    scores = torch.randint(-16, 17, cache.k_cache.shape, generator=gen, device="cuda") / 8
+    scores[..., 1:] = 0
+    cache.k_cache.copy_(scores.to(dtype))
+    cache.v_cache.copy_((cache.v_cache.float().abs() + (20 if dtype is E4M3 else 1)).clamp(max=448).to(dtype))
+    if dtype is E4M3:
+        cache.k_scale.fill_(1.0)
+    q = torch.zeros(B, rows, 1, d, dtype=BF16, device="cuda")
+    q[..., 0] = 8 + torch.arange(rows, device="cuda")[:, None] / 16
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    out, lse = gm.mercury_attn_paged(q, cache, lens)
+    gm.mercury_sync_status()
+    k, v = states(cache, n)
+    o, l, _, _ = attention(q[0], k, v, [n])
+    assert ((out[0].double() - o) / o).abs().max() <= sum_bound(n)
+    assert ((out.double() - o) / o).abs().max() <= sum_bound(n)  # the others' keys, cut elsewhere
+    assert (lse.double() - l).abs().max() <= 72 * 2.0 ** -24 + 2.0 ** -22 * l.abs().max()
+
+
+def sink(gm, dtype, rows, below, n=16384, d=128):
+    """One key far above n - 1 equal ones, its value zero: all of O comes from weights e^-below of the largest.
+    Returns O's relative error, LSE's error and the bound of a score (2^-21, as in attention())."""
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    cache = shared_cache(gm, n, d, dtype, torch.Generator("cuda").manual_seed(rows), B)
+    if dtype is E4M3:
+        cache.k_scale.fill_(1.0)
+        cache.v_scale.fill_(1.0)
+    first = cache.block_table[0, 0].long()
+    k, v = torch.zeros(cache.k_cache.shape, device="cuda"), cache.v_cache.float().abs() % 1 + 1
+    k[first, 0, 0, 0] = 1
+    v[first, 0, 0] = 0
+    cache.k_cache.copy_(k.to(dtype))
+    cache.v_cache.copy_(v.to(dtype))
+    q = torch.zeros(B, rows, 1, d, dtype=BF16, device="cuda")
+    q[..., 0] = below * math.sqrt(d)
+    out, lse = gm.mercury_attn_paged(q, cache, torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    gm.mercury_sync_status()
+    o, l, _, _ = attention(q[0], *states(cache, n), [n])
+    return ((out.double() - o) / o).abs().max().item(), (lse.double() - l).abs().max().item(), 2.0 ** -21 * below
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 16, 40])
+@pytest.mark.parametrize("below", [8.0, 14.0, 17.0, 20.0])
+def test_small_weights_beside_a_large_one(gm, rows, below):
+    off, off_lse, ds = sink(gm, BF16, rows, below)
+    assert off <= sum_bound(16384) + 2 * ds
+    assert off_lse <= 72 * 2.0 ** -24 + ds
