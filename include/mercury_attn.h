@@ -652,9 +652,13 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * row does not see do not affect it, whatever they hold; of the cache rows at
  * and after seq_lens[b] nothing is used (the rest of the last page may be
  * read).
- * Scores, sums and products are kept in fp32 and P as a sum of 16-bit terms
- * (24 bits or more), so O carries fp32 accuracy (about 1e-6 relative) from the
- * cache's values.
+ * Scores and sums are kept in fp32.  A weight exp(x_k - x_max) enters the
+ * products as a sum of 16-bit terms: three of bf16, which hold it to 2^-26 of
+ * itself, or for an e4m3 cache two of fp16, which hold it to 2^-23 of itself
+ * or 2^-48 of the row's largest weight, whichever is more.  So O is a 32-bit
+ * result: its error, relative to the weighted mean of |v|, is that of the
+ * scores (each a sum of d products in fp32) and of the sums' roundings, which
+ * grows with the square root of the keys (32K keys: about 1e-6).
  * The keys of all sequences are dealt to the SMs in equal shares on the
  * device, so neither the lengths nor their spread need to be known on the
  * host.  Parts of sequences cut between SMs go to scratch memory (2 * SMs *

@@ -174,7 +174,7 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr)
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8); bf16 operands, or fp16 for an
 // 8-bit cache.
 template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1)
 {
     if constexpr (F16)
@@ -201,28 +201,42 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// o += d, rounded to nearest, two elements an instruction (28 rows of 128 at 20K
-// to 32K keys: 184 us instead of 189 one by one).
-__device__ __forceinline__ void add_to(float (&o)[4], const float (&d)[4])
+// o += d f, rounded to nearest, two elements an instruction (28 rows of 128 at
+// 20K to 32K keys: 184 us instead of 189 one by one).
+__device__ __forceinline__ void add_to(float *o, const float *d, float f)
 {
 #pragma unroll
     for (int e = 0; e < 4; e += 2)
-        asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
-            "mov.b64 {%0, %1}, x;\n\t}"
+        asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 z, {%4, %4};\n\t"
+            "fma.rn.f32x2 x, y, z, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
             : "+f"(o[e]), "+f"(o[e + 1])
-            : "f"(d[e]), "f"(d[e + 1]));
+            : "f"(d[e]), "f"(d[e + 1]), "f"(f));
 }
 
-// p as a sum of 16-bit terms, each the nearest to what those before it leave:
-// two fp16 ones hold it to 2^-22, three bf16 ones to 2^-26.  (Two bf16 terms,
-// 2^-18, left O four times further from 64 bits than a 32-bit softmax does.)
+// p as a sum of 16-bit terms, each the nearest to what those before it leave.
+// Three bf16 ones hold it to 2^-26.  (Two, 2^-18, left O four times further from
+// 64 bits than a 32-bit softmax does.)
+//
+// Of two fp16 ones the second is kept 2^kLowShift times as large, with sums of
+// its own: fp16 ends at 2^-24, and a weight far below the largest, or the rest
+// of one, would lose its bits there, as every key does beside a sink (16K keys
+// 17 nats below one, 8 rows: their part of O 5 % off; now 2e-6).  For the same
+// reason weights are taken 2^kUp times as large, with a maximum that is raised
+// already by scores 2^kGrow above it, so that they fill fp16's upper half.
+// They are held to 2^-23, and the smallest ones to 2^-48 of the largest.
+constexpr int kLowShift = 11;
+template <bool F16>
+constexpr float kGrow = F16 ? 3.f : 8.f;
+template <bool F16>
+constexpr float kUp = F16 ? 12.f : 0.f;
+constexpr float kLow = 1.f / (1 << kLowShift);
 template <bool F16>
 __device__ __forceinline__ void split(float p0, float p1, uint32_t (&term)[F16 ? 2 : 3])
 {
     if constexpr (F16) {
         term[0] = pack_f16(p0, p1);
         const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&term[0]));
-        term[1] = pack_f16(p0 - h.x, p1 - h.y);
+        term[1] = pack_f16((p0 - h.x) * (1 << kLowShift), (p1 - h.y) * (1 << kLowShift));
     } else {
         term[0] = pack_bf16(p0, p1);
         p0 -= bf16_lo(term[0]);
@@ -614,16 +628,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     // whole job, each product lost up to a unit in O's last place, always
     // towards zero (32K keys, 64 rows: 6e-5 of O).  So its own sums, acc, are
     // short, kWindow products from zero, and are added to O's by an ordinary
-    // addition.  Heads of 128 with more than 8 rows have no registers for both
-    // and take a step's products at a time (28 rows at 20K to 32K keys: 161 us
-    // as it was, 184 so, 201 with windows; 56 rows of 64: 315, 359 and 337).
+    // addition.  With more than 8 rows, heads of 128 have no registers for both,
+    // nor have heads of 64 with 8-bit keys, whose small terms have sums of their
+    // own; those take a step's products at a time (at 20K to 32K keys, 28 rows
+    // of 128: 184 us so, 201 with windows; 16 rows of 64 in 8 bits: 98 and 107;
+    // but 56 rows of 64 in 16 bits 359 and 337).
     constexpr int TERMS = FP8 ? 2 : 3;
     constexpr int AW = RG == 0 ? 2 : 4;  // sums of this thread in each 8-column tile of O: one row's, or two
-    constexpr bool kByStep = D == 128 && RG > 0;
+    constexpr bool kByStep = RG > 0 && (D == 128 || FP8);
     constexpr int kWindow = 24, kTileProducts = C::kRg * (NT / 2) * (RG == 0 ? 1 : TERMS);
     constexpr int kFlush = kWindow > kTileProducts ? kWindow / kTileProducts : 1;  // tiles of a window
     float sums[DN][AW];
     float acc[kByStep ? 1 : DN][4];  // of eight rows the tile's lower half holds small terms
+    constexpr int ACC = FP8 && RG > 0 ? 8 : 4;  // a step's sums: the second terms' behind the first ones'
     int fresh;                       // tiles in acc
     float m_run[2], l_run[2], l_rest[2], s_mul[2];  // l_rest: what the roundings of l_run left out
     auto clear_acc = [&] {
@@ -642,11 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             for (int n = 0; n < DN; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    sums[n][e] += acc[n][e] + acc[n][2 + e];
+                    sums[n][e] += acc[n][e] + acc[n][2 + e] * (FP8 ? kLow : 1.f);
         } else if constexpr (!kByStep) {
 #pragma unroll
             for (int n = 0; n < DN; ++n)
-                add_to(sums[n], acc[n]);
+                add_to(sums[n], acc[n], 1.f);
         }
         clear_acc();
     };
@@ -818,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                             if (kb + n * 8 + t * 2 + (e & 1) >= lim[e >> 1])
                                 sc[n][e] = -INFINITY;
                 }
-                // The maximum moves only when a score exceeds it by 2^8: sum and O
+                // The maximum moves only when a score exceeds it by 2^kGrow: sum and O
                 // share whatever reference the terms were taken with, and the
                 // reduction and the rescaling stay off the common path.
                 bool grow = false;
@@ -830,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     for (int n = 1; n < NT; ++n)
                         x = fmaxf(x, fmaxf(sc[n][hf * 2], sc[n][hf * 2 + 1]));
                     top[hf] = x * s_mul[hf];
-                    grow |= top[hf] > m_run[hf] + 8.f;
+                    grow |= top[hf] > m_run[hf] + kGrow<FP8>;
                 }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -858,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 uint32_t p[NT][2][TERMS];
 #pragma unroll
                 for (int hf = 0; hf < (RG == 0 ? 1 : 2); ++hf) {
-                    const float ref = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
+                    const float ref = m_run[hf] == -INFINITY ? 0.f : kUp<FP8> - m_run[hf];
                     float sum = 0.f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -876,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     l_run[hf] = l;
                 }
                 // ---- O += P V
-                auto add_pv = [&](float (&d)[4], int n, uint32_t b0, uint32_t b1) {
+                auto add_pv = [&](float *d, int n, uint32_t b0, uint32_t b1) {
                     // eight rows take two terms at once, the second in the tile's
                     // lower half, and the third goes there too; else small ones first
                     if constexpr (RG == 0) {
@@ -886,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                     } else {
 #pragma unroll
                         for (int i = TERMS - 1; i >= 0; --i)
-                            mma<FP8>(d, p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
+                            mma<FP8>(d + (FP8 ? i * 4 : 0), p[n][0][i], p[n][1][i], p[n + 1][0][i], p[n + 1][1][i], b0, b1);
                     }
                 };
                 // A key that only some rows see still meets the others' products,
@@ -949,9 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 if constexpr (FP8 || kByStep) {
 #pragma unroll
                     for (int c = 0; c < DN; c += 2) {
-                        float step_sums[2][4] = {};
-                        float (&even)[4] = kByStep ? step_sums[0] : acc[kByStep ? 0 : c];
-                        float (&odd)[4] = kByStep ? step_sums[1] : acc[kByStep ? 0 : c + 1];
+                        float step_sums[2][ACC] = {};
+                        float *const even = kByStep ? step_sums[0] : acc[kByStep ? 0 : c];
+                        float *const odd = kByStep ? step_sums[1] : acc[kByStep ? 0 : c + 1];
                         if constexpr (FP8) {
                             // the transposed load pairs neighbouring elements of
                             // a key in each half: the low bytes of both halves
@@ -975,8 +992,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                             }
                         }
                         if constexpr (kByStep) {
-                            add_to(sums[c], even);
-                            add_to(sums[c + 1], odd);
+                            add_to(sums[c], even, 1.f);
+                            add_to(sums[c + 1], odd, 1.f);
+                            if constexpr (FP8) {
+                                add_to(sums[c], even + 4, kLow);
+                                add_to(sums[c + 1], odd + 4, kLow);
+                            }
                         }
                     }
                 } else {
@@ -1027,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             const int row = g + hf * 8;
             if (t == 0) {
-                red_m[warp * C::kWarpRows + row] = m_run[hf];
+                red_m[warp * C::kWarpRows + row] = m_run[hf] - kUp<FP8>;  // what the sums are relative to
                 red_l[warp * C::kWarpRows + row] = l;
             }
 #pragma unroll

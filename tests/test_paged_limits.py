@@ -12,8 +12,8 @@ import types
 import pytest
 import torch
 
-from tests.test_paged import (BF16, E4M3, FP32, attention, cache_struct, gather_states, gm, m,  # noqa: F401  (gm, m: fixtures)
-                              make_cache)
+from tests.test_paged import (BF16, E4M3, FP32, assert_within, attention, cache_struct, gather_states,
+                              gm, m, make_cache)  # noqa: F401  (gm, m: fixtures)
 
 
 # --------------------------------------------------------- outputs that a call makes itself
@@ -196,3 +196,40 @@ def test_small_weights_beside_a_large_one(gm, rows, below):
     off, off_lse, ds = sink(gm, BF16, rows, below)
     assert off <= sum_bound(16384) + 2 * ds
     assert off_lse <= 72 * 2.0 ** -24 + ds
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 16, 40])
+@pytest.mark.parametrize("below", [8.0, 12.0, 14.0, 17.0, 20.0])
+def test_small_weights_beside_a_large_one_in_8_bits(gm, rows, below):
+    """Weights enter the products as 16-bit terms, which hold the smallest ones to 2^-48 of the largest."""
+    off, off_lse, ds = sink(gm, E4M3, rows, below)
+    assert off <= sum_bound(16384) + 2 * ds + 2.0 ** -48 * math.exp(below)
+    assert off_lse <= 72 * 2.0 ** -24 + ds
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("rows", [1, 16, 28])
+def test_scores_that_rise_slowly(gm, dtype, rows):
+    """Each key a little above the last, up and down again: the maximum that the weights are taken relative to is
+    behind the scores by as much as the kernel lets it be, and is raised many times."""
+    n, d, page = 1500, 128, 64
+    gen = torch.Generator("cuda").manual_seed(rows)
+    cache = shared_cache(gm, n, d, dtype, gen, 3)
+    at = torch.arange(n, device="cuda")
+    wave = 40.0 * (1 - (at / 750.0 - 1).abs())
+    k = torch.zeros(cache.k_cache.shape, device="cuda")
+    k[cache.block_table[0][at // page].long(), 0, at % page, 0] = wave
+    cache.k_cache.copy_(k.to(dtype))
+    if dtype is E4M3:
+        cache.k_scale.fill_(1.0)
+    q = torch.zeros(3, rows, 1, d, dtype=BF16, device="cuda")
+    q[..., 0] = math.sqrt(d)
+    lens = torch.full((3,), n, dtype=torch.int32, device="cuda")
+    out, lse = gm.mercury_attn_paged(q, cache, lens)
+    gm.mercury_sync_status()
+    o, l, eo, el = attention(q[0], *states(cache, n), [n])
+    for b in range(3):
+        assert_within(out[b], o, eo, "O")
+        assert_within(lse[b], l, el, "LSE")
