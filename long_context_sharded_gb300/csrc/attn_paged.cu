@@ -246,6 +246,14 @@ __device__ __forceinline__ void split(float p0, float p1, uint32_t (&term)[F16 ?
     }
 }
 
+// For each element of w, two of bf16 or four of e4m3, that is infinite or NaN
+// (whose exponent bits, or all bits but the sign, are ones) its lowest bit.
+template <bool FP8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    return FP8 ? ((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u : ((w & 0x7f807f80u) + 0x00800080u) >> 15 & 0x00010001u;
+}
+
 // A copied tile's keys (or values): boxes of all its keys x kBoxB bytes (128,
 // or 64 for heads of 64 bytes), the 16-byte chunks of a row permuted so that
 // the eight rows of a matrix load hit eight different bank groups -- the
@@ -916,33 +924,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 if (edge && a.causal && n_new > 1) {
                     const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
                     constexpr int WORDS = ROWB / 4, EACH = FP8 ? 4 : 2, BITS = 32 / EACH;
-                    constexpr uint32_t NOT_FINITE = FP8 ? 0x7fu : 0x7f80u, ELEM = FP8 ? 0xffu : 0xffffu;
                     auto word = [&](int r, int w) {
                         return reinterpret_cast<uint32_t *>(smem + stage * C::kStage + C::kPart +
                                                             chunk_at<ROWB, TILE>(step * KEYS + r, w >> 2)) + (w & 3);
                     };
                     // the first such key of this lane's columns, a byte each
                     uint32_t bad = 0xffffffffu;
+#pragma unroll 1
                     for (int r = r1 - 1; r >= r0; --r)
-#pragma unroll
-                        for (int w = lane; w < WORDS; w += 32)
+#pragma unroll 1
+                        for (int w = lane; w < WORDS; w += 32) {
+                            const uint32_t found = not_finite<FP8>(*word(r, w));
 #pragma unroll
                             for (int i = 0; i < EACH; ++i)
-                                if ((*word(r, w) >> (i * BITS) & NOT_FINITE) == NOT_FINITE) {
+                                if (found >> (i * BITS) & 1u) {
                                     const int at_bit = (w / 32 * EACH + i) * 8;
                                     bad = (bad & ~(0xffu << at_bit)) | (uint32_t)r << at_bit;
                                 }
-                    if (__any_sync(0xffffffffu, bad != 0xffffffffu)) {
-                        if (C::kRg > 1)  // the other row groups' warps have looked too
-                            named_barrier_sync(2 + kg, C::kRg * 32);
+                        }
+                    // The warps of all row groups look at the same keys, and clear
+                    // the same words: none before all have looked, and none
+                    // multiplies before all have cleared.  (These barriers do not
+                    // hang on what the data is.)
+                    if (C::kRg > 1)
+                        named_barrier_sync(2 + kg, C::kRg * 32);
+                    const bool any = __any_sync(0xffffffffu, bad != 0xffffffffu);
+                    if (any) {
+#pragma unroll 1
                         for (int r = r0; r < r1; ++r)
-                            for (int w = lane; w < WORDS; w += 32)
-#pragma unroll
-                                for (int i = 0; i < EACH; ++i)
-                                    if ((*word(r, w) >> (i * BITS) & NOT_FINITE) == NOT_FINITE)
-                                        *word(r, w) &= ~(ELEM << (i * BITS));
+#pragma unroll 1
+                            for (int w = lane; w < WORDS; w += 32) {
+                                uint32_t *const x = word(r, w);
+                                const uint32_t old = *x, found = not_finite<FP8>(old);
+                                if (found)
+                                    *x = old & ~(found * ((1u << BITS) - 1u));
+                            }
                         fence_proxy_async_smem();  // before a tensor copy lands there
+                    }
+                    if (C::kRg > 1)
+                        named_barrier_sync(2 + kg, C::kRg * 32);
+                    else
                         __syncwarp();
+                    if (any) {
 #pragma unroll
                         for (int n = 0; n < DN; n += FP8 ? 2 : 1) {
                             const int w = FP8 ? n * 2 + t : n * 4 + t;

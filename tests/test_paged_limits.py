@@ -233,3 +233,43 @@ def test_scores_that_rise_slowly(gm, dtype, rows):
     for b in range(3):
         assert_within(out[b], o, eo, "O")
         assert_within(lse[b], l, el, "LSE")
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Sq", [(2, 4), (4, 4), (6, 4), (8, 4), (7, 9), (40, 3)])
+def test_whole_tokens_that_are_not_finite(gm, dtype, d, Hq, Sq):
+    """Every value of the newer drafted tokens NaN (or infinite, turn by turn): several elements of a word, for one to
+    four row groups of a tile and for two tiles.  Rows before such a token do not meet it, in any of many calls."""
+    page, B = 16, 40
+    gen = torch.Generator("cuda").manual_seed(Sq + d)
+    lens = [200 + 17 * b for b in range(B)]
+    k_cache, v_cache, table, (ks, vs) = make_cache(B, 1, d, page, -(-max(lens) // page), dtype, gen)
+    b8 = v_cache.view(torch.uint8) if dtype is E4M3 else v_cache
+    row = torch.full((d,), 0x7f, dtype=torch.uint8, device="cuda") if dtype is E4M3 else \
+        torch.tensor([math.nan, math.inf, -math.inf], device="cuda").repeat(d)[:d].to(BF16)
+    good = [b % Sq for b in range(B)]  # rows that see finite values only
+    for b, n in enumerate(lens):
+        for at in range(n - Sq + good[b], n):
+            b8[table[b, at // page].long(), 0, at % page] = row
+    q = torch.randn(B, Hq, Sq, d, generator=gen, device="cuda").to(BF16)
+    cache = gm.PagedCache(k_cache, v_cache, table, k_scale=ks, v_scale=vs)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = gm.mercury_attn_paged(q, cache, lens_t)
+    gm.mercury_sync_status()
+    for b, n in enumerate(lens):
+        k = gather_states(k_cache, ks, table[b], n)
+        v = gather_states(v_cache, vs, table[b], n - Sq + good[b])
+        if good[b]:
+            o, l, eo, el = attention(q[b, :, :good[b]], k[:, :v.shape[1]], v, [n - Sq + i + 1 for i in range(good[b])])
+            assert_within(out[b, :, :good[b]], o, eo, "O of sequence %d" % b)
+            assert_within(lse[b, :, :good[b]], l, el, "LSE of sequence %d" % b)
+        assert not torch.isfinite(out[b, :, good[b]:]).any()
+    same = torch.isfinite(out)
+    for _ in range(30):
+        again, lse2 = gm.mercury_attn_paged(q, cache, lens_t)
+        assert torch.equal(torch.isfinite(again), same) and torch.equal(again[same], out[same]) and torch.equal(lse2, lse)
+    gm.mercury_sync_status()
