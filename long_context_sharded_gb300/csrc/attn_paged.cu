@@ -480,6 +480,7 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
                     }
                 fence_proxy_async_smem();
             }
+            __syncwarp();  // every lane's zeros stand before lane 0's arrival
             const int boxes = __popc(__ballot_sync(0xffffffffu, good));
             const bool withheld = a.fault && tile == 0 && warp == 0;
             if (lane == 0 && !withheld)

@@ -273,3 +273,32 @@ def test_whole_tokens_that_are_not_finite(gm, dtype, d, Hq, Sq):
         again, lse2 = gm.mercury_attn_paged(q, cache, lens_t)
         assert torch.equal(torch.isfinite(again), same) and torch.equal(again[same], out[same]) and torch.equal(lse2, lse)
     gm.mercury_sync_status()
+
+
+# ----------------------------------------------------------------------- pages and copies
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 8), (64, 64), (128, 256), (128, 7)])
+def test_pages_outside_the_cache_count_as_zeros(gm, dtype, d, page):
+    """Keys and values of zero, for every lane that finds such a page: single pages, neighbours, a whole tile of them."""
+    B, Hq, n = 30, 4, 1500
+    gen = torch.Generator("cuda").manual_seed(page)
+    k_cache, v_cache, table, (ks, vs) = make_cache(B, 1, d, page, -(-n // page), dtype, gen)
+    wrong = torch.rand(table.shape, generator=gen, device="cuda") < torch.linspace(0, 1, B, device="cuda")[:, None]
+    table[wrong] = torch.randint(0, 2, (int(wrong.sum()),), generator=gen, device="cuda", dtype=torch.int32) * 2 ** 30 - 1
+    cache = gm.PagedCache(k_cache, v_cache, table, k_scale=ks, v_scale=vs)
+    q = torch.randn(B, Hq, 1, d, generator=gen, device="cuda").to(BF16)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        out, lse = gm.mercury_attn_paged(q, cache, lens)
+        with pytest.raises(gm.MercuryError) as e:
+            gm.mercury_sync_status()
+        assert e.value.status == gm.MERCURY_EBOUNDS
+        zero = wrong.repeat_interleave(page, 1)[:, None, :n, None]
+        for b in range(B):
+            k, v = (gather_states(c, s, table[b].clamp(0, k_cache.shape[0] - 1), n).masked_fill(zero[b], 0.0)
+                    for c, s in ((k_cache, ks), (v_cache, vs)))
+            o, l, eo, el = attention(q[b], k, v, [n])
+            assert_within(out[b], o, eo, "O of sequence %d" % b)
+            assert_within(lse[b], l, el, "LSE of sequence %d" % b)
