@@ -46,8 +46,8 @@
  *     drop_kv_free makes the attention kernel withhold one internal arrive,
  *     so the MMA issuer's or the TMA producer's bounded wait runs out and the
  *     call ends with MERCURY_ETIMEOUT -- a timeout, never a GPU fault.
- *     drop_page_copy withholds one copy of the paged attention kernel, with
- *     the same end.
+ *     drop_page_copy withholds the copies of one warp in four of the paged
+ *     attention kernel, with the same end.
  */
 #ifndef MERCURY_ATTN_H
 #define MERCURY_ATTN_H

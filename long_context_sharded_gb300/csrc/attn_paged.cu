@@ -64,6 +64,7 @@ constexpr uint32_t kRegsCompute = 216;
 constexpr int kMinLaunchRegs = (int)(kRegsCopy * 128 + kRegsCompute * kWarps * 32 + kThreads - 1) / kThreads;
 constexpr int kJoinWarps = 8;                // of a block of the second kernel
 constexpr int kJoinAhead = 4;                // parts that each has on the way
+constexpr uint32_t kEndBarrier = 15;         // named barrier at a block's end
 
 struct PagedArgs {
     CUtensorMap map_k, map_v;  // the cache in boxes of box_rows keys, where box_rows > 0
@@ -85,7 +86,7 @@ struct PagedArgs {
                     // takes longer (pages of 8, one by one: 16 of 700 to 32K 174 us instead of 170, 8-bit
                     // 84 instead of 78, 64 short ones 55.7 instead of 50.5)
     float scale_log2;
-    int fault;      // test hook: withhold one copy
+    int fault;      // test hook: withhold one copying warp's copies
     unsigned long long wait_ns;
 };
 
@@ -107,7 +108,8 @@ struct Cfg {
     static constexpr int kWarpRows = RG == 0 ? 8 : 16;
     static constexpr int kRed = kWarps * kWarpRows * 8;        // each warp's maxima and sums
     static constexpr int kRowBytes = kWarps * kWarpRows * D * 4;  // the warps' partial rows
-    static constexpr int kRowsAt = kStages * kStage + kRed + kStages * 16;
+    static constexpr int kCtl = kStages * kStage + kRed + kStages * 16;  // the block's Stop
+    static constexpr int kRowsAt = kCtl + 32;
     static constexpr bool kOwnRows = kRowsAt + kRowBytes <= 232448;
     static constexpr int kSmem = kRowsAt + (kOwnRows ? kRowBytes : 0);
     static_assert(kTile % (32 * kCopyWarps) == 0, "whole runs for each copying warp");
@@ -120,26 +122,40 @@ __device__ __forceinline__ void record_bounds(unsigned int site)
     atomicCAS(&g_paged_err_site, 0u, site);
 }
 
-// Waits for a phase of `bar`, at most `budget` ns.  A wait that runs out is
-// recorded and leaves later ones a millisecond each; the caller goes on with
-// whatever data there is, since which tiles, rows and barriers it touches does
-// not depend on them.
-__device__ __forceinline__ unsigned long long wait_long(uint64_t *bar, uint32_t parity, unsigned long long budget)
+// A block's end.  A wait that runs out sets `now`: no copy is sent after that
+// and no further wait lasts; the computing warps walk on to the end with
+// whatever data there is, since which tiles, rows and barriers they touch does
+// not depend on it.  `sent`: tiles that each copying warp has sent.
+struct Stop {
+    int now;
+    int sent[kCopyWarps];
+};
+
+__device__ __forceinline__ bool stopped(const Stop *stop)
 {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > budget) {
-            atomicOr(&g_paged_err_word, kErrTimeout);
-            atomicCAS(&g_paged_err_site, 0u, 0x904u);
-            return 1000000;
-        }
-    return budget;
+    return *reinterpret_cast<const volatile int *>(&stop->now) != 0;
 }
 
-__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, unsigned long long &budget)
+// Waits for a phase of `bar`, at most `limit` ns, or until the block stops.
+__device__ __forceinline__ void wait_long(uint64_t *bar, uint32_t parity, unsigned long long limit, Stop *stop)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (stopped(stop))
+            return;
+        if (globaltimer_ns() - t0 > limit) {
+            *reinterpret_cast<volatile int *>(&stop->now) = 1;
+            atomicOr(&g_paged_err_word, kErrTimeout);
+            atomicCAS(&g_paged_err_site, 0u, 0x904u);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, unsigned long long limit, Stop *stop)
 {
     if (!mbar_try_wait(bar, parity))
-        budget = wait_long(bar, parity, budget);
+        wait_long(bar, parity, limit, stop);
 }
 
 // 16 bytes global -> shared; zeros where !valid (the source is not read).
@@ -437,12 +453,11 @@ __device__ __forceinline__ bool find_share(const PagedArgs &a, int lane, Shares 
 // copies, which took one warp 2200 cycles.
 template <int D, bool FP8, int RG>
 __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end, char *smem, uint64_t *full,
-                                           uint64_t *empty, int warp, int lane)
+                                           uint64_t *empty, Stop *stop, int warp, int lane)
 {
     using C = Cfg<D, FP8, RG>;
     constexpr int ROWB = C::kRowB, TILE = C::kTile, NS = C::kStages, N = TILE / 32 / kCopyWarps;
     constexpr int ES = FP8 ? 1 : 2, CPR = ROWB / 16, RPP = 32 / CPR;  // chunks of a row, rows copied at a time
-    unsigned long long budget = a.wait_ns;
     // Page entries of the next tile, asked for a tile ahead: with tensor
     // copies lane l's is that of box l * kCopyWarps + warp, else those of key l
     // of this warp's runs.
@@ -459,12 +474,15 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
     look_up();
     int stage = 0;
     uint32_t phase = 1;  // a fresh ring's stages count as left
-    for (int tile = 0;; ++tile) {
+    int sent = 0;
+    while (!(a.fault && warp == 0)) {  // (the test hook: the first of the four sends nothing)
         const int next = next_pos<TILE>(at);
         const bool on = next < end;
         const int h = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
         char *const part = smem + stage * C::kStage;
-        wait_phase(empty + stage, phase, budget);
+        wait_phase(empty + stage, phase, a.wait_ns, stop);
+        if (__any_sync(0xffffffffu, stopped(stop)))
+            break;
         if (a.box_rows) {
             const int key = key_of(0);
             const int page = entry[0], row = key - page_of(a.cache, key) * a.cache.page_size;
@@ -482,11 +500,10 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
             }
             __syncwarp();  // every lane's zeros stand before lane 0's arrival
             const int boxes = __popc(__ballot_sync(0xffffffffu, good));
-            const bool withheld = a.fault && tile == 0 && warp == 0;
-            if (lane == 0 && !withheld)
+            if (lane == 0)
                 mbar_arrive_expect_tx(full + stage, boxes * a.box_rows * 2 * ROWB);
             __syncwarp();
-            if (good && !withheld) {
+            if (good) {
 #pragma unroll
                 for (int x = 0; x < ROWB / C::kBoxB; ++x) {
                     const uint32_t to = smem_u32(part) + x * TILE * C::kBoxB + first * C::kBoxB;
@@ -518,6 +535,7 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
             }
             copy_arrive(full + stage);
         }
+        ++sent;
         if (!on)
             break;
         advance<TILE>(a, at, next);
@@ -539,6 +557,29 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
             phase ^= 1;
         }
     }
+    // The block's memory is given up only when nothing is on its way there.
+    // Where no wait ran out, the computing warps have seen every tile land.
+    if (lane == 0)
+        stop->sent[warp] = sent;
+    named_barrier_sync(kEndBarrier, kThreads);
+    if (!stopped(stop))
+        return;
+    // Else the tiles that are not known to have landed are the last NS that any
+    // of the four sent: tile i goes out only when i - NS has landed in full and
+    // been left, and nothing goes out after a stop.  For the same reason this
+    // warp owes each of their barriers at most one arrival; with those made up
+    // they complete as the copies land.
+    int most = 0;
+    for (int w = 0; w < kCopyWarps; ++w)
+        most = max(most, stop->sent[w]);
+    for (int i = sent; i < most; ++i)
+        if (!a.box_rows || lane == 0)
+            mbar_arrive(full + i % NS);
+    for (int i = max(most - NS, 0); i < most; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(full + i % NS, i / NS & 1) && globaltimer_ns() - t0 <= a.wait_ns)
+            ;
+    }
 }
 
 template <int D, bool FP8, int RG>
@@ -553,9 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     float *const red_l = red_m + kWarps * C::kWarpRows;
     uint64_t *const full = reinterpret_cast<uint64_t *>(smem + NS * C::kStage + C::kRed);
     uint64_t *const empty = full + NS;
+    Stop *const stop = reinterpret_cast<Stop *>(smem + C::kCtl);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
+        stop->now = 0;
         for (int i = 0; i < NS; ++i) {
             // a tile has landed: an arrival of each copying warp and the bytes
             // of its tensor copies, or an arrival of each copying lane
@@ -590,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         return;
     if (warp >= kWarps) {
         regs_dec<kRegsCopy>();
-        copy_tiles<D, FP8, RG>(a, at, end, smem, full, empty, warp - kWarps, lane);
+        copy_tiles<D, FP8, RG>(a, at, end, smem, full, empty, stop, warp - kWarps, lane);
         return;
     }
 
@@ -598,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     regs_inc<kRegsCompute>();
     const int g = lane >> 2, t = lane & 3;
     const int kg = warp % C::kKg, rg = warp / C::kKg;  // this warp's keys of a tile, and rows
-    unsigned long long budget = a.wait_ns;
     uint32_t qf[KK][RG == 0 ? 2 : 4];
     int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
     float k_scale = 1.f;
@@ -760,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         clear_acc();
 
         for (;;) {
-            wait_phase(full + stage, phase, budget);
+            wait_phase(full + stage, phase, a.wait_ns, stop);
 #pragma unroll 1
             for (int step = kg; step < kWarps; step += C::kKg) {
                 const int kb = at.j * TILE + step * KEYS;
@@ -1152,6 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
         if (!on)
             break;
     }
+    named_barrier_arrive(kEndBarrier, kThreads);
 }
 
 // Joins the parts of the jobs that were cut between blocks.  Each block takes

@@ -7,6 +7,7 @@ definitions these tests share.
 """
 import contextlib
 import math
+import time
 import types
 
 import pytest
@@ -302,3 +303,33 @@ def test_pages_outside_the_cache_count_as_zeros(gm, dtype, d, page):
             o, l, eo, el = attention(q[b], k, v, [n])
             assert_within(out[b], o, eo, "O of sequence %d" % b)
             assert_within(lse[b], l, el, "LSE of sequence %d" % b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [64, 8, 7])
+@pytest.mark.parametrize("rows", [4, 40])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_a_long_call_whose_copies_never_come_ends(gm, monkeypatch, dtype, rows, page):
+    """Far more tiles a block than are ever on their way: a wait runs out, the block sends nothing more and ends when
+    what it had sent has landed, the status says so, and the next call is right."""
+    n, d, B = 4000, 128, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator("cuda").manual_seed(page)
+    k_cache, v_cache, table, (ks, vs) = make_cache(1, 1, d, page, -(-n // page), dtype, gen)
+    cache = gm.PagedCache(k_cache, v_cache, table.expand(B, -1).contiguous(), k_scale=ks, v_scale=vs)
+    q = torch.randn(B, rows, 1, d, generator=gen, device="cuda").to(BF16)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    want = gm.mercury_attn_paged(q, cache, lens)
+    gm.mercury_sync_status()
+    for _ in range(2):
+        with monkeypatch.context() as mp:
+            mp.setenv("MERCURY_FAULT", "drop_page_copy")
+            mp.setenv("MERCURY_WAIT_NS", "20000000")
+            began = time.monotonic()
+            gm.mercury_attn_paged(q, cache, lens)
+            with pytest.raises(gm.MercuryError) as e:
+                gm.mercury_sync_status()
+            assert e.value.status == gm.MERCURY_ETIMEOUT
+            assert time.monotonic() - began < 5  # 20 ms, not 20 ms a tile
+        out, lse = gm.mercury_attn_paged(q, cache, lens)
+        gm.mercury_sync_status()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
