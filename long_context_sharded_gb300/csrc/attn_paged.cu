@@ -15,7 +15,8 @@
 //     lengths.  A block writes the jobs it holds whole; of a job cut at a
 //     share's end it leaves the unnormalised partial sums, maximum and sum
 //     (at most two per block), which a second kernel joins by the exact
-//     log-sum-exp rule.  That kernel is resident before the first one ends.
+//     log-sum-exp rule.  Its blocks come up as those of the first leave their
+//     SMs, which they fill.
 //   * in a block four warps do nothing but look up pages and send tensor
 //     copies of whole tiles into a ring of stages, across the ends of jobs, so
 //     the memory is kept busy while the other eight change jobs; with copies
@@ -79,7 +80,6 @@ struct PagedArgs {
     int4 *ws_rec;   // [blocks]: job cut behind its first part in the block, its new tokens, -, its last
                     // block (-1: none)
     int B, Hq, Hkv, G, Sq, R, n_rt, causal, out_bf16;
-    int records;    // blocks of the first kernel, for the join kernel
     int join_warps; // warps for a row there
     int box_rows;   // keys of a tensor copy: the largest power of two that divides page_size, at most a
                     // tile; 0 below 8 (the rows of a swizzle), where keys are copied one by one, which
@@ -1197,121 +1197,111 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
     named_barrier_arrive(kEndBarrier, kThreads);
 }
 
-// Joins the parts of the jobs that were cut between blocks.  Each block takes
-// the records of every gridDim.x-th block of the first kernel, 32 in one look,
-// and of each job kJoinWarps / join_warps rows, beginning at blockIdx.y times
-// that: join_warps warps join every join_warps-th part of a row, then through
-// shared memory.
+// Joins the parts of a job that was cut between blocks: block x of this kernel
+// the job whose first part lies at the end of block x of the first kernel, if
+// there is one, and of its rows kJoinWarps / join_warps, beginning at
+// blockIdx.y times that.  join_warps warps join every join_warps-th part of a
+// row, then through shared memory.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) attn_paged_join_kernel(const __grid_constant__ PagedArgs a)
 {
     constexpr int W = kJoinWarps, PER = D / 32;
     __shared__ float part[W][D], tops[W], sums[W];
-    asm volatile("" ::"l"(a.ws_rec), "l"(a.ws_ml), "l"(a.ws_o), "r"(a.records), "r"(a.n_rt), "r"(a.R), "r"(a.Sq), "l"(a.out),
-                 "l"(a.lse), "l"(a.cache.v_scale), "r"(a.out_bf16), "r"(a.join_warps));
+    asm volatile("" ::"l"(a.ws_rec), "l"(a.ws_ml), "l"(a.ws_o), "r"(a.n_rt), "r"(a.R), "r"(a.Sq), "l"(a.out), "l"(a.lse),
+                 "l"(a.cache.v_scale), "r"(a.out_bf16), "r"(a.join_warps));
     chain_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pw = a.join_warps, rows = W / pw;
     const int row0 = blockIdx.y * rows, row = row0 + warp / pw;
-    for (int from = blockIdx.x; from < a.records; from += 32 * gridDim.x) {
-        const int mine = from + lane * gridDim.x;
-        int4 rec = make_int4(0, 0, 0, -1);
-        if (mine < a.records)
-            rec = __ldcg(a.ws_rec + mine);
-        unsigned todo = __ballot_sync(0xffffffffu, rec.w >= 0);
-        while (todo) {
-            const int l = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int first = from + l * gridDim.x, last = __shfl_sync(0xffffffffu, rec.w, l);
-            const int job = __shfl_sync(0xffffffffu, rec.x, l), n_new = __shfl_sync(0xffffffffu, rec.y, l);
-            const int bh = job / a.n_rt, job_row = (job - bh * a.n_rt) * ROWS;
-            // a row of the tile that is a row of the output
-            auto there = [&](int i) {
-                return i < ROWS && job_row + i < a.R && (a.Sq == 1 || (job_row + i) % a.Sq < n_new);
-            };
-            const int n = there(row) ? last - first + 1 : 0;
-            float top = -INFINITY, sum = 0.f, o[PER];
+    const int4 rec = __ldcg(a.ws_rec + blockIdx.x);
+    const int first = blockIdx.x, last = rec.w, job = rec.x, n_new = rec.y;
+    if (last < 0)
+        return;
+    const int bh = job / a.n_rt, job_row = (job - bh * a.n_rt) * ROWS;
+    // a row of the tile that is a row of the output
+    auto there = [&](int i) {
+        return i < ROWS && job_row + i < a.R && (a.Sq == 1 || (job_row + i) % a.Sq < n_new);
+    };
+    const int n = there(row) ? last - first + 1 : 0;
+    float top = -INFINITY, sum = 0.f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+        o[e] = 0.f;
+    constexpr int U = kJoinAhead;
+    for (int i0 = warp % pw; i0 < n; i0 += pw * U) {
+        float2 ml[U];
+        float x[U][PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * pw;
+            ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int e = 0; e < PER; ++e)
-                o[e] = 0.f;
-            constexpr int U = kJoinAhead;
-            for (int i0 = warp % pw; i0 < n; i0 += pw * U) {
-                float2 ml[U];
-                float x[U][PER];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * pw;
-                    ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                    for (int e = 0; e < PER; ++e)
-                        x[u][e] = 0.f;
-                    if (i < n) {
-                        const long long s = (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * ROWS + row;
-                        ml[u] = __ldcg(a.ws_ml + s);
-                        const float *src = a.ws_o + s * D + lane * PER;
-                        if constexpr (PER == 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
-                        } else {
-                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                            x[u][0] = v.x, x[u][1] = v.y;
-                        }
-                    }
+                x[u][e] = 0.f;
+            if (i < n) {
+                const long long s = (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * ROWS + row;
+                ml[u] = __ldcg(a.ws_ml + s);
+                const float *src = a.ws_o + s * D + lane * PER;
+                if constexpr (PER == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    x[u][0] = v.x, x[u][1] = v.y;
                 }
-                float m = top;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    m = fmaxf(m, ml[u].x);
-                const float ref = m == -INFINITY ? 0.f : m;
-                const float f0 = ex2_approx(top - ref);
-                top = m;
-                sum *= f0;
-#pragma unroll
-                for (int e = 0; e < PER; ++e)
-                    o[e] *= f0;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float f = ex2_approx(ml[u].x - ref);
-                    sum += f * ml[u].y;
-#pragma unroll
-                    for (int e = 0; e < PER; ++e)
-                        o[e] += f * x[u][e];
-                }
-            }
-            __syncthreads();  // the last job's sums have been read
-#pragma unroll
-            for (int e = 0; e < PER; ++e)
-                part[warp][lane * PER + e] = o[e];
-            if (lane == 0) {
-                tops[warp] = top;
-                sums[warp] = sum;
-            }
-            __syncthreads();
-            for (int at = tid; at < rows * D; at += W * 32) {
-                const int i = at / D, col = at % D, w0 = i * pw;
-                if (!there(row0 + i))
-                    continue;
-                top = -INFINITY;
-                for (int w = 0; w < pw; ++w)
-                    top = fmaxf(top, tops[w0 + w]);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float x = 0.f;
-                sum = 0.f;
-                for (int w = 0; w < pw; ++w) {
-                    const float f = ex2_approx(tops[w0 + w] - ref);
-                    sum += f * sums[w0 + w];
-                    x += f * part[w0 + w][col];
-                }
-                const long long at_row = (long long)bh * a.R + job_row + row0 + i;
-                x *= sum == 0.f ? 0.f : (a.cache.v_scale ? a.cache.v_scale[bh % a.Hkv] : 1.f) / sum;
-                if (a.out_bf16)
-                    ((__nv_bfloat16 *)a.out)[at_row * D + col] = __float2bfloat16_rn(x);
-                else
-                    ((float *)a.out)[at_row * D + col] = x;
-                if (col == 0)
-                    a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
         }
+        float m = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(m, ml[u].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float f0 = ex2_approx(top - ref);
+        top = m;
+        sum *= f0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            o[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = ex2_approx(ml[u].x - ref);
+            sum += f * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                o[e] += f * x[u][e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+        part[warp][lane * PER + e] = o[e];
+    if (lane == 0) {
+        tops[warp] = top;
+        sums[warp] = sum;
+    }
+    __syncthreads();
+    for (int at = tid; at < rows * D; at += W * 32) {
+        const int i = at / D, col = at % D, w0 = i * pw;
+        if (!there(row0 + i))
+            continue;
+        top = -INFINITY;
+        for (int w = 0; w < pw; ++w)
+            top = fmaxf(top, tops[w0 + w]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float x = 0.f;
+        sum = 0.f;
+        for (int w = 0; w < pw; ++w) {
+            const float f = ex2_approx(tops[w0 + w] - ref);
+            sum += f * sums[w0 + w];
+            x += f * part[w0 + w][col];
+        }
+        const long long at_row = (long long)bh * a.R + job_row + row0 + i;
+        x *= sum == 0.f ? 0.f : (a.cache.v_scale ? a.cache.v_scale[bh % a.Hkv] : 1.f) / sum;
+        if (a.out_bf16)
+            ((__nv_bfloat16 *)a.out)[at_row * D + col] = __float2bfloat16_rn(x);
+        else
+            ((float *)a.out)[at_row * D + col] = x;
+        if (col == 0)
+            a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -1389,7 +1379,6 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     }
     // a block per SM, and none that could not get a tile
     const unsigned grid = (unsigned)(most < ki.sms ? most : ki.sms);
-    a.records = (int)grid;
     // a job that fits into one tile is never cut: no parts, nothing to join
     const bool split = keys > C::kTile;
     void *ws = nullptr;
