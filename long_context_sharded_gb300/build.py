@@ -24,7 +24,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmercury_attn.so")
-BINDING_PATH = os.path.join(LIB_DIR, "mercury_binding.so")  # the serving calls' CPython extension
+# the serving calls' CPython extension, one for each interpreter's ABI and machine
+BINDING_PATH = os.path.join(LIB_DIR, "mercury_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 CHECK_LIB_DIR = os.path.join(HERE, "_lib_check")
 CHECK_LIB_PATH = os.path.join(CHECK_LIB_DIR, "libmercury_attn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "lse_merge.cu", "noalloc.cu", "gemm_shifted.cu", "schedule.cu",

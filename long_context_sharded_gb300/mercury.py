@@ -169,7 +169,7 @@ def _load_binding():
     import importlib.util
     path = _build.BINDING_PATH
     if not os.path.exists(path):
-        raise ImportError("mercury_binding.so is not built (%s); run long_context_sharded_gb300.build.build() first" % path)
+        raise ImportError("the binding's extension is not built (%s); run long_context_sharded_gb300.build.build() first" % path)
     loader = importlib.machinery.ExtensionFileLoader("mercury_binding", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("mercury_binding", path, loader=loader))
     loader.exec_module(module)

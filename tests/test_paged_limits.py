@@ -6,7 +6,9 @@ Bounds are derived where they are used; a rounding is off by at most half a step
 definitions these tests share.
 """
 import contextlib
+import importlib.util
 import math
+import sysconfig
 import time
 import types
 
@@ -333,3 +335,31 @@ def test_a_long_call_whose_copies_never_come_ends(gm, monkeypatch, dtype, rows, 
         out, lse = gm.mercury_attn_paged(q, cache, lens)
         gm.mercury_sync_status()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# -------------------------------------------------------------------- the C side's build
+
+def test_an_extension_belongs_to_one_interpreter(m, monkeypatch, tmp_path):
+    """One built for another Python, next to this one's and newer than its source, is neither reused nor loaded."""
+    from long_context_sharded_gb300 import build
+
+    def for_abi(suffix):
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: suffix if name == "EXT_SUFFIX" else None)
+        spec = importlib.util.spec_from_file_location("build_for_abi", build.__file__)
+        b = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(b)
+        monkeypatch.undo()
+        return b
+
+    assert m._build.BINDING_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    one, other = for_abi(".cpython-398-a.so"), for_abi(".cpython-399-b.so")
+    for b in (one, other):
+        b.LIB_DIR = str(tmp_path)
+        b.BINDING_PATH = str(tmp_path / b.BINDING_PATH.rsplit("/", 1)[1])
+    with open(one.BINDING_PATH, "w") as f:
+        f.write("another interpreter's")
+    assert one.build_binding() == one.BINDING_PATH  # newer than its source
+    made = other.build_binding()
+    assert made == other.BINDING_PATH != one.BINDING_PATH
+    with open(made, "rb") as f:
+        assert f.read(4) == b"\x7fELF"
