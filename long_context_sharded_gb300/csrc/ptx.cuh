@@ -86,12 +86,6 @@ __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthread
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// Arrive on it without waiting.
-__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t nthreads)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
 // ---------------------------------------------------------------- TMA
 // 3-D tiled bulk tensor load global -> shared, completion counted in bytes
 // on `bar`.  c0 is the innermost coordinate (elements).
