@@ -1480,22 +1480,7 @@ int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cach
 
 int read_and_clear_paged_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)
 {
-    unsigned int zero = 0, w = 0, st = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&w, g_paged_err_word, sizeof w);
-    if (e == cudaSuccess)
-        e = cudaMemcpyFromSymbol(&st, g_paged_err_site, sizeof st);
-    if (e == cudaSuccess && (w || st)) {
-        e = cudaMemcpyToSymbol(g_paged_err_word, &zero, sizeof zero);
-        if (e == cudaSuccess)
-            e = cudaMemcpyToSymbol(g_paged_err_site, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        snprintf(msg, msg_len, "reading the paged attention error word: %s", cudaGetErrorString(e));
-        return MERCURY_ECUDA;
-    }
-    *word = w;
-    *site = st;
-    return MERCURY_OK;
+    return read_and_clear_words(g_paged_err_word, g_paged_err_site, "paged attention", word, site, msg, msg_len);
 }
 
 }  // namespace mercury

@@ -446,22 +446,7 @@ int launch_gemm_shifted(const void *a, const void *b, int M, int N, int K, int R
 
 int read_and_clear_gemm_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)
 {
-    unsigned int zero = 0, w = 0, st = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&w, g_gemm_err_word, sizeof w);
-    if (e == cudaSuccess)
-        e = cudaMemcpyFromSymbol(&st, g_gemm_err_site, sizeof st);
-    if (e == cudaSuccess && (w || st)) {
-        e = cudaMemcpyToSymbol(g_gemm_err_word, &zero, sizeof zero);
-        if (e == cudaSuccess)
-            e = cudaMemcpyToSymbol(g_gemm_err_site, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        snprintf(msg, msg_len, "reading the GEMM error word: %s", cudaGetErrorString(e));
-        return MERCURY_ECUDA;
-    }
-    *word = w;
-    *site = st;
-    return MERCURY_OK;
+    return read_and_clear_words(g_gemm_err_word, g_gemm_err_site, "GEMM", word, site, msg, msg_len);
 }
 
 }  // namespace mercury

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 #include <stddef.h>
+#include <stdio.h>
 
 #include "../../include/mercury_attn.h"
 
@@ -50,6 +51,30 @@ int attn_split_noalloc(const void *q, const void *k, const void *v, int B, int H
 // row block against B's column shards in the order order[i][*].
 int launch_gemm_shifted(const void *a, const void *b, int M, int N, int K, int R, const int *order, float *c,
                         unsigned long long wait_ns, cudaStream_t stream, char *msg, size_t msg_len);
+
+// Read and clear a file's device error word and the site of its first error
+// (no synchronisation).  A kernel sets the word first, so where that is zero
+// there is no site to read: a status with nothing to report costs one small
+// copy a file.
+inline int read_and_clear_words(unsigned int &word_symbol, unsigned int &site_symbol, const char *what, unsigned int *word,
+                                unsigned int *site, char *msg, size_t msg_len)
+{
+    const unsigned int zero = 0;
+    *word = *site = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(word, word_symbol, sizeof zero);
+    if (e == cudaSuccess && *word) {
+        e = cudaMemcpyFromSymbol(site, site_symbol, sizeof zero);
+        if (e == cudaSuccess)
+            e = cudaMemcpyToSymbol(word_symbol, &zero, sizeof zero);
+        if (e == cudaSuccess)
+            e = cudaMemcpyToSymbol(site_symbol, &zero, sizeof zero);
+    }
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "reading the %s error word: %s", what, cudaGetErrorString(e));
+        return MERCURY_ECUDA;
+    }
+    return MERCURY_OK;
+}
 
 // Read and clear the GEMM kernel's device error word (no synchronisation).
 int read_and_clear_gemm_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);

@@ -223,22 +223,7 @@ int launch_kv_append(const void *k, const Strides &ks, const void *v, const Stri
 
 int read_and_clear_append_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)
 {
-    unsigned int zero = 0, w = 0, st = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&w, g_append_err_word, sizeof w);
-    if (e == cudaSuccess)
-        e = cudaMemcpyFromSymbol(&st, g_append_err_site, sizeof st);
-    if (e == cudaSuccess && (w || st)) {
-        e = cudaMemcpyToSymbol(g_append_err_word, &zero, sizeof zero);
-        if (e == cudaSuccess)
-            e = cudaMemcpyToSymbol(g_append_err_site, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        snprintf(msg, msg_len, "reading the append error word: %s", cudaGetErrorString(e));
-        return MERCURY_ECUDA;
-    }
-    *word = w;
-    *site = st;
-    return MERCURY_OK;
+    return read_and_clear_words(g_append_err_word, g_append_err_site, "append", word, site, msg, msg_len);
 }
 
 }  // namespace mercury

@@ -165,22 +165,7 @@ int launch(const float *o_part, const float *lse_part, int n_parts, long long ro
 
 int read_and_clear_merge_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)
 {
-    unsigned int zero = 0, w = 0, st = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&w, g_merge_err_word, sizeof w);
-    if (e == cudaSuccess)
-        e = cudaMemcpyFromSymbol(&st, g_merge_err_site, sizeof st);
-    if (e == cudaSuccess && (w || st)) {
-        e = cudaMemcpyToSymbol(g_merge_err_word, &zero, sizeof zero);
-        if (e == cudaSuccess)
-            e = cudaMemcpyToSymbol(g_merge_err_site, &zero, sizeof zero);
-    }
-    if (e != cudaSuccess) {
-        snprintf(msg, msg_len, "reading the merge error word: %s", cudaGetErrorString(e));
-        return MERCURY_ECUDA;
-    }
-    *word = w;
-    *site = st;
-    return MERCURY_OK;
+    return read_and_clear_words(g_merge_err_word, g_merge_err_site, "merge", word, site, msg, msg_len);
 }
 
 int launch_lse_merge(const float *o_part, const float *lse_part, int n_parts, long long rows, int d,

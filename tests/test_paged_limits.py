@@ -363,3 +363,33 @@ def test_an_extension_belongs_to_one_interpreter(m, monkeypatch, tmp_path):
     assert made == other.BINDING_PATH != one.BINDING_PATH
     with open(made, "rb") as f:
         assert f.read(4) == b"\x7fELF"
+
+
+# ------------------------------------------------------------------------------- reports
+
+@pytest.mark.gpu
+def test_each_report_names_its_own_site(gm):
+    """The status names where the first error since the last report was found, and forgets it."""
+    gen = torch.Generator("cuda").manual_seed(1)
+    k_cache, v_cache, table, _ = make_cache(2, 1, 64, 16, 4, BF16, gen)
+    cache = gm.PagedCache(k_cache, v_cache, table)
+    good = table.clone()
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.zeros(2, 1, 1, 64, dtype=BF16, device="cuda")
+
+    def wrong_page(fn):
+        table[1] = -1
+        fn()
+        table.copy_(good)
+
+    attn = lambda lens, **kw: gm.mercury_attn_paged(q, cache, lens, **kw)  # noqa: E731
+    append = lambda past, **kw: gm.mercury_kv_append(cache, q, q, past, **kw)  # noqa: E731
+    cases = [("0x901", lambda: attn(ints(3, -1))), ("0x902", lambda: attn(ints(3, 4), new_lens=ints(1, 2))),
+             ("0x903", lambda: wrong_page(lambda: attn(ints(3, 4)))), ("0x801", lambda: append(ints(3, 4), new_lens=ints(2, 1))),
+             ("0x802", lambda: append(ints(3, 64))), ("0x803", lambda: wrong_page(lambda: append(ints(3, 4))))]
+    for site, wrong in cases + cases[::-1]:
+        wrong()
+        with pytest.raises(gm.MercuryError, match=site) as e:
+            gm.mercury_sync_status()
+        assert e.value.status == gm.MERCURY_EBOUNDS
+        gm.mercury_sync_status()
