@@ -674,8 +674,9 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * q_strides as in mercury_rope, multiples of 8 elements, q 16-byte aligned.
  * Requirements: as mercury_kv_append for the cache; Hq % Hkv == 0;
  * 1 <= Sq <= 64 (longer prompts are mercury_attn_sharded's).  The first call
- * for a shape class on a device prepares its kernel; make it before any
- * stream capture.
+ * on a device for a cache type, head dim and class of rows a KV head (Hq/Hkv *
+ * Sq up to 8, 16, 32, or more) prepares its kernels and the scratch pool,
+ * whatever its lengths; make it before any stream capture.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
  * or MERCURY_ETIMEOUT when MERCURY_SYNC_CHECK=1.
  */

@@ -1383,16 +1383,23 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         snprintf(msg, msg_len, "paged attention kernel built with %d registers a thread, needs %d", ki.regs, kMinLaunchRegs);
         return MERCURY_ECUDA;
     }
+    // What a call of this shape class with longer sequences needs is made now
+    // too, so that it may be captured.
+    auto *join = attn_paged_join_kernel<D, C::kRows>;
+    KernelInfo ji;
+    rc = prepare_kernel((const void *)join, 0, &ji, msg, msg_len);
+    if (rc != MERCURY_OK)
+        return rc;
+    cudaMemPool_t pool;
+    rc = device_scratch_pool(&pool);
+    if (rc != MERCURY_OK)
+        return rc;
     // a block per SM, and none that could not get a tile
     const unsigned grid = (unsigned)(most < ki.sms ? most : ki.sms);
     // a job that fits into one tile is never cut: no parts, nothing to join
     const bool split = keys > C::kTile;
     void *ws = nullptr;
     if (split) {
-        cudaMemPool_t pool;
-        rc = device_scratch_pool(&pool);
-        if (rc != MERCURY_OK)
-            return rc;
         const size_t rows = (size_t)2 * grid * C::kRows;
         const size_t o_bytes = rows * D * sizeof(float), ml_bytes = rows * sizeof(float2);
         const cudaError_t e = cudaMallocFromPoolAsync(&ws, o_bytes + ml_bytes + grid * sizeof(int4), pool, stream);
@@ -1415,7 +1422,7 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         for (a.join_warps = 4; a.join_warps < kJoinWarps && a.join_warps * kJoinAhead < parts;)
             a.join_warps *= 2;
         const int rows = kJoinWarps / a.join_warps, used = C::kRows < a.R ? C::kRows : a.R;
-        e = launch_chained(attn_paged_join_kernel<D, C::kRows>, dim3(grid, (used + rows - 1) / rows), kJoinWarps * 32, 0,
+        e = launch_chained(join, dim3(grid, (used + rows - 1) / rows), kJoinWarps * 32, 0,
                            stream, a);
     }
     rc = MERCURY_OK;

@@ -8,6 +8,8 @@ definitions these tests share.
 import contextlib
 import importlib.util
 import math
+import subprocess
+import sys
 import sysconfig
 import time
 import types
@@ -15,6 +17,7 @@ import types
 import pytest
 import torch
 
+from tests.conftest import ROOT
 from tests.test_paged import (BF16, E4M3, FP32, assert_within, attention, cache_struct, gather_states,
                               gm, m, make_cache)  # noqa: F401  (gm, m: fixtures)
 
@@ -393,3 +396,41 @@ def test_each_report_names_its_own_site(gm):
             gm.mercury_sync_status()
         assert e.value.status == gm.MERCURY_EBOUNDS
         gm.mercury_sync_status()
+
+
+# -------------------------------------------------------------------------------- captures
+
+FIRST_CAPTURE = """
+import sys
+import torch
+from long_context_sharded_gb300 import mercury as m
+torch.manual_seed(0)
+k, v = (torch.randn(300, 2, 16, 64, device="cuda").bfloat16() for _ in range(2))
+table = torch.arange(300, dtype=torch.int32, device="cuda").view(2, 150)
+q, x = torch.randn(2, 4, 1, 64, device="cuda").bfloat16(), torch.randn(2, 2, 1, 64, device="cuda").bfloat16()
+short, long = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([5, 7], [2000, 2300]))
+out, lse, rot = torch.zeros(2, 4, 1, 64, device="cuda"), torch.zeros(2, 4, 1, device="cuda"), torch.zeros_like(q)
+cache, plan = m.PagedCache(k, v, table), m.mercury_rope_init(64)
+# the only call before: lengths for which nothing is split
+m.mercury_attn_paged(q, m.PagedCache(k, v, table[:, :2].contiguous()), short, out=out, lse=lse)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    m.mercury_rope(q, plan, start=3, out=rot)
+    m.mercury_kv_append(cache, x, x, short, rope=plan)
+    m.mercury_attn_paged(q, cache, long, out=out, lse=lse)
+g.replay()
+m.mercury_sync_status()
+got = [t.clone() for t in (out, lse, rot)]
+m.mercury_rope(q, plan, start=3, out=rot)
+m.mercury_attn_paged(q, cache, long, out=out, lse=lse)
+m.mercury_sync_status()
+assert all(torch.equal(a, b) for a, b in zip(got, (out, lse, rot)))
+"""
+
+
+@pytest.mark.gpu
+def test_a_call_that_split_nothing_prepares_for_one_that_does(gm):
+    """In a process of its own: after one uncaptured call of a shape class any other of it can be captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURE], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
