@@ -621,9 +621,10 @@ typedef struct mercury_paged_cache {
  * and q are not read, those of q_out and every other row of the cache are
  * left as they were.  No two tokens of a call may go to the same row of the
  * same page.
- * A position outside the block table, a page outside the cache or a new_lens
- * outside [0, S] (taken to the nearer end) is skipped and reported as
- * MERCURY_EBOUNDS by mercury_sync_status.
+ * A key or value whose position lies outside the block table or whose page
+ * lies outside the cache is not stored, and it or a new_lens outside [0, S]
+ * (taken to the nearer end) is reported as MERCURY_EBOUNDS by
+ * mercury_sync_status; the token's query is rotated all the same.
  * Requirements: B = cache->B; S >= 1; B * S < 2^31; Hq >= 1 with q; the
  * cache's fields as described, d in {64, 128}, max_pages * page_size <= 2^30,
  * k and v of the cache 16-byte aligned and page_stride a multiple of 16
@@ -652,6 +653,10 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * row does not see do not affect it, whatever they hold; of the cache rows at
  * and after seq_lens[b] nothing is used (the rest of the last page may be
  * read).
+ * A value that is infinite or NaN makes its column of O not finite in every
+ * row that sees it: NaN, where the sum would be an infinity too, since a
+ * weight enters the products as several terms, which may be zero or negative.
+ * Other columns and rows are as without it.
  * Scores and sums are kept in fp32.  A weight exp(x_k - x_max) enters the
  * products as a sum of 16-bit terms: three of bf16, which hold it to 2^-26 of
  * itself, or for an e4m3 cache two of fp16, which hold it to 2^-23 of itself
@@ -673,6 +678,8 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * to the nearer end) is reported as MERCURY_EBOUNDS by mercury_sync_status.
  * q_strides as in mercury_rope, multiples of 8 elements, q 16-byte aligned.
  * Requirements: as mercury_kv_append for the cache; Hq % Hkv == 0;
+ * B * Hkv * ceil(Hq/Hkv * Sq / 64) * (max_pages * page_size / 128 + 3) < 2^28
+ * (what the line of all tiles can count); page_stride below 2^40 bytes;
  * 1 <= Sq <= 64 (longer prompts are mercury_attn_sharded's).  The first call
  * on a device for a cache type, head dim and class of rows a KV head (Hq/Hkv *
  * Sq up to 8, 16, 32, or more) prepares its kernels and the scratch pool,

@@ -6,6 +6,7 @@ Bounds are derived where they are used; a rounding is off by at most half a step
 definitions these tests share.
 """
 import contextlib
+import ctypes
 import importlib.util
 import math
 import subprocess
@@ -434,3 +435,74 @@ def test_a_call_that_split_nothing_prepares_for_one_that_does(gm):
     """In a process of its own: after one uncaptured call of a shape class any other of it can be captured."""
     r = subprocess.run([sys.executable, "-c", FIRST_CAPTURE], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------- what the header says
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Sq", [(2, 1), (8, 1), (32, 1), (16, 4)])
+def test_infinite_values_that_every_row_sees(gm, d, Hq, Sq):
+    """Their columns are not finite in the rows of their head, for single tokens and drafted ones; all else is right."""
+    n, page, Hkv, B = 700, 16, 2, 3
+    gen = torch.Generator("cuda").manual_seed(d + Hq)
+    k_cache, v_cache, table, _ = make_cache(B, Hkv, d, page, -(-n // page), BF16, gen)
+    for i, value in enumerate((math.inf, -math.inf, math.nan)):
+        v_cache[table[i, 7].long(), 1, 5, i + 3] = value
+    q = torch.randn(B, Hq, Sq, d, generator=gen, device="cuda").to(BF16)
+    out, lse = gm.mercury_attn_paged(q, gm.PagedCache(k_cache, v_cache, table),
+                                     torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    gm.mercury_sync_status()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for i in range(B):
+        hit[i, Hq // Hkv:, :, i + 3] = True
+    assert torch.equal(~torch.isfinite(out), hit)
+    for b in range(B):
+        k, v = gather_states(k_cache, None, table[b], n), gather_states(v_cache, None, table[b], n)
+        o, l, eo, el = attention(q[b], k, torch.where(torch.isfinite(v), v, 0.0), [n - Sq + i + 1 for i in range(Sq)])
+        assert_within(out[b][~hit[b]], o[~hit[b]], eo[~hit[b]], "O")
+        assert_within(lse[b], l, el, "LSE")
+
+
+@pytest.mark.gpu
+def test_append_rounds_to_even_in_8_bits(gm):
+    """300 is nearer to 288 than to 320, 304 lies between them and goes to the even one, 320."""
+    k_cache, v_cache, table, _ = make_cache(1, 1, 64, 4, 1, E4M3, torch.Generator("cuda").manual_seed(0))
+    one = torch.ones(1, device="cuda")
+    k = torch.zeros(1, 1, 1, 64, dtype=BF16, device="cuda")
+    x = [1e5, -1e5, math.inf, -math.inf, 300.0, 304.0, -304.0, 272.0, 1e-3, 2.0 ** -10, -2.0 ** -10, 3 * 2.0 ** -10]
+    k[..., :len(x)] = torch.tensor(x, device="cuda").to(BF16)
+    k[..., 63] = math.nan
+    gm.mercury_kv_append(gm.PagedCache(k_cache, v_cache, table, k_scale=one, v_scale=one), k, k,
+                         torch.zeros(1, dtype=torch.int32, device="cuda"))
+    gm.mercury_sync_status()
+    for c in (k_cache, v_cache):
+        row = c.view(torch.uint8)[table[0, 0].long(), 0, 0].view(E4M3).float().tolist()
+        assert row[:len(x)] == [448.0, -448.0, 448.0, -448.0, 288.0, 320.0, -320.0, 256.0, 2.0 ** -9, 0.0, 0.0, 2.0 ** -8]
+        assert math.isnan(row[63])
+
+
+@pytest.mark.gpu
+def test_inputs_are_left_as_they_were(gm):
+    gen = torch.Generator("cuda").manual_seed(2)
+    k_cache, v_cache, table, _ = make_cache(2, 2, 64, 16, 4, BF16, gen)
+    cache, plan = gm.PagedCache(k_cache, v_cache, table), gm.mercury_rope_init(64)
+    q, k, v = (torch.randn(2, h, 3, 64, generator=gen, device="cuda").to(BF16) for h in (4, 2, 2))
+    past, pos = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([3, 20], [[5, 6, 7], [8, 9, 10]]))
+    total = past + 3
+    inputs = (q, k, v, past, pos, total, table)
+    before = [t.clone() for t in inputs]
+    rot = gm.mercury_kv_append(cache, k, v, past, rope=plan, q=q)
+    stored = k_cache.clone(), v_cache.clone()
+    gm.mercury_rope(q, plan, pos, inverse=True)
+    gm.mercury_attn_paged(rot, cache, total)
+    gm.mercury_sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(inputs, before))
+    assert torch.equal(k_cache, stored[0]) and torch.equal(v_cache, stored[1])
+
+
+def test_a_table_of_too_many_tiles_is_refused(m):
+    P = 0x100000
+    c = cache_struct(m, max_pages=1 << 26, table_stride=1 << 26, B=40)
+    assert m.lib.mercury_attn_paged(P, None, ctypes.byref(c), P, None, 40, 4, 1, 1, P, P, None) == m.MERCURY_EINVAL
+    assert b"tiles" in m.lib.mercury_last_error()
