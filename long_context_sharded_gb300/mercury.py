@@ -598,17 +598,16 @@ def _on_current(dev, what):
         raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (what, dev, cur))
 
 
-def _new_output(make, shape, dtype, dev, stream):
-    """A call's own output, made (and filled, where `make` fills) on the stream
+def _new_output(make, shape, dtype, like, dev, stream):
+    """A call's own output beside `like`, made (and filled, where `make` fills) on the stream
     that the call runs on: on the caller's current stream a fill could land
     behind the kernel's rows, and a reused block still be in use.  The tensor
     stays out of reuse until what the caller's stream does with it is done."""
     T = _torch_names
-    device = "cuda:%d" % dev
     if stream is None or _stream_ptr(stream) == T.raw_stream(dev):
-        return make(shape, dtype=dtype, device=device)
-    with T.stream_context(T.external_stream(_stream_ptr(stream), device=device)):
-        t = make(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=like.device)
+    with T.stream_context(T.external_stream(_stream_ptr(stream), device=like.device)):
+        t = make(shape, dtype=dtype, device=like.device)
     t.record_stream(T.current_stream(dev))
     return t
 
@@ -672,7 +671,7 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
         sx = _Strides(sx[0], sx[1], sx[2])
     px = x.data_ptr()
     if out is None:
-        out = _new_output(T.empty, shape, dtype, dev, stream)
+        out = _new_output(T.empty, shape, dtype, x, dev, stream)
         po, so = out.data_ptr(), None
     elif out is x:
         po, so = px, sx
@@ -806,7 +805,7 @@ def mercury_kv_append(cache: PagedCache, k, v, past_lens, new_lens=None, rope=No
         pq = q.data_ptr()
         if q_out is None:
             # rows behind new_lens are not written: zeros rather than whatever was there
-            q_out = _new_output(T.empty if new_lens is None else T.zeros, qshape, bf16, dev, stream)
+            q_out = _new_output(T.empty if new_lens is None else T.zeros, qshape, bf16, q, dev, stream)
             po = q_out.data_ptr()
         elif q_out is q:
             po, so = pq, sq
@@ -849,9 +848,9 @@ def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, s
     # rows behind new_lens are not written: zeros rather than whatever was there
     make = T.empty if new_lens is None else T.zeros
     if out is None:
-        out = _new_output(make, shape, out_dtype, dev, stream)
+        out = _new_output(make, shape, out_dtype, q, dev, stream)
     if lse is None:
-        lse = _new_output(make, (B, Hq, Sq), T.fp32, dev, stream)
+        lse = _new_output(make, (B, Hq, Sq), T.fp32, q, dev, stream)
     rc = fn(q.data_ptr(), sq, cache._ref, _flat(seq_lens, T.int32, dev, (B,), "seq_lens"),
             None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), B, Hq, Sq,
             1 if causal else 0, _flat(out, out_dtype, dev, shape, "out"), _flat(lse, T.fp32, dev, (B, Hq, Sq), "lse"),
