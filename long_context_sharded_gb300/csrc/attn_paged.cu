@@ -25,18 +25,21 @@
 //   * both products run on warp-level matrix instructions: the rows of one KV
 //     head fill 8 to 64 rows of a tile, and the operands come straight from
 //     the copied tile.  P goes in as three bf16 terms (two fp16 ones with 8-bit
-//     keys), which keeps O as near to 64 bits as a 32-bit softmax; with at most
-//     8 rows two of them share an instruction, whose lower half would idle.
+//     keys), and the matrix unit's sums are kept short, which keeps O as near
+//     to 64 bits as a 32-bit softmax; with at most 8 rows two terms share an
+//     instruction, whose lower half would idle.
 //
 // Measured on a GB300, of the measured copy bandwidth (6770 GB/s): 16 sequences
-// of 700 to 32K tokens, 64 query and 8 KV heads of 128: 162 us, 100 %; one
-// sequence of 128K: 81.5 us, 97 %; 8 sequences of 20K to 32K with 16 rows a KV
-// head: 135 us, 95 %; with 28 rows, where the matrix instructions begin to
-// bound it, 161 us, 79 %.  8-bit keys and values, 4 rows: 72 us, 89 %, with 16
-// rows 78 us, bound by the conversions (64 of a warp's 450 instructions a step
-// of 32 keys for each product) and the latency of two warps a quarter of an
-// SM.  One 4K sequence takes 8.3 us, of which the start (lengths, pages, the
-// first tile) is 3.5 and the second kernel 2.
+// of 700 to 32K tokens, 64 query and 8 KV heads of 128: 160 us, 101 %; one
+// sequence of 128K: 81 us, 98 %; 8 sequences of 20K to 32K with 16 rows a KV
+// head: 134 us, 95 %; with 28 rows, where the matrix instructions and the
+// additions of their sums bound it, 176 us, 72 %, with 56 rows 313 us, 41 %.
+// 8-bit keys and values, 4 rows: 72 us, 89 %, bound by the conversions (64 of a
+// warp's 450 instructions a step of 32 keys for each product) and the latency of
+// two warps a quarter of an SM; 16 rows 86 us, 74 %, 28 rows 151 us, 42 %, 56
+// rows 283 us, 23 %, each row group converting for itself.  One 4K sequence
+// takes 8.6 us, of which the start (lengths, pages, the first tile) is 3.5 and
+// the second kernel 2.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -968,8 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_paged_kernel(const __grid_co
                 // element is taken as zero, and made NaN in its column of O in
                 // the rows that see it (their sum of p's terms times an
                 // infinity is one anyway).  In here, not in a second version of
-                // the products, whose registers slowed the first (128K keys:
-                // 83.3 us instead of 81.5; 8-bit, 64 rows: 263 instead of 245).
+                // the products, whose registers slowed the first (128K keys: by
+                // 2 %; 8-bit, 64 rows: by 7).
                 if (edge && a.causal && n_new > 1) {
                     const int r0 = max(seen_by_all - kb, 0), r1 = min(at.keys - kb, KEYS);
                     constexpr int WORDS = ROWB / 4, EACH = FP8 ? 4 : 2, BITS = 32 / EACH;

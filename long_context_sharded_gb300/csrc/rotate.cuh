@@ -93,8 +93,8 @@ __device__ __forceinline__ void store_chunk(float *p, const float (&y)[VE])
 // two sides of that quotient (four roundings of 2^-24 each do not reach 2^-21),
 // so where both round to the same byte it is the quotient's.  Where they do not
 // (next to a tie), or r is zero, infinite or near either, the elements are
-// divided.  (6 x 1000 tokens of 24 heads of 64: 10.5 us with divisions
-// throughout, 8.9 so; 6 x 8000 of 48 heads of 128: 132 and 121.)
+// divided.  (6 x 1000 tokens of 24 heads of 64: 10.6 us with divisions
+// throughout, 8.2 so; 6 x 8000 of 48 heads of 128: 138 and 122.)
 struct Quotient {
     float scale, lo, hi;
     bool divide;
@@ -220,7 +220,7 @@ struct RotUnit {
 // compiler would keep each load behind the stores before it.)  With SCALED,
 // scales[head] goes the same way; two heads at a time then, since with the
 // quantisation's registers four spill (6 x 1000 tokens of 24 heads of 64: 8.2
-// us instead of 10.7; 6 x 8000 of 48 of 128: 122 and 150).  Twice as many of
+// us instead of 10.8; 6 x 8000 of 48 of 128: 122 and 150).  Twice as many of
 // 8-byte chunks, for as many bytes on the way (32K prompt of 40 heads, 24
 // elements rotated: 118 us instead of 134).  FEW: see rot_few.
 template <typename T, int VE, bool TURN, bool SCALED, bool FEW, typename Ready, typename Store>
