@@ -863,7 +863,8 @@ def _attn_paged(fn, out_dtype, q, cache, seq_lens, new_lens, causal, out, lse, s
 def mercury_attn_paged(q, cache: PagedCache, seq_lens, new_lens=None, causal: bool = True, out=None, lse=None,
                        stream=None):
     """Attention of the newest tokens q [B,Hq,Sq,d] bf16 of every sequence over
-    the cache's first seq_lens[b] tokens; returns (out fp32, lse fp32)."""
+    the cache's first seq_lens[b] tokens; returns (out fp32, lse fp32), made on
+    the call's stream where they are not given (rows behind new_lens[b]: 0)."""
     return _attn_paged(lib.mercury_attn_paged, _names().fp32, q, cache, seq_lens, new_lens, causal, out, lse, stream)
 
 
