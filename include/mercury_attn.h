@@ -510,6 +510,7 @@ MERCURY_API void mercury_tune_cache_clear(void);
 #define MERCURY_ELEM_BF16 0
 #define MERCURY_ELEM_E4M3 1
 #define MERCURY_ELEM_FP32 2
+#define MERCURY_ELEM_E2M1 3
 
 /* Frequency scalings of mercury_rope_frequencies. */
 #define MERCURY_ROPE_NONE   0
@@ -586,16 +587,22 @@ MERCURY_API int mercury_rope(const void *x, const long long *x_strides, const in
                              const long long *out_strides, void *stream);
 
 /* A paged cache of keys and values: the caller's device arrays and their
- * sizes.  A plain host struct read during each call. */
+ * sizes.  A plain host struct read during each call.
+ *
+ * A row of an E2M1 cache is d/2 + d/16 bytes: d codes of four bits, two a byte,
+ * the first in the lower half, then an e4m3 scale for each 16 of them.  A
+ * code's lower three bits stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, its fourth for
+ * the sign; an element is code * its 16 elements' scale * its head's.  Its
+ * page_size is a multiple of 8. */
 typedef struct mercury_paged_cache {
-    void *k;                  /* [num_pages][Hkv][page_size][d] */
+    void *k;                  /* [num_pages][Hkv][page_size][d]; E2M1: [num_pages][Hkv][page_size] rows of bytes */
     void *v;                  /* the same */
-    const float *k_scale;     /* [Hkv] fp32, E4M3 only: an element is its byte's value times this */
+    const float *k_scale;     /* [Hkv] fp32, E4M3 and E2M1 only: an element is what its row holds times this */
     const float *v_scale;
     const int *block_table;   /* [B][max_pages] int32 */
-    long long page_stride;    /* elements from page to page, >= Hkv * page_size * d */
+    long long page_stride;    /* elements (E2M1: bytes) from page to page, >= those of a page */
     long long table_stride;   /* elements from row to row of block_table, >= max_pages */
-    int elem;                 /* MERCURY_ELEM_BF16 or MERCURY_ELEM_E4M3 */
+    int elem;                 /* MERCURY_ELEM_BF16, MERCURY_ELEM_E4M3 or MERCURY_ELEM_E2M1 */
     int Hkv;
     int d;
     int page_size;
@@ -612,7 +619,15 @@ typedef struct mercury_paged_cache {
  * where new_lens is NULL), goes to position past_lens[b] + i.  With a rope
  * plan the key is rotated by that position, in fp32, before its one rounding
  * to the cache's type; a plan of NULL stores it as it is.  An E4M3 cache holds
- * x / scale[head] rounded to nearest and saturated at +-448.
+ * x / scale[head] rounded to nearest and saturated at +-448.  For an E2M1 one
+ * each 16 elements' scale is the e4m3 s nearest to their largest magnitude
+ * over 6 scale[head], at most 448, and each code the nearest to x / (s
+ * scale[head]), saturated at +-6, ties to even in both; where s is 0 the codes
+ * are.  These are the nearest to the real quotients of the rotated key, not of
+ * its 32-bit rounding: the products that decide are made exactly, or for a
+ * rotated key to 2^-48.  (Head scales are finite and of magnitudes 2^-60 to
+ * 2^60; other ones give codes that nothing is said about.)  A NaN makes the
+ * scale of its 16 elements NaN; an infinity alone is held as +-6 * 448.
  * q [B, Hq, S, d] bf16 (optional): the queries of the same tokens, rotated
  * likewise into q_out (which may be q itself, with its strides); q NULL means
  * q_out is not touched.
@@ -656,11 +671,12 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * A value that is infinite or NaN makes its column of O not finite in every
  * row that sees it: NaN, where the sum would be an infinity too, since a
  * weight enters the products as several terms, which may be zero or negative.
- * Other columns and rows are as without it.
+ * Other columns and rows are as without it.  (Of an e2m1 cache only a block's
+ * scale can be NaN, which is all 16 columns'.)
  * Scores and sums are kept in fp32.  A weight exp(x_k - x_max) enters the
  * products as a sum of 16-bit terms: three of bf16, which hold it to 2^-26 of
- * itself, or for an e4m3 cache two of fp16, which hold it to 2^-23 of itself
- * or 2^-48 of the row's largest weight, whichever is more.  So O is a 32-bit
+ * itself, or for an e4m3 or e2m1 cache two of fp16, which hold it to 2^-23 of
+ * itself or 2^-48 of the row's largest weight, whichever is more.  So O is a 32-bit
  * result: its error, relative to the weighted mean of |v|, is that of the
  * scores (each a sum of d products in fp32) and of the sums' roundings, which
  * grows with the square root of the keys (32K keys: about 1e-6).
@@ -697,6 +713,86 @@ MERCURY_API int mercury_attn_paged_bf16(const void *q, const long long *q_stride
                                         const mercury_paged_cache *cache, const int *seq_lens,
                                         const int *new_lens, int B, int Hq, int Sq, int causal, void *out,
                                         float *lse, void *stream);
+
+/*
+ * mercury_attn_paged_mass -- the attention weight that each cached key got from
+ * the newest tokens.
+ *
+ * out[b][h][k] = mass[b][h][k] + the sum, over the query heads of KV head h and
+ * the new tokens i < n of sequence b that see key k, of
+ * exp(q.k / sqrt(d) - lse[b][head][i]), for k < seq_lens[b]; other entries of
+ * out are left as they were.  q, q_strides, cache, seq_lens, new_lens, B, Hq,
+ * Sq and causal as in mercury_attn_paged, whose lse [B, Hq, Sq] this takes; a
+ * row whose lse is infinite gives nothing.
+ * mass, out [B, Hkv, width] fp32, contiguous; mass NULL: zeros; out may be
+ * mass.  Weights are computed and added in fp32, a key's in a fixed order, so
+ * that results do not change between calls.
+ * A seq_lens that exceeds width is taken as width and reported, and so are
+ * lengths and pages out of range, as in mercury_attn_paged.
+ * Requirements: as mercury_attn_paged (but for the number of tiles); width >= 1.
+ * More than 512 rows a KV head (Hq/Hkv * Sq) read the keys once for each 512.
+ * The first call on a device for a cache type and head dim prepares its kernel;
+ * make it before any stream capture.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
+ * when MERCURY_SYNC_CHECK=1.
+ */
+MERCURY_API int mercury_attn_paged_mass(const void *q, const long long *q_strides, const mercury_paged_cache *cache,
+                                        const int *seq_lens, const int *new_lens, int B, int Hq, int Sq, int causal,
+                                        const float *lse, const float *mass, float *out, long long width,
+                                        void *stream);
+
+/*
+ * mercury_kv_evict -- the tokens of every sequence that matter most into a
+ * shorter cache.
+ *
+ * Of the n = seq_lens[b] tokens of sequence b each KV head keeps m = min(n,
+ * keep): where n <= keep all, else the first `first`, the last `last`, and of
+ * the others those with the most of mass[b][h][:], of two with the same the
+ * earlier (a NaN counts as less than every number).  They keep their order:
+ * token j < m of the shorter cache `into` is token kept[b][h][j] of `cache`, its
+ * row copied as it is, and out_mass[b][h][j] (where out_mass is given) its
+ * mass.  out_lens[b] = m.  Everything else of into, kept [B, Hkv, keep] and
+ * out_mass [B, Hkv, out_width] is left as it was.
+ * The heads of a sequence keep different tokens, so a token's place is no
+ * longer its position: queries and keys are rotated by positions that the
+ * caller counts on (a key's was stored with it), and of the shorter cache's
+ * tokens mercury_attn_paged's causal order holds, since it is kept.
+ * mass [B, Hkv, width] fp32, contiguous, as mercury_attn_paged_mass gives it.
+ * into: pages of its own for each sequence, of any page size, none of them
+ * among cache's pages of any sequence (the two structs may name the same
+ * arrays); the same elem, Hkv, d, B and head scales.
+ * A seq_lens outside the block table or above width is taken to the nearer end,
+ * a page outside cache counts as rows of zeros, a row whose page lies outside
+ * into is not stored; each is reported as MERCURY_EBOUNDS.
+ * Requirements: the caches as in mercury_kv_append; 1 <= keep <= what into's
+ * table holds; first + last <= keep; out_width >= keep; out_lens and out_mass
+ * are not seq_lens and mass.  The first call on a device for a cache type and
+ * head dim loads its kernels; make it before any stream capture.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
+ * when MERCURY_SYNC_CHECK=1.
+ */
+MERCURY_API int mercury_kv_evict(const mercury_paged_cache *cache, const mercury_paged_cache *into,
+                                 const float *mass, long long width, const int *seq_lens, int B, int keep, int first,
+                                 int last, int *out_lens, int *kept, float *out_mass, long long out_width,
+                                 void *stream);
+
+/*
+ * mercury_kv_read -- a cache's keys and values as dense bf16 tensors, for
+ * mercury_attn_sharded of a prompt's chunk behind what is cached.
+ *
+ * k_out, v_out [B, Hkv, S, d] bf16, contiguous, 16-byte aligned: token i <
+ * seq_lens[b] of every sequence, its value (with the scales, in fp32) rounded
+ * once; rows i >= seq_lens[b] are left as they were.
+ * A seq_lens outside the block table or above S is taken to the nearer end, a
+ * page outside the cache counts as zeros; both are reported as MERCURY_EBOUNDS.
+ * Requirements: the cache as in mercury_kv_append; S >= 1.  The first call on a
+ * device for a cache type and head dim loads its kernel; make it before any
+ * stream capture.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
+ * when MERCURY_SYNC_CHECK=1.
+ */
+MERCURY_API int mercury_kv_read(const mercury_paged_cache *cache, const int *seq_lens, int B, int S, void *k_out,
+                                void *v_out, void *stream);
 
 #ifdef __cplusplus
 }

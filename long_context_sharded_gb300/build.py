@@ -29,7 +29,7 @@ BINDING_PATH = os.path.join(LIB_DIR, "mercury_binding" + (sysconfig.get_config_v
 CHECK_LIB_DIR = os.path.join(HERE, "_lib_check")
 CHECK_LIB_PATH = os.path.join(CHECK_LIB_DIR, "libmercury_attn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "lse_merge.cu", "noalloc.cu", "gemm_shifted.cu", "schedule.cu",
-           "paged_api.cu", "rope.cu", "kv_append.cu", "attn_paged.cu"]
+           "paged_api.cu", "rope.cu", "kv_append.cu", "attn_paged.cu", "attn_paged4.cu", "attn_mass.cu", "kv_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

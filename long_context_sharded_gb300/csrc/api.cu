@@ -138,7 +138,7 @@ int check_attn_args(const void *q, const void *k, const void *v, int B, int Hq, 
 // found by the checked build, or by the paged kernels in any build).
 int collect_device_errors(cudaStream_t stream)
 {
-    constexpr int n = 5;
+    constexpr int n = 8;
     unsigned int w[n] = {}, site[n] = {};
     int rc = read_and_clear_device_error(stream, &w[0], &site[0], g_msg, sizeof g_msg);
     if (rc == MERCURY_OK)
@@ -149,6 +149,12 @@ int collect_device_errors(cudaStream_t stream)
         rc = read_and_clear_append_error(&w[3], &site[3], g_msg, sizeof g_msg);
     if (rc == MERCURY_OK)
         rc = read_and_clear_paged_error(&w[4], &site[4], g_msg, sizeof g_msg);
+    if (rc == MERCURY_OK)
+        rc = read_and_clear_paged4_error(&w[5], &site[5], g_msg, sizeof g_msg);
+    if (rc == MERCURY_OK)
+        rc = read_and_clear_mass_error(&w[6], &site[6], g_msg, sizeof g_msg);
+    if (rc == MERCURY_OK)
+        rc = read_and_clear_evict_error(&w[7], &site[7], g_msg, sizeof g_msg);
     if (rc != MERCURY_OK)
         return rc;
     for (int i = 3; i < n; ++i)

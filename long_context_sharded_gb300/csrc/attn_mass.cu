@@ -1,0 +1,430 @@
+// attn_mass.cu -- the attention weight that every cached key got from the
+// newest tokens of its sequence.
+//
+// out[b][h][k] = mass[b][h][k] + sum over the rows r of KV head h (its query
+// heads' new tokens) of exp(q_r.k / sqrt(d) - lse_r), over the rows that see
+// key k; lse_r is what attention gave.
+//
+// Each key is read once, values not at all.  A key belongs to one warp, which
+// adds its rows in a fixed order: no atomics, the same bits in every run.  Keys
+// are the matrix instructions' first operand (16 rows), straight from memory
+// into registers: the order of elements within a product's inner axis is free,
+// so a lane takes whole 16-byte (8- or 4-byte) runs of two keys, and the
+// queries, held in shared memory as operands, in the same order.  All rows of
+// the head go over the registers that hold 16 keys, so many rows cost no
+// further reads, and an 8- or 4-bit key is widened once.  All tiles of all
+// heads, in order, are dealt to the blocks in equal contiguous shares, counted
+// on the device from seq_lens.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "paged_split.cuh"
+#include "ptx.cuh"
+
+namespace mercury {
+
+namespace {
+
+constexpr int kMassWarps = 8;
+constexpr int kMassThreads = kMassWarps * 32;
+constexpr int kMassTile = kMassWarps * 16;  // keys of a block's tile
+constexpr int kMassRows = 512;              // rows of a launch
+
+struct MassArgs {
+    PagedArgs p;        // q, qs, cache, seq_lens, new_lens, B, Hkv, G, Sq, R, causal
+    const float *lse;   // [B][Hkv][R]
+    const float *mass;  // [B][Hkv][width], or none
+    float *out;         // the same
+    long long width;
+    int r0, rows;       // this launch's rows of each head
+    float mul, mul_lo;  // log2(e) / sqrt(d)
+};
+
+// A row of queries: factor on its scores (its second part: what rounding left
+// out), -lse in log2 units (-inf: counts nothing) likewise.
+struct Row {
+    float mul, mul_lo, nl, nl_lo;
+};
+
+// 16 keys as the first operand: rows g and g + 8.
+template <int ELEM, int D>
+struct Keys;
+
+template <int D>
+struct Keys<MERCURY_ELEM_BF16, D> {
+    static constexpr int kRun = 8;  // elements of a lane's run
+    static constexpr bool kF16 = false;
+    static constexpr int kRowB = 2 * D;
+    uint4 w[2][D / 32];
+    __device__ __forceinline__ void load(int i, const char *row, int t)
+    {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+            w[i][j] = row ? __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16)) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[2 * j][i] = w[i][j].x;
+                f[2 * j][2 + i] = w[i][j].y;
+                f[2 * j + 1][i] = w[i][j].z;
+                f[2 * j + 1][2 + i] = w[i][j].w;
+            }
+    }
+};
+
+template <int D>
+struct Keys<MERCURY_ELEM_E4M3, D> {
+    static constexpr int kRun = 16;
+    static constexpr bool kF16 = true;
+    static constexpr int kRowB = D;
+    uint4 w[2][D / 64];
+    __device__ __forceinline__ void load(int i, const char *row, int t)
+    {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            w[i][j] = row ? __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16)) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t x[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[4 * j + k][i] = e4m3_to_f16(x[k]);
+                    f[4 * j + k][2 + i] = e4m3_to_f16(x[k] >> 16);
+                }
+            }
+    }
+};
+
+template <int D>
+struct Keys<MERCURY_ELEM_E2M1, D> {
+    static constexpr int kRun = D / 8;
+    static constexpr bool kF16 = true;
+    static constexpr int kRowB = D / 2 + D / 16;
+    uint32_t w[2][2][D / 64], s[2][2];  // [key][run]
+    __device__ __forceinline__ void load(int i, const char *row, int t)
+    {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (D == 128) {
+                const uint2 x = row ? *reinterpret_cast<const uint2 *>(row + j * 32 + t * 8) : make_uint2(0, 0);
+                w[i][j][0] = x.x;
+                w[i][j][1] = x.y;
+            } else {
+                w[i][j][0] = row ? *reinterpret_cast<const uint32_t *>(row + j * 16 + t * 4) : 0u;
+            }
+            s[i][j] = row ? *reinterpret_cast<const uint8_t *>(row + D / 2 + j * (D / 32) + t * (D / 8) / 16) : 0u;
+        }
+    }
+    __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t scale = e4m3_to_f16(s[i][j] | s[i][j] << 8);
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t x = w[i][j][k] >> (16 * n);
+                        uint32_t lo, hi;
+                        asm("{\n\t.reg .b8 x, y;\n\tmov.b16 {x, y}, %2;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t"
+                            "cvt.rn.f16x2.e2m1x2 %1, y;\n\tmul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+                            : "=&r"(lo), "=&r"(hi)
+                            : "h"((uint16_t)x), "r"(scale));
+                        const int kk = j * (D / 32) + 2 * k + n;
+                        f[kk][i] = lo;
+                        f[kk][2 + i] = hi;
+                    }
+            }
+    }
+};
+
+// Tiles of sequence b.
+__device__ __forceinline__ int mass_keys(const MassArgs &a, int b)
+{
+    return (int)min((long long)keys_of(a.p, b), a.width);
+}
+
+__device__ __forceinline__ int mass_tiles(const MassArgs &a, int b)
+{
+    return (mass_keys(a, b) + kMassTile - 1) / kMassTile;
+}
+
+// Where a share's first tile lies.
+struct Spot {
+    int b, h, j;      // sequence, head, tile
+    int keys, tiles;  // of the sequence
+};
+
+template <int ELEM, int D>
+__global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid_constant__ MassArgs a)
+{
+    using K = Keys<ELEM, D>;
+    constexpr int KK = D / 16, RUN = K::kRun;
+    extern __shared__ __align__(16) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int n_rt = (a.rows + 7) / 8;
+    uint2 *const qs = reinterpret_cast<uint2 *>(smem);                       // [row tile][k-step][lane]
+    Row *const rows = reinterpret_cast<Row *>(smem + n_rt * KK * 32 * 8);    // [row]
+    const PagedArgs &p = a.p;
+    const PagedView &c = p.cache;
+    chain_wait();
+    if (blockIdx.x == 0 && a.r0 == 0)
+        for (int b = tid; b < p.B; b += kMassThreads) {
+            if (p.seq_lens[b] != mass_keys(a, b))
+                record_bounds(0xb01);
+            if (p.new_lens && p.new_lens[b] != new_of(p, b))
+                record_bounds(0xb02);
+        }
+    // the tiles of all heads in order, in equal shares
+    long long total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        total += __reduce_add_sync(0xffffffffu, b < p.B ? mass_tiles(a, b) : 0);
+    }
+    total *= p.Hkv;
+    long long at = total * blockIdx.x / gridDim.x;
+    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    if (at >= end)
+        return;
+    Spot s = {0, 0, 0, 0, 0};
+    long long base = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int b = b0 + lane;
+        const int mine = b < p.B ? mass_tiles(a, b) : 0;
+        const int incl = warp_scan(mine, lane);
+        const unsigned in = __ballot_sync(0xffffffffu, (base + incl) * p.Hkv > at);
+        if (in) {
+            const int l = __ffs(in) - 1;
+            s.b = b0 + l;
+            base += __shfl_sync(0xffffffffu, incl - mine, l);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    s.keys = mass_keys(a, s.b);
+    s.tiles = mass_tiles(a, s.b);
+    s.h = (int)((at - base * p.Hkv) / s.tiles);
+    s.j = (int)(at - base * p.Hkv - (long long)s.h * s.tiles);
+
+    auto next_of = [&](Spot x) {
+        if (++x.j == x.tiles) {
+            x.j = 0;
+            if (++x.h == p.Hkv) {
+                x.h = 0;
+                do {
+                    ++x.b;  // there is one: the tile lies before the share's end
+                    x.keys = mass_keys(a, x.b);
+                    x.tiles = mass_tiles(a, x.b);
+                } while (x.tiles == 0);
+            }
+        }
+        return x;
+    };
+    K keys;
+    float prev = 0.f;  // of key g (t = 0) or g + 8 (t = 1)
+    auto load = [&](const Spot &x) {
+        const int k0 = x.j * kMassTile + warp * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = k0 + g + 8 * i;
+            const char *row = nullptr;
+            if (key < x.keys) {
+                const int pg = page_of(c, key), page = c.table[x.b * c.table_stride + pg];
+                if (page >= 0 && page < c.num_pages)
+                    row = c.k + page * c.page_stride * (ELEM == MERCURY_ELEM_BF16 ? 2 : 1) +
+                          ((long long)x.h * c.page_size + key - pg * c.page_size) * K::kRowB;
+                else
+                    record_bounds(0xb03);  // such keys count as zeros
+            }
+            keys.load(i, row, t);
+        }
+        const int key = k0 + g + 8 * t;
+        prev = 0.f;
+        if (a.mass && t < 2 && key < x.keys)
+            prev = a.mass[((long long)x.b * p.Hkv + x.h) * a.width + key];
+    };
+    load(s);
+    int job = -1;
+    for (;;) {
+        const Spot now = s;
+        const int n_new = new_of(p, now.b);
+        const int this_job = now.b * p.Hkv + now.h;
+        uint32_t f[KK][4];
+        keys.widen(f);
+        const float was = prev;
+        const bool on = ++at < end;
+        if (on) {
+            s = next_of(now);
+            load(s);  // on its way while this tile is computed
+        }
+        if (this_job != job) {
+            // this head's queries
+            job = this_job;
+            __syncthreads();
+            float ks = 1.f;
+            if (K::kF16)
+                ks = c.k_scale[now.h];
+            for (int rt = warp; rt < n_rt; rt += kMassWarps) {
+                const int r = a.r0 + rt * 8 + g;
+                const int head = p.Sq == 1 ? r : r / p.Sq, i = r - head * p.Sq;
+                const bool live = rt * 8 + g < a.rows && i < n_new;
+                const __nv_bfloat16 *src = p.q + now.b * p.qs.b + (now.h * p.G + head) * p.qs.h + i * p.qs.s;
+                uint2 q[KK];
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+                    q[kk] = live ? *reinterpret_cast<const uint2 *>(src + kk / (RUN / 4) * (4 * RUN) + t * RUN +
+                                                                    kk % (RUN / 4) * 4)
+                                 : make_uint2(0, 0);
+                float mul = a.mul, mul_lo = a.mul_lo;
+                if constexpr (K::kF16) {
+                    // to fp16, scaled by a power of two that brings the row's
+                    // largest element to [2^14, 2^15): exact down to 2^-28 of it
+                    float top = 0.f;
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk)
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(q[kk].x)), fabsf(bf16_hi(q[kk].x))),
+                                               fmaxf(fabsf(bf16_lo(q[kk].y)), fabsf(bf16_hi(q[kk].y)))));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+                    up = min(max(up, -110), 110);
+                    const float to = __uint_as_float((uint32_t)(127 + up) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        q[kk].x = pack_f16(bf16_lo(q[kk].x) * to, bf16_hi(q[kk].x) * to);
+                        q[kk].y = pack_f16(bf16_lo(q[kk].y) * to, bf16_hi(q[kk].y) * to);
+                    }
+                    const float hi = a.mul * ks;
+                    mul_lo = (fmaf(a.mul, ks, -hi) + a.mul_lo * ks) * back;
+                    mul = hi * back;
+                }
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+                    qs[(rt * KK + kk) * 32 + lane] = q[kk];
+                if (t == 0) {
+                    // lse times log2(e), in two parts: their rounding would be that
+                    // of the whole exponent
+                    constexpr float kLog2eLo = 1.9259629911266174e-8f;  // log2(e) less its nearest float
+                    const float l = live ? a.lse[(long long)this_job * p.R + r] : INFINITY;
+                    const float hi = -l * kLog2e;
+                    rows[rt * 8 + g] = Row{mul, mul_lo, hi, fabsf(l) < INFINITY ? fmaf(-l, kLog2e, -hi) - l * kLog2eLo : 0.f};
+                }
+            }
+            __syncthreads();
+        }
+        const int k0 = now.j * kMassTile + warp * 16;
+        const int seen_by_all = p.causal ? now.keys - n_new + 1 : now.keys;
+        const bool edge = k0 + 16 > seen_by_all;
+        float sum[2] = {0.f, 0.f};
+        if (k0 < now.keys)
+#pragma unroll 2
+            for (int rt = 0; rt < n_rt; ++rt) {
+                // in 2 sums of d/2 products each, added at the end
+                float x[2][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const uint2 q = qs[(rt * KK + kk) * 32 + lane];
+                    mma<K::kF16>(x[kk & 1], f[kk][0], f[kk][1], f[kk][2], f[kk][3], q.x, q.y);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Row r = rows[rt * 8 + 2 * t + e];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float y = x[0][2 * i + e] + x[1][2 * i + e];
+                        float w = ex2_approx(fmaf(y, r.mul, r.nl) + fmaf(y, r.mul_lo, r.nl_lo));
+                        if (edge) {
+                            const int row = a.r0 + rt * 8 + 2 * t + e;
+                            const int lim = p.causal ? now.keys - n_new + row % p.Sq + 1 : now.keys;
+                            w = k0 + g + 8 * i < lim ? w : 0.f;
+                        }
+                        sum[i] += r.nl == -INFINITY ? 0.f : w;
+                    }
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        }
+        const int key = k0 + g + 8 * t;
+        if (t < 2 && key < now.keys)
+            a.out[(long long)this_job * a.width + key] = was + (t ? sum[1] : sum[0]);
+        if (!on)
+            break;
+    }
+}
+
+template <int ELEM, int D>
+int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    auto *kernel = attn_mass_kernel<ELEM, D>;
+    constexpr int kRowSmem = D / 16 * 4 * 8 + (int)sizeof(Row);
+    KernelInfo ki;
+    int rc = prepare_kernel((const void *)kernel, kMassRows * kRowSmem, &ki, msg, msg_len);
+    if (rc != MERCURY_OK)
+        return rc;
+    const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
+    const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
+    for (a.r0 = 0; a.r0 < a.p.R; a.r0 += kMassRows) {
+        a.rows = a.p.R - a.r0 < kMassRows ? a.p.R - a.r0 : kMassRows;
+        const int smem = (a.rows + 7) / 8 * 8 * kRowSmem;
+        const int per_sm = smem <= 100000 ? 2 : 1;
+        const long long grid = most < (long long)ki.sms * per_sm ? most : (long long)ki.sms * per_sm;
+        const cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), kMassThreads, smem, stream, a);
+        if (e != cudaSuccess) {
+            snprintf(msg, msg_len, "attention weight launch: %s", cudaGetErrorString(e));
+            return MERCURY_ECUDA;
+        }
+        a.mass = a.out;  // further rows are added to what the first ones gave
+    }
+    return MERCURY_OK;
+}
+
+template <int D>
+int launch_elem(MassArgs &a, int elem, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    return elem == MERCURY_ELEM_BF16   ? launch<MERCURY_ELEM_BF16, D>(a, stream, msg, msg_len)
+           : elem == MERCURY_ELEM_E4M3 ? launch<MERCURY_ELEM_E4M3, D>(a, stream, msg, msg_len)
+                                       : launch<MERCURY_ELEM_E2M1, D>(a, stream, msg, msg_len);
+}
+
+}  // namespace
+
+int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
+                     const int *new_lens, int B, int Hq, int Sq, int causal, const float *lse, const float *mass,
+                     float *out, long long width, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    MassArgs a = {};
+    a.p = paged_args(q, qs, cache, seq_lens, new_lens, B, Hq, Sq, causal, nullptr, nullptr, 0, 0, 0);
+    a.lse = lse;
+    a.mass = mass;
+    a.out = out;
+    a.width = width;
+    const double mul = 1.4426950408889634074 / sqrt((double)cache.d);
+    a.mul = (float)mul;
+    a.mul_lo = (float)(mul - (double)a.mul);
+    return cache.d == 128 ? launch_elem<128>(a, cache.elem, stream, msg, msg_len)
+                          : launch_elem<64>(a, cache.elem, stream, msg, msg_len);
+}
+
+int read_and_clear_mass_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len)
+{
+    return read_and_clear_words(g_paged_err_word, g_paged_err_site, "attention weight", word, site, msg, msg_len);
+}
+
+}  // namespace mercury

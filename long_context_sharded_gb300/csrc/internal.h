@@ -123,7 +123,27 @@ int launch_attn_paged(const void *q, const Strides &qs, const mercury_paged_cach
                       const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
                       unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg, size_t msg_len);
 
+// The same over a 4-bit cache (attn_paged4.cu).
+int launch_attn_paged4(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
+                       const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
+                       unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg, size_t msg_len);
+
+// The attention weight of every cached key (attn_mass.cu).
+int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
+                     const int *new_lens, int B, int Hq, int Sq, int causal, const float *lse, const float *mass,
+                     float *out, long long width, cudaStream_t stream, char *msg, size_t msg_len);
+
+// A cache's heaviest tokens into a shorter one; a cache read back (kv_evict.cu).
+int launch_kv_evict(const mercury_paged_cache &cache, const mercury_paged_cache &into, const float *mass, long long width,
+                    const int *seq_lens, int keep, int first, int last, int *out_lens, int *kept, float *out_mass,
+                    long long out_width, cudaStream_t stream, char *msg, size_t msg_len);
+int launch_kv_read(const mercury_paged_cache &cache, const int *seq_lens, int S, void *k, void *v, cudaStream_t stream,
+                   char *msg, size_t msg_len);
+
 // Read and clear those kernels' device error words (no synchronisation).
+int read_and_clear_paged4_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
+int read_and_clear_mass_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
+int read_and_clear_evict_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
 int read_and_clear_append_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
 int read_and_clear_paged_error(unsigned int *word, unsigned int *site, char *msg, size_t msg_len);
 

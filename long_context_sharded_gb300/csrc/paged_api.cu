@@ -86,10 +86,10 @@ int check_cache(const mercury_paged_cache *c, int B)
         return set_error(MERCURY_EINVAL, "cache is NULL");
     if (!c->k || !c->v || !c->block_table)
         return set_error(MERCURY_EINVAL, "cache: null pointer");
-    if (c->elem != MERCURY_ELEM_BF16 && c->elem != MERCURY_ELEM_E4M3)
-        return set_error(MERCURY_EINVAL, "cache: elem must be BF16 or E4M3 (got %d)", c->elem);
-    if (c->elem == MERCURY_ELEM_E4M3 && (!c->k_scale || !c->v_scale))
-        return set_error(MERCURY_EINVAL, "cache: an E4M3 cache needs k_scale and v_scale");
+    if (c->elem != MERCURY_ELEM_BF16 && c->elem != MERCURY_ELEM_E4M3 && c->elem != MERCURY_ELEM_E2M1)
+        return set_error(MERCURY_EINVAL, "cache: elem must be BF16, E4M3 or E2M1 (got %d)", c->elem);
+    if (c->elem != MERCURY_ELEM_BF16 && (!c->k_scale || !c->v_scale))
+        return set_error(MERCURY_EINVAL, "cache: an E4M3 or E2M1 cache needs k_scale and v_scale");
     if (c->d != 64 && c->d != 128)
         return set_error(MERCURY_EINVAL, "head dim must be 64 or 128 (got %d)", c->d);
     if (c->Hkv < 1 || c->page_size < 1 || c->num_pages < 1 || c->max_pages < 1 || c->B < 1)
@@ -101,14 +101,18 @@ int check_cache(const mercury_paged_cache *c, int B)
     if ((long long)c->max_pages * c->page_size > (1LL << 30))
         return set_error(MERCURY_EINVAL, "max_pages * page_size must be at most 2^30 (got %lld)",
                          (long long)c->max_pages * c->page_size);
-    if ((double)c->Hkv * c->page_size * c->d > 4.6e18 || c->page_stride < (long long)c->Hkv * c->page_size * c->d ||
+    // of a row: elements, or an E2M1 cache's bytes
+    const int row = c->elem == MERCURY_ELEM_E2M1 ? c->d / 2 + c->d / 16 : c->d;
+    if (c->elem == MERCURY_ELEM_E2M1 && c->page_size % 8 != 0)
+        return set_error(MERCURY_EINVAL, "cache: an E2M1 cache's page_size must be a multiple of 8 (got %d)", c->page_size);
+    if ((double)c->Hkv * c->page_size * row > 4.6e18 || c->page_stride < (long long)c->Hkv * c->page_size * row ||
         (double)c->page_stride * c->num_pages > 2.3e18)
         return set_error(MERCURY_EINVAL, "cache: page_stride %lld is less than a page, or sizes overflow",
                          c->page_stride);
     if (c->table_stride < c->max_pages)
         return set_error(MERCURY_EINVAL, "cache: table_stride (%lld) is less than max_pages (%d)", c->table_stride,
                          c->max_pages);
-    const int es = c->elem == MERCURY_ELEM_E4M3 ? 1 : 2;
+    const int es = c->elem == MERCURY_ELEM_BF16 ? 2 : 1;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride * es % 16 != 0)
         return set_error(MERCURY_EALIGN, "cache: k and v must be 16-byte aligned and pages multiples of 16 bytes apart");
     if (!aligned(c->block_table, 4) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
@@ -116,12 +120,10 @@ int check_cache(const mercury_paged_cache *c, int B)
     return MERCURY_OK;
 }
 
-int attn_paged(const void *q, const long long *q_strides, const mercury_paged_cache *cache, const int *seq_lens,
-               const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
-               void *stream)
+// What every call over a cache with queries [B, Hq, Sq, d] asks of them.
+int check_queries(const void *q, const long long *q_strides, const mercury_paged_cache *cache, const int *seq_lens,
+                  const int *new_lens, int B, int Hq, int Sq, Strides *qs)
 {
-    if (!q || !seq_lens || !out || !lse)
-        return set_error(MERCURY_EINVAL, "null pointer argument");
     int rc = check_cache(cache, B);
     if (rc)
         return rc;
@@ -132,23 +134,38 @@ int attn_paged(const void *q, const long long *q_strides, const mercury_paged_ca
                          Sq);
     if ((double)B * Hq * Sq > (double)INT_MAX)
         return set_error(MERCURY_EINVAL, "B*Hq*Sq exceeds 2^31");
-    Strides qs;
-    rc = read_strides(q_strides, Hq, Sq, cache->d, "q", &qs);
+    rc = read_strides(q_strides, Hq, Sq, cache->d, "q", qs);
     if (rc == MERCURY_OK)
-        rc = check_extent(qs, B, Hq, Sq, "q");
+        rc = check_extent(*qs, B, Hq, Sq, "q");
     if (rc)
         return rc;
-    if (!aligned(q, 16) || qs.b % 8 != 0 || qs.h % 8 != 0 || qs.s % 8 != 0)
+    if (!aligned(q, 16) || qs->b % 8 != 0 || qs->h % 8 != 0 || qs->s % 8 != 0)
         return set_error(MERCURY_EALIGN, "q must be 16-byte aligned, with strides of multiples of 8 elements");
+    if (!aligned(seq_lens, 4) || !aligned(new_lens, 4))
+        return set_error(MERCURY_EALIGN, "seq_lens and new_lens must be 4-byte aligned");
+    return MERCURY_OK;
+}
+
+int attn_paged(const void *q, const long long *q_strides, const mercury_paged_cache *cache, const int *seq_lens,
+               const int *new_lens, int B, int Hq, int Sq, int causal, void *out, float *lse, int out_bf16,
+               void *stream)
+{
+    if (!q || !seq_lens || !out || !lse)
+        return set_error(MERCURY_EINVAL, "null pointer argument");
+    Strides qs;
+    int rc = check_queries(q, q_strides, cache, seq_lens, new_lens, B, Hq, Sq, &qs);
+    if (rc)
+        return rc;
     if (!aligned(out, 16))
         return set_error(MERCURY_EALIGN, "out must be 16-byte aligned");
-    if (!aligned(lse, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4))
-        return set_error(MERCURY_EALIGN, "lse, seq_lens and new_lens must be 4-byte aligned");
+    if (!aligned(lse, 4))
+        return set_error(MERCURY_EALIGN, "lse must be 4-byte aligned");
     size_t len;
     char *msg = error_buffer(&len);
     cudaStream_t s = (cudaStream_t)stream;
-    rc = launch_attn_paged(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, out, lse, out_bf16,
-                           device_wait_ns(), paged_fault(), s, msg, len);
+    auto *launch = cache->elem == MERCURY_ELEM_E2M1 ? launch_attn_paged4 : launch_attn_paged;
+    rc = launch(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, out, lse, out_bf16, device_wait_ns(),
+                paged_fault(), s, msg, len);
     return finish_call(rc, s);
 }
 
@@ -332,6 +349,87 @@ int mercury_attn_paged_bf16(const void *q, const long long *q_strides, const mer
 {
     CallRange range(__func__);
     return attn_paged(q, q_strides, cache, seq_lens, new_lens, B, Hq, Sq, causal, out, lse, 1, stream);
+}
+
+int mercury_attn_paged_mass(const void *q, const long long *q_strides, const mercury_paged_cache *cache,
+                            const int *seq_lens, const int *new_lens, int B, int Hq, int Sq, int causal,
+                            const float *lse, const float *mass, float *out, long long width, void *stream)
+{
+    CallRange range(__func__);
+    if (!q || !seq_lens || !lse || !out)
+        return set_error(MERCURY_EINVAL, "null pointer argument");
+    Strides qs;
+    int rc = check_queries(q, q_strides, cache, seq_lens, new_lens, B, Hq, Sq, &qs);
+    if (rc)
+        return rc;
+    if (width < 1 || (double)width * B * cache->Hkv > 4.6e18)
+        return set_error(MERCURY_EINVAL, "width must be >= 1, and B * Hkv * width below 2^62 (got %lld)", width);
+    if (!aligned(lse, 4) || !aligned(mass, 4) || !aligned(out, 4))
+        return set_error(MERCURY_EALIGN, "lse, mass and out must be 4-byte aligned");
+    size_t len;
+    char *msg = error_buffer(&len);
+    cudaStream_t s = (cudaStream_t)stream;
+    rc = launch_attn_mass(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, lse, mass, out, width, s, msg, len);
+    return finish_call(rc, s);
+}
+
+int mercury_kv_evict(const mercury_paged_cache *cache, const mercury_paged_cache *into, const float *mass,
+                     long long width, const int *seq_lens, int B, int keep, int first, int last, int *out_lens,
+                     int *kept, float *out_mass, long long out_width, void *stream)
+{
+    CallRange range(__func__);
+    if (!mass || !seq_lens || !out_lens || !kept)
+        return set_error(MERCURY_EINVAL, "null pointer argument");
+    int rc = check_cache(cache, B);
+    if (rc == MERCURY_OK)
+        rc = check_cache(into, B);
+    if (rc)
+        return rc;
+    if (into->elem != cache->elem || into->Hkv != cache->Hkv || into->d != cache->d)
+        return set_error(MERCURY_EINVAL, "both caches must have the same elem, Hkv and d");
+    if (keep < 1 || first < 0 || last < 0 || (long long)first + last > keep)
+        return set_error(MERCURY_EINVAL, "keep must be >= 1 and first and last >= 0, together at most keep (got %d, %d, %d)",
+                         keep, first, last);
+    if (keep > (long long)into->max_pages * into->page_size)
+        return set_error(MERCURY_EINVAL, "keep (%d) exceeds the shorter cache's table (%lld)", keep,
+                         (long long)into->max_pages * into->page_size);
+    if (width < 1 || (double)width * B * cache->Hkv > 4.6e18)
+        return set_error(MERCURY_EINVAL, "width must be >= 1, and B * Hkv * width below 2^62 (got %lld)", width);
+    if (out_mass && (out_width < keep || (double)out_width * B * cache->Hkv > 4.6e18))
+        return set_error(MERCURY_EINVAL, "out_width must be at least keep, and B * Hkv * out_width below 2^62 (got %lld)",
+                         out_width);
+    if (out_lens == seq_lens || (out_mass && out_mass == mass))
+        return set_error(MERCURY_EINVAL, "out_lens and out_mass may not be seq_lens and mass");
+    if (!aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(out_lens, 4) || !aligned(kept, 4) || !aligned(out_mass, 4))
+        return set_error(MERCURY_EALIGN, "mass, seq_lens, out_lens, kept and out_mass must be 4-byte aligned");
+    size_t len;
+    char *msg = error_buffer(&len);
+    cudaStream_t s = (cudaStream_t)stream;
+    rc = launch_kv_evict(*cache, *into, mass, width, seq_lens, keep, first, last, out_lens, kept, out_mass, out_width, s,
+                         msg, len);
+    return finish_call(rc, s);
+}
+
+int mercury_kv_read(const mercury_paged_cache *cache, const int *seq_lens, int B, int S, void *k_out, void *v_out,
+                    void *stream)
+{
+    CallRange range(__func__);
+    if (!seq_lens || !k_out || !v_out)
+        return set_error(MERCURY_EINVAL, "null pointer argument");
+    int rc = check_cache(cache, B);
+    if (rc)
+        return rc;
+    if (S < 1)
+        return set_error(MERCURY_EINVAL, "S must be >= 1 (got %d)", S);
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+        return set_error(MERCURY_EALIGN, "k_out and v_out must be 16-byte aligned");
+    if (!aligned(seq_lens, 4))
+        return set_error(MERCURY_EALIGN, "seq_lens must be 4-byte aligned");
+    size_t len;
+    char *msg = error_buffer(&len);
+    cudaStream_t s = (cudaStream_t)stream;
+    rc = launch_kv_read(*cache, seq_lens, S, k_out, v_out, s, msg, len);
+    return finish_call(rc, s);
 }
 
 }  // extern "C"

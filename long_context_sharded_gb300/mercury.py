@@ -21,6 +21,9 @@ The functions keep the C names:
   mercury_kv_append(cache, k, v, past_lens, new_lens=None, rope=None, q=None, q_out=None, stream=None)
   mercury_attn_paged(q, cache, seq_lens, new_lens=None, causal=True, out=None, lse=None, stream=None)
   mercury_attn_paged_bf16(...) the same, O in bf16
+  mercury_attn_paged_mass(q, cache, seq_lens, lse, new_lens=None, causal=True, mass=None, out=None, stream=None)
+  mercury_kv_evict(cache, into, mass, seq_lens, keep, first=0, last=0, out_lens=None, kept=None, out_mass=None, stream=None)
+  mercury_kv_read(cache, seq_lens, S=None, k_out=None, v_out=None, stream=None)
 Tensors: q [B,Hq,Sq,d], k/v [B,Hkv,Skv,d] bf16 CUDA tensors, contiguous.
 """
 from __future__ import annotations
@@ -57,10 +60,10 @@ EXPORTED = ("mercury_plan_shift", "mercury_attn_sharded", "mercury_attn_partial"
             "mercury_plan_schedules", "mercury_attn_run_schedule", "mercury_tune_schedule",
             "mercury_tune_cache_clear", "mercury_choose_runs", "mercury_rope_frequencies",
             "mercury_rope_init", "mercury_rope", "mercury_kv_append", "mercury_attn_paged",
-            "mercury_attn_paged_bf16")
+            "mercury_attn_paged_bf16", "mercury_attn_paged_mass", "mercury_kv_evict", "mercury_kv_read")
 
 MERCURY_MAX_ROT = 256
-ELEM_BF16, ELEM_E4M3, ELEM_FP32 = 0, 1, 2
+ELEM_BF16, ELEM_E4M3, ELEM_FP32, ELEM_E2M1 = 0, 1, 2, 3
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -153,6 +156,9 @@ def _load() -> ctypes.CDLL:
     lib.mercury_kv_append.argtypes = [p, p, p, p, i32, i32, p, p, p, p, p, p, i32, p, p, p]
     lib.mercury_attn_paged.argtypes = [p, p, p, p, p, i32, i32, i32, i32, p, p, p]
     lib.mercury_attn_paged_bf16.argtypes = lib.mercury_attn_paged.argtypes
+    lib.mercury_attn_paged_mass.argtypes = [p, p, p, p, p, i32, i32, i32, i32, p, p, p, i64, p]
+    lib.mercury_kv_evict.argtypes = [p, p, p, i64, p, i32, i32, i32, i32, p, p, p, i64, p]
+    lib.mercury_kv_read.argtypes = [p, p, i32, i32, p, p, p]
     for name in EXPORTED:
         if name not in ("mercury_last_error", "mercury_tune_cache_clear"):
             getattr(lib, name).restype = i32
@@ -699,10 +705,12 @@ def mercury_rope(x, plan: RopePlan, positions=None, start: int = 0, inverse: boo
 class PagedCache:
     """A paged key-value cache over the caller's tensors, checked once.
 
-    k_cache, v_cache: [num_pages, Hkv, page_size, d], bf16 or float8_e4m3fn,
-    each page contiguous (pages may lie further apart, as slices of a larger
-    allocation do, equally far in both); block_table: int32 [B, max_pages];
-    k_scale, v_scale: fp32 [Hkv], for e4m3 only.  The object keeps the tensors
+    k_cache, v_cache: [num_pages, Hkv, page_size, d], bf16 or float8_e4m3fn, or
+    for a 4-bit cache uint8 [num_pages, Hkv, page_size, d/2 + d/16] (rows of
+    e2m1 codes, two a byte, then an e4m3 scale for each 16; page_size a multiple
+    of 8), each page contiguous (pages may lie further apart, as slices of a
+    larger allocation do, equally far in both); block_table: int32 [B,
+    max_pages]; k_scale, v_scale: fp32 [Hkv], for e4m3 and 4-bit caches only.  The object keeps the tensors
     alive; their contents (the block table's too) may change between calls."""
 
     def __init__(self, k_cache, v_cache, block_table, k_scale=None, v_scale=None):
@@ -715,8 +723,9 @@ class PagedCache:
             if t.get_device() != torch.cuda.current_device():
                 raise ValueError("%s is on %s but the current device is cuda:%d"
                                  % (what, t.device, torch.cuda.current_device()))
-        if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-            raise TypeError("k_cache must be torch.bfloat16 or torch.float8_e4m3fn (got %s)" % k_cache.dtype)
+        if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+            raise TypeError("k_cache must be torch.bfloat16 or torch.float8_e4m3fn, or torch.uint8 for a 4-bit cache "
+                            "(got %s)" % k_cache.dtype)
         if v_cache.dtype is not k_cache.dtype:
             raise TypeError("v_cache must be %s like k_cache (got %s)" % (k_cache.dtype, v_cache.dtype))
         if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
@@ -724,6 +733,11 @@ class PagedCache:
                              % (tuple(k_cache.shape), tuple(v_cache.shape)))
         n, Hkv, page_size, d = k_cache.shape
         page = Hkv * page_size * d
+        e2m1 = k_cache.dtype is torch.uint8
+        if e2m1:
+            if d not in (36, 72):
+                raise ValueError("the rows of a 4-bit cache are d/2 + d/16 bytes, 36 or 72 (got %d)" % d)
+            d = d * 16 // 9
         for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
             if n and not t[0].is_contiguous():
                 raise ValueError("the pages of %s must be contiguous" % what)
@@ -736,14 +750,14 @@ class PagedCache:
         if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or (
                 block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]):
             raise ValueError("block_table must be [B, max_pages] with contiguous rows")
-        e4m3 = k_cache.dtype is torch.float8_e4m3fn
+        scaled = k_cache.dtype is not torch.bfloat16
         scales = []
         for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if not e4m3 and t is not None:
-                raise ValueError("%s is for e4m3 caches only" % what)
-            if e4m3:
+            if not scaled and t is not None:
+                raise ValueError("%s is for e4m3 and 4-bit caches only" % what)
+            if scaled:
                 if t is None:
-                    raise ValueError("an e4m3 cache needs %s" % what)
+                    raise ValueError("%s cache needs %s" % ("a 4-bit" if e2m1 else "an e4m3", what))
                 _check_shape(t, (Hkv,), what)
                 scales.append(_dev_ptr(t, "torch.float32", what))
             else:
@@ -755,7 +769,7 @@ class PagedCache:
         self.B, self.Hkv, self.d = block_table.shape[0], Hkv, d
         self.struct = PagedCacheStruct(
             k_cache.data_ptr(), v_cache.data_ptr(), scales[0], scales[1], block_table.data_ptr(), stride,
-            max(block_table.stride(0), block_table.shape[1]), ELEM_E4M3 if e4m3 else ELEM_BF16, Hkv, d, page_size, n,
+            max(block_table.stride(0), block_table.shape[1]), ELEM_E2M1 if e2m1 else ELEM_E4M3 if scaled else ELEM_BF16, Hkv, d, page_size, n,
             block_table.shape[1], self.B)
         self._ref = ctypes.byref(self.struct)
         self.address = ctypes.addressof(self.struct)
@@ -873,3 +887,114 @@ def mercury_attn_paged_bf16(q, cache: PagedCache, seq_lens, new_lens=None, causa
     """As mercury_attn_paged, with O returned in bf16 (lse fp32)."""
     return _attn_paged(lib.mercury_attn_paged_bf16, _names().bf16, q, cache, seq_lens, new_lens, causal, out, lse,
                        stream)
+
+
+def _cache_call(cache, stream):
+    """(torch names, the cache's device, the call's stream) of a call over `cache`."""
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    T = _torch_names
+    dev = cache.device_index
+    _on_current(dev, "the cache")
+    return T, dev, T.raw_stream(dev) if stream is None else _stream_ptr(stream)
+
+
+def _shape3(t, cache, what):
+    """The width of a [B, Hkv, width] tensor."""
+    shape = getattr(t, "shape", None)
+    if shape is None or len(shape) != 3 or shape[0] != cache.B or shape[1] != cache.Hkv:
+        raise ValueError("%s must be [B=%d, Hkv=%d, width]" % (what, cache.B, cache.Hkv))
+    return shape[2]
+
+
+def mercury_attn_paged_mass(q, cache: PagedCache, seq_lens, lse, new_lens=None, causal: bool = True, mass=None, out=None,
+                            stream=None):
+    """The attention weight that each cached key got from the newest tokens q
+    [B,Hq,Sq,d] bf16, whose log-sum-exp `lse` mercury_attn_paged gave: out
+    [B,Hkv,width] fp32 = mass + the weights' sums over a KV head's rows, entries
+    behind seq_lens[b] left as they were.  mass None: zeros; out may be mass; by
+    default a new tensor of mass's shape (or as wide as the block table), 0
+    behind seq_lens[b]."""
+    T, dev, ptr = _cache_call(cache, stream)
+    shape = _shape4(q, "q")
+    B, Hq, Sq, d = shape
+    if B != cache.B or d != cache.d:
+        raise ValueError("q must be [B=%d, Hq, Sq, d=%d] (got %s)" % (cache.B, cache.d, tuple(shape)))
+    sq = _strides(q, T.bf16, dev, "q")
+    if sq is not None:
+        sq = _Strides(sq[0], sq[1], sq[2])
+    if mass is not None:
+        width = _shape3(mass, cache, "mass")
+    elif out is not None:
+        width = _shape3(out, cache, "out")
+    else:
+        width = cache.struct.max_pages * cache.struct.page_size
+    whole = (B, cache.Hkv, width)
+    if out is None:
+        out = _new_output(T.zeros, whole, T.fp32, q, dev, stream)
+    rc = lib.mercury_attn_paged_mass(
+        q.data_ptr(), sq, cache._ref, _flat(seq_lens, T.int32, dev, (B,), "seq_lens"),
+        None if new_lens is None else _flat(new_lens, T.int32, dev, (B,), "new_lens"), B, Hq, Sq, 1 if causal else 0,
+        _flat(lse, T.fp32, dev, (B, Hq, Sq), "lse"), None if mass is None else _flat(mass, T.fp32, dev, whole, "mass"),
+        _flat(out, T.fp32, dev, whole, "out"), width, ptr)
+    if rc:
+        _check(rc)
+    return out
+
+
+def mercury_kv_evict(cache: PagedCache, into: PagedCache, mass, seq_lens, keep: int, first: int = 0, last: int = 0,
+                     out_lens=None, kept=None, out_mass=None, stream=None):
+    """The first, the last and the heaviest other tokens of every sequence and
+    KV head, `keep` in all, from `cache` into the pages of `into`, in their
+    order; mass [B,Hkv,width] fp32.  Returns (out_lens [B] int32, kept
+    [B,Hkv,keep] int32: the token that each kept one was), made where they are
+    not given (kept: -1 behind out_lens[b]); out_mass [B,Hkv,>=keep] fp32, where
+    given, gets the kept tokens' mass."""
+    T, dev, ptr = _cache_call(cache, stream)
+    if not isinstance(into, PagedCache):
+        raise TypeError("into must be a PagedCache")
+    if into.device_index != dev:
+        raise ValueError("both caches must be on the same device")
+    B, Hkv = cache.B, cache.Hkv
+    width = _shape3(mass, cache, "mass")
+    if out_lens is None:
+        out_lens = _new_output(T.empty, (B,), T.int32, mass, dev, stream)
+    if kept is None:
+        kept = _new_output(_minus_ones, (B, Hkv, keep), T.int32, mass, dev, stream)
+    more = 0 if out_mass is None else _shape3(out_mass, cache, "out_mass")
+    rc = lib.mercury_kv_evict(
+        cache._ref, into._ref, _flat(mass, T.fp32, dev, (B, Hkv, width), "mass"), width,
+        _flat(seq_lens, T.int32, dev, (B,), "seq_lens"), B, keep, first, last, _flat(out_lens, T.int32, dev, (B,), "out_lens"),
+        _flat(kept, T.int32, dev, (B, Hkv, keep), "kept"),
+        None if out_mass is None else _flat(out_mass, T.fp32, dev, (B, Hkv, more), "out_mass"), more, ptr)
+    if rc:
+        _check(rc)
+    return out_lens, kept
+
+
+def _minus_ones(shape, dtype, device):
+    import torch
+    return torch.full(shape, -1, dtype=dtype, device=device)
+
+
+def mercury_kv_read(cache: PagedCache, seq_lens, S: int = None, k_out=None, v_out=None, stream=None):
+    """The cached keys and values of every sequence as dense bf16 tensors
+    [B,Hkv,S,d], tokens i < seq_lens[b] (rows behind them: left as they were, 0
+    where the call makes the tensors); S by default the outputs', or what the
+    block table holds.  Returns (k, v)."""
+    T, dev, ptr = _cache_call(cache, stream)
+    for t in (k_out, v_out):
+        if S is None and t is not None:
+            S = _shape4(t, "k_out and v_out")[2]
+    if S is None:
+        S = cache.struct.max_pages * cache.struct.page_size
+    whole = (cache.B, cache.Hkv, S, cache.d)
+    if k_out is None:
+        k_out = _new_output(T.zeros, whole, T.bf16, cache.k_cache, dev, stream)
+    if v_out is None:
+        v_out = _new_output(T.zeros, whole, T.bf16, cache.k_cache, dev, stream)
+    rc = lib.mercury_kv_read(cache._ref, _flat(seq_lens, T.int32, dev, (cache.B,), "seq_lens"), cache.B, S,
+                             _flat(k_out, T.bf16, dev, whole, "k_out"), _flat(v_out, T.bf16, dev, whole, "v_out"), ptr)
+    if rc:
+        _check(rc)
+    return k_out, v_out
