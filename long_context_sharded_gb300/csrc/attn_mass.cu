@@ -135,19 +135,14 @@ struct Keys<MERCURY_ELEM_E2M1, D> {
             for (int j = 0; j < 2; ++j) {
                 const uint32_t scale = e4m3_to_f16(s[i][j] | s[i][j] << 8);
 #pragma unroll
-                for (int k = 0; k < D / 64; ++k)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t x = w[i][j][k] >> (16 * n);
-                        uint32_t lo, hi;
-                        asm("{\n\t.reg .b8 x, y;\n\tmov.b16 {x, y}, %2;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t"
-                            "cvt.rn.f16x2.e2m1x2 %1, y;\n\tmul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
-                            : "=&r"(lo), "=&r"(hi)
-                            : "h"((uint16_t)x), "r"(scale));
-                        const int kk = j * (D / 32) + 2 * k + n;
-                        f[kk][i] = lo;
-                        f[kk][2 + i] = hi;
-                    }
+                for (int k = 0; k < D / 64; ++k) {
+                    const uint32_t x = w[i][j][k];
+                    const int kk = j * (D / 32) + 2 * k;
+                    f[kk][i] = mul_f16(e2m1_to_f16<0>(x), scale);
+                    f[kk][2 + i] = mul_f16(e2m1_to_f16<1>(x), scale);
+                    f[kk + 1][i] = mul_f16(e2m1_to_f16<2>(x), scale);
+                    f[kk + 1][2 + i] = mul_f16(e2m1_to_f16<3>(x), scale);
+                }
             }
     }
 };

@@ -41,11 +41,13 @@ namespace mercury {
 
 namespace {
 
-// NR: 8-row groups of a row tile.  Every computing warp has all its rows and
-// its own 32 keys of each tile.
-template <int D, int NR>
+// ROWS: rows of a row tile, 4, 8 or 16.  Every computing warp has all its rows
+// and its own 32 keys of each tile.  With four rows both terms of a weight
+// share an instruction: columns 0 to 3 are the rows' first terms, 4 to 7 their
+// second ones.
+template <int D, int ROWS>
 struct Cfg {
-    static constexpr int kWarps = NR == 1 ? 16 : 8;  // computing warps
+    static constexpr int kWarps = ROWS <= 8 ? 12 : 8;  // computing warps
     static constexpr int kThreads = (kWarps + kCopyWarps) * 32;
     static constexpr int kRowB = D / 2 + D / 16;  // bytes of one key
     static constexpr int kRun = D / 16;           // bytes of a run of a row that a thread takes
@@ -53,20 +55,21 @@ struct Cfg {
     static constexpr int kTile = kKeys * kWarps;
     static constexpr int kPart = kTile * kRowB;
     static constexpr int kStage = 2 * kPart;
-    static constexpr int kRows = 8 * NR;
-    static constexpr int kRed = kWarps * kRows * 8;            // each warp's maxima and sums
-    static constexpr int kRowBytes = kWarps * kRows * D * 4;   // the warps' partial rows
+    static constexpr int kCols = ROWS == 16 ? 16 : 8;          // columns of S' and O'
+    static constexpr int kRed = kWarps * ROWS * 8;             // each warp's maxima and sums
+    static constexpr int kRowBytes = kWarps * kCols * D * 4;   // the warps' partial columns
     static constexpr bool kOwnRows = kRowBytes > kStage;       // in memory of their own, or in a stage
     static constexpr int kRoom = 232448 - 256 - kRed - (kOwnRows ? kRowBytes : 0);
     static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
     static constexpr int kCtl = kStages * kStage + kRed + kStages * 16;
-    static constexpr int kRowsAt = (kCtl + 32 + 15) / 16 * 16;
-    static constexpr int kSmem = kRowsAt + (kOwnRows ? kRowBytes : 0);
+    static constexpr int kPartsAt = (kCtl + 32 + 15) / 16 * 16;
+    static constexpr int kSmem = kPartsAt + (kOwnRows ? kRowBytes : 0);
     static_assert(kStages >= 2 && kSmem <= 232448, "a stage to read and one on its way");
+    static_assert(kTile % kUnits == 0, "whole eighths of a tile");
     // registers a thread after the split (setmaxnreg); their sum may not
     // exceed what the launch provides
-    static constexpr uint32_t kRegsCopy = NR == 1 ? 64 : 72;
-    static constexpr uint32_t kRegsCompute = NR == 1 ? 104 : 216;
+    static constexpr uint32_t kRegsCopy = ROWS <= 8 ? 64 : 72;
+    static constexpr uint32_t kRegsCompute = ROWS <= 8 ? 144 : 216;
     static constexpr int kMinLaunchRegs = (int)(kRegsCopy * 128 + kRegsCompute * kWarps * 32 + kThreads - 1) / kThreads;
 };
 
@@ -79,32 +82,19 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Byte I of w, two e2m1 codes, as fp16: exact, the lower half's in the lower.
-template <int I>
-__device__ __forceinline__ uint32_t e2m1_to_f16(uint32_t w)
-{
-    uint32_t r;
-    if constexpr (I == 0)
-        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 1)
-        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, y;\n\t}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 2)
-        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, z;\n\t}" : "=r"(r) : "r"(w));
-    else
-        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, w;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
 template <int I>
 struct Byte {
     static constexpr int value = I;
 };
 
-__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b)
+// D = A B, fp16 operands.
+__device__ __forceinline__ void mma_first(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
 {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements, two of a row a lane.
@@ -134,11 +124,11 @@ __device__ __forceinline__ int key_at(int g)
 // The copying warps: every tile of the share into the ring, a stage as soon as
 // the computing warps have left it.  A tile's runs of box_rows keys, each in
 // one page, are dealt to the lanes of the four warps in turn.
-template <int D, int NR>
+template <int D, int ROWS>
 __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end, char *smem, uint64_t *full,
                                            uint64_t *empty, Stop *stop, int warp, int lane)
 {
-    using C = Cfg<D, NR>;
+    using C = Cfg<D, ROWS>;
     constexpr int ROWB = C::kRowB, TILE = C::kTile, NS = C::kStages;
     const int first = (lane * kCopyWarps + warp) * a.box_rows;  // this lane's run
     // its page, asked for a tile ahead
@@ -191,8 +181,8 @@ __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end
         if (at.j == 0 && warp == 0) {
             // a new job: its queries into L2 by the time the computing warps
             // get there
-            const int h1 = a.n_rt == 1 ? at.hr : at.hr / a.n_rt, row0 = (at.hr - h1 * a.n_rt) * C::kRows;
-            for (int r = row0 + lane; r < min(row0 + C::kRows, a.R); r += 32) {
+            const int h1 = a.n_rt == 1 ? at.hr : at.hr / a.n_rt, row0 = (at.hr - h1 * a.n_rt) * ROWS;
+            for (int r = row0 + lane; r < min(row0 + ROWS, a.R); r += 32) {
                 const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
                 const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h1 * a.G + head) * a.qs.h + s * a.qs.s;
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
@@ -250,16 +240,18 @@ __device__ __forceinline__ int part_at(int row, int col)
     return (((col >> 2) ^ (((row >> 1) & 3) | (row & 1) << 2)) << 2) + (col & 3);
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(const __grid_constant__ PagedArgs a)
+template <int D, int ROWS>
+__global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(const __grid_constant__ PagedArgs a)
 {
-    using C = Cfg<D, NR>;
+    using C = Cfg<D, ROWS>;
     constexpr int ROWB = C::kRowB, KEYS = C::kKeys, TILE = C::kTile, NS = C::kStages, kWarps = C::kWarps;
     constexpr int RUN = C::kRun, RW = RUN / 4;  // bytes and words of a thread's run of a row
     constexpr int KK = D / 16, DT = D / 16;     // k-steps of S', 16-row tiles of O'
+    constexpr bool TWO = ROWS == 4;             // two terms in one instruction
+    constexpr int NR = C::kCols / 8, TERMS = TWO ? 1 : 2;
     extern __shared__ __align__(1024) char smem[];
     float *const red_m = reinterpret_cast<float *>(smem + NS * C::kStage);
-    float *const red_l = red_m + kWarps * C::kRows;
+    float *const red_l = red_m + kWarps * ROWS;
     uint64_t *const full = reinterpret_cast<uint64_t *>(smem + NS * C::kStage + C::kRed);
     uint64_t *const empty = full + NS;
     Stop *const stop = reinterpret_cast<Stop *>(smem + C::kCtl);
@@ -295,26 +287,26 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
         return;
     if (warp >= kWarps) {
         regs_dec<C::kRegsCopy>();
-        copy_tiles<D, NR>(a, at, end, smem, full, empty, stop, warp - kWarps, lane);
+        copy_tiles<D, ROWS>(a, at, end, smem, full, empty, stop, warp - kWarps, lane);
         return;
     }
 
     // ---- the computing warps
     regs_inc<C::kRegsCompute>();
     const int g = lane >> 2, t = lane & 3;
-    // Row g of the second operand is query row nr * 8 + g; of S' and O' this
-    // thread has the columns nr * 8 + 2t and + 1.
+    // Row g of the second operand is query row nr * 8 + g (of four rows each is
+    // there twice); of S' and O' this thread has the columns nr * 8 + 2t and + 1.
     uint32_t qf[NR][KK][2];
     int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
     float k_scale = 1.f;
     auto load_q = [&]() {
         h_kv = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
-        row0 = (at.hr - h_kv * a.n_rt) * C::kRows;
+        row0 = (at.hr - h_kv * a.n_rt) * ROWS;
         n_new = new_of(a, at.b);
         k_scale = a.cache.k_scale[h_kv];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            const int r = row0 + nr * 8 + g;
+            const int r = row0 + (TWO ? g & 3 : nr * 8 + g);
             const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
             const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h_kv * a.G + head) * a.qs.h + s * a.qs.s;
 #pragma unroll
@@ -338,6 +330,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
     const int key_g = key_at<D>(g), key_x = key_at<D>(2 * t), key_y = key_at<D>(2 * t + 1);
     const char *const k_lane = smem + (warp * KEYS + key_g) * ROWB;
     const char *const v_lane = smem + C::kPart + warp * KEYS * ROWB;
+    const float whole_p = t < 2 ? 1.f : 1 << kLowShift, less_p = t < 2 ? 0.f : 1 << kLowShift;
     int stage = 0;
     uint32_t phase = 0;
     // this warp is done with the stage
@@ -394,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                 m_run[nr][e] = -INFINITY;
                 l_run[nr][e] = 0.f;
                 l_rest[nr][e] = 0.f;
-                const int s = (row0 + nr * 8 + 2 * t + e) % a.Sq;
+                const int s = (row0 + (TWO ? (2 * t + e) & 3 : nr * 8 + 2 * t + e)) % a.Sq;
                 lim[nr][e] = a.causal ? at.keys - n_new + min(s, n_new - 1) + 1 : at.keys;
             }
 #pragma unroll
@@ -411,13 +404,6 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                 const char *const k_s = k_lane + stage * C::kStage, *const v_s = v_lane + stage * C::kStage;
                 // ---- S' = K Q'
                 float sc[NR][2][4];
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[nr][m][e] = 0.f;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     // rows g and g + 8 of the product: keys key_g + 2m and + 1
@@ -446,7 +432,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                                 f[i] = mul_f16(f[i], s[i & 1][r]);
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr) {
-                                mma<true>(sc[nr][m], f[0], f[1], f[2], f[3], qf[nr][kk][0], qf[nr][kk][1]);
+                                if (kk == 0)
+                                    mma_first(sc[nr][m], f[0], f[1], f[2], f[3], qf[nr][kk][0], qf[nr][kk][1]);
+                                else
+                                    mma<true>(sc[nr][m], f[0], f[1], f[2], f[3], qf[nr][kk][0], qf[nr][kk][1]);
                                 mma<true>(sc[nr][m], f[4], f[5], f[6], f[7], qf[nr][kk + 1][0], qf[nr][kk + 1][1]);
                             }
                         }
@@ -499,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                         }
                 }
                 // ---- P' as two fp16 terms, a key a column: p[..][m][half][term]
-                uint32_t p[NR][2][2][2];
+                uint32_t p[NR][2][2][TERMS];
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
                     float ref[2], sum[2] = {0.f, 0.f};
@@ -514,10 +503,17 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                             const float p1 = ex2_approx(fmaf(sc[nr][m][2 * i + 1], s_mul[nr][1], ref[1]));
                             sum[0] += p0;
                             sum[1] += p1;
-                            uint32_t term[2];
-                            split<true>(p0, p1, term);
-                            p[nr][m][i][0] = transpose8(term[0]);
-                            p[nr][m][i][1] = transpose8(term[1]);
+                            if constexpr (TWO) {
+                                // p, or in the upper columns what its first term leaves, 2^kLowShift times as large
+                                const uint32_t h = pack_f16(p0, p1);
+                                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                                p[nr][m][i][0] = transpose8(pack_f16(fmaf(p0, whole_p, -x.x * less_p), fmaf(p1, whole_p, -x.y * less_p)));
+                            } else {
+                                uint32_t term[2];
+                                split<true>(p0, p1, term);
+                                p[nr][m][i][0] = transpose8(term[0]);
+                                p[nr][m][i][TERMS - 1] = transpose8(term[1]);
+                            }
                         }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -585,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                 }
                 auto tile_of = [&](int i, int w, auto byte) {
                     constexpr int I = decltype(byte)::value;
-                    float d[NR][2][4] = {};
+                    float d[NR][TERMS][4];
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         const uint32_t a0 = mul_f16(e2m1_to_f16<I>(lo[2 * m][w]), vs[2 * m]);
@@ -595,13 +591,17 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                            for (int term = 0; term < 2; ++term)
-                                mma<true>(d[nr][term], a0, a1, a2, a3, p[nr][m][0][term], p[nr][m][1][term]);
+                            for (int term = 0; term < TERMS; ++term)
+                                if (m == 0)
+                                    mma_first(d[nr][term], a0, a1, a2, a3, p[nr][m][0][term], p[nr][m][1][term]);
+                                else
+                                    mma<true>(d[nr][term], a0, a1, a2, a3, p[nr][m][0][term], p[nr][m][1][term]);
                     }
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) {
                         add_to(sums[nr][i], d[nr][0], 1.f);
-                        add_to(sums[nr][i], d[nr][1], kLow);
+                        if constexpr (!TWO)
+                            add_to(sums[nr][i], d[nr][TERMS - 1], kLow);
                     }
                 };
 #pragma unroll
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
         }
         // through memory of their own, or through the stage, once no warp reads
         // the tile any more
-        float *const rows = reinterpret_cast<float *>(C::kOwnRows ? smem + C::kRowsAt : smem + stage * C::kStage);
+        float *const rows = reinterpret_cast<float *>(C::kOwnRows ? smem + C::kPartsAt : smem + stage * C::kStage);
         if (C::kOwnRows)
             release();
         named_barrier_sync(1, kWarps * 32);
@@ -645,11 +645,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int row = nr * 8 + 2 * t + e;
-                if (g == 0) {
-                    red_m[warp * C::kRows + row] = m_run[nr][e] - kUp<true>;  // what the sums are relative to
-                    red_l[warp * C::kRows + row] = l;
+                if (g == 0 && row < ROWS) {
+                    red_m[warp * ROWS + row] = m_run[nr][e] - kUp<true>;  // what the sums are relative to
+                    red_l[warp * ROWS + row] = l;
                 }
-                float *const mine = rows + (warp * C::kRows + row) * D;
+                float *const mine = rows + (warp * C::kCols + row) * D;
 #pragma unroll
                 for (int i = 0; i < DT; i += 2)
                     *reinterpret_cast<float4 *>(mine + part_at(row, g * 2 * RUN + 2 * i)) =
@@ -658,26 +658,30 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
         if (!C::kOwnRows)
             fence_proxy_async_smem();
         named_barrier_sync(1, kWarps * 32);
-        for (int u = tid; u < C::kRows * (D / 2); u += kWarps * 32) {
+        for (int u = tid; u < ROWS * (D / 2); u += kWarps * 32) {
             const int row = u / (D / 2), col = u % (D / 2) * 2, r = done_row0 + row;
             if (r >= a.R)
                 continue;
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                top = fmaxf(top, red_m[w * C::kRows + row]);
+                top = fmaxf(top, red_m[w * ROWS + row]);
             const float ref = top == -INFINITY ? 0.f : top;
             float sum = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2_approx(red_m[w * C::kRows + row] - ref);
-                sum += f * red_l[w * C::kRows + row];
-                const float2 x = *reinterpret_cast<const float2 *>(rows + (w * C::kRows + row) * D + part_at(row, col));
+                const float f = ex2_approx(red_m[w * ROWS + row] - ref);
+                sum += f * red_l[w * ROWS + row];
+                float2 x = *reinterpret_cast<const float2 *>(rows + (w * C::kCols + row) * D + part_at(row, col));
+                if constexpr (TWO) {
+                    const float2 y = *reinterpret_cast<const float2 *>(rows + (w * C::kCols + row + 4) * D + part_at(row + 4, col));
+                    x = make_float2(x.x + kLow * y.x, x.y + kLow * y.y);
+                }
                 o0 += f * x.x;
                 o1 += f * x.y;
             }
             if (!whole) {
-                const long long at_ws = (long long)(2 * blockIdx.x + (first_j == 0 ? 1 : 0)) * C::kRows + row;
+                const long long at_ws = (long long)(2 * blockIdx.x + (first_j == 0 ? 1 : 0)) * ROWS + row;
                 *reinterpret_cast<float2 *>(a.ws_o + at_ws * D + col) = make_float2(o0, o1);
                 if (col == 0)
                     a.ws_ml[at_ws] = make_float2(top, sum);
@@ -703,25 +707,27 @@ __global__ void __launch_bounds__(Cfg<D, NR>::kThreads, 1) attn_paged4_kernel(co
     named_barrier_arrive(kEndBarrier, C::kThreads);
 }
 
-template <int D, int NR>
+template <int D, int ROWS>
 int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    using C = Cfg<D, NR>;
+    using C = Cfg<D, ROWS>;
     long long most;
-    const int rc = count_tiles<C::kRows, C::kTile>(a, &most, msg, msg_len);
+    const int rc = count_tiles<ROWS, C::kTile>(a, &most, msg, msg_len);
     if (rc != MERCURY_OK)
         return rc;
-    // runs of a power of two of keys that divides page_size (a multiple of 8)
-    for (a.box_rows = 8; a.box_rows < C::kTile && a.cache.page_size % (2 * a.box_rows) == 0;)
+    // runs of a power of two of keys that divides page_size (a multiple of 8) and the tile
+    for (a.box_rows = 8; C::kTile % (2 * a.box_rows) == 0 && a.cache.page_size % (2 * a.box_rows) == 0;)
         a.box_rows *= 2;
-    return launch_split<D, C::kRows, C::kTile>(a, most, attn_paged4_kernel<D, NR>, C::kSmem, C::kThreads, C::kMinLaunchRegs,
+    return launch_split<D, ROWS, C::kTile>(a, most, attn_paged4_kernel<D, ROWS>, C::kSmem, C::kThreads, C::kMinLaunchRegs,
                                                stream, msg, msg_len);
 }
 
 template <int D>
 int launch_rows(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    return a.R <= 8 ? launch<D, 1>(a, stream, msg, msg_len) : launch<D, 2>(a, stream, msg, msg_len);
+    return a.R <= 4   ? launch<D, 4>(a, stream, msg, msg_len)
+           : a.R <= 8 ? launch<D, 8>(a, stream, msg, msg_len)
+                      : launch<D, 16>(a, stream, msg, msg_len);
 }
 
 }  // namespace

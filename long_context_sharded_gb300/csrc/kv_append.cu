@@ -56,15 +56,12 @@ struct AppendArgs {
     mercury_rope_plan plan;
 };
 
-template <bool T>
-struct Turn {
-    static constexpr bool value = T;
-};
-
-// One head's unit (two chunks of 8 of 16-byte accesses, as loaded) into a row of
-// a 4-bit cache.  The chunks of a unit of the rotated part (turned or, of values,
-// not) are halves of two blocks, whose other halves the neighbouring lane has;
-// any other unit's make one block.
+// One head's unit (two chunks of 8 elements, as loaded) into a row of a 4-bit
+// cache.  The chunks of a unit of the rotated part (turned or, of values, not)
+// are halves of two blocks, whose other halves the neighbouring lane has; any
+// other unit's make one block.  The code is kept short, since it is not
+// waited for instructions that it was bound by: what has to be settled is
+// settled out of line.
 template <bool TURN>
 __device__ __forceinline__ void keep4(const RotUnit<8> &unit, const mercury_rope_plan &plan,
                                       const unsigned long long *turns, long long pos, char *row, int d, float scale,
@@ -72,83 +69,97 @@ __device__ __forceinline__ void keep4(const RotUnit<8> &unit, const mercury_rope
 {
     const bool apart = unit.rotated, turned = TURN && apart;
     const float g = fabsf(scale);
-    float y[2][8], e[2][8];
+    float y[2][8], top[2] = {0.f, 0.f}, off[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[0][i] = x0[i];
         y[1][i] = x1[i];
-        e[0][i] = e[1][i] = 0.f;
     }
-    // element i of chunk k's pair, and whether it is the pair's second
-    auto real = [&](int k, int i) {
-        const int j = unit.interleaved ? i & ~1 : i;
-        const float a = unit.interleaved ? (k ? x1[j] : x0[j]) : x0[j], b = unit.interleaved ? (k ? x1[j + 1] : x0[j + 1]) : x1[j];
-        const int pair = unit.interleaved ? ((k ? unit.at1 : unit.at0) + j) / 2 : unit.at0 + j;
-        return rotated_real(a, b, unit.interleaved ? i & 1 : k, turns[pair] * (unsigned long long)pos, plan.magnitude);
-    };
     if (turned) {
         unit.turn(y[0], y[1]);
-        const float f = kRotationError * fabsf(plan.magnitude);
+        float a = 0.f, b = 0.f;  // the largest sum of a pair's magnitudes in each chunk
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (unit.interleaved) {
-                e[0][i] = f * (fabsf(x0[i]) + fabsf(x0[i ^ 1]));
-                e[1][i] = f * (fabsf(x1[i]) + fabsf(x1[i ^ 1]));
-            } else {
-                e[0][i] = e[1][i] = f * (fabsf(x0[i]) + fabsf(x1[i]));
-            }
+        for (int i = 0; i < 8; ++i) {
+            a = fmaxf(a, fabsf(x0[i]) + fabsf(unit.interleaved ? x0[i ^ 1] : x1[i]));
+            b = fmaxf(b, fabsf(x1[i]) + fabsf(unit.interleaved ? x1[i ^ 1] : x0[i]));
+        }
+        off[0] = kRotationError * fabsf(plan.magnitude) * a;
+        off[1] = kRotationError * fabsf(plan.magnitude) * b;
     }
-    // magnitudes, what they are known to, NaN of each chunk's block
-    float top[2] = {0.f, 0.f}, off[2] = {0.f, 0.f}, nan[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            top[k] = fmaxf(top[k], fabsf(y[k][i]));
-            off[k] = fmaxf(off[k], e[k][i]);
-            nan[k] += y[k][i] * 0.f;  // NaN for an infinity too, which is looked at below
-        }
-    const unsigned int lane = threadIdx.x & 31, both = 3u << (lane & ~1u);
+        for (int i = 0; i < 8; ++i)
+            top[k] = max_nan(top[k], fabsf(y[k][i]));
+    const unsigned int both = 3u << (threadIdx.x & 30u);
     if (apart) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            top[k] = fmaxf(top[k], __shfl_xor_sync(both, top[k], 1));
-            off[k] = fmaxf(off[k], __shfl_xor_sync(both, off[k], 1));
-            nan[k] += __shfl_xor_sync(both, nan[k], 1);
+            top[k] = max_nan(top[k], __shfl_xor_sync(both, top[k], 1));
+            if (TURN)
+                off[k] = fmaxf(off[k], __shfl_xor_sync(both, off[k], 1));
         }
     } else {
-        top[0] = top[1] = fmaxf(top[0], top[1]);
-        nan[0] = nan[1] = nan[0] + nan[1];
+        top[0] = top[1] = max_nan(top[0], top[1]);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        uint32_t byte = 0x7fu, codes = 0;
-        bool is_nan = nan[k] != 0.f;
-        if (is_nan && top[k] == INFINITY) {
-            // infinities are saturated unless there is a NaN beside them
-            is_nan = false;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                is_nan |= y[k][i] != y[k][i] || (!apart && y[k ^ 1][i] != y[k ^ 1][i]);
-            if (apart)
-                is_nan |= __shfl_xor_sync(both, (int)is_nan, 1) != 0;
-        }
-        if (!is_nan) {
-            byte = block_scale(top[k], top[k] == INFINITY ? 0.f : off[k], g, [&] {
-                double x = 0.0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x = fmax(x, fabs(real(k, i)));
-                return fmax(x, __shfl_xor_sync(both, x, 1));  // (both lanes are here: they have the same bounds)
-            });
-            codes = block_codes(y[k], e[k], e4m3_value(byte), g, [&](int i) { return real(k, i); });
-            if (scale < 0.f)
-                codes ^= 0x88888888u;
-        }
         const int at = k ? unit.at1 : unit.at0;
-        *reinterpret_cast<uint32_t *>(row + at / 2) = codes;
+        // an infinity, which is held as 6 * 448, leaves no bounds
+        const float by = top[k] < INFINITY ? off[k] : 0.f;
+        auto source = [&](float (&first)[8], float (&second)[8], float (&copy)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                copy[i] = y[k][i];
+                first[i] = unit.interleaved ? (k ? x1[i & ~1] : x0[i & ~1]) : x0[i];
+                second[i] = unit.interleaved ? (k ? x1[i | 1] : x0[i | 1]) : x1[i];
+            }
+            return Source{first, second, (unsigned long long)pos, turns, plan.magnitude, at, plan.rot_dim, unit.interleaved};
+        };
+        const uint32_t ends = scale_ends(top[k], by, g);
+        uint32_t byte = ends & 0xffu;
+        if (byte != ends >> 8) {
+            float first[8], second[8], copy[8];
+            const Source from = source(first, second, copy);
+            byte = settle_scale<8>(byte, ends >> 8, top[k], by, g, copy, by > 0.f ? &from : nullptr, both);
+        }
+        uint32_t lo, w;
+        code_ends(y[k], by, byte == 0x7fu ? 0.f : e4m3_value(byte), g, lo, w);
+        const uint32_t differ = lo ^ (w & 0x77777777u);
+        if (differ) {
+            float first[8], second[8], copy[8];
+            const Source from = source(first, second, copy);
+            w = (w & 0x88888888u) | settle_codes(lo, differ, e4m3_value(byte), g, copy, by > 0.f ? &from : nullptr);
+        }
+        *reinterpret_cast<uint32_t *>(row + at / 2) = scale < 0.f ? w ^ 0x88888888u : w;
         if (at % 16 == 0)
             row[d / 2 + at / 16] = (char)byte;
+    }
+}
+
+// The unit of heads h = 0 .. n - 1 into a 4-bit cache: the next head's loads on
+// their way while one is turned and stored.
+template <bool TURN>
+__device__ __forceinline__ void walk4(const __nv_bfloat16 *src, long long stride, const float *scales, int n,
+                                      const RotUnit<8> &unit, const mercury_rope_plan &plan,
+                                      const unsigned long long *turns, long long pos, char *row, long long head_stride, int d)
+{
+    Chunk<__nv_bfloat16, 8> a, b;
+    float scale = scales[0];
+    a.load(src + unit.at0);
+    b.load(src + unit.at1);
+#pragma unroll 1
+    for (int h = 0; h < n; ++h) {
+        float x0[8], x1[8];
+        a.widen(x0);
+        b.widen(x1);
+        const float s = scale;
+        if (h + 1 < n) {
+            a.load(src + (h + 1) * stride + unit.at0);
+            b.load(src + (h + 1) * stride + unit.at1);
+            scale = scales[h + 1];
+        }
+        keep4<TURN>(unit, plan, turns, pos, row + h * head_stride, d, s, x0, x1);
     }
 }
 
@@ -236,20 +247,13 @@ __global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) append_kernel(const 
                                     });
         }
         if constexpr (FP4) {
-            auto keep_row = [&](char *cache, float scale, int h, auto turn, const float (&x0)[VE], const float (&x1)[VE]) {
-                if (row >= 0)
-                    keep4<decltype(turn)::value>(unit, a.plan, turns, pos, cache + row + h * head_stride, a.d, scale, x0, x1);
-            };
-            if (k0 < k1)
-                walk_heads<T, VE, false, true, FEW>(a.k + b * a.ks.b + i * a.ks.s + k0 * a.ks.h, a.ks.h, c.k_scale + k0, k1 - k0,
-                                                    unit, ready, [&](int h, const float (&x0)[VE], const float (&x1)[VE], float scale) {
-                                                        keep_row(c.k, scale, k0 + h, Turn<true>(), x0, x1);
-                                                    });
-            if (v0 < v1)
-                walk_heads<T, VE, false, true, FEW>(a.v + b * a.vs.b + i * a.vs.s + v0 * a.vs.h, a.vs.h, c.v_scale + v0, v1 - v0,
-                                                    unit, ready, [&](int h, const float (&x0)[VE], const float (&x1)[VE], float scale) {
-                                                        keep_row(c.v, scale, v0 + h, Turn<false>(), x0, x1);
-                                                    });
+            ready();
+            if (k0 < k1 && row >= 0)
+                walk4<true>(a.k + b * a.ks.b + i * a.ks.s + k0 * a.ks.h, a.ks.h, c.k_scale + k0, k1 - k0, unit, a.plan, turns,
+                            pos, c.k + row + k0 * head_stride, head_stride, a.d);
+            if (v0 < v1 && row >= 0)
+                walk4<false>(a.v + b * a.vs.b + i * a.vs.s + v0 * a.vs.h, a.vs.h, c.v_scale + v0, v1 - v0, unit, a.plan, turns,
+                             pos, c.v + row + v0 * head_stride, head_stride, a.d);
             continue;
         }
         if (k0 < k1)
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) append_kernel(const 
 template <int ELEM, int VE>
 int launch(AppendArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    const RotShape g = rot_shape(a.tokens, a.Hq + 2 * a.cache.Hkv, a.d, a.plan.rot_dim, VE, sms);
+    const RotShape g = rot_shape(a.tokens, a.Hq + 2 * a.cache.Hkv, a.d, a.plan.rot_dim, VE, sms, ELEM == MERCURY_ELEM_E2M1 ? 6 : 3);
     if (g.blocks * g.head_groups > 0x7fffffffLL) {
         snprintf(msg, msg_len, "too many tokens for one call (%lld)", (long long)a.tokens);
         return MERCURY_EINVAL;
@@ -324,25 +328,23 @@ __global__ void __launch_bounds__(kRotThreads) append_blocks_kernel(const __grid
     auto second = [&](int j) { return a.plan.interleaved ? (j & 1) != 0 : j >= rot / 2; };
     auto first_at = [&](int j) { return a.plan.interleaved ? j & ~1 : pair_of(j); };
     const int step = a.plan.interleaved ? 1 : rot / 2;
-    float y[16], e[16];
+    float y[16], x[16], z[16];
     float top = 0.f, off = 0.f;
-    bool nan = false;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const int j = at + k;
-        e[k] = 0.f;
         if (!value && j < rot) {
-            const float x = __bfloat162float(src[first_at(j)]), z = __bfloat162float(src[first_at(j) + step]);
+            x[k] = __bfloat162float(src[first_at(j)]);
+            z[k] = __bfloat162float(src[first_at(j) + step]);
             float cs, sn;
             rope_cos_sin(turns[pair_of(j)], pos, a.plan.magnitude, cs, sn);
-            y[k] = second(j) ? z * cs + x * sn : x * cs - z * sn;
-            e[k] = kRotationError * fabsf(a.plan.magnitude) * (fabsf(x) + fabsf(z));
+            y[k] = second(j) ? z[k] * cs + x[k] * sn : x[k] * cs - z[k] * sn;
+            off = fmaxf(off, kRotationError * fabsf(a.plan.magnitude) * (fabsf(x[k]) + fabsf(z[k])));
         } else {
-            y[k] = __bfloat162float(src[j]);
+            // (of itself and no partner at no angle, where a block's part is turned)
+            x[k] = z[k] = y[k] = __bfloat162float(src[j]);
         }
-        top = fmaxf(top, fabsf(y[k]));
-        off = fmaxf(off, e[k]);
-        nan |= y[k] != y[k];
+        top = max_nan(top, fabsf(y[k]));
     }
     const bool in_table = pos >= 0 && pos < (long long)c.max_pages * c.page_size;
     if (!in_table) {
@@ -357,36 +359,28 @@ __global__ void __launch_bounds__(kRotThreads) append_blocks_kernel(const __grid
     char *const row = (value ? c.v : c.k) + page * c.page_stride +
                       ((long long)h * c.page_size + pos - (long long)p * c.page_size) * row_size;
     const float scale = (value ? c.v_scale : c.k_scale)[h], g = fabsf(scale);
-    auto real = [&](int k) {
-        const int j = at + k;
-        return rotated_real(__bfloat162float(src[first_at(j)]), __bfloat162float(src[first_at(j) + step]), second(j),
-                            turns[pair_of(j)] * (unsigned long long)pos, a.plan.magnitude);
-    };
-    uint32_t byte = 0x7fu, codes[2] = {0u, 0u};
-    if (!nan) {
-        byte = block_scale(top, top == INFINITY ? 0.f : off, g, [&] {
-            double x = 0.0;
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k)
-                x = fmax(x, at + k < rot && !value ? fabs(real(k)) : fabs((double)__bfloat162float(src[at + k])));
-            return x;
-        });
-        const float s = e4m3_value(byte);
+    const float by = top < INFINITY ? off : 0.f;
+    Source from = {x, z, (unsigned long long)pos, turns, a.plan.magnitude, at, rot, a.plan.interleaved};
+    const uint32_t ends = scale_ends(top, by, g);
+    uint32_t byte = ends & 0xffu;
+    if (byte != ends >> 8)
+        byte = settle_scale<16>(byte, ends >> 8, top, by, g, y, by > 0.f ? &from : nullptr, 0u);
+    const float s = byte == 0x7fu ? 0.f : e4m3_value(byte);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float y8[8], e8[8];
+    for (int k = 0; k < 2; ++k) {
+        float part[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y8[j] = y[8 * k + j];
-                e8[j] = e[8 * k + j];
-            }
-            codes[k] = block_codes(y8, e8, s, g, [&](int j) { return real(8 * k + j); });
-            if (scale < 0.f)
-                codes[k] ^= 0x88888888u;
+        for (int j = 0; j < 8; ++j)
+            part[j] = y[8 * k + j];
+        uint32_t lo, w;
+        code_ends(part, by, s, g, lo, w);
+        const uint32_t differ = lo ^ (w & 0x77777777u);
+        if (differ) {
+            const Source half = {x + 8 * k, z + 8 * k, from.pos, turns, a.plan.magnitude, at + 8 * k, rot, a.plan.interleaved};
+            w = (w & 0x88888888u) | settle_codes(lo, differ, s, g, y + 8 * k, by > 0.f ? &half : nullptr);
         }
+        *reinterpret_cast<uint32_t *>(row + at / 2 + 4 * k) = scale < 0.f ? w ^ 0x88888888u : w;
     }
-    *reinterpret_cast<uint32_t *>(row + at / 2) = codes[0];
-    *reinterpret_cast<uint32_t *>(row + at / 2 + 4) = codes[1];
     row[a.d / 2 + at / 16] = (char)byte;
 }
 

@@ -38,6 +38,8 @@ __device__ __noinline__ void record_bounds(unsigned int site)
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kHeld = 32768;  // a block holds so many tokens' ranks in shared memory; of more it reads them anew
 
 struct SelectArgs {
     const float *mass;  // [B][Hkv][width]
@@ -46,6 +48,7 @@ struct SelectArgs {
     float *out_mass;       // [B][Hkv][out_width], or none
     int Hkv, keep, first, last;
     int most;              // tokens that the table and mass can hold
+    int held;              // ranks that a block holds
     long long width, out_width;
 };
 
@@ -56,8 +59,9 @@ __device__ __forceinline__ uint32_t rank_of(float x)
     return x != x ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Inclusive scan over the block's 1024 threads; total: of all of them.
-__device__ __forceinline__ int block_scan(int x, int *warps, int tid, int &total)
+// Inclusive scan over the block's 1024 threads.  `warps` is not used again
+// before a barrier.
+__device__ __forceinline__ int block_scan(int x, int *warps, int tid)
 {
     const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -69,138 +73,298 @@ __device__ __forceinline__ int block_scan(int x, int *warps, int tid, int &total
     if (lane == 31)
         warps[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int w = warps[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o)
-                w += y;
-        }
-        warps[lane] = w;
-    }
-    __syncthreads();
-    total = warps[kSelectWarps - 1];
-    x += warp ? warps[warp - 1] : 0;
-    __syncthreads();
+    const int sums = warps[lane];
+    return x + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The word, or four, at p of the cluster's block `rank`.
+__device__ __forceinline__ int cluster_load(const int *p, uint32_t rank)
+{
+    int x;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.b32 %0, [a];\n\t}"
+                 : "=r"(x)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
     return x;
 }
 
-// A block a head of a sequence.  The k-th largest rank is found digit by digit
-// (11, 11 and 10 bits), from a histogram of the tokens that share the digits so
-// far; then each warp counts, and after a scan writes, its run of the tokens.
+__device__ __forceinline__ int4 cluster_load4(const int *p, uint32_t rank)
+{
+    int4 x;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(smem_u32(p)), "r"(rank)
+                 : "memory");
+    return x;
+}
+
+constexpr int kListed = 4096;  // tokens of the first digit that are listed
+
+struct __align__(16) SelectSmem {
+    int bins[3][kBins];    // of each digit
+    int halves[2][kBins];  // the cluster's, summed over half of its blocks each
+    uint32_t list[kListed];
+    int warps[6][kSelectWarps], found[3][3], counts[2], listed;
+    uint4 ranks[1];        // [held / 4]
+};
+
+// A cluster of CS blocks a head of a sequence, each with a run of its tokens.
+// The k-th largest rank is found digit by digit (11, 11 and 10 bits): a
+// histogram in each block of those of its tokens that share the digits so far,
+// summed by all blocks of the cluster, which then know the next digit.  Mostly
+// few tokens share the first digit; those are listed, and the other two digits
+// found by each block from all lists, which spares two exchanges of histograms
+// (5000 cycles each).  Then each block counts what it keeps, and each warp of
+// it, and writes it behind what those before it keep.  mass is read once, as
+// ranks into shared memory.
+template <int CS>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ SelectArgs a)
 {
-    __shared__ int bins[kBins];
-    __shared__ int warps[kSelectWarps], found[2];
-    chain_wait();
+    extern __shared__ __align__(16) char smem[];
+    SelectSmem &sm = *reinterpret_cast<SelectSmem *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bh = blockIdx.x, b = bh / a.Hkv;
+    const uint32_t me = CS > 1 ? cluster_rank() : 0u;
+    for (int i = tid; i < 3 * kBins; i += kSelectThreads)
+        (&sm.bins[0][0])[i] = 0;
+    if (tid == 0)
+        sm.listed = 0;
+    chain_wait();
+    const int bh = blockIdx.x / CS, b = bh / a.Hkv;
     const int given = a.seq_lens[b], n = min(max(given, 0), a.most);
-    const int m = min(n, a.keep);
-    if (bh % a.Hkv == 0 && tid == 0) {
+    if (bh % a.Hkv == 0 && me == 0 && tid == 0) {
         if (given != n)
             record_bounds(0xa01);
-        a.out_lens[b] = m;
+        a.out_lens[b] = min(n, a.keep);
     }
     const float *const mass = a.mass + bh * a.width;
     int *const kept = a.kept + (long long)bh * a.keep;
     float *const out_mass = a.out_mass ? a.out_mass + bh * a.out_width : nullptr;
+    // this block's run: whole warps' runs of 128 tokens
+    constexpr int LINE = 128;
+    const int each = (n + CS * kSelectWarps * LINE - 1) / (CS * kSelectWarps * LINE) * LINE;  // of a warp
+    const int from = min((int)me * each * kSelectWarps, n), to = min(from + each * kSelectWarps, n);
     if (n <= a.keep) {
-        for (int i = tid; i < n; i += kSelectThreads) {
+        for (int i = from + tid; i < to; i += kSelectThreads) {
             kept[i] = i;
             if (out_mass)
                 out_mass[i] = mass[i];
         }
-        return;
+        return;  // (all blocks of the cluster do)
     }
-    // (keep >= first + last, and n > keep: the two ends do not meet)
+    // (keep >= first + last, and n > keep: the two ends do not meet.)  The ends
+    // rank above every number.
     const int lo = a.first, hi = n - a.last;
-    int want = a.keep - a.first - a.last;  // of the others
-    uint32_t prefix = 0;
-    int ties = 0;                          // tokens at the threshold that are kept
-    if (want > 0) {
-        int shift = 21, bits = 11;
-        for (int pass = 0; pass < 3; ++pass) {
-            for (int i = tid; i < kBins; i += kSelectThreads)
-                bins[i] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += kSelectThreads) {
-                const uint32_t r = rank_of(mass[i]);
-                if (pass == 0 || r >> (shift + bits) == prefix)
-                    atomicAdd(&bins[r >> shift & ((1u << bits) - 1u)], 1);
-            }
-            __syncthreads();
-            // from the top: thread t has the bins 2t' and 2t' + 1, t' = 1023 - t
-            const int top = kBins - 1 - 2 * tid;
-            const int c1 = bins[top], c0 = bins[top - 1];
-            int total;
-            const int incl = block_scan(c0 + c1, warps, tid, total), before = incl - c0 - c1;
-            if (before < want && want <= incl) {
-                const bool upper = before + c1 >= want;
-                found[0] = upper ? top : top - 1;
-                found[1] = upper ? before : before + c1;
-            }
-            __syncthreads();
-            prefix = prefix << bits | (uint32_t)found[0];
-            want -= found[1];
-            const int next = pass == 1 ? 10 : 11;
-            __syncthreads();
-            if (pass < 2) {
-                bits = pass == 0 ? 11 : next;
-                shift -= bits;
-            }
-        }
-        ties = want;
-    } else {
-        prefix = 0xffffffffu;  // (no weight ranks above it)
+    const bool held = to - from <= a.held;
+    auto fetch = [&](int i) {  // of tokens i .. i + 3; nothing behind the run
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x[k] = i + k < to ? mass[i + k] : 0.f;
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            r[k] = i + k < lo || i + k >= hi ? 0xffffffffu : rank_of(x[k]);
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    };
+    if (held) {
+#pragma unroll 2
+        for (int i = from + 4 * tid; i < to; i += 4 * kSelectThreads)
+            sm.ranks[(i - from) / 4] = fetch(i);
     }
-    const bool none = a.keep == a.first + a.last;
-    // each warp's run of tokens
-    const int each = (n + kSelectWarps * 32 - 1) / (kSelectWarps * 32) * 32, from = min(warp * each, n),
-              to = min(from + each, n);
-    auto look = [&](int i, bool &sure, bool &tie) {
-        sure = tie = false;
-        if (i < to) {
-            const bool end = i < lo || i >= hi;
-            const uint32_t r = end || none ? 0u : rank_of(mass[i]);
-            sure = end || (!none && r > prefix);
-            tie = !end && !none && r == prefix;
+    __syncthreads();
+    auto ranks = [&](int i) { return held ? sm.ranks[(i - from) / 4] : fetch(i); };
+    int want = a.keep;
+    uint32_t prefix = 0;
+    bool listed = false;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+        const int shift = kShift[pass], bits = kBits[pass];
+        auto count = [&](uint32_t r) { atomicAdd(&sm.bins[pass][r >> shift & ((1u << bits) - 1u)], 1); };
+        if (pass > 0 && listed) {
+            // of the block warp / (kSelectWarps / CS)
+            const uint32_t k = warp / (kSelectWarps / CS);
+            const int many = cluster_load(&sm.listed, k);
+            for (int i = tid % (kSelectThreads / CS); i < many; i += kSelectThreads / CS) {
+                const uint32_t r = (uint32_t)cluster_load((const int *)&sm.list[i], k);
+                if (r >> (shift + bits) == prefix)
+                    count(r);
+            }
+        } else {
+#pragma unroll 2
+            for (int i = from + 4 * tid; i < to; i += 4 * kSelectThreads) {
+                const uint4 r = ranks(i);
+                const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i + k < to && (pass == 0 || x[k] >> (shift + bits) == prefix))
+                        count(x[k]);
+            }
         }
+        // from the top: thread t has the bins 2t' and 2t' + 1, t' = 1023 - t
+        const int top = kBins - 1 - 2 * tid;
+        int2 c;
+        if (CS > 1 && !listed) {
+            cluster_sync();
+            // four bins of half of the blocks a thread
+            int4 x[CS > 1 ? CS / 2 : 1];
+            const int quad = tid % (kBins / 4) * 4, half = tid / (kBins / 4);
+#pragma unroll
+            for (int k = 0; k < CS / 2; ++k)
+                x[k] = cluster_load4(&sm.bins[pass][quad], (me + half * (CS / 2) + k) % CS);
+#pragma unroll
+            for (int k = 1; k < CS / 2; ++k)
+                x[0] = make_int4(x[0].x + x[k].x, x[0].y + x[k].y, x[0].z + x[k].z, x[0].w + x[k].w);
+            *reinterpret_cast<int4 *>(&sm.halves[half][quad]) = x[0];
+            __syncthreads();
+            const int2 y = *reinterpret_cast<const int2 *>(&sm.halves[0][top - 1]);
+            c = *reinterpret_cast<const int2 *>(&sm.halves[1][top - 1]);
+            c = make_int2(c.x + y.x, c.y + y.y);
+        } else {
+            __syncthreads();
+            c = *reinterpret_cast<const int2 *>(&sm.bins[pass][top - 1]);
+        }
+        const int incl = block_scan(c.x + c.y, sm.warps[pass], tid), before = incl - c.x - c.y;
+        if (before < want && want <= incl) {
+            const bool upper = before + c.y >= want;
+            sm.found[pass][0] = upper ? top : top - 1;
+            sm.found[pass][1] = upper ? before : before + c.y;
+            sm.found[pass][2] = upper ? c.y : c.x;
+        }
+        __syncthreads();
+        prefix = prefix << bits | (uint32_t)sm.found[pass][0];
+        want -= sm.found[pass][1];
+        if (CS > 1 && pass == 0) {
+            listed = sm.found[0][2] <= kListed;  // of all blocks
+            if (listed) {
+#pragma unroll 2
+                for (int i = from + 4 * tid; i < to; i += 4 * kSelectThreads) {
+                    const uint4 r = ranks(i);
+                    const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (i + k < to && x[k] >> shift == prefix)
+                            sm.list[atomicAdd(&sm.listed, 1)] = x[k];
+                }
+                cluster_sync();
+            }
+        }
+    }
+    const int ties = want;  // tokens at the threshold that are kept, the first ones
+    const int first = from + warp * each, end = min(first + each, to);
+    // of a thread's four tokens: those above the threshold, those at it (in the upper half)
+    auto look = [&](int i, uint32_t (&x)[4]) {
+        const uint4 r = i < end ? ranks(i) : make_uint4(0, 0, 0, 0);
+        x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < end)
+                c += (x[k] > prefix) + ((x[k] == prefix) << 16);
+        return c;
     };
     int n_sure = 0, n_tie = 0;
-    for (int i = from; i < to; i += 32) {
-        bool sure, tie;
-        look(i + lane, sure, tie);
-        n_sure += __popc(__ballot_sync(0xffffffffu, sure));
-        n_tie += __popc(__ballot_sync(0xffffffffu, tie));
+#pragma unroll 2
+    for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
+        uint32_t x[4];
+        const int c = look(i, x);
+        n_sure += c & 0xffff;
+        n_tie += c >> 16;
     }
-    int total;
-    int at_sure = block_scan(lane == 0 ? n_sure : 0, warps, tid, total) - n_sure;
-    int at_tie = block_scan(lane == 0 ? n_tie : 0, warps, tid, total) - n_tie;
-    at_sure = __shfl_sync(0xffffffffu, at_sure, 0);
-    at_tie = __shfl_sync(0xffffffffu, at_tie, 0);
-    const unsigned below = (1u << lane) - 1u;
-    for (int i = from; i < to; i += 32) {
-        bool sure, tie;
-        look(i + lane, sure, tie);
-        const unsigned s = __ballot_sync(0xffffffffu, sure), t = __ballot_sync(0xffffffffu, tie);
-        const int rank = at_tie + __popc(t & below);  // of the ties before this one
-        if (sure || (tie && rank < ties)) {
-            const int slot = at_sure + __popc(s & below) + min(rank, ties);
-            kept[slot] = i + lane;
-            if (out_mass)
-                out_mass[slot] = mass[i + lane];
+    n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+    n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+    const int sure_incl = block_scan(lane == 0 ? n_sure : 0, sm.warps[3], tid);
+    const int tie_incl = block_scan(lane == 0 ? n_tie : 0, sm.warps[4], tid);
+    if (tid == kSelectThreads - 1) {
+        sm.counts[0] = sure_incl;
+        sm.counts[1] = tie_incl;
+    }
+    int at_sure = __shfl_sync(0xffffffffu, sure_incl - n_sure, 0), at_tie = __shfl_sync(0xffffffffu, tie_incl - n_tie, 0);
+    if constexpr (CS > 1) {
+        cluster_sync();
+        const bool ahead = lane < (int)me;
+        at_sure += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[0], lane) : 0);
+        at_tie += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[1], lane) : 0);
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
+        uint32_t x[4];
+        const int c = look(i, x);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
         }
-        at_sure += __popc(s);
-        at_tie += __popc(t);
+        int sure = at_sure + (incl & 0xffff) - (c & 0xffff), tie = at_tie + (incl >> 16) - (c >> 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k >= end)
+                continue;
+            const bool above = x[k] > prefix, at = x[k] == prefix;
+            if (above || (at && tie < ties)) {
+                const int slot = sure + min(tie, ties);
+                kept[slot] = i + k;
+                if (out_mass)
+                    out_mass[slot] = mass[i + k];
+            }
+            sure += above;
+            tie += at;
+        }
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
+        at_sure += all & 0xffff;
+        at_tie += all >> 16;
     }
+    if constexpr (CS > 1)  // a block's counts and list are read until here
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int CS>
+int launch_select(SelectArgs &s, long long heads, cudaStream_t stream, char *msg, size_t msg_len)
+{
+    KernelInfo ki;
+    const int rc = prepare_kernel((const void *)evict_select_kernel<CS>, (int)sizeof(SelectSmem) + kHeld * 4, &ki, msg, msg_len);
+    if (rc != MERCURY_OK)
+        return rc;
+    const int line = CS * kSelectWarps * 128, run = ((s.most - 1) / line + 1) * (kSelectWarps * 128);
+    s.held = run < kHeld ? run : kHeld;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(heads * CS));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = sizeof(SelectSmem) + s.held * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {CS, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = CS > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CS>, s);
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "cache eviction launch: %s", cudaGetErrorString(e));
+        return MERCURY_ECUDA;
+    }
+    return MERCURY_OK;
 }
 
 // ------------------------------------------------------------------ and their rows
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveAhead = 4;  // rows that a thread has on the way, of keys and of values
+constexpr int kMoveAhead = 2;  // rows that a thread has on the way, of keys and of values
 
 struct MoveArgs {
     PagedView src, dst;
@@ -348,16 +512,26 @@ struct Held<MERCURY_ELEM_E2M1> {
         // bits and then once more
         const uint32_t s2 = e4m3_to_f16(s | s << 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = w[i / 4] >> (8 * (i % 4)) & 0xffu;
-            uint32_t x;
-            asm("{\n\t.reg .b8 lo, hi;\n\tmov.b16 {lo, hi}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, lo;\n\tmul.rn.f16x2 %0, %0, %2;\n\t}"
-                : "=r"(x)
-                : "h"((uint16_t)byte), "r"(s2));
-            o[i] = scaled_bf16(x, scale);
+        for (int i = 0; i < 2; ++i) {
+            o[4 * i] = scaled_bf16(mul_f16(e2m1_to_f16<0>(w[i]), s2), scale);
+            o[4 * i + 1] = scaled_bf16(mul_f16(e2m1_to_f16<1>(w[i]), s2), scale);
+            o[4 * i + 2] = scaled_bf16(mul_f16(e2m1_to_f16<2>(w[i]), s2), scale);
+            o[4 * i + 3] = scaled_bf16(mul_f16(e2m1_to_f16<3>(w[i]), s2), scale);
         }
     }
 };
+
+// 16 elements: a whole sector where the output allows it (two stores of 16
+// bytes each write half of one).
+__device__ __forceinline__ void store_block(__nv_bfloat16 *p, const uint32_t (&o)[8])
+{
+    if (((uintptr_t)p & 31u) == 0) {
+        st_global_v8(p, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(p + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
 
 template <int ELEM, int D>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ ReadArgs a)
@@ -400,11 +574,9 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
         const long long to = ((long long)bh * a.S + base + i * TOKENS) * D + blk * 16;
         uint32_t o[8];
         x[i].widen(o, ks);
-        *reinterpret_cast<uint4 *>(a.k + to) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(a.k + to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        store_block(a.k + to, o);
         y[i].widen(o, vs);
-        *reinterpret_cast<uint4 *>(a.v + to) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(a.v + to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        store_block(a.v + to, o);
     }
 }
 
@@ -441,19 +613,36 @@ int launch_kv_evict(const mercury_paged_cache &cache, const mercury_paged_cache 
                     long long out_width, cudaStream_t stream, char *msg, size_t msg_len)
 {
     const long long held = (long long)cache.max_pages * cache.page_size;
-    SelectArgs s = {mass, seq_lens, out_lens, kept, out_mass, cache.Hkv, keep, first, last,
-                    (int)(held < width ? held : width), width, out_width};
+    SelectArgs s = {};
+    s.mass = mass;
+    s.seq_lens = seq_lens;
+    s.out_lens = out_lens;
+    s.kept = kept;
+    s.out_mass = out_mass;
+    s.Hkv = cache.Hkv;
+    s.keep = keep;
+    s.first = first;
+    s.last = last;
+    s.most = (int)(held < width ? held : width);
+    s.width = width;
+    s.out_width = out_width;
     const long long heads = (long long)cache.B * cache.Hkv;
-    if (heads > 0x7fffffffLL) {
+    if (heads * kMaxCluster > 0x7fffffffLL) {
         snprintf(msg, msg_len, "too many heads for one call (%lld)", heads);
         return MERCURY_EINVAL;
     }
-    const cudaError_t e =
-        launch_chained(evict_select_kernel, dim3((unsigned)heads), kSelectThreads, 0, stream, s);
-    if (e != cudaSuccess) {
-        snprintf(msg, msg_len, "cache eviction launch: %s", cudaGetErrorString(e));
-        return MERCURY_ECUDA;
-    }
+    // As many blocks of a head as leave one for each SM, where each gets 2K
+    // tokens or more.
+    int sms = 0;
+    int rc = device_sm_count(&sms);
+    if (rc != MERCURY_OK)
+        return rc;
+    rc = heads * 8 <= sms && s.most > 8192   ? launch_select<8>(s, heads, stream, msg, msg_len)
+         : heads * 4 <= sms && s.most > 4096 ? launch_select<4>(s, heads, stream, msg, msg_len)
+         : heads * 2 <= sms && s.most > 2048 ? launch_select<2>(s, heads, stream, msg, msg_len)
+                                             : launch_select<1>(s, heads, stream, msg, msg_len);
+    if (rc != MERCURY_OK)
+        return rc;
     MoveArgs a;
     a.src = make_view(cache);
     a.dst = make_view(into);

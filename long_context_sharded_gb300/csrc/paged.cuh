@@ -149,4 +149,27 @@ __device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t w)
     return r;
 }
 
+// Byte I of w, two e2m1 codes, as fp16: exact, the lower half's in the lower.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_to_f16(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 1)
+        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, y;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 2)
+        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, z;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b8 x, y, z, w;\n\tmov.b32 {x, y, z, w}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, w;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 }  // namespace mercury

@@ -55,58 +55,6 @@ constexpr float kWider = 0x1p-21f;
 // 9.4e-8, and five roundings of 6e-8 each).
 constexpr float kRotationError = 6e-7f;
 
-// The scale's byte.  amax: the largest magnitude, known to e; g > 0;
-// real(): the largest magnitude in 64 bits, asked for where e > 0.
-template <typename Real>
-__device__ __forceinline__ uint32_t block_scale(float amax, float e, float g, Real real)
-{
-    if (amax == INFINITY)
-        return 0x7eu;
-    const float r = 1.f / (6.f * g);
-    const uint32_t both = pack_e4m3(fmaxf(amax - e, 0.f) * r * (1.f - kWider), (amax + e) * r * (1.f + kWider));
-    const uint32_t lo = both & 0xffu, hi = both >> 8;
-    if (lo == hi)
-        return lo;
-    const float m = 3.f * (e4m3_value(lo) + e4m3_value(hi));  // 6 times the border between them
-    const int side = e > 0.f ? side_of(real(), m, g) : side_of(amax, m, g);
-    return side > 0 || (side == 0 && (lo & 1u)) ? hi : lo;
-}
-
-// N codes, four bits each.  y: the elements, known to e[]; s, g > 0: the scales;
-// real(i): element i in 64 bits, asked for where e[i] > 0.
-template <int N, typename Real>
-__device__ __forceinline__ uint32_t block_codes(const float (&y)[N], const float (&e)[N], float s, float g, Real real)
-{
-    uint32_t w = 0, differ = 0;
-    // where s is zero the codes are, and where s g has left the 32-bit range the
-    // codes are what the products make of that
-    const float r = s > 0.f ? 1.f / (s * g) : 0.f;
-    const float below = r * (1.f - kWider), above = r * (1.f + kWider);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float a = fabsf(y[i]), b = fabsf(y[i + 1]);
-        const uint32_t lo = pack_e2m1(fmaxf(a - e[i], 0.f) * below, fmaxf(b - e[i + 1], 0.f) * below);
-        const uint32_t hi = pack_e2m1((a + e[i]) * above, (b + e[i + 1]) * above);
-        w |= lo << (4 * i);
-        differ |= (lo ^ hi) << (4 * i);
-    }
-    if (differ) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (differ >> (4 * i) & 15u) {
-                const uint32_t c = w >> (4 * i) & 7u;
-                // the border above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5
-                const float m = s * (c < 4 ? 0.5f * c + 0.25f : c < 6 ? (float)c - 1.5f : 5.f);
-                const int side = e[i] > 0.f ? side_of(fabs(real(i)), m, g) : side_of(fabsf(y[i]), m, g);
-                w += (side > 0 || (side == 0 && (c & 1u)) ? 1u : 0u) << (4 * i);
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        w |= (y[i] < 0.f ? 8u : 0u) << (4 * i);
-    return w;
-}
-
 // Element a (or with `second` b) of a pair at one position, in 64 bits.
 // phase: the position's angle in turns of 2^-64.
 __device__ __noinline__ double rotated_real(float a, float b, bool second, unsigned long long phase, float magnitude)
@@ -114,6 +62,107 @@ __device__ __noinline__ double rotated_real(float a, float b, bool second, unsig
     double s, c;
     sincospi((double)(long long)phase * 0x1p-63, &s, &c);
     return (second ? (double)b * c + (double)a * s : (double)a * c - (double)b * s) * magnitude;
+}
+
+// Where N elements of a block come from, for the rare ones that are settled in
+// 64 bits: N of x, from element `at` of the head on, pairs of the plan's.
+struct Source {
+    const float *first, *second;  // of each element's pair
+    unsigned long long pos;
+    const unsigned long long *turns;
+    float magnitude;
+    int at, rot, interleaved;
+    __device__ __forceinline__ double real(int i) const
+    {
+        const int j = at + i;
+        if (j >= rot)  // a block may be turned in part
+            return first[i];
+        const int pair = interleaved ? j / 2 : j < rot / 2 ? j : j - rot / 2;
+        return rotated_real(first[i], second[i], interleaved ? j & 1 : j >= rot / 2, turns[pair] * pos, magnitude);
+    }
+};
+
+// Which of the two scales' bytes (neighbours) a block's is: amax is next to 6 g
+// times the border between them.  `from` where the elements were rotated:
+// amax is then that of both halves of the block, y[N] this thread's half, and
+// the threads of `both` settle it together.
+template <int N>
+__device__ __noinline__ uint32_t settle_scale(uint32_t lo, uint32_t hi, float amax, float off, float g, const float *y,
+                                              const Source *from, unsigned int both)
+{
+    const float m = 3.f * (e4m3_value(lo) + e4m3_value(hi));  // 6 times the border
+    int side;
+    if (from) {
+        double x = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i)
+            if (fabsf(y[i]) + 2.f * off >= amax)  // it may be the largest
+                x = fmax(x, fabs(from->real(i)));
+        if (both) {
+            __syncwarp(both);
+            x = fmax(x, __shfl_xor_sync(both, x, 1));
+        }
+        side = side_of(x, m, g);
+    } else {
+        side = side_of(amax, m, g);
+    }
+    return side > 0 || (side == 0 && (lo & 1u)) ? hi : lo;
+}
+
+// w with the codes settled whose bits in `differ` are not all zero: each is
+// that of w or the next.
+__device__ __noinline__ uint32_t settle_codes(uint32_t w, uint32_t differ, float s, float g, const float *y, const Source *from)
+{
+    while (differ) {
+        const int i = (__ffs(differ) - 1) / 4;
+        differ &= ~(15u << (4 * i));
+        const uint32_t c = w >> (4 * i) & 7u;
+        // the border above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5
+        const float m = s * (c < 4 ? 0.5f * c + 0.25f : c < 6 ? (float)c - 1.5f : 5.f);
+        const int side = from ? side_of(fabs(from->real(i)), m, g) : side_of(fabsf(y[i]), m, g);
+        w += (side > 0 || (side == 0 && (c & 1u)) ? 1u : 0u) << (4 * i);
+    }
+    return w;
+}
+
+// Largest magnitude, NaN where there is one.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The two ends' bytes for a block whose largest magnitude is amax, known to
+// off: the lower end's in the lower byte.  (A NaN gives NaN, an infinity 448.)
+__device__ __forceinline__ uint32_t scale_ends(float amax, float off, float g)
+{
+    const float r = 1.f / (6.f * g);
+    return pack_e4m3(max_nan(amax - off, 0.f) * r * (1.f - kWider), (amax + off) * r * (1.f + kWider));
+}
+
+// Eight codes of four bits: the lower ends' magnitudes in lo, and in hi the
+// upper ends' with the elements' signs.  s g: both scales; off: what the
+// elements are known to.  Where s is zero all codes are.
+__device__ __forceinline__ void code_ends(const float (&y)[8], float off, float s, float g, uint32_t &lo, uint32_t &hi)
+{
+    const float r = s > 0.f ? 1.f / (s * g) : 0.f;
+    const float below = r * (1.f - kWider), above = r * (1.f + kWider);
+    const float more = off * above * (1.f + kWider);
+    lo = hi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        float l[2], h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float a = fabsf(y[i + j]);
+            l[j] = fmaf(a, below, -more);  // (below zero: a zero of either sign)
+            h[j] = copysignf(fmaf(a, above, more), y[i + j]);
+        }
+        lo |= pack_e2m1(l[0], l[1]) << (4 * i);
+        hi |= pack_e2m1(h[0], h[1]) << (4 * i);
+    }
+    lo &= 0x77777777u;
 }
 
 }  // namespace mercury
