@@ -40,13 +40,17 @@ struct MassArgs {
     float *out;         // the same
     long long width;
     int r0, rows;       // this launch's rows of each head
-    float mul, mul_lo;  // log2(e) / sqrt(d)
+    float mul, mul_lo;  // log2(e) / sqrt(d), and what its rounding leaves out
 };
 
-// A row of queries: factor on its scores (its second part: what rounding left
-// out), -lse in log2 units (-inf: counts nothing) likewise.
+// A row of queries: a weight is 2^(score * mul + nl) * rest.  nl, lse in log2
+// units, would cost the weight its rounding (lse 20: 1e-6), and mul's rounding
+// as much; so nl is taken with the rounded mul, which leaves of the latter what
+// score and lse differ by, and what nl's rounding leaves out goes to rest.
+// A row that counts nothing: nl = -inf, rest = 0.
 struct Row {
-    float mul, mul_lo, nl, nl_lo;
+    float mul, nl, rest;
+    int step;  // of the new tokens
 };
 
 // 16 keys as the first operand: rows g and g + 8.
@@ -157,6 +161,11 @@ __device__ __forceinline__ int mass_tiles(const MassArgs &a, int b)
 {
     return (mass_keys(a, b) + kMassTile - 1) / kMassTile;
 }
+
+template <bool M>
+struct Masked {
+    static constexpr bool value = M;
+};
 
 // Where a share's first tile lies.
 struct Spot {
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                     q[kk] = live ? *reinterpret_cast<const uint2 *>(src + kk / (RUN / 4) * (4 * RUN) + t * RUN +
                                                                     kk % (RUN / 4) * 4)
                                  : make_uint2(0, 0);
-                float mul = a.mul, mul_lo = a.mul_lo;
+                float mul = a.mul, mul_lo = a.mul_lo;  // to log2 units, of the product of the operands
                 if constexpr (K::kF16) {
                     // to fp16, scaled by a power of two that brings the row's
                     // largest element to [2^14, 2^15): exact down to 2^-28 of it
@@ -311,21 +320,21 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                 for (int kk = 0; kk < KK; ++kk)
                     qs[(rt * KK + kk) * 32 + lane] = q[kk];
                 if (t == 0) {
-                    // lse times log2(e), in two parts: their rounding would be that
-                    // of the whole exponent
-                    constexpr float kLog2eLo = 1.9259629911266174e-8f;  // log2(e) less its nearest float
                     const float l = live ? a.lse[(long long)this_job * p.R + r] : INFINITY;
-                    const float hi = -l * kLog2e;
-                    rows[rt * 8 + g] = Row{mul, mul_lo, hi, fabsf(l) < INFINITY ? fmaf(-l, kLog2e, -hi) - l * kLog2eLo : 0.f};
+                    constexpr float kLog2eLo = 1.9259629911266174e-8f;  // log2(e) less its nearest float
+                    const float nl = -l * kLog2e;
+                    const float off = mul == 0.f ? 0.f : mul_lo / mul;
+                    const float more = fmaf(-l, kLog2e, -nl) - l * kLog2eLo + l * kLog2e * off;  // what nl leaves out
+                    const bool counts = fabsf(l) < INFINITY || l != l;
+                    rows[rt * 8 + g] = Row{mul, counts ? nl : -INFINITY, counts ? exp2f(more) : 0.f, i};
                 }
             }
             __syncthreads();
         }
         const int k0 = now.j * kMassTile + warp * 16;
         const int seen_by_all = p.causal ? now.keys - n_new + 1 : now.keys;
-        const bool edge = k0 + 16 > seen_by_all;
         float sum[2] = {0.f, 0.f};
-        if (k0 < now.keys)
+        auto add_rows = [&](auto masked) {
 #pragma unroll 2
             for (int rt = 0; rt < n_rt; ++rt) {
                 // in 2 sums of d/2 products each, added at the end
@@ -340,17 +349,22 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                     const Row r = rows[rt * 8 + 2 * t + e];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float y = x[0][2 * i + e] + x[1][2 * i + e];
-                        float w = ex2_approx(fmaf(y, r.mul, r.nl) + fmaf(y, r.mul_lo, r.nl_lo));
-                        if (edge) {
-                            const int row = a.r0 + rt * 8 + 2 * t + e;
-                            const int lim = p.causal ? now.keys - n_new + row % p.Sq + 1 : now.keys;
-                            w = k0 + g + 8 * i < lim ? w : 0.f;
+                        float w = ex2_approx(fmaf(x[0][2 * i + e] + x[1][2 * i + e], r.mul, r.nl));
+                        if constexpr (decltype(masked)::value) {
+                            const int lim = p.causal ? seen_by_all + r.step : now.keys;
+                            w = k0 + g + 8 * i < lim && r.rest != 0.f ? w : 0.f;
                         }
-                        sum[i] += r.nl == -INFINITY ? 0.f : w;
+                        sum[i] = fmaf(w, r.rest, sum[i]);
                     }
                 }
             }
+        };
+        if (k0 + 16 > seen_by_all) {
+            if (k0 < now.keys)
+                add_rows(Masked<true>());
+        } else {
+            add_rows(Masked<false>());
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);

@@ -42,16 +42,16 @@ namespace mercury {
 namespace {
 
 // ROWS: rows of a row tile, 4, 8 or 16.  Every computing warp has all its rows
-// and its own 32 keys of each tile.  With four rows both terms of a weight
+// and its own 32 H keys of each tile.  With four rows both terms of a weight
 // share an instruction: columns 0 to 3 are the rows' first terms, 4 to 7 their
 // second ones.
-template <int D, int ROWS>
+template <int D, int ROWS, int H>
 struct Cfg {
-    static constexpr int kWarps = ROWS <= 8 ? 12 : 8;  // computing warps
+    static constexpr int kWarps = 8;              // computing warps
     static constexpr int kThreads = (kWarps + kCopyWarps) * 32;
     static constexpr int kRowB = D / 2 + D / 16;  // bytes of one key
     static constexpr int kRun = D / 16;           // bytes of a run of a row that a thread takes
-    static constexpr int kKeys = 32;              // keys of a warp's step
+    static constexpr int kKeys = 32 * H;          // keys of a warp's step
     static constexpr int kTile = kKeys * kWarps;
     static constexpr int kPart = kTile * kRowB;
     static constexpr int kStage = 2 * kPart;
@@ -59,17 +59,18 @@ struct Cfg {
     static constexpr int kRed = kWarps * ROWS * 8;             // each warp's maxima and sums
     static constexpr int kRowBytes = kWarps * kCols * D * 4;   // the warps' partial columns
     static constexpr bool kOwnRows = kRowBytes > kStage;       // in memory of their own, or in a stage
-    static constexpr int kRoom = 232448 - 256 - kRed - (kOwnRows ? kRowBytes : 0);
+    static constexpr int kQueries = kCols * D * 2 + kCols * 4;  // the job's, as operands, and their factors
+    static constexpr int kRoom = 232448 - 256 - kRed - kQueries - (kOwnRows ? kRowBytes : 0);
     static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
     static constexpr int kCtl = kStages * kStage + kRed + kStages * 16;
-    static constexpr int kPartsAt = (kCtl + 32 + 15) / 16 * 16;
+    static constexpr int kQueriesAt = (kCtl + 32 + 15) / 16 * 16;
+    static constexpr int kPartsAt = kQueriesAt + kQueries;
     static constexpr int kSmem = kPartsAt + (kOwnRows ? kRowBytes : 0);
     static_assert(kStages >= 2 && kSmem <= 232448, "a stage to read and one on its way");
     static_assert(kTile % kUnits == 0, "whole eighths of a tile");
     // registers a thread after the split (setmaxnreg); their sum may not
     // exceed what the launch provides
-    static constexpr uint32_t kRegsCopy = ROWS <= 8 ? 64 : 72;
-    static constexpr uint32_t kRegsCompute = ROWS <= 8 ? 144 : 216;
+    static constexpr uint32_t kRegsCopy = 72, kRegsCompute = 216;
     static constexpr int kMinLaunchRegs = (int)(kRegsCopy * 128 + kRegsCompute * kWarps * 32 + kThreads - 1) / kThreads;
 };
 
@@ -124,11 +125,11 @@ __device__ __forceinline__ int key_at(int g)
 // The copying warps: every tile of the share into the ring, a stage as soon as
 // the computing warps have left it.  A tile's runs of box_rows keys, each in
 // one page, are dealt to the lanes of the four warps in turn.
-template <int D, int ROWS>
+template <int D, int ROWS, int H>
 __device__ __forceinline__ void copy_tiles(const PagedArgs &a, Place at, int end, char *smem, uint64_t *full,
                                            uint64_t *empty, Stop *stop, int warp, int lane)
 {
-    using C = Cfg<D, ROWS>;
+    using C = Cfg<D, ROWS, H>;
     constexpr int ROWB = C::kRowB, TILE = C::kTile, NS = C::kStages;
     const int first = (lane * kCopyWarps + warp) * a.box_rows;  // this lane's run
     // its page, asked for a tile ahead
@@ -240,10 +241,10 @@ __device__ __forceinline__ int part_at(int row, int col)
     return (((col >> 2) ^ (((row >> 1) & 3) | (row & 1) << 2)) << 2) + (col & 3);
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(const __grid_constant__ PagedArgs a)
+template <int D, int ROWS, int H>
+__global__ void __launch_bounds__(Cfg<D, ROWS, H>::kThreads, 1) attn_paged4_kernel(const __grid_constant__ PagedArgs a)
 {
-    using C = Cfg<D, ROWS>;
+    using C = Cfg<D, ROWS, H>;
     constexpr int ROWB = C::kRowB, KEYS = C::kKeys, TILE = C::kTile, NS = C::kStages, kWarps = C::kWarps;
     constexpr int RUN = C::kRun, RW = RUN / 4;  // bytes and words of a thread's run of a row
     constexpr int KK = D / 16, DT = D / 16;     // k-steps of S', 16-row tiles of O'
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
         return;
     if (warp >= kWarps) {
         regs_dec<C::kRegsCopy>();
-        copy_tiles<D, ROWS>(a, at, end, smem, full, empty, stop, warp - kWarps, lane);
+        copy_tiles<D, ROWS, H>(a, at, end, smem, full, empty, stop, warp - kWarps, lane);
         return;
     }
 
@@ -296,33 +297,66 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
     const int g = lane >> 2, t = lane & 3;
     // Row g of the second operand is query row nr * 8 + g (of four rows each is
     // there twice); of S' and O' this thread has the columns nr * 8 + 2t and + 1.
-    uint32_t qf[NR][KK][2];
+    // The operands and the rows' factors lie in shared memory (kept in registers
+    // by every warp, they left room for no more than 12 of them): warp nr loads
+    // those of its rows when a job is known, and puts them there between the two
+    // barriers of the job before.
+    uint2 *const queries = reinterpret_cast<uint2 *>(smem + C::kQueriesAt);  // [nr][k-step][lane]
+    float *const factors = reinterpret_cast<float *>(queries + NR * KK * 32);  // [column]
     int h_kv, row0, n_new;  // of the current job: KV head, first row, new tokens
+    uint2 q[KK];
     float k_scale = 1.f;
     auto load_q = [&]() {
         h_kv = a.n_rt == 1 ? at.hr : at.hr / a.n_rt;
         row0 = (at.hr - h_kv * a.n_rt) * ROWS;
         n_new = new_of(a, at.b);
-        k_scale = a.cache.k_scale[h_kv];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            const int r = row0 + (TWO ? g & 3 : nr * 8 + g);
+        if (warp < NR) {
+            k_scale = a.cache.k_scale[h_kv];
+            const int r = row0 + (TWO ? g & 3 : warp * 8 + g);
             const int head = a.Sq == 1 ? r : r / a.Sq, s = r - head * a.Sq;
             const __nv_bfloat16 *src = a.q + at.b * a.qs.b + (h_kv * a.G + head) * a.qs.h + s * a.qs.s;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                uint2 w = make_uint2(0, 0);
-                if (r < a.R)
-                    w = *reinterpret_cast<const uint2 *>(src + kk / (KK / 2) * (D / 2) + t * (D / 8) + kk % (KK / 2) * 4);
-                qf[nr][kk][0] = w.x;
-                qf[nr][kk][1] = w.y;
-            }
+            for (int kk = 0; kk < KK; ++kk)
+                q[kk] = r < a.R ? *reinterpret_cast<const uint2 *>(src + kk / (KK / 2) * (D / 2) + t * (D / 8) + kk % (KK / 2) * 4)
+                                : make_uint2(0, 0);
         }
     };
+    auto put_q = [&]() {
+        if (warp >= NR)
+            return;
+        // a factor of at least 2^-120, so that a masked score stays -inf
+        // under it; the scale's sign goes to the queries
+        float kmul = a.scale_log2 * k_scale;
+        const uint32_t flip = kmul < 0.f ? 0x80008000u : 0u;
+        kmul = fabsf(kmul);
+        // The queries are taken to fp16: scaled by a power of two that
+        // brings the row's largest element to [2^14, 2^15), their 8 bits
+        // fit exactly down to 2^-28 of it.
+        float top = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(q[kk].x)), fabsf(bf16_hi(q[kk].x))),
+                                   fmaxf(fabsf(bf16_lo(q[kk].y)), fabsf(bf16_hi(q[kk].y)))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // exponent of 2^(14 - e), kept where both it and its inverse are normal
+        int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+        up = min(max(up, -110), 110);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        const float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
+        if (t == 0)
+            factors[warp * 8 + g] = mul < 7.5e-37f ? 7.5e-37f : mul;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            queries[(warp * KK + kk) * 32 + lane] = make_uint2(pack_f16(bf16_lo(q[kk].x) * f, bf16_hi(q[kk].x) * f) ^ flip,
+                                                               pack_f16(bf16_lo(q[kk].y) * f, bf16_hi(q[kk].y) * f) ^ flip);
+    };
     load_q();
+    put_q();
+    named_barrier_sync(1, kWarps * 32);
 
     // O' of 16 elements a thread, by tiles: [0, 1] of the even ones, [2, 3] of
-    // the odd.  The matrix unit truncates, so its own sums are short, a step's,
+    // the odd.  The matrix unit truncates, so its own sums are short, 32 keys',
     // and are added to these by rounding additions.
     float sums[NR][DT][4];
     float m_run[NR][2], l_run[NR][2], l_rest[NR][2], s_mul[NR][2];  // l_rest: what l_run's roundings left out
@@ -330,6 +364,9 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
     const int key_g = key_at<D>(g), key_x = key_at<D>(2 * t), key_y = key_at<D>(2 * t + 1);
     const char *const k_lane = smem + (warp * KEYS + key_g) * ROWB;
     const char *const v_lane = smem + C::kPart + warp * KEYS * ROWB;
+    // which bytes of a row's scales this thread's runs have, and of two rows' its block
+    const uint32_t k_pick = D == 128 ? t | (4 + t) << 4 : t / 2 | (2 + t / 2) << 4;
+    const uint32_t v_pick = D == 128 ? (g & 3) | (4 + (g & 3)) << 4 | 0x4400 : g / 2 | (4 + g / 2) << 4 | 0x4400;
     const float whole_p = t < 2 ? 1.f : 1 << kLowShift, less_p = t < 2 ? 0.f : 1 << kLowShift;
     int stage = 0;
     uint32_t phase = 0;
@@ -349,41 +386,11 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
         const int first_j = at.j;
         int left = min(at.tiles - at.j, (end - at.pos + kUnits - 1) / kUnits);  // its tiles here
         at.pos += (left - 1) * kUnits;                                          // of the last of them
-        // a factor of at least 2^-120, so that a masked score stays -inf
-        // under it; the scale's sign goes to the queries
-        float kmul = a.scale_log2 * k_scale;
-        const uint32_t flip = kmul < 0.f ? 0x80008000u : 0u;
-        kmul = fabsf(kmul);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            // The queries are taken to fp16: scaled by a power of two that
-            // brings the row's largest element to [2^14, 2^15), their 8 bits
-            // fit exactly down to 2^-28 of it.
-            float top = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t x = qf[nr][kk][0], y = qf[nr][kk][1];
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x))),
-                                       fmaxf(fabsf(bf16_lo(y)), fabsf(bf16_hi(y)))));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // exponent of 2^(14 - e), kept where both it and its inverse are normal
-            int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
-            up = min(max(up, -110), 110);
-            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-            float mul = kmul * __uint_as_float((uint32_t)(127 - up) << 23);
-            mul = mul < 7.5e-37f ? 7.5e-37f : mul;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t &x = qf[nr][kk][i];
-                    x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f) ^ flip;
-                }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                s_mul[nr][e] = __shfl_sync(0xffffffffu, mul, (2 * t + e) * 4);
+                s_mul[nr][e] = factors[nr * 8 + 2 * t + e];
                 m_run[nr][e] = -INFINITY;
                 l_run[nr][e] = 0.f;
                 l_rest[nr][e] = 0.f;
@@ -403,55 +410,100 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
             if (kb < at.keys) {
                 const char *const k_s = k_lane + stage * C::kStage, *const v_s = v_lane + stage * C::kStage;
                 // ---- S' = K Q'
-                float sc[NR][2][4];
+                float sc[H][NR][2][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    // rows g and g + 8 of the product: keys key_g + 2m and + 1
-                    uint32_t x[2][2][RW], s[2][2];  // [row][run]
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const char *const row = k_s + (2 * m + i) * ROWB;
-                        load_run(x[i][0], row + t * RUN);
-                        load_run(x[i][1], row + D / 4 + t * RUN);
-                        const uint32_t s0 = *reinterpret_cast<const uint8_t *>(row + D / 2 + t * RUN / 8);
-                        const uint32_t s1 = *reinterpret_cast<const uint8_t *>(row + D / 2 + D / 32 + t * RUN / 8);
-                        const uint32_t both = e4m3_to_f16(s0 | s1 << 8);
-                        s[i][0] = __byte_perm(both, 0, 0x1010);
-                        s[i][1] = __byte_perm(both, 0, 0x3232);
-                    }
+                    for (int m = 0; m < 2; ++m) {
+                        // rows g and g + 8 of the product: keys key_g + 2m and + 1
+                        uint32_t x[2][2][RW], s[2][2];  // [row][run]
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int w = 0; w < RW; ++w) {
-                            const int kk = r * (KK / 2) + w * 2;
-                            const uint32_t x0 = x[0][r][w], x1 = x[1][r][w];
-                            uint32_t f[8] = {e2m1_to_f16<0>(x0), e2m1_to_f16<0>(x1), e2m1_to_f16<1>(x0), e2m1_to_f16<1>(x1),
-                                             e2m1_to_f16<2>(x0), e2m1_to_f16<2>(x1), e2m1_to_f16<3>(x0), e2m1_to_f16<3>(x1)};
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                f[i] = mul_f16(f[i], s[i & 1][r]);
-#pragma unroll
-                            for (int nr = 0; nr < NR; ++nr) {
-                                if (kk == 0)
-                                    mma_first(sc[nr][m], f[0], f[1], f[2], f[3], qf[nr][kk][0], qf[nr][kk][1]);
-                                else
-                                    mma<true>(sc[nr][m], f[0], f[1], f[2], f[3], qf[nr][kk][0], qf[nr][kk][1]);
-                                mma<true>(sc[nr][m], f[4], f[5], f[6], f[7], qf[nr][kk + 1][0], qf[nr][kk + 1][1]);
-                            }
+                        for (int i = 0; i < 2; ++i) {
+                            const char *const row = k_s + (32 * h + 2 * m + i) * ROWB;
+                            load_run(x[i][0], row + t * RUN);
+                            load_run(x[i][1], row + D / 4 + t * RUN);
+                            uint32_t all[RW];  // the row's scales
+                            load_run(all, row + D / 2);
+                            const uint32_t both = e4m3_to_f16(__byte_perm(all[0], all[RW - 1], k_pick));
+                            s[i][0] = __byte_perm(both, 0, 0x1010);
+                            s[i][1] = __byte_perm(both, 0, 0x3232);
                         }
-                }
-                // ---- the masked keys of a column count as -inf
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int w = 0; w < RW; ++w) {
+                                const int kk = r * (KK / 2) + w * 2;
+                                const uint32_t x0 = x[0][r][w], x1 = x[1][r][w];
+                                uint32_t f[8] = {e2m1_to_f16<0>(x0), e2m1_to_f16<0>(x1), e2m1_to_f16<1>(x0), e2m1_to_f16<1>(x1),
+                                                 e2m1_to_f16<2>(x0), e2m1_to_f16<2>(x1), e2m1_to_f16<3>(x0), e2m1_to_f16<3>(x1)};
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    f[i] = mul_f16(f[i], s[i & 1][r]);
+#pragma unroll
+                                for (int nr = 0; nr < NR; ++nr) {
+                                    float *const d = sc[h][nr][m];
+                                    const uint2 q0 = queries[(nr * KK + kk) * 32 + lane], q1 = queries[(nr * KK + kk + 1) * 32 + lane];
+                                    if (kk == 0)
+                                        mma_first(d, f[0], f[1], f[2], f[3], q0.x, q0.y);
+                                    else
+                                        mma<true>(d, f[0], f[1], f[2], f[3], q0.x, q0.y);
+                                    mma<true>(d, f[4], f[5], f[6], f[7], q1.x, q1.y);
+                                }
+                            }
+                    }
+                // Of part c of 32 keys, for O', the thread has block g of keys key_x + c
+                // and key_y + c, the inner axis's columns 2t and 2t + 1: their scales.
+                uint32_t vs[H][4];
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const char *const row = v_s + (32 * h + c) * ROWB + D / 2 + (D == 128 ? g / 4 * 4 : 0);
+                        vs[h][c] = __byte_perm(*reinterpret_cast<const uint32_t *>(row + key_x * ROWB),
+                                               *reinterpret_cast<const uint32_t *>(row + key_y * ROWB), v_pick);
+                    }
                 const int seen_by_all = a.causal ? at.keys - n_new + 1 : at.keys;
-                const bool edge = kb + KEYS > seen_by_all;
-                if (edge) {
+                if (kb + KEYS > seen_by_all) {
+                    // The masked keys of a column count as -inf.  Scales of values
+                    // behind the last key may be anything: those count as zeros.  So
+                    // do those of NaN that only some rows see, whose product with a
+                    // weight of 0 would be NaN; the rows that see one get NaN in its
+                    // block's elements.
+                    int bad = 0x7fffffff;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (kb + 32 * h + key_g + 2 * m + (e >> 1) >= lim[nr][e & 1])
+                                        sc[h][nr][m][e] = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int key = kb + 32 * h + (i ? key_y : key_x) + c;
+                                const bool nan = (vs[h][c] >> (8 * i) & 0x7fu) == 0x7fu;
+                                if (key >= at.keys || (nan && a.causal && n_new > 1)) {
+                                    vs[h][c] &= i ? 0x00ffu : 0xff00u;
+                                    if (key < at.keys)
+                                        bad = min(bad, key);
+                                }
+                            }
+                    }
+                    bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 1));
+                    bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 2));
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int e = 0; e < 2; ++e)
+                            if (bad < lim[nr][e]) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (kb + key_g + 2 * m + (e >> 1) >= lim[nr][e & 1])
-                                    sc[nr][m][e] = -INFINITY;
+                                for (int i = 0; i < DT; ++i)
+                                    sums[nr][i][e] = sums[nr][i][2 + e] = __int_as_float(0x7fffffff);
+                            }
                 }
                 // The maximum moves only when a score exceeds it by 2^kGrow: sum and O
                 // share whatever reference the terms were taken with, and the
@@ -462,7 +514,10 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float x = fmaxf(fmaxf(sc[nr][0][e], sc[nr][0][2 + e]), fmaxf(sc[nr][1][e], sc[nr][1][2 + e]));
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            x = fmaxf(x, fmaxf(fmaxf(sc[h][nr][0][e], sc[h][nr][0][2 + e]), fmaxf(sc[h][nr][1][e], sc[h][nr][1][2 + e])));
                         top[nr][e] = x * s_mul[nr][e];
                         grow |= top[nr][e] > m_run[nr][e] + kGrow<true>;
                     }
@@ -488,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
                         }
                 }
                 // ---- P' as two fp16 terms, a key a column: p[..][m][half][term]
-                uint32_t p[NR][2][2][TERMS];
+                uint32_t p[H][NR][2][2][TERMS];
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
                     float ref[2], sum[2] = {0.f, 0.f};
@@ -496,25 +551,28 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
                     for (int e = 0; e < 2; ++e)
                         ref[e] = m_run[nr][e] == -INFINITY ? 0.f : kUp<true> - m_run[nr][e];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float p0 = ex2_approx(fmaf(sc[nr][m][2 * i], s_mul[nr][0], ref[0]));
-                            const float p1 = ex2_approx(fmaf(sc[nr][m][2 * i + 1], s_mul[nr][1], ref[1]));
-                            sum[0] += p0;
-                            sum[1] += p1;
-                            if constexpr (TWO) {
-                                // p, or in the upper columns what its first term leaves, 2^kLowShift times as large
-                                const uint32_t h = pack_f16(p0, p1);
-                                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                                p[nr][m][i][0] = transpose8(pack_f16(fmaf(p0, whole_p, -x.x * less_p), fmaf(p1, whole_p, -x.y * less_p)));
-                            } else {
-                                uint32_t term[2];
-                                split<true>(p0, p1, term);
-                                p[nr][m][i][0] = transpose8(term[0]);
-                                p[nr][m][i][TERMS - 1] = transpose8(term[1]);
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float p0 = ex2_approx(fmaf(sc[h][nr][m][2 * i], s_mul[nr][0], ref[0]));
+                                const float p1 = ex2_approx(fmaf(sc[h][nr][m][2 * i + 1], s_mul[nr][1], ref[1]));
+                                sum[0] += p0;
+                                sum[1] += p1;
+                                uint32_t (&to)[TERMS] = p[h][nr][m][i];
+                                if constexpr (TWO) {
+                                    // p, or in the upper columns what its first term leaves, 2^kLowShift times as large
+                                    const uint32_t w = pack_f16(p0, p1);
+                                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                                    to[0] = transpose8(pack_f16(fmaf(p0, whole_p, -x.x * less_p), fmaf(p1, whole_p, -x.y * less_p)));
+                                } else {
+                                    uint32_t term[2];
+                                    split<true>(p0, p1, term);
+                                    to[0] = transpose8(term[0]);
+                                    to[TERMS - 1] = transpose8(term[1]);
+                                }
                             }
-                        }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         // with what is left of earlier roundings: equal weights,
@@ -525,91 +583,56 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
                         l_run[nr][e] = l;
                     }
                 }
-                // ---- O' += V' P'.  Of part c the thread has block g of keys key_x + c
-                // and key_y + c, the inner axis's columns 2t and 2t + 1.
-                uint32_t vs[4];
+                // ---- O' += V' P'
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const char *const row = v_s + c * ROWB + D / 2 + g * RUN / 8;
-                    vs[c] = *reinterpret_cast<const uint8_t *>(row + key_x * ROWB) |
-                            (uint32_t)*reinterpret_cast<const uint8_t *>(row + key_y * ROWB) << 8;
-                }
-                if (edge) {
-                    // Scales of rows behind the last key may be anything: those count
-                    // as zeros.  So do those of NaN that only some rows see, whose
-                    // product with a weight of 0 would be NaN; the rows that see
-                    // one get NaN in its block's elements.
-                    int bad = 0x7fffffff;
+                for (int h = 0; h < H; ++h) {
+                    uint32_t scale[4], lo[4][RW], hi[4][RW];  // codes of both keys side by side: even elements, odd ones
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        scale[c] = e4m3_to_f16(vs[h][c]);
+                        uint32_t x[RW], y[RW];
+                        load_run(x, v_s + (32 * h + key_x + c) * ROWB + g * RUN);
+                        load_run(y, v_s + (32 * h + key_y + c) * ROWB + g * RUN);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int key = kb + (i ? key_y : key_x) + c;
-                            const bool nan = (vs[c] >> (8 * i) & 0x7fu) == 0x7fu;
-                            if (key >= at.keys || (nan && a.causal && n_new > 1)) {
-                                vs[c] &= i ? 0x00ffu : 0xff00u;
-                                if (key < at.keys)
-                                    bad = min(bad, key);
-                            }
+                        for (int w = 0; w < RW; ++w) {
+                            lo[c][w] = select_bits(x[w], y[w] << 4, 0x0f0f0f0fu);
+                            hi[c][w] = select_bits(x[w] >> 4, y[w], 0x0f0f0f0fu);
                         }
-                    bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 1));
-                    bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 2));
+                    }
+                    auto tile_of = [&](int i, int w, auto byte) {
+                        constexpr int I = decltype(byte)::value;
+                        float d[NR][TERMS][4];
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t a0 = mul_f16(e2m1_to_f16<I>(lo[2 * m][w]), scale[2 * m]);
+                            const uint32_t a1 = mul_f16(e2m1_to_f16<I>(hi[2 * m][w]), scale[2 * m]);
+                            const uint32_t a2 = mul_f16(e2m1_to_f16<I>(lo[2 * m + 1][w]), scale[2 * m + 1]);
+                            const uint32_t a3 = mul_f16(e2m1_to_f16<I>(hi[2 * m + 1][w]), scale[2 * m + 1]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (bad < lim[nr][e]) {
+                            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                for (int i = 0; i < DT; ++i)
-                                    sums[nr][i][e] = sums[nr][i][2 + e] = __int_as_float(0x7fffffff);
-                            }
-                }
+                                for (int term = 0; term < TERMS; ++term) {
+                                    const uint32_t b0 = p[h][nr][m][0][term], b1 = p[h][nr][m][1][term];
+                                    if (m == 0)
+                                        mma_first(d[nr][term], a0, a1, a2, a3, b0, b1);
+                                    else
+                                        mma<true>(d[nr][term], a0, a1, a2, a3, b0, b1);
+                                }
+                        }
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    vs[c] = e4m3_to_f16(vs[c]);
-                uint32_t lo[4][RW], hi[4][RW];  // codes of both keys side by side: even elements, odd ones
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[RW], y[RW];
-                    load_run(x, v_s + (key_x + c) * ROWB + g * RUN);
-                    load_run(y, v_s + (key_y + c) * ROWB + g * RUN);
+                        for (int nr = 0; nr < NR; ++nr) {
+                            add_to(sums[nr][i], d[nr][0], 1.f);
+                            if constexpr (!TWO)
+                                add_to(sums[nr][i], d[nr][TERMS - 1], kLow);
+                        }
+                    };
 #pragma unroll
                     for (int w = 0; w < RW; ++w) {
-                        lo[c][w] = select_bits(x[w], y[w] << 4, 0x0f0f0f0fu);
-                        hi[c][w] = select_bits(x[w] >> 4, y[w], 0x0f0f0f0fu);
+                        tile_of(w * 4, w, Byte<0>());
+                        tile_of(w * 4 + 1, w, Byte<1>());
+                        tile_of(w * 4 + 2, w, Byte<2>());
+                        tile_of(w * 4 + 3, w, Byte<3>());
                     }
-                }
-                auto tile_of = [&](int i, int w, auto byte) {
-                    constexpr int I = decltype(byte)::value;
-                    float d[NR][TERMS][4];
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t a0 = mul_f16(e2m1_to_f16<I>(lo[2 * m][w]), vs[2 * m]);
-                        const uint32_t a1 = mul_f16(e2m1_to_f16<I>(hi[2 * m][w]), vs[2 * m]);
-                        const uint32_t a2 = mul_f16(e2m1_to_f16<I>(lo[2 * m + 1][w]), vs[2 * m + 1]);
-                        const uint32_t a3 = mul_f16(e2m1_to_f16<I>(hi[2 * m + 1][w]), vs[2 * m + 1]);
-#pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                            for (int term = 0; term < TERMS; ++term)
-                                if (m == 0)
-                                    mma_first(d[nr][term], a0, a1, a2, a3, p[nr][m][0][term], p[nr][m][1][term]);
-                                else
-                                    mma<true>(d[nr][term], a0, a1, a2, a3, p[nr][m][0][term], p[nr][m][1][term]);
-                    }
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) {
-                        add_to(sums[nr][i], d[nr][0], 1.f);
-                        if constexpr (!TWO)
-                            add_to(sums[nr][i], d[nr][TERMS - 1], kLow);
-                    }
-                };
-#pragma unroll
-                for (int w = 0; w < RW; ++w) {
-                    tile_of(w * 4, w, Byte<0>());
-                    tile_of(w * 4 + 1, w, Byte<1>());
-                    tile_of(w * 4 + 2, w, Byte<2>());
-                    tile_of(w * 4 + 3, w, Byte<3>());
                 }
             }
             if (--left == 0)
@@ -636,6 +659,8 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
         if (C::kOwnRows)
             release();
         named_barrier_sync(1, kWarps * 32);
+        if (on)
+            put_q();  // no warp reads the last job's any more
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -707,10 +732,10 @@ __global__ void __launch_bounds__(Cfg<D, ROWS>::kThreads, 1) attn_paged4_kernel(
     named_barrier_arrive(kEndBarrier, C::kThreads);
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int H>
 int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    using C = Cfg<D, ROWS>;
+    using C = Cfg<D, ROWS, H>;
     long long most;
     const int rc = count_tiles<ROWS, C::kTile>(a, &most, msg, msg_len);
     if (rc != MERCURY_OK)
@@ -718,16 +743,26 @@ int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     // runs of a power of two of keys that divides page_size (a multiple of 8) and the tile
     for (a.box_rows = 8; C::kTile % (2 * a.box_rows) == 0 && a.cache.page_size % (2 * a.box_rows) == 0;)
         a.box_rows *= 2;
-    return launch_split<D, ROWS, C::kTile>(a, most, attn_paged4_kernel<D, ROWS>, C::kSmem, C::kThreads, C::kMinLaunchRegs,
+    return launch_split<D, ROWS, C::kTile>(a, most, attn_paged4_kernel<D, ROWS, H>, C::kSmem, C::kThreads, C::kMinLaunchRegs,
                                                stream, msg, msg_len);
 }
 
 template <int D>
 int launch_rows(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    return a.R <= 4   ? launch<D, 4>(a, stream, msg, msg_len)
-           : a.R <= 8 ? launch<D, 8>(a, stream, msg, msg_len)
-                      : launch<D, 16>(a, stream, msg, msg_len);
+    if (a.R > 8)
+        return launch<D, 16, 1>(a, stream, msg, msg_len);
+    // Steps of 64 keys leave more to overlap than of 32, but tiles of 512 keys
+    // go round the SMs only where there are many (one sequence of 128K: 38.6 us
+    // instead of 41.1; of 4K, 64 tiles of 512: 9.2 instead of 8.2).
+    int sms = 0;
+    const int rc = device_sm_count(&sms);
+    if (rc != MERCURY_OK)
+        return rc;
+    const long long tiles = (long long)a.cache.max_pages * a.cache.page_size / 512 * a.B * a.Hkv;
+    if (tiles < 2 * sms)
+        return a.R <= 4 ? launch<D, 4, 1>(a, stream, msg, msg_len) : launch<D, 8, 1>(a, stream, msg, msg_len);
+    return a.R <= 4 ? launch<D, 4, 2>(a, stream, msg, msg_len) : launch<D, 8, 2>(a, stream, msg, msg_len);
 }
 
 }  // namespace

@@ -27,6 +27,11 @@ static int (*g_attn)(const void *, const ll *, const mercury_paged_cache *, cons
                      float *, float *, void *);
 static int (*g_attn_bf16)(const void *, const ll *, const mercury_paged_cache *, const int *, const int *, int, int, int, int,
                           void *, float *, void *);
+static int (*g_mass)(const void *, const ll *, const mercury_paged_cache *, const int *, const int *, int, int, int, int,
+                     const float *, const float *, float *, ll, void *);
+static int (*g_evict)(const mercury_paged_cache *, const mercury_paged_cache *, const float *, ll, const int *, int, int, int,
+                      int, int *, int *, float *, ll, void *);
+static int (*g_read)(const mercury_paged_cache *, const int *, int, int, void *, void *, void *);
 static PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_stride, *s_data_ptr;
 
 /* A tensor as a call sees it. */
@@ -262,11 +267,137 @@ static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(rc);
 }
 
-/* init(bf16, fp32, int32, current_device, current_stream, addresses of the four library functions) */
+/* A [B, Hkv, width] fp32 tensor of a cache, or (where it may be) None (NULL). */
+static int look_mass(PyObject *t, long dev, const mercury_paged_cache *c, int optional, float **p, ll *width)
+{
+    View v;
+    *p = NULL;
+    *width = 0;
+    if (t == Py_None)
+        return optional;
+    if (!look(t, g_fp32, dev, 3, 0, &v) || v.n[0] != c->B || v.n[1] != c->Hkv)
+        return 0;
+    *p = (float *)v.p;
+    *width = v.n[2];
+    return 1;
+}
+
+/* mass(q, cache address, device, seq_lens, lse, new_lens or None, causal, mass or None, out) -> status or None */
+static PyObject *py_mass(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    View q, l;
+    const mercury_paged_cache *c;
+    const int *lens, *fresh;
+    float *mass, *out;
+    void *stream;
+    long dev;
+    ll width, more;
+    int rc, causal;
+    if (n != 9)
+        Py_RETURN_NONE;
+    c = (const mercury_paged_cache *)PyLong_AsVoidPtr(a[1]);
+    dev = PyErr_Occurred() ? -1 : PyLong_AsLong(a[2]);
+    causal = PyErr_Occurred() ? 0 : PyObject_IsTrue(a[6]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    if (!look(a[0], g_bf16, dev, 4, 1, &q) || q.n[0] != c->B || q.n[3] != c->d || !fits(&q, 1) || !fits(&q, 2))
+        Py_RETURN_NONE;
+    if (a[3] == Py_None || !look_lens(a[3], dev, c->B, &lens) || !look_lens(a[5], dev, c->B, &fresh))
+        Py_RETURN_NONE;
+    if (!look(a[4], g_fp32, dev, 3, 0, &l) || l.n[0] != q.n[0] || l.n[1] != q.n[1] || l.n[2] != q.n[2])
+        Py_RETURN_NONE;
+    if (!look_mass(a[7], dev, c, 1, &mass, &more) || !look_mass(a[8], dev, c, 0, &out, &width) || (mass && more != width))
+        Py_RETURN_NONE;
+    if (!on_device(dev, &stream))
+        Py_RETURN_NONE;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_mass(q.p, q.strides, c, lens, fresh, c->B, (int)q.n[1], (int)q.n[2], causal, (const float *)l.p, mass, out, width,
+                stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* evict(cache address, into address, device, mass, seq_lens, keep, first, last, out_lens, kept, out_mass or None)
+ * -> status or None */
+static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    View kept;
+    const mercury_paged_cache *c, *into;
+    const int *lens, *out_lens;
+    float *mass, *out_mass;
+    void *stream;
+    long dev, num[3];
+    ll width, out_width;
+    int rc;
+    if (n != 11)
+        Py_RETURN_NONE;
+    c = (const mercury_paged_cache *)PyLong_AsVoidPtr(a[0]);
+    into = PyErr_Occurred() ? NULL : (const mercury_paged_cache *)PyLong_AsVoidPtr(a[1]);
+    dev = PyErr_Occurred() ? -1 : PyLong_AsLong(a[2]);
+    for (int i = 0; i < 3; ++i)
+        num[i] = PyErr_Occurred() ? 0 : PyLong_AsLong(a[5 + i]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    for (int i = 0; i < 3; ++i)
+        if (num[i] < 0 || num[i] > 0x7fffffff)
+            Py_RETURN_NONE;
+    if (!look_mass(a[3], dev, c, 0, &mass, &width) || !look_mass(a[10], dev, c, 1, &out_mass, &out_width))
+        Py_RETURN_NONE;
+    if (a[4] == Py_None || !look_lens(a[4], dev, c->B, &lens) || a[8] == Py_None || !look_lens(a[8], dev, c->B, &out_lens))
+        Py_RETURN_NONE;
+    if (!look(a[9], g_int32, dev, 3, 0, &kept) || kept.n[0] != c->B || kept.n[1] != c->Hkv || kept.n[2] != num[0])
+        Py_RETURN_NONE;
+    if (!on_device(dev, &stream))
+        Py_RETURN_NONE;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_evict(c, into, mass, width, lens, c->B, (int)num[0], (int)num[1], (int)num[2], (int *)out_lens, (int *)kept.p, out_mass,
+                 out_width, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* read(cache address, device, seq_lens, k_out, v_out) -> status or None */
+static PyObject *py_read(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    View k, v;
+    const mercury_paged_cache *c;
+    const int *lens;
+    void *stream;
+    long dev;
+    int rc;
+    if (n != 5)
+        Py_RETURN_NONE;
+    c = (const mercury_paged_cache *)PyLong_AsVoidPtr(a[0]);
+    dev = PyErr_Occurred() ? -1 : PyLong_AsLong(a[1]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    if (a[2] == Py_None || !look_lens(a[2], dev, c->B, &lens))
+        Py_RETURN_NONE;
+    if (!look(a[3], g_bf16, dev, 4, 0, &k) || !look(a[4], g_bf16, dev, 4, 0, &v) || k.n[0] != c->B || k.n[1] != c->Hkv ||
+        k.n[3] != c->d || !fits(&k, 2))
+        Py_RETURN_NONE;
+    for (int i = 0; i < 4; ++i)
+        if (k.n[i] != v.n[i])
+            Py_RETURN_NONE;
+    if (!on_device(dev, &stream))
+        Py_RETURN_NONE;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_read(c, lens, c->B, (int)k.n[2], k.p, v.p, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* init(bf16, fp32, int32, current_device, current_stream, addresses of the seven library functions) */
 static PyObject *py_init(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 9) {
-        PyErr_SetString(PyExc_TypeError, "init takes nine arguments");
+    if (n != 12) {
+        PyErr_SetString(PyExc_TypeError, "init takes twelve arguments");
         return NULL;
     }
     g_bf16 = Py_NewRef(a[0]);
@@ -278,6 +409,9 @@ static PyObject *py_init(PyObject *self, PyObject *const *a, Py_ssize_t n)
     *(void **)&g_append = PyLong_AsVoidPtr(a[6]);
     *(void **)&g_attn = PyLong_AsVoidPtr(a[7]);
     *(void **)&g_attn_bf16 = PyLong_AsVoidPtr(a[8]);
+    *(void **)&g_mass = PyLong_AsVoidPtr(a[9]);
+    *(void **)&g_evict = PyLong_AsVoidPtr(a[10]);
+    *(void **)&g_read = PyLong_AsVoidPtr(a[11]);
     if (PyErr_Occurred())
         return NULL;
     Py_RETURN_NONE;
@@ -288,6 +422,9 @@ static PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, "mercury_rope, or None"},
     {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, "mercury_kv_append, or None"},
     {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, "mercury_attn_paged, or None"},
+    {"mass", (PyCFunction)(void (*)(void))py_mass, METH_FASTCALL, "mercury_attn_paged_mass, or None"},
+    {"evict", (PyCFunction)(void (*)(void))py_evict, METH_FASTCALL, "mercury_kv_evict, or None"},
+    {"read", (PyCFunction)(void (*)(void))py_read, METH_FASTCALL, "mercury_kv_read, or None"},
     {NULL, NULL, 0, NULL},
 };
 

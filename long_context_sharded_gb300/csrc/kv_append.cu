@@ -51,6 +51,7 @@ struct AppendArgs {
     const int *past, *new_lens;
     PagedView cache;
     int Hq, S, d, head_groups, heads_per_thread, units, tokens_per_block;
+    int kv_groups, kv_per_thread;  // of a 4-bit cache: those of keys and values, which come first
     long long tokens;
     int copy_rest;  // q_out is not q itself
     mercury_rope_plan plan;
@@ -89,8 +90,8 @@ __device__ __forceinline__ void keep4(const RotUnit<8> &unit, const mercury_rope
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            top[k] = max_nan(top[k], fabsf(y[k][i]));
+        for (int i = 0; i < 8; i += 2)
+            top[k] = max_nan(top[k], y[k][i], y[k][i + 1]);
     const unsigned int both = 3u << (threadIdx.x & 30u);
     if (apart) {
 #pragma unroll
@@ -180,7 +181,16 @@ __global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) append_kernel(const 
     const int b = (unsigned int)token / (unsigned int)a.S, i = (int)token - b * a.S;
     const PagedView &c = a.cache;
     const int Hkv = c.Hkv, Hq = a.Hq;
-    const int h0 = group * a.heads_per_thread, h1 = min(Hq + 2 * Hkv, h0 + a.heads_per_thread);
+    int h0 = group * a.heads_per_thread, h1 = min(Hq + 2 * Hkv, h0 + a.heads_per_thread);
+    if constexpr (FP4) {
+        if (group < a.kv_groups) {
+            h0 = Hq + group * a.kv_per_thread;
+            h1 = min(Hq + 2 * Hkv, h0 + a.kv_per_thread);
+        } else {
+            h0 = (group - a.kv_groups) * a.heads_per_thread;
+            h1 = min(Hq, h0 + a.heads_per_thread);
+        }
+    }
     const long long past = a.past[b];
     const int n_new = a.new_lens ? a.new_lens[b] : a.S;
     if ((n_new < 0 || n_new > a.S) && i == 0)
@@ -274,7 +284,21 @@ __global__ void __launch_bounds__(kRotThreads, FEW ? 3 : 2) append_kernel(const 
 template <int ELEM, int VE>
 int launch(AppendArgs &a, int sms, cudaStream_t stream, char *msg, size_t msg_len)
 {
-    const RotShape g = rot_shape(a.tokens, a.Hq + 2 * a.cache.Hkv, a.d, a.plan.rot_dim, VE, sms, ELEM == MERCURY_ELEM_E2M1 ? 6 : 3);
+    RotShape g = rot_shape(a.tokens, a.Hq + 2 * a.cache.Hkv, a.d, a.plan.rot_dim, VE, sms);
+    if constexpr (ELEM == MERCURY_ELEM_E2M1) {
+        // A 4-bit key or value takes a thread several times as long as a query
+        // does: they go by fewer heads a thread, and first (8K tokens of 32 + 8 +
+        // 8 heads, and 32K read back: 75.1 us, with one rule for all 80.4).
+        const RotShape q = rot_shape(a.tokens, a.Hq > 0 ? a.Hq : 1, a.d, a.plan.rot_dim, VE, sms);
+        const int kv = 2 * a.cache.Hkv;
+        int most = 4;
+        while (most > 1 && g.blocks * ((kv + most - 1) / most) < 2LL * sms)
+            most /= 2;
+        a.kv_per_thread = most;
+        a.kv_groups = (kv + most - 1) / most;
+        g.heads_per_thread = q.heads_per_thread;
+        g.head_groups = a.kv_groups + (a.Hq + q.heads_per_thread - 1) / q.heads_per_thread;
+    }
     if (g.blocks * g.head_groups > 0x7fffffffLL) {
         snprintf(msg, msg_len, "too many tokens for one call (%lld)", (long long)a.tokens);
         return MERCURY_EINVAL;
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(kRotThreads) append_blocks_kernel(const __grid
             // (of itself and no partner at no angle, where a block's part is turned)
             x[k] = z[k] = y[k] = __bfloat162float(src[j]);
         }
-        top = max_nan(top, fabsf(y[k]));
+        top = max_nan(top, y[k]);
     }
     const bool in_table = pos >= 0 && pos < (long long)c.max_pages * c.page_size;
     if (!in_table) {

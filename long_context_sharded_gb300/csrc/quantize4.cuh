@@ -7,8 +7,8 @@
 // cache holds does not hang on how sines are computed or sums are ordered.
 //
 // A value known to e (0 where it was not rotated) has its quotient bracketed by
-// two 32-bit products, wider by 2^-21 than e, which covers their roundings (four
-// of 2^-24); where both ends round to the same code, that is it.  Where they do
+// two 32-bit products, wider by 2^-21 than e, which covers their roundings (the
+// reciprocal's 2^-23, and three of 2^-24); where both ends round to the same code, that is it.  Where they do
 // not, the border between the two is next to the value, and the two are
 // compared: exactly in 32 bits, by the product's rounding error, or for a
 // rotated value in 64 bits (one in some 10^5; as 0.2 % of warps meet one, that
@@ -20,12 +20,25 @@
 
 namespace mercury {
 
-// Two floats as the nearest e2m1 codes (saturated at 6), lo in the lower half
-// of the byte.
-__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi)
+// Eight floats as the nearest e2m1 codes (saturated at 6), the first in the
+// lowest four bits.
+__device__ __forceinline__ uint32_t pack_e2m1(const float (&x)[8])
 {
-    uint16_t r;
-    asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\tmov.b16 %0, {x, 0};\n\t}" : "=h"(r) : "f"(hi), "f"(lo));
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+// 1 / x to 2^-23 of it.
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -129,7 +142,14 @@ __device__ __noinline__ uint32_t settle_codes(uint32_t w, uint32_t differ, float
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -137,8 +157,8 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // off: the lower end's in the lower byte.  (A NaN gives NaN, an infinity 448.)
 __device__ __forceinline__ uint32_t scale_ends(float amax, float off, float g)
 {
-    const float r = 1.f / (6.f * g);
-    return pack_e4m3(max_nan(amax - off, 0.f) * r * (1.f - kWider), (amax + off) * r * (1.f + kWider));
+    const float r = reciprocal(6.f * g);
+    return pack_e4m3((amax - off < 0.f ? 0.f : amax - off) * r * (1.f - kWider), (amax + off) * r * (1.f + kWider));
 }
 
 // Eight codes of four bits: the lower ends' magnitudes in lo, and in hi the
@@ -146,23 +166,17 @@ __device__ __forceinline__ uint32_t scale_ends(float amax, float off, float g)
 // elements are known to.  Where s is zero all codes are.
 __device__ __forceinline__ void code_ends(const float (&y)[8], float off, float s, float g, uint32_t &lo, uint32_t &hi)
 {
-    const float r = s > 0.f ? 1.f / (s * g) : 0.f;
+    const float r = s > 0.f ? reciprocal(s * g) : 0.f;
     const float below = r * (1.f - kWider), above = r * (1.f + kWider);
     const float more = off * above * (1.f + kWider);
-    lo = hi = 0;
+    float l[8], h[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        float l[2], h[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float a = fabsf(y[i + j]);
-            l[j] = fmaf(a, below, -more);  // (below zero: a zero of either sign)
-            h[j] = copysignf(fmaf(a, above, more), y[i + j]);
-        }
-        lo |= pack_e2m1(l[0], l[1]) << (4 * i);
-        hi |= pack_e2m1(h[0], h[1]) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+        l[i] = fmaf(fabsf(y[i]), below, -more);  // (below zero: a zero of either sign)
+        h[i] = copysignf(fmaf(fabsf(y[i]), above, more), y[i]);
     }
-    lo &= 0x77777777u;
+    lo = pack_e2m1(l) & 0x77777777u;
+    hi = pack_e2m1(h);
 }
 
 }  // namespace mercury

@@ -281,7 +281,7 @@ struct RotShape {
     long long blocks;
 };
 
-inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int sms, int halves = 3)
+inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int sms)
 {
     RotShape g;
     g.units = rot / (2 * VE) + (d - rot + 2 * VE - 1) / (2 * VE);
@@ -297,7 +297,7 @@ inline RotShape rot_shape(long long tokens, int H, int d, int rot, int VE, int s
     // tokens of 24 heads into an 8-bit cache, with a division for every element: 12.8 us with 16,
     // 11.7 with 2).
     int hp = 16;
-    while (hp > 1 && 2 * g.blocks * ((H + hp - 1) / hp) < (long long)halves * sms)
+    while (hp > 1 && 2 * g.blocks * ((H + hp - 1) / hp) < 3LL * sms)
         hp /= 2;
     g.heads_per_thread = hp;
     g.head_groups = (H + hp - 1) / hp;

@@ -543,7 +543,8 @@ def _names():
         T = _Torch()
         _fast.init(T.bf16, T.fp32, T.int32, T.current_device, T.raw_stream,
                    *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                       lib.mercury_rope, lib.mercury_kv_append, lib.mercury_attn_paged, lib.mercury_attn_paged_bf16)))
+                       lib.mercury_rope, lib.mercury_kv_append, lib.mercury_attn_paged, lib.mercury_attn_paged_bf16,
+                       lib.mercury_attn_paged_mass, lib.mercury_kv_evict, lib.mercury_kv_read)))
         _torch_names = T
     return _torch_names
 
@@ -915,6 +916,12 @@ def mercury_attn_paged_mass(q, cache: PagedCache, seq_lens, lse, new_lens=None, 
     behind seq_lens[b] left as they were.  mass None: zeros; out may be mass; by
     default a new tensor of mass's shape (or as wide as the block table), 0
     behind seq_lens[b]."""
+    if out is not None and stream is None and isinstance(cache, PagedCache):
+        rc = _fast.mass(q, cache.address, cache.device_index, seq_lens, lse, new_lens, causal, mass, out)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return out
     T, dev, ptr = _cache_call(cache, stream)
     shape = _shape4(q, "q")
     B, Hq, Sq, d = shape
@@ -950,6 +957,14 @@ def mercury_kv_evict(cache: PagedCache, into: PagedCache, mass, seq_lens, keep: 
     [B,Hkv,keep] int32: the token that each kept one was), made where they are
     not given (kept: -1 behind out_lens[b]); out_mass [B,Hkv,>=keep] fp32, where
     given, gets the kept tokens' mass."""
+    if out_lens is not None and kept is not None and stream is None and isinstance(cache, PagedCache) and \
+            isinstance(into, PagedCache) and into.device_index == cache.device_index:
+        rc = _fast.evict(cache.address, into.address, cache.device_index, mass, seq_lens, keep, first, last, out_lens, kept,
+                         out_mass)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return out_lens, kept
     T, dev, ptr = _cache_call(cache, stream)
     if not isinstance(into, PagedCache):
         raise TypeError("into must be a PagedCache")
@@ -982,6 +997,12 @@ def mercury_kv_read(cache: PagedCache, seq_lens, S: int = None, k_out=None, v_ou
     [B,Hkv,S,d], tokens i < seq_lens[b] (rows behind them: left as they were, 0
     where the call makes the tensors); S by default the outputs', or what the
     block table holds.  Returns (k, v)."""
+    if k_out is not None and v_out is not None and S is None and stream is None and isinstance(cache, PagedCache):
+        rc = _fast.read(cache.address, cache.device_index, seq_lens, k_out, v_out)
+        if rc is not None:
+            if rc:
+                _check(rc)
+            return k_out, v_out
     T, dev, ptr = _cache_call(cache, stream)
     for t in (k_out, v_out):
         if S is None and t is not None:
