@@ -338,11 +338,14 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
 #pragma unroll 2
             for (int rt = 0; rt < n_rt; ++rt) {
                 // in 2 sums of d/2 products each, added at the end
-                float x[2][4] = {};
+                float x[2][4];
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     const uint2 q = qs[(rt * KK + kk) * 32 + lane];
-                    mma<K::kF16>(x[kk & 1], f[kk][0], f[kk][1], f[kk][2], f[kk][3], q.x, q.y);
+                    if (kk < 2)
+                        mma_first<K::kF16>(x[kk], f[kk][0], f[kk][1], f[kk][2], f[kk][3], q.x, q.y);
+                    else
+                        mma<K::kF16>(x[kk & 1], f[kk][0], f[kk][1], f[kk][2], f[kk][3], q.x, q.y);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {

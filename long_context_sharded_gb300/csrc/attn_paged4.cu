@@ -88,16 +88,6 @@ struct Byte {
     static constexpr int value = I;
 };
 
-// D = A B, fp16 operands.
-__device__ __forceinline__ void mma_first(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%10, %10, %10, %10};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // The transpose of an 8 x 8 matrix of 16-bit elements, two of a row a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
@@ -412,45 +402,56 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, H>::kThreads, 1) attn_paged4_kern
                 // ---- S' = K Q'
                 float sc[H][NR][2][4];
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int h0 = 0; h0 < H; ++h0) {
+                    constexpr int HN = 1;
+                    // Part j: 16 keys, rows g and g + 8 of the product, keys key_g + 2m and
+                    // + 1.  The parts' products are independent of one another, and go
+                    // in turn.
+                    uint32_t x[2 * HN][2][2][RW], s[2 * HN][2][2];  // [part][row][run]
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        // rows g and g + 8 of the product: keys key_g + 2m and + 1
-                        uint32_t x[2][2][RW], s[2][2];  // [row][run]
+                    for (int j = 0; j < 2 * HN; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const char *const row = k_s + (32 * h + 2 * m + i) * ROWB;
-                            load_run(x[i][0], row + t * RUN);
-                            load_run(x[i][1], row + D / 4 + t * RUN);
+                            const char *const row = k_s + (32 * (h0 + j / 2) + 2 * (j & 1) + i) * ROWB;
+                            load_run(x[j][i][0], row + t * RUN);
+                            load_run(x[j][i][1], row + D / 4 + t * RUN);
                             uint32_t all[RW];  // the row's scales
                             load_run(all, row + D / 2);
                             const uint32_t both = e4m3_to_f16(__byte_perm(all[0], all[RW - 1], k_pick));
-                            s[i][0] = __byte_perm(both, 0, 0x1010);
-                            s[i][1] = __byte_perm(both, 0, 0x3232);
+                            s[j][i][0] = __byte_perm(both, 0, 0x1010);
+                            s[j][i][1] = __byte_perm(both, 0, 0x3232);
                         }
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                            for (int w = 0; w < RW; ++w) {
-                                const int kk = r * (KK / 2) + w * 2;
-                                const uint32_t x0 = x[0][r][w], x1 = x[1][r][w];
+                        for (int w = 0; w < RW; ++w) {
+                            const int kk = r * (KK / 2) + w * 2;
+                            uint2 q[NR][2];
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    q[nr][i] = queries[(nr * KK + kk + i) * 32 + lane];
+#pragma unroll
+                            for (int j = 0; j < 2 * HN; ++j) {
+                                const uint32_t x0 = x[j][0][r][w], x1 = x[j][1][r][w];
                                 uint32_t f[8] = {e2m1_to_f16<0>(x0), e2m1_to_f16<0>(x1), e2m1_to_f16<1>(x0), e2m1_to_f16<1>(x1),
                                                  e2m1_to_f16<2>(x0), e2m1_to_f16<2>(x1), e2m1_to_f16<3>(x0), e2m1_to_f16<3>(x1)};
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
-                                    f[i] = mul_f16(f[i], s[i & 1][r]);
+                                    f[i] = mul_f16(f[i], s[j][i & 1][r]);
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr) {
-                                    float *const d = sc[h][nr][m];
-                                    const uint2 q0 = queries[(nr * KK + kk) * 32 + lane], q1 = queries[(nr * KK + kk + 1) * 32 + lane];
+                                    float *const d = sc[h0 + j / 2][nr][j & 1];
                                     if (kk == 0)
-                                        mma_first(d, f[0], f[1], f[2], f[3], q0.x, q0.y);
+                                        mma_first<true>(d, f[0], f[1], f[2], f[3], q[nr][0].x, q[nr][0].y);
                                     else
-                                        mma<true>(d, f[0], f[1], f[2], f[3], q0.x, q0.y);
-                                    mma<true>(d, f[4], f[5], f[6], f[7], q1.x, q1.y);
+                                        mma<true>(d, f[0], f[1], f[2], f[3], q[nr][0].x, q[nr][0].y);
+                                    mma<true>(d, f[4], f[5], f[6], f[7], q[nr][1].x, q[nr][1].y);
                                 }
                             }
-                    }
+                        }
+                }
                 // Of part c of 32 keys, for O', the thread has block g of keys key_x + c
                 // and key_y + c, the inner axis's columns 2t and 2t + 1: their scales.
                 uint32_t vs[H][4];
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, ROWS, H>::kThreads, 1) attn_paged4_kern
                                 for (int term = 0; term < TERMS; ++term) {
                                     const uint32_t b0 = p[h][nr][m][0][term], b1 = p[h][nr][m][1][term];
                                     if (m == 0)
-                                        mma_first(d[nr][term], a0, a1, a2, a3, b0, b1);
+                                        mma_first<true>(d[nr][term], a0, a1, a2, a3, b0, b1);
                                     else
                                         mma<true>(d[nr][term], a0, a1, a2, a3, b0, b1);
                                 }
