@@ -695,11 +695,13 @@ MERCURY_API int mercury_kv_append(const void *k, const long long *k_strides, con
  * q_strides as in mercury_rope, multiples of 8 elements, q 16-byte aligned.
  * Requirements: as mercury_kv_append for the cache; Hq % Hkv == 0;
  * B * Hkv * ceil(Hq/Hkv * Sq / 64) * (max_pages * page_size / 128 + 3) < 2^28
- * (what the line of all tiles can count); page_stride below 2^40 bytes;
+ * (what the line of all tiles can count; for an e2m1 cache 16 and 256 in place
+ * of 64 and 128); page_stride below 2^40 bytes;
  * 1 <= Sq <= 64 (longer prompts are mercury_attn_sharded's).  The first call
  * on a device for a cache type, head dim and class of rows a KV head (Hq/Hkv *
- * Sq up to 8, 16, 32, or more) prepares its kernels and the scratch pool,
- * whatever its lengths; make it before any stream capture.
+ * Sq up to 8, 16, 32, or more; for an e2m1 cache 4, 8, or more) prepares its
+ * kernels and the scratch pool, whatever its lengths; make it before any stream
+ * capture.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
  * or MERCURY_ETIMEOUT when MERCURY_SYNC_CHECK=1.
  */

@@ -352,12 +352,12 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                     const Row r = rows[rt * 8 + 2 * t + e];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float w = ex2_approx(fmaf(x[0][2 * i + e] + x[1][2 * i + e], r.mul, r.nl));
-                        if constexpr (decltype(masked)::value) {
-                            const int lim = p.causal ? seen_by_all + r.step : now.keys;
-                            w = k0 + g + 8 * i < lim && r.rest != 0.f ? w : 0.f;
-                        }
-                        sum[i] = fmaf(w, r.rest, sum[i]);
+                        const float w = ex2_approx(fmaf(x[0][2 * i + e] + x[1][2 * i + e], r.mul, r.nl));
+                        bool counts = r.rest != 0.f;  // (a product with 0 would let a key's infinity or NaN through)
+                        if constexpr (decltype(masked)::value)
+                            counts &= k0 + g + 8 * i < (p.causal ? seen_by_all + r.step : now.keys);
+                        if (counts)
+                            sum[i] = fmaf(w, r.rest, sum[i]);
                     }
                 }
             }

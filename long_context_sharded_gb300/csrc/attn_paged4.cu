@@ -737,6 +737,15 @@ template <int D, int ROWS, int H>
 int launch(PagedArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
     using C = Cfg<D, ROWS, H>;
+    if constexpr (ROWS <= 8) {
+        // A call of other lengths may take the other step: its kernel is made
+        // ready now too, so that such a call may be captured.
+        KernelInfo other;
+        const int rc = prepare_kernel((const void *)attn_paged4_kernel<D, ROWS, 3 - H>, Cfg<D, ROWS, 3 - H>::kSmem, &other, msg,
+                                      msg_len);
+        if (rc != MERCURY_OK)
+            return rc;
+    }
     long long most;
     const int rc = count_tiles<ROWS, C::kTile>(a, &most, msg, msg_len);
     if (rc != MERCURY_OK)

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         return make_uint4(r[0], r[1], r[2], r[3]);
     };
     if (held) {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = from + 4 * tid; i < to; i += 4 * kSelectThreads)
             sm.ranks[(i - from) / 4] = fetch(i);
     }
@@ -310,19 +310,35 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
                 incl += y;
         }
         int sure = at_sure + (incl & 0xffff) - (c & 0xffff), tie = at_tie + (incl >> 16) - (c >> 16);
+        int slot[4];
+        bool other = false;  // a rank that is not a weight's own: an end's, NaN's, a zero's
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (i + k >= end)
-                continue;
             const bool above = x[k] > prefix, at = x[k] == prefix;
-            if (above || (at && tie < ties)) {
-                const int slot = sure + min(tie, ties);
-                kept[slot] = i + k;
-                if (out_mass)
-                    out_mass[slot] = mass[i + k];
+            slot[k] = i + k < end && (above || (at && tie < ties)) ? sure + min(tie, ties) : -1;
+            other |= slot[k] >= 0 && (x[k] == 0xffffffffu || x[k] == 0u || x[k] == 0x80000000u);
+            sure += i + k < end && above;
+            tie += i + k < end && at;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (slot[k] >= 0)
+                kept[slot[k]] = i + k;
+        if (out_mass) {
+            float w[4];
+            if (__any_sync(0xffffffffu, other)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = slot[k] >= 0 ? mass[i + k] : 0.f;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = __uint_as_float(x[k] & 0x80000000u ? x[k] ^ 0x80000000u : ~x[k]);
             }
-            sure += above;
-            tie += at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (slot[k] >= 0)
+                    out_mass[slot[k]] = w[k];
         }
         const int all = __shfl_sync(0xffffffffu, incl, 31);
         at_sure += all & 0xffff;
@@ -333,12 +349,15 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 }
 
 template <int CS>
-int launch_select(SelectArgs &s, long long heads, cudaStream_t stream, char *msg, size_t msg_len)
+int prepare_select(char *msg, size_t msg_len)
 {
     KernelInfo ki;
-    const int rc = prepare_kernel((const void *)evict_select_kernel<CS>, (int)sizeof(SelectSmem) + kHeld * 4, &ki, msg, msg_len);
-    if (rc != MERCURY_OK)
-        return rc;
+    return prepare_kernel((const void *)evict_select_kernel<CS>, (int)sizeof(SelectSmem) + kHeld * 4, &ki, msg, msg_len);
+}
+
+template <int CS>
+int launch_select(SelectArgs &s, long long heads, cudaStream_t stream, char *msg, size_t msg_len)
+{
     const int line = CS * kSelectWarps * 128, run = ((s.most - 1) / line + 1) * (kSelectWarps * 128);
     s.held = run < kHeld ? run : kHeld;
     cudaLaunchConfig_t cfg = {};
@@ -635,6 +654,15 @@ int launch_kv_evict(const mercury_paged_cache &cache, const mercury_paged_cache 
     // tokens or more.
     int sms = 0;
     int rc = device_sm_count(&sms);
+    // (all of them, so that a call of other sizes may be captured)
+    if (rc == MERCURY_OK)
+        rc = prepare_select<1>(msg, msg_len);
+    if (rc == MERCURY_OK)
+        rc = prepare_select<2>(msg, msg_len);
+    if (rc == MERCURY_OK)
+        rc = prepare_select<4>(msg, msg_len);
+    if (rc == MERCURY_OK)
+        rc = prepare_select<8>(msg, msg_len);
     if (rc != MERCURY_OK)
         return rc;
     rc = heads * 8 <= sms && s.most > 8192   ? launch_select<8>(s, heads, stream, msg, msg_len)

@@ -528,6 +528,52 @@ def test_mass_of_keys_that_some_rows_see(gm, elem):
         assert torch.isfinite(out[b, :, :n]).all() and (out[b, :, n - 1] == 0).all() and (out[b, :, n:] == 9.0).all()
 
 
+@pytest.mark.gpu
+def test_mass_of_keys_with_infinities(gm):
+    """An infinite key's weight is 0 in the rows that it scores -inf in, whatever fills the row tile."""
+    r = run4(gm, 1, 3, 1, 1, 128, 16, [100], seed=22, elem=BF16)
+    r["q"].copy_(r["q"].abs() + 0.1)
+    r["k"][r["table"][0, 2].long(), 0, 5] = -math.inf  # token 37
+    out, lse = gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    got = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse)
+    gm.mercury_sync_status()
+    assert torch.isfinite(lse).all() and torch.isfinite(got).all() and got[0, 0, 37] == 0
+    assert abs(got.sum().item() - 3) < 1e-4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+def test_both_ways_into_the_calls(gm, elem):
+    """The short way from Python and the long one (a stream given) make the same call; strided queries too."""
+    r = run4(gm, 3, 8, 2, 2, 64, 16, [300, 40, 700], seed=23, elem=elem)
+    wide = torch.zeros(3, 2, 8, 96, dtype=BF16, device="cuda").transpose(1, 2)
+    q = wide[..., 32:]
+    q.copy_(r["q"])
+    s = torch.cuda.current_stream()
+    outs = [torch.full((3, 2, 700), 9.0, device="cuda") for _ in range(3)]
+    gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"], out=outs[0])
+    gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"], out=outs[1], stream=s)
+    gm.mercury_attn_paged_mass(q, r["cache"], r["lens"], r["lse"], out=outs[2])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    kv = [[torch.full((3, 2, 700, 64), 9.0, dtype=BF16, device="cuda") for _ in range(2)] for _ in range(2)]
+    gm.mercury_kv_read(r["cache"], r["lens"], k_out=kv[0][0], v_out=kv[0][1])
+    gm.mercury_kv_read(r["cache"], r["lens"], k_out=kv[1][0], v_out=kv[1][1], stream=s)
+    assert all(torch.equal(a, b) for a, b in zip(*kv))
+    gen = torch.Generator("cuda").manual_seed(7)
+    got = []
+    for stream in (None, s):
+        k2, v2, table2, _ = make_any(3, 2, 64, 16, 8, elem, gen)
+        for c in (k2, v2):
+            c.view(torch.uint8).zero_()
+        table2.copy_(torch.arange(24, device="cuda").view(3, 8))
+        into = gm.PagedCache(k2, v2, table2, k_scale=r["ks"], v_scale=r["vs"])
+        out_lens, kept = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, 2, 100, dtype=torch.int32, device="cuda")
+        gm.mercury_kv_evict(r["cache"], into, outs[0], r["lens"], 100, last=10, out_lens=out_lens, kept=kept, stream=stream)
+        got.append((out_lens, kept, k2.view(torch.uint8), v2.view(torch.uint8)))
+    gm.mercury_sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ----------------------------------------------------------------------------------- eviction
 
 def kept_of(mass, n, keep, first, last):
@@ -595,6 +641,52 @@ def test_evict_keeps_the_heaviest(gm, elem, kind, B, Hkv, d, page, into_page, le
             written[table2[b, at // into_page].long(), h, at % into_page] = True
     for z, w in zip((k2, v2), was):
         assert torch.equal(z.view(torch.uint8)[~written], w[~written])
+
+
+def order_of(mass, n, keep, first, last):
+    """kept_of for long sequences, of all heads at once: mass [heads, width] without NaN."""
+    at = torch.arange(n, device=mass.device)
+    want = torch.where((at < first) | (at >= n - last), math.inf, mass[:, :n].double())
+    return torch.sort(want, dim=1, descending=True, stable=True)[1][:, :keep].sort(dim=1)[0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+@pytest.mark.parametrize("B,Hkv,n,keep", [
+    (20, 8, 40000, 3333),   # more heads than SMs, and more tokens than a block holds
+    (1, 1, 300000, 70001),  # one head, more tokens than its cluster holds
+    (1, 8, 33000, 32999),
+    (9, 5, 6000, 16),
+])
+def test_evict_long_sequences(gm, kind, B, Hkv, n, keep):
+    gen = torch.Generator("cuda").manual_seed(n)
+    page, d, first, last = 64, 64, 5, 9
+    pages = -(-n // page)
+    k = random_rows((B * pages, Hkv, page), d, gen)
+    table = torch.randperm(B * pages, generator=gen, device="cuda").to(torch.int32).view(B, pages)
+    into_pages = -(-keep // page)
+    k2 = torch.zeros(B * into_pages, Hkv, page, 36, dtype=torch.uint8, device="cuda")
+    v2 = torch.zeros_like(k2)
+    table2 = torch.arange(B * into_pages, dtype=torch.int32, device="cuda").view(B, into_pages)
+    one = torch.ones(Hkv, device="cuda")
+    cache, into = gm.PagedCache(k, k, table, k_scale=one, v_scale=one), gm.PagedCache(k2, v2, table2, k_scale=one, v_scale=one)
+    mass = torch.exp(3 * torch.randn(B, Hkv, n, generator=gen, device="cuda"))
+    if kind == "ties":
+        mass = torch.randint(0, 4, mass.shape, generator=gen, device="cuda").float()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    small = torch.zeros(B, Hkv, keep, device="cuda")
+    got, kept = gm.mercury_kv_evict(cache, into, mass, lens, keep, first=first, last=last, out_mass=small)
+    gm.mercury_sync_status()
+    assert (got == keep).all()
+    want = order_of(mass.view(B * Hkv, n), n, keep, first, last).view(B, Hkv, keep)
+    assert torch.equal(kept.long(), want)
+    assert torch.equal(small, mass.gather(2, want))
+    at = torch.arange(keep, device="cuda")
+    for b in {0, B - 1}:
+        for h in {0, Hkv - 1}:
+            rows = k[table[b, want[b, h] // page].long(), h, want[b, h] % page]
+            for z in (k2, v2):
+                assert torch.equal(z[table2[b, at // page].long(), h, at % page], rows)
 
 
 # ------------------------------------------------------------------------------------ together
