@@ -32,6 +32,7 @@ constexpr int kMassWarps = 8;
 constexpr int kMassThreads = kMassWarps * 32;
 constexpr int kMassTile = kMassWarps * 16;  // keys of a block's tile
 constexpr int kMassRows = 512;              // rows of a launch
+constexpr int kWideRows = 256;              // and where the tensor unit takes them
 
 struct MassArgs {
     PagedArgs p;        // q, qs, cache, seq_lens, new_lens, B, Hkv, G, Sq, R, causal
@@ -40,6 +41,7 @@ struct MassArgs {
     float *out;         // the same
     long long width;
     int r0, rows;       // this launch's rows of each head
+    int wide;           // rows of the tensor unit's product, or 0
     float mul, mul_lo;  // log2(e) / sqrt(d), and what its rounding leaves out
 };
 
@@ -173,38 +175,32 @@ struct Spot {
     int keys, tiles;  // of the sequence
 };
 
-template <int ELEM, int D>
-__global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid_constant__ MassArgs a)
+__device__ __forceinline__ void check_lengths(const MassArgs &a, int tid)
 {
-    using K = Keys<ELEM, D>;
-    constexpr int KK = D / 16, RUN = K::kRun;
-    extern __shared__ __align__(16) char smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int n_rt = (a.rows + 7) / 8;
-    uint2 *const qs = reinterpret_cast<uint2 *>(smem);                       // [row tile][k-step][lane]
-    Row *const rows = reinterpret_cast<Row *>(smem + n_rt * KK * 32 * 8);    // [row]
-    const PagedArgs &p = a.p;
-    const PagedView &c = p.cache;
-    chain_wait();
     if (blockIdx.x == 0 && a.r0 == 0)
-        for (int b = tid; b < p.B; b += kMassThreads) {
-            if (p.seq_lens[b] != mass_keys(a, b))
+        for (int b = tid; b < a.p.B; b += kMassThreads) {
+            if (a.p.seq_lens[b] != mass_keys(a, b))
                 record_bounds(0xb01);
-            if (p.new_lens && p.new_lens[b] != new_of(p, b))
+            if (a.p.new_lens && a.p.new_lens[b] != new_of(a.p, b))
                 record_bounds(0xb02);
         }
-    // the tiles of all heads in order, in equal shares
+}
+
+// The tiles of all heads in order, in equal shares: this block's are at .. end -
+// 1, the first of them s.
+__device__ __forceinline__ bool find_share(const MassArgs &a, int lane, Spot &s, long long &at, long long &end)
+{
+    const PagedArgs &p = a.p;
     long long total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         total += __reduce_add_sync(0xffffffffu, b < p.B ? mass_tiles(a, b) : 0);
     }
     total *= p.Hkv;
-    long long at = total * blockIdx.x / gridDim.x;
-    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    at = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
     if (at >= end)
-        return;
-    Spot s = {0, 0, 0, 0, 0};
+        return false;
     long long base = 0;
     for (int b0 = 0;; b0 += 32) {
         const int b = b0 + lane;
@@ -223,21 +219,66 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
     s.tiles = mass_tiles(a, s.b);
     s.h = (int)((at - base * p.Hkv) / s.tiles);
     s.j = (int)(at - base * p.Hkv - (long long)s.h * s.tiles);
+    return true;
+}
 
-    auto next_of = [&](Spot x) {
-        if (++x.j == x.tiles) {
-            x.j = 0;
-            if (++x.h == p.Hkv) {
-                x.h = 0;
-                do {
-                    ++x.b;  // there is one: the tile lies before the share's end
-                    x.keys = mass_keys(a, x.b);
-                    x.tiles = mass_tiles(a, x.b);
-                } while (x.tiles == 0);
-            }
+// The tile behind x; there is one in the share.
+__device__ __forceinline__ Spot next_spot(const MassArgs &a, Spot x)
+{
+    if (++x.j == x.tiles) {
+        x.j = 0;
+        if (++x.h == a.p.Hkv) {
+            x.h = 0;
+            do {
+                ++x.b;
+                x.keys = mass_keys(a, x.b);
+                x.tiles = mass_tiles(a, x.b);
+            } while (x.tiles == 0);
         }
-        return x;
-    };
+    }
+    return x;
+}
+
+// A row's constants.  mul (with mul_lo, what its rounding left out): from the
+// product of the operands to log2 units; l: its lse.
+__device__ __forceinline__ Row row_of(float mul, float mul_lo, float l, int step)
+{
+    constexpr float kLog2eLo = 1.9259629911266174e-8f;  // log2(e) less its nearest float
+    const float nl = -l * kLog2e;
+    const float off = mul == 0.f ? 0.f : mul_lo / mul;
+    const float more = fmaf(-l, kLog2e, -nl) - l * kLog2eLo + l * kLog2e * off;  // what nl leaves out
+    const bool counts = fabsf(l) < INFINITY || l != l;
+    return Row{mul, counts ? nl : -INFINITY, counts ? exp2f(more) : 0.f, step};
+}
+
+// The power of two that brings `top` to [2^14, 2^15), and its inverse, both normal.
+__device__ __forceinline__ void scale_of(float top, float &to, float &back)
+{
+    int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
+    up = min(max(up, -110), 110);
+    to = __uint_as_float((uint32_t)(127 + up) << 23);
+    back = __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+template <int ELEM, int D>
+__global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid_constant__ MassArgs a)
+{
+    using K = Keys<ELEM, D>;
+    constexpr int KK = D / 16, RUN = K::kRun;
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int n_rt = (a.rows + 7) / 8;
+    uint2 *const qs = reinterpret_cast<uint2 *>(smem);                       // [row tile][k-step][lane]
+    Row *const rows = reinterpret_cast<Row *>(smem + n_rt * KK * 32 * 8);    // [row]
+    const PagedArgs &p = a.p;
+    const PagedView &c = p.cache;
+    chain_wait();
+    check_lengths(a, tid);
+    Spot s;
+    long long at, end;
+    if (!find_share(a, lane, s, at, end))
+        return;
+    auto next_of = [&](const Spot &x) { return next_spot(a, x); };
     K keys;
     float prev = 0.f;  // of key g (t = 0) or g + 8 (t = 1)
     auto load = [&](const Spot &x) {
@@ -304,9 +345,8 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                                                fmaxf(fabsf(bf16_lo(q[kk].y)), fabsf(bf16_hi(q[kk].y)))));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    int up = 14 + 127 - (int)(__float_as_uint(top) >> 23);
-                    up = min(max(up, -110), 110);
-                    const float to = __uint_as_float((uint32_t)(127 + up) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
+                    float to, back;
+                    scale_of(top, to, back);
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
                         q[kk].x = pack_f16(bf16_lo(q[kk].x) * to, bf16_hi(q[kk].x) * to);
@@ -320,13 +360,7 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
                 for (int kk = 0; kk < KK; ++kk)
                     qs[(rt * KK + kk) * 32 + lane] = q[kk];
                 if (t == 0) {
-                    const float l = live ? a.lse[(long long)this_job * p.R + r] : INFINITY;
-                    constexpr float kLog2eLo = 1.9259629911266174e-8f;  // log2(e) less its nearest float
-                    const float nl = -l * kLog2e;
-                    const float off = mul == 0.f ? 0.f : mul_lo / mul;
-                    const float more = fmaf(-l, kLog2e, -nl) - l * kLog2eLo + l * kLog2e * off;  // what nl leaves out
-                    const bool counts = fabsf(l) < INFINITY || l != l;
-                    rows[rt * 8 + g] = Row{mul, counts ? nl : -INFINITY, counts ? exp2f(more) : 0.f, i};
+                    rows[rt * 8 + g] = row_of(mul, mul_lo, live ? a.lse[(long long)this_job * p.R + r] : INFINITY, i);
                 }
             }
             __syncthreads();
@@ -381,6 +415,351 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
     }
 }
 
+// Many rows: on the tensor unit.  A tile's 128 keys are M, the rows N (64, 128
+// or 256 of a launch), and each of eight warps reads the scores of 32 keys and
+// half of the rows back, a key a lane, so that a lane adds up its key's weights
+// without any exchange.  Keys are widened to 16 bits on their way into shared
+// memory; the product's time (128 rows: 256 cycles a tile) is a fraction of the
+// exponentials' (512), and two blocks an SM overlap one's product and loads
+// with the other's exponentials.  What a row costs there is its constants, read
+// from shared memory by every warp: so there is only one (of four rows at a
+// time), the exponent's summand; the factor is one for all rows, since their
+// queries are scaled by one power of two (of a row far below the largest
+// elements are lost that are 2^-38 of it, and scores enter by their absolute
+// error), and what rounding the summand leaves out, 2^-24 of lse, is left out.
+template <int ELEM, int D>
+struct Raw {  // half of a key's row
+    static constexpr int kWords = ELEM == MERCURY_ELEM_BF16 ? D / 4 : ELEM == MERCURY_ELEM_E4M3 ? D / 8 : D / 16 + 1;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const char *row, int half)
+    {
+        if (!row) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                w[i] = 0;
+            return;
+        }
+        if constexpr (ELEM == MERCURY_ELEM_E2M1) {
+            // rows of 72 (36) bytes
+#pragma unroll
+            for (int i = 0; i < D / 16; i += D / 64) {
+                const char *const from = row + half * (D / 4) + 4 * i;
+                if constexpr (D == 128) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(from);
+                    w[i] = x.x;
+                    w[i + 1] = x.y;
+                } else {
+                    w[i] = *reinterpret_cast<const uint32_t *>(from);
+                }
+            }
+            if constexpr (D == 128)
+                w[kWords - 1] = *reinterpret_cast<const uint32_t *>(row + 64 + 4 * half);
+            else
+                w[kWords - 1] = *reinterpret_cast<const uint16_t *>(row + 32 + 2 * half);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(row + half * (kWords * 4) + 4 * i));
+                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+            }
+        }
+    }
+    // elements 8 i .. + 7 as four words of the operand
+    __device__ __forceinline__ void widen(int i, uint32_t (&o)[4]) const
+    {
+        if constexpr (ELEM == MERCURY_ELEM_BF16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = w[4 * i + k];
+        } else if constexpr (ELEM == MERCURY_ELEM_E4M3) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                o[2 * k] = e4m3_to_f16(w[2 * i + k]);
+                o[2 * k + 1] = e4m3_to_f16(w[2 * i + k] >> 16);
+            }
+        } else {
+            const uint32_t b = w[kWords - 1] >> (8 * (i / 2)) & 0xffu, scale = e4m3_to_f16(b | b << 8);
+            o[0] = mul_f16(e2m1_to_f16<0>(w[i]), scale);
+            o[1] = mul_f16(e2m1_to_f16<1>(w[i]), scale);
+            o[2] = mul_f16(e2m1_to_f16<2>(w[i]), scale);
+            o[3] = mul_f16(e2m1_to_f16<3>(w[i]), scale);
+        }
+    }
+};
+
+// Where 16-byte chunk c of a row lies in an operand of `rows` rows: column
+// blocks of 64 elements, rows of 128 bytes, chunks permuted by the row (the
+// 128-byte swizzle).
+__device__ __forceinline__ int operand_at(int row, int c, int rows)
+{
+    return c / 8 * rows * 128 + row * 128 + ((c % 8 ^ (row & 7)) << 4);
+}
+
+constexpr int wide_smem(int D, int N)
+{
+    return 128 * D * 2 + N * D * 2 + N * 8 + 128 * 4 + 32;
+}
+
+template <int ELEM, int D>
+__global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const __grid_constant__ MassArgs a)
+{
+    constexpr bool kF16 = ELEM != MERCURY_ELEM_BF16;
+    constexpr int ROWB = ELEM == MERCURY_ELEM_BF16 ? 2 * D : ELEM == MERCURY_ELEM_E4M3 ? D : D / 2 + D / 16;
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.wide;
+    char *const keys_at = smem, *const queries_at = smem + 128 * D * 2;
+    float *const summands = reinterpret_cast<float *>(queries_at + N * D * 2);  // -inf: the row counts nothing
+    int *const steps = reinterpret_cast<int *>(summands + N);                   // of the new tokens
+    float *const halves = reinterpret_cast<float *>(steps + N);
+    uint64_t *const done = reinterpret_cast<uint64_t *>(halves + 128);
+    uint32_t *const slot = reinterpret_cast<uint32_t *>(done + 1);
+    int *const largest = reinterpret_cast<int *>(slot + 1);  // magnitude of the job's queries (bits)
+    const PagedArgs &p = a.p;
+    const PagedView &c = p.cache;
+    chain_wait();
+    check_lengths(a, tid);
+    Spot now;
+    long long at, end;
+    if (!find_share(a, lane, now, at, end))
+        return;
+    if (tid == 0) {
+        *largest = 0;
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(slot, N);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+
+    Raw<ELEM, D> raw;  // half (tid & 1) of key tid / 2
+    float prev = 0.f;  // of key tid (the first 128 threads)
+    // A tile's pages are asked for a tile before its keys are, and these a tile
+    // before they are used.
+    int page = -1;
+    auto look_up = [&](const Spot &x) {
+        const int key = x.j * kMassTile + tid / 2;
+        if (key < x.keys)
+            page = c.table[x.b * c.table_stride + page_of(c, key)];
+    };
+    auto load = [&](const Spot &x) {
+        const int key = x.j * kMassTile + tid / 2;
+        const char *row = nullptr;
+        if (key < x.keys) {
+            if (page >= 0 && page < c.num_pages)
+                row = c.k + page * c.page_stride * (ELEM == MERCURY_ELEM_BF16 ? 2 : 1) +
+                      ((long long)x.h * c.page_size + key - page_of(c, key) * c.page_size) * ROWB;
+            else
+                record_bounds(0xb03);  // such keys count as zeros
+        }
+        raw.load(row, tid & 1);
+        const int mine = x.j * kMassTile + tid;
+        prev = 0.f;
+        if (a.mass && tid < 128 && mine < x.keys)
+            prev = a.mass[((long long)x.b * p.Hkv + x.h) * a.width + mine];
+    };
+    look_up(now);
+    load(now);
+    Spot next = now;
+    if (at + 1 < end) {
+        next = next_spot(a, now);
+        look_up(next);
+    }
+    uint32_t idesc = 0, parity = 0;
+    if (N == 64)
+        idesc = idesc_bf16_f32(128, 64, false);
+    else if (N == 128)
+        idesc = idesc_bf16_f32(128, 128, false);
+    else
+        idesc = idesc_bf16_f32(128, 256, false);
+    if (kF16)
+        idesc &= ~((1u << 7) | (1u << 10));  // both operands fp16
+    int job = -1;
+    float mul = a.mul;
+    bool late = false;
+    for (;;) {
+        const int n_new = new_of(p, now.b);
+        const int this_job = now.b * p.Hkv + now.h;
+        if (this_job != job) {
+            // this head's queries (the last product that read the others is done)
+            job = this_job;
+            constexpr int LPR = D / 8, EACH = kMassThreads / LPR, U = 8;  // lanes of a row, rows at a time, loads on their way
+            const int ch = tid % LPR;
+            auto fetch = [&](int n, uint4 &x, float *l) {
+                const int r = a.r0 + n, head = p.Sq == 1 ? r : r / p.Sq, i = r - head * p.Sq;
+                x = make_uint4(0, 0, 0, 0);
+                if (n < a.rows && i < n_new) {
+                    x = *reinterpret_cast<const uint4 *>(p.q + now.b * p.qs.b + (now.h * p.G + head) * p.qs.h + i * p.qs.s + ch * 8);
+                    if (l && ch == 0)
+                        *l = a.lse[(long long)this_job * p.R + r];
+                }
+                return i;
+            };
+            float mul_lo = a.mul_lo, to = 1.f;
+            mul = a.mul;
+            uint4 x[U];
+            float l[U];
+            int step[U];
+            if constexpr (kF16) {
+                float top = 0.f;
+                for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        l[u] = INFINITY;
+                        step[u] = fetch(n0 + u * EACH, x[u], &l[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(x[u].x)), fabsf(bf16_hi(x[u].x))),
+                                                     fmaxf(fabsf(bf16_lo(x[u].y)), fabsf(bf16_hi(x[u].y)))),
+                                               fmaxf(fmaxf(fabsf(bf16_lo(x[u].z)), fabsf(bf16_hi(x[u].z))),
+                                                     fmaxf(fabsf(bf16_lo(x[u].w)), fabsf(bf16_hi(x[u].w))))));
+                }
+                atomicMax(largest, __reduce_max_sync(0xffffffffu, __float_as_int(top)));  // (magnitudes: their bits are in order)
+                __syncthreads();
+                float back;
+                scale_of(__int_as_float(*largest), to, back);
+                const float ks = c.k_scale[now.h], hi = a.mul * ks;
+                mul_lo = (fmaf(a.mul, ks, -hi) + a.mul_lo * ks) * back;
+                mul = hi * back;
+            }
+            for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
+                if (!kF16 || N > U * EACH) {  // (else they are here)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        l[u] = INFINITY;
+                        step[u] = fetch(n0 + u * EACH, x[u], &l[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int n = n0 + u * EACH;
+                    if (n >= N)
+                        break;
+                    if (kF16)
+                        x[u] = make_uint4(pack_f16(bf16_lo(x[u].x) * to, bf16_hi(x[u].x) * to), pack_f16(bf16_lo(x[u].y) * to, bf16_hi(x[u].y) * to),
+                                          pack_f16(bf16_lo(x[u].z) * to, bf16_hi(x[u].z) * to), pack_f16(bf16_lo(x[u].w) * to, bf16_hi(x[u].w) * to));
+                    *reinterpret_cast<uint4 *>(queries_at + operand_at(n, ch, N)) = x[u];
+                    if (ch == 0) {
+                        // (of mul and lse in log2 units, as in row_of)
+                        const float off = mul == 0.f ? 0.f : mul_lo / mul;
+                        summands[n] = fabsf(l[u]) < INFINITY || l[u] != l[u] ? fmaf(-l[u], kLog2e, l[u] * kLog2e * off) : -INFINITY;
+                        steps[n] = step[u];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[4];
+            raw.widen(i, o);
+            *reinterpret_cast<uint4 *>(keys_at + operand_at(tid / 2, (tid & 1) * (D / 16) + i, 128)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        const float was = prev;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (tid == 0)
+            *largest = 0;  // (the next job's comes behind another barrier)
+        if (warp == 0) {
+            tc_fence_after();
+            const uint32_t leader = elect_lane();
+            const uint64_t dk = smem_desc_sw128(smem_u32(keys_at), 16, 1024), dq = smem_desc_sw128(smem_u32(queries_at), 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss_w(tmem, dk + (uint32_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
+                          dq + (uint32_t)((kk / 4 * N * 128 + kk % 4 * 32) >> 4), idesc, kk > 0 ? 1u : 0u, leader);
+            if (!p.fault)  // (the test hook: the product's end is never told)
+                umma_commit_w(done, leader);
+        }
+        const Spot tile = now;
+        const bool on = ++at < end;
+        if (on) {
+            now = next;
+            load(now);  // on its way while this tile is computed
+            if (at + 1 < end) {
+                next = next_spot(a, now);
+                look_up(next);
+            }
+        }
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(done, parity))
+            if (globaltimer_ns() - t0 > p.wait_ns) {
+                late = true;
+                break;
+            }
+        parity ^= 1;
+        tc_fence_after();
+        const int k0 = tile.j * kMassTile, quarter = warp & 3, half = warp >> 2;
+        const int key = k0 + quarter * 32 + lane;
+        const int seen_by_all = p.causal ? tile.keys - n_new + 1 : tile.keys;
+        float sum = 0.f;
+        auto add_rows = [&](auto masked) {
+            sum = 0.f;
+            for (int n = half * (N / 2); n < half * (N / 2) + N / 2; n += 32) {
+                uint32_t x[32];
+                tmem_ld_x32(tmem + ((uint32_t)(quarter * 32) << 16) + n, x);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(summands + n + k);
+                    const float nl[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = ex2_approx(fmaf(__uint_as_float(x[k + e]), mul, nl[e]));
+                        if constexpr (decltype(masked)::value) {
+                            if (nl[e] != -INFINITY && key < (p.causal ? seen_by_all + steps[n + k + e] : tile.keys))
+                                sum += w;
+                        } else {
+                            sum += w;
+                        }
+                    }
+                }
+            }
+        };
+        // (An infinite or NaN key gives NaN in rows that count nothing, too: such
+        // sums are made again, row by row.)
+        bool all = k0 + kMassTile > seen_by_all;
+        if (!all) {
+            add_rows(Masked<false>());
+            all = __any_sync(0xffffffffu, !(fabsf(sum) < INFINITY));
+        }
+        if (all)
+            add_rows(Masked<true>());
+        if (half)
+            halves[tid - 128] = sum;
+        tc_fence_before();
+        late = __syncthreads_or(late);
+        if (late)
+            break;
+        if (!half && key < tile.keys)
+            a.out[(long long)this_job * a.width + key] = was + (sum + halves[tid]);
+        if (!on)
+            break;
+    }
+    if (late) {
+        if (tid == 0) {
+            atomicOr(&g_paged_err_word, kErrTimeout);
+            atomicCAS(&g_paged_err_site, 0u, 0xb04u);
+        }
+        // the product may still be on its way: its memory is given up once it
+        // has ended, waited for with a limit too
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(done, parity ^ 1) && globaltimer_ns() - t0 <= p.wait_ns)
+            ;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, N);
+    }
+}
+
 template <int ELEM, int D>
 int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
 {
@@ -390,14 +769,22 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     int rc = prepare_kernel((const void *)kernel, kMassRows * kRowSmem, &ki, msg, msg_len);
     if (rc != MERCURY_OK)
         return rc;
+    KernelInfo wi;
+    auto *wide_kernel = attn_mass_wide_kernel<ELEM, D>;
+    rc = prepare_kernel((const void *)wide_kernel, wide_smem(D, kWideRows), &wi, msg, msg_len);
+    if (rc != MERCURY_OK)
+        return rc;
     const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
     const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
-    for (a.r0 = 0; a.r0 < a.p.R; a.r0 += kMassRows) {
-        a.rows = a.p.R - a.r0 < kMassRows ? a.p.R - a.r0 : kMassRows;
-        const int smem = (a.rows + 7) / 8 * 8 * kRowSmem;
-        const int per_sm = smem <= 100000 ? 2 : 1;
+    const bool wide = a.p.R > 32;
+    const int each = wide ? kWideRows : kMassRows;
+    for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
+        a.rows = a.p.R - a.r0 < each ? a.p.R - a.r0 : each;
+        a.wide = !wide ? 0 : a.rows <= 64 ? 64 : a.rows <= 128 ? 128 : 256;
+        const int smem = wide ? wide_smem(D, a.wide) : (a.rows + 7) / 8 * 8 * kRowSmem;
+        const int per_sm = smem <= 110000 ? 2 : 1;
         const long long grid = most < (long long)ki.sms * per_sm ? most : (long long)ki.sms * per_sm;
-        const cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), kMassThreads, smem, stream, a);
+        const cudaError_t e = launch_chained(wide ? wide_kernel : kernel, dim3((unsigned)grid), kMassThreads, smem, stream, a);
         if (e != cudaSuccess) {
             snprintf(msg, msg_len, "attention weight launch: %s", cudaGetErrorString(e));
             return MERCURY_ECUDA;
@@ -419,10 +806,11 @@ int launch_elem(MassArgs &a, int elem, cudaStream_t stream, char *msg, size_t ms
 
 int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
                      const int *new_lens, int B, int Hq, int Sq, int causal, const float *lse, const float *mass,
-                     float *out, long long width, cudaStream_t stream, char *msg, size_t msg_len)
+                     float *out, long long width, unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg,
+                     size_t msg_len)
 {
     MassArgs a = {};
-    a.p = paged_args(q, qs, cache, seq_lens, new_lens, B, Hq, Sq, causal, nullptr, nullptr, 0, 0, 0);
+    a.p = paged_args(q, qs, cache, seq_lens, new_lens, B, Hq, Sq, causal, nullptr, nullptr, 0, wait_ns, fault);
     a.lse = lse;
     a.mass = mass;
     a.out = out;

@@ -131,7 +131,8 @@ int launch_attn_paged4(const void *q, const Strides &qs, const mercury_paged_cac
 // The attention weight of every cached key (attn_mass.cu).
 int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache &cache, const int *seq_lens,
                      const int *new_lens, int B, int Hq, int Sq, int causal, const float *lse, const float *mass,
-                     float *out, long long width, cudaStream_t stream, char *msg, size_t msg_len);
+                     float *out, long long width, unsigned long long wait_ns, int fault, cudaStream_t stream, char *msg,
+                     size_t msg_len);
 
 // A cache's heaviest tokens into a shorter one; a cache read back (kv_evict.cu).
 int launch_kv_evict(const mercury_paged_cache &cache, const mercury_paged_cache &into, const float *mass, long long width,

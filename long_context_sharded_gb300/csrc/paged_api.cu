@@ -369,7 +369,8 @@ int mercury_attn_paged_mass(const void *q, const long long *q_strides, const mer
     size_t len;
     char *msg = error_buffer(&len);
     cudaStream_t s = (cudaStream_t)stream;
-    rc = launch_attn_mass(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, lse, mass, out, width, s, msg, len);
+    rc = launch_attn_mass(q, qs, *cache, seq_lens, new_lens, B, Hq, Sq, causal ? 1 : 0, lse, mass, out, width,
+                          device_wait_ns(), paged_fault(), s, msg, len);
     return finish_call(rc, s);
 }
 

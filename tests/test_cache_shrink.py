@@ -476,7 +476,13 @@ def weights(r, lse, lens, new, causal, prev, width):
     (3, 6, 2, 4, 128, 8, [4, 260, 999], None, True),
     (3, 6, 2, 4, 128, 24, [4, 260, 999], None, False),
     (5, 16, 2, 5, 64, 16, [500, 3, 40, 2, 0], [4, 3, 0, 5, 2], True),
-    (2, 12, 1, 64, 128, 32, [1000, 64], [64, 33], True),  # 768 rows: two passes
+    (2, 12, 1, 64, 128, 32, [1000, 64], [64, 33], True),  # 768 rows: three passes of the tensor unit's product
+    (3, 8, 1, 4, 64, 16, [500, 4, 130], None, True),      # 32 rows, the most that go by warps
+    (3, 11, 1, 3, 64, 16, [500, 3, 130], None, True),     # 33 rows
+    (2, 8, 2, 16, 128, 16, [16, 1100], None, False),      # 64 rows
+    (2, 8, 2, 17, 128, 8, [40, 1100], [17, 3], True),     # 68
+    (6, 32, 8, 40, 64, 64, [40, 700, 41, 0, 127, 129], None, True),  # 160
+    (2, 9, 1, 64, 128, 16, [64, 333], None, True),        # 576
     (40, 3, 3, 1, 128, 16, list(range(40)), None, True),
 ])
 def test_mass_adds_the_weights(gm, elem, prev, B, Hq, Hkv, Sq, d, page, lens, new, causal):
@@ -830,6 +836,26 @@ def test_pages_and_lengths_out_of_range_are_reported(gm, elem):
                 expect(lambda: gm.mercury_kv_append(cache, kk, kk, torch.tensor(past, dtype=torch.int32, device="cuda")))
             expect(lambda: gm.mercury_kv_append(cache, kk, kk, zero, new_lens=torch.tensor([2, 3, -1], dtype=torch.int32, device="cuda")))
         del k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E2M1])
+def test_a_product_whose_end_is_never_told_ends_in_a_timeout(gm, monkeypatch, elem):
+    """Weights of many rows: the wait for the tensor unit runs out, the status says so, and the next call is right."""
+    r = run4(gm, 2, 8, 2, 32, 128, 16, [300, 200], seed=62, elem=elem)
+    first = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"])
+    gm.mercury_sync_status()
+    monkeypatch.setenv("MERCURY_FAULT", "drop_page_copy")
+    monkeypatch.setenv("MERCURY_WAIT_NS", "20000000")
+    gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"])
+    with pytest.raises(gm.MercuryError) as e:
+        gm.mercury_sync_status()
+    assert e.value.status == gm.MERCURY_ETIMEOUT
+    monkeypatch.delenv("MERCURY_FAULT")
+    monkeypatch.delenv("MERCURY_WAIT_NS")
+    again = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"])
+    gm.mercury_sync_status()
+    assert torch.equal(first, again)
 
 
 @pytest.mark.gpu
