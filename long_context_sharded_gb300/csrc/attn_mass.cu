@@ -776,7 +776,7 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         return rc;
     const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
     const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
-    const bool wide = a.p.R > 32;
+    const bool wide = a.p.R > 64;  // (64 rows of 8 x 26K: 139 us so in 16 bits, by warps 126; 128 rows 155 and 194)
     const int each = wide ? kWideRows : kMassRows;
     for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
         a.rows = a.p.R - a.r0 < each ? a.p.R - a.r0 : each;

@@ -477,8 +477,8 @@ def weights(r, lse, lens, new, causal, prev, width):
     (3, 6, 2, 4, 128, 24, [4, 260, 999], None, False),
     (5, 16, 2, 5, 64, 16, [500, 3, 40, 2, 0], [4, 3, 0, 5, 2], True),
     (2, 12, 1, 64, 128, 32, [1000, 64], [64, 33], True),  # 768 rows: three passes of the tensor unit's product
-    (3, 8, 1, 4, 64, 16, [500, 4, 130], None, True),      # 32 rows, the most that go by warps
-    (3, 11, 1, 3, 64, 16, [500, 3, 130], None, True),     # 33 rows
+    (3, 16, 1, 4, 64, 16, [500, 4, 130], None, True),     # 64 rows, the most that go by warps
+    (3, 13, 1, 5, 64, 16, [500, 5, 1300], None, True),    # 65 rows
     (2, 8, 2, 16, 128, 16, [16, 1100], None, False),      # 64 rows
     (2, 8, 2, 17, 128, 8, [40, 1100], [17, 3], True),     # 68
     (6, 32, 8, 40, 64, 64, [40, 700, 41, 0, 127, 129], None, True),  # 160
