@@ -67,9 +67,15 @@ struct Keys<MERCURY_ELEM_BF16, D> {
     uint4 w[2][D / 32];
     __device__ __forceinline__ void load(int i, const char *row, int t)
     {
+        if (!row) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+                w[i][j] = make_uint4(0, 0, 0, 0);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
-            w[i][j] = row ? __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16)) : make_uint4(0, 0, 0, 0);
+            w[i][j] = __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16));
     }
     __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
     {
@@ -93,9 +99,15 @@ struct Keys<MERCURY_ELEM_E4M3, D> {
     uint4 w[2][D / 64];
     __device__ __forceinline__ void load(int i, const char *row, int t)
     {
+        if (!row) {
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+                w[i][j] = make_uint4(0, 0, 0, 0);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
-            w[i][j] = row ? __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16)) : make_uint4(0, 0, 0, 0);
+            w[i][j] = __ldcs(reinterpret_cast<const uint4 *>(row + j * 64 + t * 16));
     }
     __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
     {
@@ -118,28 +130,43 @@ struct Keys<MERCURY_ELEM_E2M1, D> {
     static constexpr int kRun = D / 8;
     static constexpr bool kF16 = true;
     static constexpr int kRowB = D / 2 + D / 16;
-    uint32_t w[2][2][D / 64], s[2][2];  // [key][run]
+    uint32_t w[2][2][D / 64], s[2][D / 64];  // [key][run], all of a row's scales
     __device__ __forceinline__ void load(int i, const char *row, int t)
     {
+        if (!row) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (D == 128) {
-                const uint2 x = row ? *reinterpret_cast<const uint2 *>(row + j * 32 + t * 8) : make_uint2(0, 0);
+            for (int j = 0; j < D / 64; ++j)
+                w[i][0][j] = w[i][1][j] = s[i][j] = 0;
+            return;
+        }
+        if constexpr (D == 128) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(row + j * 32 + t * 8);
                 w[i][j][0] = x.x;
                 w[i][j][1] = x.y;
-            } else {
-                w[i][j][0] = row ? *reinterpret_cast<const uint32_t *>(row + j * 16 + t * 4) : 0u;
             }
-            s[i][j] = row ? *reinterpret_cast<const uint8_t *>(row + D / 2 + j * (D / 32) + t * (D / 8) / 16) : 0u;
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + 64);
+            s[i][0] = x.x;
+            s[i][1] = x.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[i][j][0] = *reinterpret_cast<const uint32_t *>(row + j * 16 + t * 4);
+            s[i][0] = *reinterpret_cast<const uint32_t *>(row + 32);
         }
     }
     __device__ __forceinline__ void widen(uint32_t (&f)[D / 16][4]) const
     {
+        // this lane's two runs' scales
+        const int t = threadIdx.x & 3;
+        const uint32_t pick = D == 128 ? t | (4 + t) << 4 : t / 2 | (2 + t / 2) << 4;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t both = e4m3_to_f16(__byte_perm(s[i][0], s[i][D / 64 - 1], pick));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t scale = e4m3_to_f16(s[i][j] | s[i][j] << 8);
+                const uint32_t scale = __byte_perm(both, 0, j ? 0x3232 : 0x1010);
 #pragma unroll
                 for (int k = 0; k < D / 64; ++k) {
                     const uint32_t x = w[i][j][k];
@@ -150,6 +177,7 @@ struct Keys<MERCURY_ELEM_E2M1, D> {
                     f[kk + 1][2 + i] = mul_f16(e2m1_to_f16<3>(x), scale);
                 }
             }
+        }
     }
 };
 
@@ -281,21 +309,30 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
     auto next_of = [&](const Spot &x) { return next_spot(a, x); };
     K keys;
     float prev = 0.f;  // of key g (t = 0) or g + 8 (t = 1)
+    const bool one_page = c.page_size % 16 == 0;  // the 16 keys of a warp lie in one
+    const long long page_bytes = c.page_stride * (ELEM == MERCURY_ELEM_BF16 ? 2 : 1), head_bytes = (long long)c.page_size * K::kRowB;
     auto load = [&](const Spot &x) {
         const int k0 = x.j * kMassTile + warp * 16;
+        if (k0 >= x.keys)
+            return;
+        // (behind the last key: that key again, whose sum is not written)
+        const int last = x.keys - 1 - k0;
+        auto row_at = [&](int key) -> const char * {
+            const int pg = page_of(c, key), page = c.table[x.b * c.table_stride + pg];
+            if (page >= 0 && page < c.num_pages)
+                return c.k + page * page_bytes + x.h * head_bytes + (key - pg * c.page_size) * (long long)K::kRowB;
+            record_bounds(0xb03);  // such keys count as zeros
+            return nullptr;
+        };
+        if (one_page) {
+            const char *const row = row_at(k0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int key = k0 + g + 8 * i;
-            const char *row = nullptr;
-            if (key < x.keys) {
-                const int pg = page_of(c, key), page = c.table[x.b * c.table_stride + pg];
-                if (page >= 0 && page < c.num_pages)
-                    row = c.k + page * c.page_stride * (ELEM == MERCURY_ELEM_BF16 ? 2 : 1) +
-                          ((long long)x.h * c.page_size + key - pg * c.page_size) * K::kRowB;
-                else
-                    record_bounds(0xb03);  // such keys count as zeros
-            }
-            keys.load(i, row, t);
+            for (int i = 0; i < 2; ++i)
+                keys.load(i, row ? row + min(g + 8 * i, last) * K::kRowB : nullptr, t);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                keys.load(i, row_at(k0 + min(g + 8 * i, last)), t);
         }
         const int key = k0 + g + 8 * t;
         prev = 0.f;
@@ -303,10 +340,9 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
             prev = a.mass[((long long)x.b * p.Hkv + x.h) * a.width + key];
     };
     load(s);
-    int job = -1;
+    int job = -1, n_new = 0;
     for (;;) {
         const Spot now = s;
-        const int n_new = new_of(p, now.b);
         const int this_job = now.b * p.Hkv + now.h;
         uint32_t f[KK][4];
         keys.widen(f);
@@ -319,6 +355,7 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid
         if (this_job != job) {
             // this head's queries
             job = this_job;
+            n_new = new_of(p, now.b);
             __syncthreads();
             float ks = 1.f;
             if (K::kF16)
