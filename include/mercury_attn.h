@@ -731,12 +731,16 @@ MERCURY_API int mercury_attn_paged_bf16(const void *q, const long long *q_stride
  * that results do not change between calls.
  * A seq_lens that exceeds width is taken as width and reported, and so are
  * lengths and pages out of range, as in mercury_attn_paged.
+ * A weight is good to 2^-22 of |score| + |lse|, and to the score's own error (a
+ * sum of d products in fp32).  Up to 64 rows a KV head (Hq/Hkv * Sq) go by
+ * warp-level products, more on the tensor unit, where the keys are read once
+ * for each 256.  Its waits are bounded (MERCURY_WAIT_NS); one that runs out is
+ * reported as MERCURY_ETIMEOUT.
  * Requirements: as mercury_attn_paged (but for the number of tiles); width >= 1.
- * More than 512 rows a KV head (Hq/Hkv * Sq) read the keys once for each 512.
- * The first call on a device for a cache type and head dim prepares its kernel;
+ * The first call on a device for a cache type and head dim prepares its kernels;
  * make it before any stream capture.
- * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
- * when MERCURY_SYNC_CHECK=1.
+ * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS or
+ * MERCURY_ETIMEOUT when MERCURY_SYNC_CHECK=1.
  */
 MERCURY_API int mercury_attn_paged_mass(const void *q, const long long *q_strides, const mercury_paged_cache *cache,
                                         const int *seq_lens, const int *new_lens, int B, int Hq, int Sq, int causal,

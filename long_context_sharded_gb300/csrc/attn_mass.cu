@@ -5,16 +5,27 @@
 // heads' new tokens) of exp(q_r.k / sqrt(d) - lse_r), over the rows that see
 // key k; lse_r is what attention gave.
 //
-// Each key is read once, values not at all.  A key belongs to one warp, which
-// adds its rows in a fixed order: no atomics, the same bits in every run.  Keys
-// are the matrix instructions' first operand (16 rows), straight from memory
-// into registers: the order of elements within a product's inner axis is free,
-// so a lane takes whole 16-byte (8- or 4-byte) runs of two keys, and the
-// queries, held in shared memory as operands, in the same order.  All rows of
-// the head go over the registers that hold 16 keys, so many rows cost no
-// further reads, and an 8- or 4-bit key is widened once.  All tiles of all
-// heads, in order, are dealt to the blocks in equal contiguous shares, counted
-// on the device from seq_lens.
+// Each key is read once, values not at all.  A key belongs to one warp (or, of
+// many rows, to two, which add up half of them each), in a fixed order: no
+// atomics, the same bits in every run.  All tiles of all heads, in order, are
+// dealt to the blocks in equal contiguous shares, counted on the device from
+// seq_lens.
+//
+// Few rows (a decode step, a few drafted tokens): warp-level products.  Keys
+// are the first operand (16 rows), straight from memory into registers: the
+// order of elements within a product's inner axis is free, so a lane takes
+// whole 16-byte (8- or 4-byte) runs of two keys, and the queries, held in shared
+// memory as operands, in the same order.  All rows of the head go over the
+// registers that hold 16 keys, so further rows cost no further reads, and an 8-
+// or 4-bit key is widened once.  More than 64 rows: the tensor unit, below.
+//
+// Measured on a GB300, of the measured copy bandwidth (6680 GB/s) or the
+// product's rate: one token of 8 sequences of 20K to 32K, 32 query and 8 KV
+// heads of 128: 16-bit keys 69 us, 95 %; e4m3 50 us, 67 %, e2m1 51 us, 37 %:
+// not by bytes, but by a tile's chain of look-up, load, widening and products
+// (16-bit keys take 320 instructions for 16 keys of a warp).  Rows a KV head, 16
+// bits: 16 72 us, 32 86, 64 122, 128 155, 256 215 (515 TFLOP/s); e2m1 57, 74,
+// 107, 108, 156.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -31,8 +42,8 @@ namespace {
 constexpr int kMassWarps = 8;
 constexpr int kMassThreads = kMassWarps * 32;
 constexpr int kMassTile = kMassWarps * 16;  // keys of a block's tile
-constexpr int kMassRows = 512;              // rows of a launch
-constexpr int kWideRows = 256;              // and where the tensor unit takes them
+constexpr int kMassRows = 64;               // rows that go by warps; more by the tensor unit,
+constexpr int kWideRows = 256;              // so many a launch
 
 struct MassArgs {
     PagedArgs p;        // q, qs, cache, seq_lens, new_lens, B, Hkv, G, Sq, R, causal
@@ -813,7 +824,10 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         return rc;
     const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
     const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
-    const bool wide = a.p.R > 64;  // (64 rows of 8 x 26K: 139 us so in 16 bits, by warps 126; 128 rows 155 and 194)
+    // (8 sequences of 20K to 32K, 8 KV heads of 128, 16 bits: 64 rows by warps 122 us
+    // and on the tensor unit 139, 128 rows 190 and 155; 4 bits: 107 and 88, 178 and
+    // 108; one of 4K, 16 bits: 6.7 and 9.0, 9.4 and 9.8)
+    const bool wide = a.p.R > kMassRows;
     const int each = wide ? kWideRows : kMassRows;
     for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
         a.rows = a.p.R - a.r0 < each ? a.p.R - a.r0 : each;

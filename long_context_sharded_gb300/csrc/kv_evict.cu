@@ -8,7 +8,14 @@
 //
 // Reading back.  k_out[b][h][i] = the values of token i's row, rounded once.
 //
-// Both are bound by memory: a row is read once and written once.
+// Rows are read once and written once; what is left is the selection, a chain
+// of steps that each wait for the one before.
+//
+// Measured on a GB300: one sequence of 32K, 8 KV heads of 128, to 4K, 16 bits: 18
+// us (5 us of bytes); 16 sequences of 500 to 16K to 2K, 8 bits: 38 us (20 us of
+// bytes).  Each kernel alone and cold: selection 14 and 18 us, rows 10 and 23;
+// with one block a head the first selection took 30 us.  32K tokens of a 4-bit
+// cache read back: 29 us, 89 % of the measured copy bandwidth.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -383,7 +390,9 @@ int launch_select(SelectArgs &s, long long heads, cudaStream_t stream, char *msg
 // ------------------------------------------------------------------ and their rows
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveAhead = 2;  // rows that a thread has on the way, of keys and of values
+// Rows that a thread has on the way, of keys and of values: more of them leave
+// fewer blocks (16 sequences to 2K: 36 us with 2, 38 with 1, 39 with 4, 48 with 8).
+constexpr int kMoveAhead = 2;
 
 struct MoveArgs {
     PagedView src, dst;
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
         const int sp = page_of(s, token);
         const int page = s.table[b * s.table_stride + sp];
         if (page >= 0 && page < s.num_pages)
-            from[i] = page * s.page_stride * (long long)1 +
+            from[i] = page * s.page_stride +
                       ((long long)h * s.page_size + token - sp * s.page_size) * (UNITS * sizeof(U));
         else
             record_bounds(0xa02);
