@@ -24,8 +24,8 @@
 // heads of 128: 16-bit keys 69 us, 95 %; e4m3 50 us, 67 %, e2m1 51 us, 37 %:
 // not by bytes, but by a tile's chain of look-up, load, widening and products
 // (16-bit keys take 320 instructions for 16 keys of a warp).  Rows a KV head, 16
-// bits: 16 72 us, 32 86, 64 122, 128 155, 256 215 (515 TFLOP/s); e2m1 57, 74,
-// 107, 108, 156.
+// bits: 16 72 us, 32 86, 64 122, 128 157, 256 219 (505 TFLOP/s); e2m1 57, 74,
+// 107, 109, 154.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -54,6 +54,7 @@ struct MassArgs {
     int r0, rows;       // this launch's rows of each head
     int wide;           // rows of the tensor unit's product, or 0
     float mul, mul_lo;  // log2(e) / sqrt(d), and what its rounding leaves out
+    unsigned long long per_sq;  // 2^40 / Sq, rounded up
 };
 
 // A row of queries: a weight is 2^(score * mul + nl) * rest.  nl, lse in log2
@@ -635,39 +636,58 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
         if (this_job != job) {
             // this head's queries (the last product that read the others is done)
             job = this_job;
-            constexpr int LPR = D / 8, EACH = kMassThreads / LPR, U = 8;  // lanes of a row, rows at a time, loads on their way
+            // lanes of a row, rows at a time, loads on their way (16-bit keys, whose
+            // next tile takes more registers: with 8 they spill, 128 rows 213 us)
+            constexpr int LPR = D / 8, EACH = kMassThreads / LPR, U = kF16 ? 8 : 4;
             const int ch = tid % LPR;
-            auto fetch = [&](int n, uint4 &x, float *l) {
-                const int r = a.r0 + n, head = p.Sq == 1 ? r : r / p.Sq, i = r - head * p.Sq;
-                x = make_uint4(0, 0, 0, 0);
-                if (n < a.rows && i < n_new) {
-                    x = *reinterpret_cast<const uint4 *>(p.q + now.b * p.qs.b + (now.h * p.G + head) * p.qs.h + i * p.qs.s + ch * 8);
-                    if (l && ch == 0)
-                        *l = a.lse[(long long)this_job * p.R + r];
-                }
-                return i;
+            const __nv_bfloat16 *const head_q = p.q + now.b * p.qs.b + now.h * p.G * p.qs.h;
+            const float *const head_lse = a.lse + (long long)this_job * p.R;
+            // (as 16-bit integers, whose order is theirs)
+            auto magnitude = [](uint32_t w) {
+                w &= 0x7fff7fffu;
+                return w & ~__vcmpgeu2(w, 0x7f807f80u);
             };
             float mul_lo = a.mul_lo, to = 1.f;
             mul = a.mul;
             uint4 x[U];
-            float l[U];
-            int step[U];
-            if constexpr (kF16) {
-                float top = 0.f;
-                for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
+            // Rows' elements; their lse and new tokens go where the rows' constants
+            // do.  Where all rows share a scale, one that counts nothing is taken as
+            // zeros: the scale may not hang on what it holds (nor on an infinity).
+            auto load_rows = [&](int n0) {
+                float l[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        l[u] = INFINITY;
-                        step[u] = fetch(n0 + u * EACH, x[u], &l[u]);
+                for (int u = 0; u < U; ++u) {
+                    const int n = n0 + u * EACH, r = a.r0 + n, head = (int)(r * a.per_sq >> 40), i = r - head * p.Sq;
+                    x[u] = make_uint4(0, 0, 0, 0);
+                    l[u] = INFINITY;
+                    if (n < a.rows && i < n_new) {
+                        x[u] = *reinterpret_cast<const uint4 *>(head_q + head * p.qs.h + i * p.qs.s + ch * 8);
+                        if (kF16 || ch == 0)
+                            l[u] = head_lse[r];
                     }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int n = n0 + u * EACH, r = a.r0 + n;
+                    if (kF16) {
+                        const uint32_t keep = fabsf(l[u]) == INFINITY ? 0u : 0xffffffffu;
+                        x[u].x &= keep, x[u].y &= keep, x[u].z &= keep, x[u].w &= keep;
+                    }
+                    if (ch == 0 && n < N) {
+                        summands[n] = l[u];
+                        steps[n] = r - (int)(r * a.per_sq >> 40) * p.Sq;
+                    }
+                }
+            };
+            if constexpr (kF16) {
+                uint32_t top = 0;
+                for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
+                    load_rows(n0);
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(x[u].x)), fabsf(bf16_hi(x[u].x))),
-                                                     fmaxf(fabsf(bf16_lo(x[u].y)), fabsf(bf16_hi(x[u].y)))),
-                                               fmaxf(fmaxf(fabsf(bf16_lo(x[u].z)), fabsf(bf16_hi(x[u].z))),
-                                                     fmaxf(fabsf(bf16_lo(x[u].w)), fabsf(bf16_hi(x[u].w))))));
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(magnitude(x[u].x), magnitude(x[u].y)), __vmaxu2(magnitude(x[u].z), magnitude(x[u].w))));
                 }
-                atomicMax(largest, __reduce_max_sync(0xffffffffu, __float_as_int(top)));  // (magnitudes: their bits are in order)
+                atomicMax(largest, __reduce_max_sync(0xffffffffu, (int)max(top << 16, top & 0xffff0000u)));  // (their bits are in order)
                 __syncthreads();
                 float back;
                 scale_of(__int_as_float(*largest), to, back);
@@ -676,13 +696,8 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                 mul = hi * back;
             }
             for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
-                if (!kF16 || N > U * EACH) {  // (else they are here)
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        l[u] = INFINITY;
-                        step[u] = fetch(n0 + u * EACH, x[u], &l[u]);
-                    }
-                }
+                if (!kF16 || N > U * EACH)  // (else they are here)
+                    load_rows(n0);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int n = n0 + u * EACH;
@@ -694,9 +709,8 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                     *reinterpret_cast<uint4 *>(queries_at + operand_at(n, ch, N)) = x[u];
                     if (ch == 0) {
                         // (of mul and lse in log2 units, as in row_of)
-                        const float off = mul == 0.f ? 0.f : mul_lo / mul;
-                        summands[n] = fabsf(l[u]) < INFINITY || l[u] != l[u] ? fmaf(-l[u], kLog2e, l[u] * kLog2e * off) : -INFINITY;
-                        steps[n] = step[u];
+                        const float off = mul == 0.f ? 0.f : mul_lo / mul, l = summands[n];
+                        summands[n] = fabsf(l) < INFINITY || l != l ? fmaf(-l, kLog2e, l * kLog2e * off) : -INFINITY;
                     }
                 }
             }
@@ -825,8 +839,8 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
     const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
     // (8 sequences of 20K to 32K, 8 KV heads of 128, 16 bits: 64 rows by warps 122 us
-    // and on the tensor unit 139, 128 rows 190 and 155; 4 bits: 107 and 88, 178 and
-    // 108; one of 4K, 16 bits: 6.7 and 9.0, 9.4 and 9.8)
+    // and on the tensor unit 139, 128 rows 190 and 157; 4 bits: 107 and 88, 178 and
+    // 109; one of 4K, 16 bits: 6.7 and 9.0, 9.4 and 10.6)
     const bool wide = a.p.R > kMassRows;
     const int each = wide ? kWideRows : kMassRows;
     for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
@@ -866,6 +880,7 @@ int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache
     a.mass = mass;
     a.out = out;
     a.width = width;
+    a.per_sq = ((1ULL << 40) + Sq - 1) / Sq;  // (Sq <= 64: exact for every row below 2^34)
     const double mul = 1.4426950408889634074 / sqrt((double)cache.d);
     a.mul = (float)mul;
     a.mul_lo = (float)(mul - (double)a.mul);

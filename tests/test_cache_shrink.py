@@ -549,6 +549,25 @@ def test_mass_of_keys_with_infinities(gm):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("Sq", [8, 24])
+@pytest.mark.parametrize("fill", [math.inf, 1e38, math.nan])
+def test_mass_of_rows_that_count_nothing(gm, elem, Sq, fill):
+    """A row whose lse is infinite gives nothing, whatever its query holds, and the others what they would."""
+    r = run4(gm, 2, 4, 1, Sq, 128, 16, [300, 1100], seed=24, elem=elem)
+    lse = r["lse"].clone()
+    lse[0, 1, 3] = math.inf
+    lse[1, 3, Sq - 1] = -math.inf
+    ref, bound = weights(r, lse, [300, 1100], None, True, torch.zeros(2, 1, 1100, device="cuda"), 1100)
+    q = r["q"].clone()
+    q[0, 1, 3, 5] = q[1, 3, Sq - 1, 64:] = fill
+    got = gm.mercury_attn_paged_mass(q, r["cache"], r["lens"], lse)
+    gm.mercury_sync_status()
+    for b, n in enumerate([300, 1100]):
+        assert_within(got[b, :, :n], ref[b, :, :n], bound[b, :, :n], "sequence %d" % b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
 def test_both_ways_into_the_calls(gm, elem):
     """The short way from Python and the long one (a stream given) make the same call; strided queries too."""
     r = run4(gm, 3, 8, 2, 2, 64, 16, [300, 40, 700], seed=23, elem=elem)
