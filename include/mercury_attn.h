@@ -772,7 +772,8 @@ MERCURY_API int mercury_attn_paged_mass(const void *q, const long long *q_stride
  * into is not stored; each is reported as MERCURY_EBOUNDS.
  * Requirements: the caches as in mercury_kv_append; 1 <= keep <= what into's
  * table holds; first + last <= keep; out_width >= keep; out_lens and out_mass
- * are not seq_lens and mass.  The first call on a device for a cache type and
+ * are not seq_lens and mass; into's table and arrays are not both cache's.  The
+ * first call on a device for a cache type and
  * head dim loads its kernels; make it before any stream capture.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
  * when MERCURY_SYNC_CHECK=1.
@@ -791,8 +792,8 @@ MERCURY_API int mercury_kv_evict(const mercury_paged_cache *cache, const mercury
  * once; rows i >= seq_lens[b] are left as they were.
  * A seq_lens outside the block table or above S is taken to the nearer end, a
  * page outside the cache counts as zeros; both are reported as MERCURY_EBOUNDS.
- * Requirements: the cache as in mercury_kv_append; S >= 1.  The first call on a
- * device for a cache type and head dim loads its kernel; make it before any
+ * Requirements: the cache as in mercury_kv_append; S >= 1; k_out is not v_out.
+ * The first call on a device for a cache type and head dim loads its kernel; make it before any
  * stream capture.
  * Errors: MERCURY_EINVAL, MERCURY_EALIGN, MERCURY_ECUDA, and MERCURY_EBOUNDS
  * when MERCURY_SYNC_CHECK=1.

@@ -349,6 +349,8 @@ static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
         Py_RETURN_NONE;
     if (a[4] == Py_None || !look_lens(a[4], dev, c->B, &lens) || a[8] == Py_None || !look_lens(a[8], dev, c->B, &out_lens))
         Py_RETURN_NONE;
+    if (a[10] != Py_None && out_width < num[0])  /* refused on the long way (an empty tensor's pointer is NULL) */
+        Py_RETURN_NONE;
     if (!look(a[9], g_int32, dev, 3, 0, &kept) || kept.n[0] != c->B || kept.n[1] != c->Hkv || kept.n[2] != num[0])
         Py_RETURN_NONE;
     if (!on_device(dev, &stream))

@@ -403,6 +403,9 @@ int mercury_kv_evict(const mercury_paged_cache *cache, const mercury_paged_cache
         return set_error(MERCURY_EINVAL, "out_lens and out_mass may not be seq_lens and mass");
     if (!aligned(mass, 4) || !aligned(seq_lens, 4) || !aligned(out_lens, 4) || !aligned(kept, 4) || !aligned(out_mass, 4))
         return set_error(MERCURY_EALIGN, "mass, seq_lens, out_lens, kept and out_mass must be 4-byte aligned");
+    // (rows would be stored where others have yet to be read)
+    if (into->block_table == cache->block_table && (into->k == cache->k || into->v == cache->v))
+        return set_error(MERCURY_EINVAL, "a sequence cannot be shortened within its own pages");
     size_t len;
     char *msg = error_buffer(&len);
     cudaStream_t s = (cudaStream_t)stream;
@@ -426,6 +429,8 @@ int mercury_kv_read(const mercury_paged_cache *cache, const int *seq_lens, int B
         return set_error(MERCURY_EALIGN, "k_out and v_out must be 16-byte aligned");
     if (!aligned(seq_lens, 4))
         return set_error(MERCURY_EALIGN, "seq_lens must be 4-byte aligned");
+    if (k_out == v_out)
+        return set_error(MERCURY_EINVAL, "k_out and v_out must be two tensors");
     size_t len;
     char *msg = error_buffer(&len);
     cudaStream_t s = (cudaStream_t)stream;

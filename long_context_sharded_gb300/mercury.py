@@ -972,11 +972,15 @@ def mercury_kv_evict(cache: PagedCache, into: PagedCache, mass, seq_lens, keep: 
         raise ValueError("both caches must be on the same device")
     B, Hkv = cache.B, cache.Hkv
     width = _shape3(mass, cache, "mass")
+    if keep < 1:
+        raise ValueError("keep must be >= 1 (got %d)" % keep)
     if out_lens is None:
         out_lens = _new_output(T.empty, (B,), T.int32, mass, dev, stream)
     if kept is None:
         kept = _new_output(_minus_ones, (B, Hkv, keep), T.int32, mass, dev, stream)
     more = 0 if out_mass is None else _shape3(out_mass, cache, "out_mass")
+    if out_mass is not None and more < keep:
+        raise ValueError("out_mass must have at least keep=%d entries a head (got %d)" % (keep, more))
     rc = lib.mercury_kv_evict(
         cache._ref, into._ref, _flat(mass, T.fp32, dev, (B, Hkv, width), "mass"), width,
         _flat(seq_lens, T.int32, dev, (B,), "seq_lens"), B, keep, first, last, _flat(out_lens, T.int32, dev, (B,), "out_lens"),
@@ -1009,6 +1013,8 @@ def mercury_kv_read(cache: PagedCache, seq_lens, S: int = None, k_out=None, v_ou
             S = _shape4(t, "k_out and v_out")[2]
     if S is None:
         S = cache.struct.max_pages * cache.struct.page_size
+    if S < 1:
+        raise ValueError("S must be >= 1 (got %d)" % S)
     whole = (cache.B, cache.Hkv, S, cache.d)
     if k_out is None:
         k_out = _new_output(T.zeros, whole, T.bf16, cache.k_cache, dev, stream)

@@ -154,6 +154,18 @@ def test_read_refusals(m, kw, code):
     assert m.lib.mercury_kv_read(a["cache"], a["lens"], a["B"], a["S"], a["k"], a["v"], None) == code
 
 
+def test_rows_are_not_moved_within_the_same_pages(m):
+    """The same table and arrays are refused; of the same arrays with another table only what else is wrong."""
+    def evict(k=P, v=P, table=P):
+        a, b = cache_struct(m), cache_struct(m, k=k, v=v, block_table=table)
+        return m.lib.mercury_kv_evict(ctypes.byref(a), ctypes.byref(b), P, 64, P, 2, 8, 0, 0, P + 64, P, None, 0, None)
+
+    for kw in (dict(), dict(k=P + 4096), dict(v=P + 4096)):
+        assert evict(**kw) == m.MERCURY_EINVAL and b"own pages" in m.lib.mercury_last_error()
+    assert m.lib.mercury_kv_read(ctypes.byref(cache_struct(m)), P, 2, 64, P, P, None) == m.MERCURY_EINVAL
+    assert b"two tensors" in m.lib.mercury_last_error()
+
+
 # ---------------------------------------------------------------------------------- append
 
 @pytest.mark.gpu
@@ -921,3 +933,27 @@ def test_binding_refusals_on_the_device(gm):
             gm.mercury_kv_read(cache, lens, **kw)
     with pytest.raises(TypeError):
         gm.mercury_kv_read(None, lens)
+
+
+@pytest.mark.gpu
+def test_more_refusals_on_the_device(gm):
+    r = run4(gm, 2, 4, 2, 1, 128, 16, [20, 9], seed=72)
+    cache, lens, mass = r["cache"], r["lens"], torch.zeros(2, 2, 64, device="cuda")
+    other = gm.PagedCache(r["k"].clone(), r["v"].clone(), r["table"].clone(), k_scale=r["ks"], v_scale=r["vs"])
+    out_lens, kept = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, 8, dtype=torch.int32, device="cuda")
+    for made in (dict(), dict(out_lens=out_lens, kept=kept)):
+        with pytest.raises(gm.MercuryError):  # in place
+            gm.mercury_kv_evict(cache, cache, mass, lens, 8, **made)
+        for n in (0, 7):
+            with pytest.raises(ValueError):
+                gm.mercury_kv_evict(cache, other, mass, lens, 8, out_mass=torch.zeros(2, 2, n, device="cuda"), **made)
+        for keep in (0, -1):
+            with pytest.raises(ValueError):
+                gm.mercury_kv_evict(cache, other, mass, lens, keep, **made)
+    x = torch.zeros(2, 2, 8, 128, dtype=BF16, device="cuda")
+    with pytest.raises(gm.MercuryError):
+        gm.mercury_kv_read(cache, lens.clamp(max=8), k_out=x, v_out=x)
+    for S in (0, -1):
+        with pytest.raises(ValueError):
+            gm.mercury_kv_read(cache, lens, S=S)
+    gm.mercury_sync_status()
