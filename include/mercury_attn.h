@@ -732,8 +732,8 @@ MERCURY_API int mercury_attn_paged_bf16(const void *q, const long long *q_stride
  * A seq_lens that exceeds width is taken as width and reported, and so are
  * lengths and pages out of range, as in mercury_attn_paged.
  * A weight is good to 2^-22 of |score| + |lse|, and to the score's own error (a
- * sum of d products in fp32).  Up to 64 rows a KV head (Hq/Hkv * Sq) go by
- * warp-level products, more on the tensor unit, where the keys are read once
+ * sum of d products in fp32).  Up to 48 or 64 rows a KV head (Hq/Hkv * Sq) go
+ * by warp-level products, more on the tensor unit, where the keys are read once
  * for each 256.  Its waits are bounded (MERCURY_WAIT_NS); one that runs out is
  * reported as MERCURY_ETIMEOUT.
  * Requirements: as mercury_attn_paged (but for the number of tiles); width >= 1.

@@ -17,7 +17,7 @@
 // whole 16-byte (8- or 4-byte) runs of two keys, and the queries, held in shared
 // memory as operands, in the same order.  All rows of the head go over the
 // registers that hold 16 keys, so further rows cost no further reads, and an 8-
-// or 4-bit key is widened once.  More than 64 rows: the tensor unit, below.
+// or 4-bit key is widened once.  More than 48 or 64 rows: the tensor unit, below.
 //
 // Measured on a GB300, of the measured copy bandwidth (6680 GB/s) or the
 // product's rate: one token of 8 sequences of 20K to 32K, 32 query and 8 KV
@@ -25,7 +25,7 @@
 // not by bytes, but by a tile's chain of look-up, load, widening and products
 // (16-bit keys take 320 instructions for 16 keys of a warp).  Rows a KV head, 16
 // bits: 16 72 us, 32 86, 64 122, 128 157, 256 219 (505 TFLOP/s); e2m1 57, 74,
-// 107, 109, 154.
+// 87, 109, 154; heads of 64, one token: 41, 36 and 40 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -42,7 +42,7 @@ namespace {
 constexpr int kMassWarps = 8;
 constexpr int kMassThreads = kMassWarps * 32;
 constexpr int kMassTile = kMassWarps * 16;  // keys of a block's tile
-constexpr int kMassRows = 64;               // rows that go by warps; more by the tensor unit,
+constexpr int kMassRows = 64;               // most rows that go by warps; more by the tensor unit,
 constexpr int kWideRows = 256;              // so many a launch
 
 struct MassArgs {
@@ -300,8 +300,16 @@ __device__ __forceinline__ void scale_of(float top, float &to, float &back)
     back = __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
+// Blocks an SM: rows of 64 leave too few bytes on their way with two (one token
+// of 8 sequences of 26K, 16 bits 46.7 us and with three 40.7, e4m3 40.9 and 36.0,
+// e2m1 43.8 and 40.1; four spill: 48, 38, 49), rows of 128 spill with three.
+constexpr int blocks_of(int D)
+{
+    return D == 64 ? 3 : 2;
+}
+
 template <int ELEM, int D>
-__global__ void __launch_bounds__(kMassThreads, 2) attn_mass_kernel(const __grid_constant__ MassArgs a)
+__global__ void __launch_bounds__(kMassThreads, blocks_of(D)) attn_mass_kernel(const __grid_constant__ MassArgs a)
 {
     using K = Keys<ELEM, D>;
     constexpr int KK = D / 16, RUN = K::kRun;
@@ -838,16 +846,21 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
         return rc;
     const long long keys = (long long)a.p.cache.max_pages * a.p.cache.page_size;
     const long long most = ((keys < a.width ? keys : a.width) + kMassTile - 1) / kMassTile * a.p.B * a.p.Hkv;
-    // (8 sequences of 20K to 32K, 8 KV heads of 128, 16 bits: 64 rows by warps 122 us
-    // and on the tensor unit 139, 128 rows 190 and 157; 4 bits: 107 and 88, 178 and
-    // 109; one of 4K, 16 bits: 6.7 and 9.0, 9.4 and 10.6)
-    const bool wide = a.p.R > kMassRows;
+    // On the tensor unit a tile takes the same time up to 64 rows; there it pays
+    // from some 50 on where keys are narrow and each block has many tiles (8 x 8
+    // heads, 32K, 64 rows by warps and on the tensor unit: d 64 16 bits 101 us and
+    // 82, e4m3 92 and 76; d 128 e2m1 130 and 104, but e4m3 128 and 133, 16 bits 149
+    // and 169; 48 rows: d 64 87 and 82, e2m1 110 and 104; 2K tiles, d 64 e4m3: 16.0
+    // and 16.5; one sequence of 4K: 6.3 and 9.5).  128 rows, d 128, 8 x 20K to 32K:
+    // 16 bits 190 us and 157, 4 bits 178 and 109.
+    const bool narrow_keys = D == 64 || ELEM == MERCURY_ELEM_E2M1;
+    const bool wide = a.p.R > kMassRows || (a.p.R > 48 && narrow_keys && most >= 24LL * ki.sms);
     const int each = wide ? kWideRows : kMassRows;
     for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
         a.rows = a.p.R - a.r0 < each ? a.p.R - a.r0 : each;
         a.wide = !wide ? 0 : a.rows <= 64 ? 64 : a.rows <= 128 ? 128 : 256;
         const int smem = wide ? wide_smem(D, a.wide) : (a.rows + 7) / 8 * 8 * kRowSmem;
-        const int per_sm = smem <= 110000 ? 2 : 1;
+        const int per_sm = wide ? 2 : blocks_of(D);
         const long long grid = most < (long long)ki.sms * per_sm ? most : (long long)ki.sms * per_sm;
         const cudaError_t e = launch_chained(wide ? wide_kernel : kernel, dim3((unsigned)grid), kMassThreads, smem, stream, a);
         if (e != cudaSuccess) {

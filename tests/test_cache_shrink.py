@@ -524,6 +524,24 @@ def test_mass_adds_the_weights(gm, elem, prev, B, Hq, Hkv, Sq, d, page, lens, ne
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Sq", [12, 13, 16])
+def test_mass_over_long_caches(gm, elem, d, Sq):
+    """48, 52 and 64 rows over a table of many tiles, where another way is taken."""
+    lens, new = [40000, 70, 31111], [Sq, 3, Sq - 1]
+    r = run4(gm, 3, 16, 4, Sq, d, 64, lens, new=new, seed=Sq + d, elem=elem)
+    lse = torch.where(r["lse"] == 9.0, math.inf, r["lse"])
+    got = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse, new_lens=r["new"])
+    gm.mercury_sync_status()
+    width = got.shape[2]
+    ref, bound = weights(r, lse, lens, new, True, torch.zeros(3, 4, width, device="cuda"), width)
+    for b, n in enumerate(lens):
+        assert_within(got[b, :, :n], ref[b, :, :n], bound[b, :, :n], "sequence %d" % b)
+        assert (got[b, :, n:] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
 def test_mass_of_keys_that_some_rows_see(gm, elem):
     """NaN keys behind the last one count nothing; one that only later rows see is theirs."""
     lens, page = [131, 50], 16
