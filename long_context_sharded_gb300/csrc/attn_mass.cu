@@ -849,9 +849,10 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     // On the tensor unit a tile takes the same time up to 64 rows; there it pays
     // from some 50 on where keys are narrow and each block has many tiles (8 x 8
     // heads, 32K, 64 rows by warps and on the tensor unit: d 64 16 bits 101 us and
-    // 82, e4m3 92 and 76; d 128 e2m1 130 and 104, but e4m3 128 and 133, 16 bits 149
-    // and 169; 48 rows: d 64 87 and 82, e2m1 110 and 104; 2K tiles, d 64 e4m3: 16.0
-    // and 16.5; one sequence of 4K: 6.3 and 9.5).  128 rows, d 128, 8 x 20K to 32K:
+    // 82, e4m3 88 and 76; d 128 e2m1 130 and 104, but e4m3 128 and 133, 16 bits 149
+    // and 169; 48 rows: d 64 16 bits 87 and 82, e4m3 75 and 76, d 128 e2m1 110 and
+    // 104; 2K tiles, d 64 e4m3, 64 rows: 15.9 and 16.5; one sequence of 4K, d 128:
+    // 6.3 and 9.5).  128 rows, d 128, 8 x 20K to 32K:
     // 16 bits 190 us and 157, 4 bits 178 and 109.
     const bool narrow_keys = D == 64 || ELEM == MERCURY_ELEM_E2M1;
     const bool wide = a.p.R > kMassRows || (a.p.R > 48 && narrow_keys && most >= 24LL * ki.sms);
