@@ -11,9 +11,9 @@
 // Rows are read once and written once; what is left is the selection, a chain
 // of steps that each wait for the one before.
 //
-// Measured on a GB300: one sequence of 32K, 8 KV heads of 128, to 4K, 16 bits: 18
-// us (5 us of bytes); 16 sequences of 500 to 16K to 2K, 8 bits: 38 us (20 us of
-// bytes).  Each kernel alone and cold: selection 14 and 18 us, rows 10 and 23;
+// Measured on a GB300: one sequence of 32K, 8 KV heads of 128, to 4K, 16 bits: 17
+// us (5 us of bytes); 16 sequences of 500 to 16K to 2K, 8 bits: 35 us (20 us of
+// bytes).  Each kernel alone and cold: selection 14 and 15 us, rows 10 and 23;
 // with one block a head the first selection took 30 us.  32K tokens of a 4-bit
 // cache read back: 29 us, 89 % of the measured copy bandwidth.
 #include <cuda_runtime.h>
@@ -59,11 +59,17 @@ struct SelectArgs {
     long long width, out_width;
 };
 
-// A weight's place in the order of all: NaN below everything, -0 equal to 0.
-__device__ __forceinline__ uint32_t rank_of(float x)
+// A number's place in the order of all, -0 equal to 0.
+__device__ __forceinline__ uint32_t rank_of_number(float x)
 {
     const uint32_t u = __float_as_uint(x + 0.f);
-    return x != x ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+
+// A weight's: NaN below everything.
+__device__ __forceinline__ uint32_t rank_of(float x)
+{
+    return x != x ? 0u : rank_of_number(x);
 }
 
 // Inclusive scan over the block's 1024 threads.  `warps` is not used again
@@ -117,6 +123,11 @@ __device__ __forceinline__ int4 cluster_load4(const int *p, uint32_t rank)
     return x;
 }
 
+template <bool T>
+struct Ties {
+    static constexpr bool value = T;
+};
+
 constexpr int kListed = 4096;  // tokens of the first digit that are listed
 
 struct __align__(16) SelectSmem {
@@ -132,10 +143,12 @@ struct __align__(16) SelectSmem {
 // histogram in each block of those of its tokens that share the digits so far,
 // summed by all blocks of the cluster, which then know the next digit.  Mostly
 // few tokens share the first digit; those are listed, and the other two digits
-// found by each block from all lists, which spares two exchanges of histograms
-// (5000 cycles each).  Then each block counts what it keeps, and each warp of
-// it, and writes it behind what those before it keep.  mass is read once, as
-// ranks into shared memory.
+// found by each block from all lists, which spares a pass over the tokens and
+// two exchanges of histograms (5000 cycles each).  Then each block counts what
+// it keeps, and each warp of it, and writes it behind what those before it keep.
+// mass is read once, as ranks into shared memory.
+// What bounds a head of 16K in one block is the integer unit: ends, NaN and
+// ties looked at token by token it was busy 94 % (18 us; now 65 %, 15 us).
 template <int CS>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ SelectArgs a)
 {
@@ -174,23 +187,29 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     // rank above every number.
     const int lo = a.first, hi = n - a.last;
     const bool held = to - from <= a.held;
-    auto fetch = [&](int i) {  // of tokens i .. i + 3; nothing behind the run
-        float x[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            x[k] = i + k < to ? mass[i + k] : 0.f;
+    const bool quads = ((uintptr_t)mass & 15u) == 0;  // (runs begin at multiples of 128)
+    // Of tokens i .. i + 3, whose weights are x where they all are numbers inside
+    // the run and between the ends: 0 behind the run.
+    auto inner = [&](int i) { return i >= lo && i + 4 <= hi && i + 4 <= to; };
+    auto weights = [&](int i) {
+        return quads ? *reinterpret_cast<const float4 *>(mass + i)
+                     : make_float4(mass[i], mass[i + 1], mass[i + 2], mass[i + 3]);
+    };
+    auto ranks_of = [&](int i, float4 x, bool is_inner) {
+        const float all = (x.x + x.y) + (x.z + x.w);  // NaN with one of them (and with infinities of both signs)
+        if (is_inner && all == all)
+            return make_uint4(rank_of_number(x.x), rank_of_number(x.y), rank_of_number(x.z), rank_of_number(x.w));
         uint32_t r[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            r[k] = i + k < lo || i + k >= hi ? 0xffffffffu : rank_of(x[k]);
+            r[k] = i + k >= to ? 0u : i + k < lo || i + k >= hi ? 0xffffffffu : rank_of(mass[i + k]);
         return make_uint4(r[0], r[1], r[2], r[3]);
     };
-    if (held) {
-#pragma unroll 4
-        for (int i = from + 4 * tid; i < to; i += 4 * kSelectThreads)
-            sm.ranks[(i - from) / 4] = fetch(i);
-    }
-    __syncthreads();
+    auto fetch = [&](int i) {
+        const bool in = inner(i);
+        return ranks_of(i, in ? weights(i) : make_float4(0.f, 0.f, 0.f, 0.f), in);
+    };
+    __syncthreads();  // the bins are zero
     auto ranks = [&](int i) { return held ? sm.ranks[(i - from) / 4] : fetch(i); };
     int want = a.keep;
     uint32_t prefix = 0;
@@ -203,11 +222,35 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         if (pass > 0 && listed) {
             // of the block warp / (kSelectWarps / CS)
             const uint32_t k = warp / (kSelectWarps / CS);
-            const int many = cluster_load(&sm.listed, k);
+            const int many = CS > 1 ? cluster_load(&sm.listed, k) : sm.listed;
             for (int i = tid % (kSelectThreads / CS); i < many; i += kSelectThreads / CS) {
-                const uint32_t r = (uint32_t)cluster_load((const int *)&sm.list[i], k);
+                const uint32_t r = CS > 1 ? (uint32_t)cluster_load((const int *)&sm.list[i], k) : sm.list[i];
                 if (r >> (shift + bits) == prefix)
                     count(r);
+            }
+        } else if (pass == 0) {
+            constexpr int U = 4;  // loads on their way
+            for (int i0 = from + 4 * tid; i0 < to; i0 += U * 4 * kSelectThreads) {
+                float4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * 4 * kSelectThreads;
+                    w[u] = inner(i) ? weights(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * 4 * kSelectThreads;
+                    if (i >= to)
+                        break;
+                    const uint4 r = ranks_of(i, w[u], inner(i));
+                    if (held)
+                        sm.ranks[(i - from) / 4] = r;
+                    const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (i + k < to)
+                            count(x[k]);
+                }
             }
         } else {
 #pragma unroll 2
@@ -216,7 +259,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
                 const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (i + k < to && (pass == 0 || x[k] >> (shift + bits) == prefix))
+                    if (x[k] >> (shift + bits) == prefix && i + k < to)
                         count(x[k]);
             }
         }
@@ -253,7 +296,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         __syncthreads();
         prefix = prefix << bits | (uint32_t)sm.found[pass][0];
         want -= sm.found[pass][1];
-        if (CS > 1 && pass == 0) {
+        if (pass == 0) {
             listed = sm.found[0][2] <= kListed;  // of all blocks
             if (listed) {
 #pragma unroll 2
@@ -262,95 +305,108 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
                     const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (i + k < to && x[k] >> shift == prefix)
+                        if (x[k] >> shift == prefix && i + k < to)
                             sm.list[atomicAdd(&sm.listed, 1)] = x[k];
                 }
-                cluster_sync();
+                if (CS > 1)
+                    cluster_sync();
+                else
+                    __syncthreads();
             }
         }
     }
-    const int ties = want;  // tokens at the threshold that are kept, the first ones
     const int first = from + warp * each, end = min(first + each, to);
-    // of a thread's four tokens: those above the threshold, those at it (in the upper half)
-    auto look = [&](int i, uint32_t (&x)[4]) {
-        const uint4 r = i < end ? ranks(i) : make_uint4(0, 0, 0, 0);
-        x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
-        int c = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < end)
-                c += (x[k] > prefix) + ((x[k] == prefix) << 16);
-        return c;
-    };
-    int n_sure = 0, n_tie = 0;
-#pragma unroll 2
-    for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
-        uint32_t x[4];
-        const int c = look(i, x);
-        n_sure += c & 0xffff;
-        n_tie += c >> 16;
-    }
-    n_sure = __reduce_add_sync(0xffffffffu, n_sure);
-    n_tie = __reduce_add_sync(0xffffffffu, n_tie);
-    const int sure_incl = block_scan(lane == 0 ? n_sure : 0, sm.warps[3], tid);
-    const int tie_incl = block_scan(lane == 0 ? n_tie : 0, sm.warps[4], tid);
-    if (tid == kSelectThreads - 1) {
-        sm.counts[0] = sure_incl;
-        sm.counts[1] = tie_incl;
-    }
-    int at_sure = __shfl_sync(0xffffffffu, sure_incl - n_sure, 0), at_tie = __shfl_sync(0xffffffffu, tie_incl - n_tie, 0);
-    if constexpr (CS > 1) {
-        cluster_sync();
-        const bool ahead = lane < (int)me;
-        at_sure += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[0], lane) : 0);
-        at_tie += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[1], lane) : 0);
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    }
-    for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
-        uint32_t x[4];
-        const int c = look(i, x);
-        int incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += y;
-        }
-        int sure = at_sure + (incl & 0xffff) - (c & 0xffff), tie = at_tie + (incl >> 16) - (c >> 16);
-        int slot[4];
-        bool other = false;  // a rank that is not a weight's own: an end's, NaN's, a zero's
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool above = x[k] > prefix, at = x[k] == prefix;
-            slot[k] = i + k < end && (above || (at && tie < ties)) ? sure + min(tie, ties) : -1;
-            other |= slot[k] >= 0 && (x[k] == 0xffffffffu || x[k] == 0u || x[k] == 0x80000000u);
-            sure += i + k < end && above;
-            tie += i + k < end && at;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (slot[k] >= 0)
-                kept[slot[k]] = i + k;
-        if (out_mass) {
-            float w[4];
-            if (__any_sync(0xffffffffu, other)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = slot[k] >= 0 ? mass[i + k] : 0.f;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = __uint_as_float(x[k] & 0x80000000u ? x[k] ^ 0x80000000u : ~x[k]);
-            }
+    // Writes what is kept.  TIES: not all tokens at the threshold are, but the
+    // first `ties` of them.
+    auto write = [&](auto with_ties) {
+        constexpr bool TIES = decltype(with_ties)::value;
+        const int ties = want;
+        // of a thread's four tokens: those above the threshold (without ties: or at
+        // it, which is not 0 then), and those at it (in the upper half)
+        auto look = [&](int i, uint32_t (&x)[4]) {
+            const uint4 r = i < end ? ranks(i) : make_uint4(0, 0, 0, 0);
+            x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+            int c = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (slot[k] >= 0)
-                    out_mass[slot[k]] = w[k];
+                if (!TIES)
+                    c += x[k] >= prefix;
+                else if (i + k < end)
+                    c += (x[k] > prefix) + ((x[k] == prefix) << 16);
+            return c;
+        };
+        int n_sure = 0, n_tie = 0;
+#pragma unroll 2
+        for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
+            uint32_t x[4];
+            const int c = look(i, x);
+            n_sure += TIES ? c & 0xffff : c;
+            n_tie += TIES ? c >> 16 : 0;
         }
-        const int all = __shfl_sync(0xffffffffu, incl, 31);
-        at_sure += all & 0xffff;
-        at_tie += all >> 16;
-    }
+        n_sure = __reduce_add_sync(0xffffffffu, n_sure);
+        const int sure_incl = block_scan(lane == 0 ? n_sure : 0, sm.warps[3], tid);
+        int at_sure = __shfl_sync(0xffffffffu, sure_incl - n_sure, 0), at_tie = 0;
+        if (tid == kSelectThreads - 1)
+            sm.counts[0] = sure_incl;
+        if (TIES) {
+            n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+            const int tie_incl = block_scan(lane == 0 ? n_tie : 0, sm.warps[4], tid);
+            at_tie = __shfl_sync(0xffffffffu, tie_incl - n_tie, 0);
+            if (tid == kSelectThreads - 1)
+                sm.counts[1] = tie_incl;
+        }
+        if constexpr (CS > 1) {
+            cluster_sync();
+            const bool ahead = lane < (int)me;
+            at_sure += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[0], lane) : 0);
+            if (TIES)
+                at_tie += __reduce_add_sync(0xffffffffu, ahead ? cluster_load(&sm.counts[1], lane) : 0);
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        }
+        for (int i = first + 4 * lane; i - 4 * lane < end; i += LINE) {
+            uint32_t x[4];
+            const int c = look(i, x);
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            const int all = __shfl_sync(0xffffffffu, incl, 31);
+            int sure = at_sure + (TIES ? (incl & 0xffff) - (c & 0xffff) : incl - c), tie = TIES ? at_tie + (incl >> 16) - (c >> 16) : 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool stays;
+                int slot;
+                if (TIES) {
+                    const bool above = x[k] > prefix, at = x[k] == prefix, in = i + k < end;
+                    stays = in && (above || (at && tie < ties));
+                    slot = sure + min(tie, ties);
+                    sure += in && above;
+                    tie += in && at;
+                } else {
+                    stays = x[k] >= prefix;
+                    slot = sure;
+                    sure += stays;
+                }
+                if (stays) {
+                    kept[slot] = i + k;
+                    if (out_mass)  // (an end's rank, NaN's and a zero's is not its weight's own)
+                        out_mass[slot] = x[k] == 0xffffffffu || x[k] == 0u || x[k] == 0x80000000u
+                                             ? mass[i + k]
+                                             : __uint_as_float(x[k] & 0x80000000u ? x[k] ^ 0x80000000u : ~x[k]);
+                }
+            }
+            at_sure += TIES ? all & 0xffff : all;
+            at_tie += TIES ? all >> 16 : 0;
+        }
+    };
+    // (without ties the threshold is above 0: else all tokens would stay)
+    if (sm.found[2][2] == want)
+        write(Ties<false>());
+    else
+        write(Ties<true>());
     if constexpr (CS > 1)  // a block's counts and list are read until here
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -391,7 +447,8 @@ int launch_select(SelectArgs &s, long long heads, cudaStream_t stream, char *msg
 
 constexpr int kMoveThreads = 256;
 // Rows that a thread has on the way, of keys and of values: more of them leave
-// fewer blocks (16 sequences to 2K: 36 us with 2, 38 with 1, 39 with 4, 48 with 8).
+// fewer blocks (16 sequences to 2K, the slower selection before: 36 us with 2, 38
+// with 1, 39 with 4, 48 with 8).
 constexpr int kMoveAhead = 2;
 
 struct MoveArgs {
