@@ -131,11 +131,10 @@ __device__ __forceinline__ void keep4(const RotUnit<8> &unit, const mercury_rope
         }
         uint32_t lo, w;
         code_ends(y[k], by, byte == 0x7fu ? 0.f : e4m3_value(byte), g, lo, w);
-        const uint32_t differ = lo ^ (w & 0x77777777u);
-        if (differ) {
+        if (lo != (w & 0x77777777u)) {
             float first[8], second[8], copy[8];
             const Source from = source(first, second, copy);
-            w = (w & 0x88888888u) | settle_codes(lo, differ, e4m3_value(byte), g, copy, by > 0.f ? &from : nullptr);
+            w = settle_codes(lo, w, e4m3_value(byte), g, copy, by > 0.f ? &from : nullptr);
         }
         *reinterpret_cast<uint32_t *>(row + at / 2) = scale < 0.f ? w ^ 0x88888888u : w;
         if (at % 16 == 0)
@@ -403,10 +402,9 @@ __global__ void __launch_bounds__(kRotThreads) append_blocks_kernel(const __grid
             part[j] = y[8 * k + j];
         uint32_t lo, w;
         code_ends(part, by, s, g, lo, w);
-        const uint32_t differ = lo ^ (w & 0x77777777u);
-        if (differ) {
+        if (lo != (w & 0x77777777u)) {
             const Source half = {x + 8 * k, z + 8 * k, from.pos, turns, a.plan.magnitude, at + 8 * k, rot, a.plan.interleaved};
-            w = (w & 0x88888888u) | settle_codes(lo, differ, s, g, y + 8 * k, by > 0.f ? &half : nullptr);
+            w = settle_codes(lo, w, s, g, y + 8 * k, by > 0.f ? &half : nullptr);
         }
         *reinterpret_cast<uint32_t *>(row + at / 2 + 4 * k) = scale < 0.f ? w ^ 0x88888888u : w;
     }

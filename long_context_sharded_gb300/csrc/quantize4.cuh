@@ -9,10 +9,12 @@
 // A value known to e (0 where it was not rotated) has its quotient bracketed by
 // two 32-bit products, wider by 2^-21 than e, which covers their roundings (the
 // reciprocal's 2^-23, and three of 2^-24); where both ends round to the same code, that is it.  Where they do
-// not, the border between the two is next to the value, and the two are
-// compared: exactly in 32 bits, by the product's rounding error, or for a
-// rotated value in 64 bits (one in some 10^5; as 0.2 % of warps meet one, that
-// costs little).
+// not, the borders between the two are near the value, and it is compared with
+// them: exactly in 32 bits, by the product's rounding error, or for a rotated
+// value in 64 bits (one in some 10^5; as 0.2 % of warps meet one, that costs
+// little).  There is one border mostly, and more where a rotation leaves a block
+// far smaller than the elements that it was turned from (one half of a head
+// small, and a small angle): e grows with those.
 #pragma once
 #include <stdint.h>
 
@@ -95,18 +97,15 @@ struct Source {
     }
 };
 
-// Which of the two scales' bytes (neighbours) a block's is: amax is next to 6 g
-// times the border between them.  `from` where the elements were rotated:
-// amax is then that of both halves of the block, y[N] this thread's half, and
-// the threads of `both` settle it together.
+// Which of the scales' bytes lo to hi a block's is.  `from` where the elements
+// were rotated: amax is then that of both halves of the block, y[N] this
+// thread's half, and the threads of `both` settle it together.
 template <int N>
 __device__ __noinline__ uint32_t settle_scale(uint32_t lo, uint32_t hi, float amax, float off, float g, const float *y,
                                               const Source *from, unsigned int both)
 {
-    const float m = 3.f * (e4m3_value(lo) + e4m3_value(hi));  // 6 times the border
-    int side;
+    double x = 0.0;
     if (from) {
-        double x = 0.0;
 #pragma unroll 1
         for (int i = 0; i < N; ++i)
             if (fabsf(y[i]) + 2.f * off >= amax)  // it may be the largest
@@ -115,25 +114,40 @@ __device__ __noinline__ uint32_t settle_scale(uint32_t lo, uint32_t hi, float am
             __syncwarp(both);
             x = fmax(x, __shfl_xor_sync(both, x, 1));
         }
-        side = side_of(x, m, g);
-    } else {
-        side = side_of(amax, m, g);
     }
-    return side > 0 || (side == 0 && (lo & 1u)) ? hi : lo;
+#pragma unroll 1
+    for (; lo < hi; ++lo) {
+        const float m = 3.f * (e4m3_value(lo) + e4m3_value(lo + 1));  // 6 times the border above lo
+        const int side = from ? side_of(x, m, g) : side_of(amax, m, g);
+        if (side < 0 || (side == 0 && !(lo & 1u)))
+            break;
+    }
+    return lo;
 }
 
-// w with the codes settled whose bits in `differ` are not all zero: each is
-// that of w or the next.
-__device__ __noinline__ uint32_t settle_codes(uint32_t w, uint32_t differ, float s, float g, const float *y, const Source *from)
+// The magnitudes lo with the codes settled that are others in hi, which has the
+// elements' signs: a code is one of those between the two, and of a rotated
+// element the sign, too, is that of its real value.  Returns the codes with
+// signs.
+__device__ __noinline__ uint32_t settle_codes(uint32_t lo, uint32_t hi, float s, float g, const float *y, const Source *from)
 {
+    uint32_t w = hi, differ = lo ^ (hi & 0x77777777u);
+#pragma unroll 1
     while (differ) {
-        const int i = (__ffs(differ) - 1) / 4;
-        differ &= ~(15u << (4 * i));
-        const uint32_t c = w >> (4 * i) & 7u;
-        // the border above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5
-        const float m = s * (c < 4 ? 0.5f * c + 0.25f : c < 6 ? (float)c - 1.5f : 5.f);
-        const int side = from ? side_of(fabs(from->real(i)), m, g) : side_of(fabsf(y[i]), m, g);
-        w += (side > 0 || (side == 0 && (c & 1u)) ? 1u : 0u) << (4 * i);
+        const int i = (__ffs(differ) - 1) / 4, at = 4 * i;
+        differ &= ~(15u << at);
+        const double x = from ? from->real(i) : 0.0;
+        uint32_t c = lo >> at & 7u, sign = hi >> at & 8u;
+        for (const uint32_t most = hi >> at & 7u; c < most; ++c) {
+            // the border above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5
+            const float m = s * (c < 4 ? 0.5f * c + 0.25f : c < 6 ? (float)c - 1.5f : 5.f);
+            const int side = from ? side_of(fabs(x), m, g) : side_of(fabsf(y[i]), m, g);
+            if (side < 0 || (side == 0 && !(c & 1u)))
+                break;
+        }
+        if (from)
+            sign = x < 0.0 ? 8u : 0u;
+        w = (w & ~(15u << at)) | (c | sign) << at;
     }
     return w;
 }
@@ -172,10 +186,12 @@ __device__ __forceinline__ void code_ends(const float (&y)[8], float off, float 
     float l[8], h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        l[i] = fmaf(fabsf(y[i]), below, -more);  // (below zero: a zero of either sign)
+        l[i] = fmaf(fabsf(y[i]), below, -more);
         h[i] = copysignf(fmaf(fabsf(y[i]), above, more), y[i]);
     }
-    lo = pack_e2m1(l) & 0x77777777u;
+    lo = pack_e2m1(l);
+    const uint32_t less = lo & 0x88888888u;  // a lower end below zero is zero
+    lo &= ~(less - (less >> 3)) & 0x77777777u;
     hi = pack_e2m1(h);
 }
 

@@ -1,0 +1,67 @@
+"""The 4-bit cache, weights of cached keys and eviction where they are hardest:
+rotated blocks far smaller than what they were turned from.
+
+Bounds as in test_cache_shrink.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_cache_shrink import quantize
+from tests.test_paged import BF16, frequencies, gm, m, rotate  # noqa: F401
+
+
+# ---------------------------------------------------------------------------------- append
+
+def append4(gm, k, v, past, scale, rope, interleaved, aligned):
+    """k, v [B,Hkv,S,d] into a 4-bit cache of pages of 8 that lie in order: the rows of both, [B,Hkv,S,bytes].
+    Not aligned: by blocks of 16 elements, element by element."""
+    B, Hkv, S, d = k.shape
+    pages = -(-(int(past.max()) + S) // 8)
+    caches = [torch.zeros(B * pages, Hkv, 8, d // 2 + d // 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    cache = gm.PagedCache(*caches, table, k_scale=scale, v_scale=scale)
+    if not aligned:
+        k, v = (torch.nn.functional.pad(x, (1, 0))[..., 1:] for x in (k, v))
+    plan = gm.mercury_rope_init(rope[0], base=rope[1], interleaved=interleaved) if rope else None
+    gm.mercury_kv_append(cache, k, v, past, rope=plan)
+    gm.mercury_sync_status()
+    at = past[:, None].long() + torch.arange(S, device="cuda")
+    page, b = at // 8, torch.arange(B, device="cuda")[:, None]
+    return [c[table[b, page].long(), :, at % 8].transpose(1, 2) for c in caches]
+
+
+def codes_of(rows, d):
+    return torch.stack((rows[..., :d // 2] & 15, rows[..., :d // 2] >> 4), -1).flatten(-2).long()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("scale", [8 * 4 / 2688, 1e-4, -1e-4, 1e-8])
+@pytest.mark.parametrize("d,rot,base,interleaved", [
+    (128, 128, 1e4, False), (128, 128, 1e7, False), (64, 64, 5e7, False), (128, 96, 1e6, False), (64, 24, 1e7, False),
+    (128, 128, 1e7, True)])
+def test_4_bit_append_of_halves_far_apart(gm, aligned, scale, d, rot, base, interleaved):
+    """One side of all pairs up to 1e8 times smaller than the other, or zero, at positions where a turn is small: what
+    32 bits know of such a block then spans several codes, and several scales."""
+    gen = torch.Generator("cuda").manual_seed(rot + int(base) % 97)
+    B, Hkv, S = 96, 2, 4
+    k = torch.randn(B, Hkv, S, d, generator=gen, device="cuda") * 8
+    ratio = torch.logspace(0, 8, B, device="cuda")
+    ratio[::8] = torch.inf  # zeros
+    small = torch.arange(rot, device="cuda")
+    small = small[small % 2 == 0] if interleaved else small[:rot // 2]
+    k[..., small] /= ratio[:, None, None, None]
+    k[1::2] = k[1::2].roll(rot // 2, -1) if rot == d and not interleaved else k[1::2]  # the other half
+    k = k.to(BF16)
+    past = (torch.arange(B, device="cuda") % 3).to(torch.int32) * 2  # (position 0 turns nothing)
+    sc = torch.full((Hkv,), scale, device="cuda")
+    rows = append4(gm, k, k, past, sc, (rot, base), interleaved, aligned)
+    pos = past[:, None].long() + torch.arange(S, device="cuda")
+    for got, ref in zip(rows, (rotate(k, pos, frequencies(rot, base), interleaved), k.double())):
+        codes, sbytes = quantize(ref, sc[:, None])
+        mine = codes_of(got, d)
+        assert torch.equal(got[..., d // 2:].long(), sbytes)
+        assert torch.equal(mine & 7, codes)
+        some = codes > 0
+        assert torch.equal((mine >> 3)[some].bool(), ((ref < 0) != (scale < 0))[some])
