@@ -623,7 +623,7 @@ typedef struct mercury_paged_cache {
  * each 16 elements' scale is the e4m3 s nearest to their largest magnitude
  * over 6 scale[head], at most 448, and each code the nearest to x / (s
  * scale[head]), saturated at +-6, ties to even in both; where s is 0 the codes
- * are.  These are the nearest to the real quotients of the rotated key, not of
+ * are, and a zero is stored without a sign.  These are the nearest to the real quotients of the rotated key, not of
  * its 32-bit rounding: the products that decide are made exactly, or for a
  * rotated key to 2^-48.  (Head scales are finite and of magnitudes 2^-60 to
  * 2^60; other ones give codes that nothing is said about.)  A NaN makes the

@@ -136,7 +136,7 @@ __device__ __forceinline__ void keep4(const RotUnit<8> &unit, const mercury_rope
             const Source from = source(first, second, copy);
             w = settle_codes(lo, w, e4m3_value(byte), g, copy, by > 0.f ? &from : nullptr);
         }
-        *reinterpret_cast<uint32_t *>(row + at / 2) = scale < 0.f ? w ^ 0x88888888u : w;
+        *reinterpret_cast<uint32_t *>(row + at / 2) = stored_codes(w, scale);
         if (at % 16 == 0)
             row[d / 2 + at / 16] = (char)byte;
     }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kRotThreads) append_blocks_kernel(const __grid
             const Source half = {x + 8 * k, z + 8 * k, from.pos, turns, a.plan.magnitude, at + 8 * k, rot, a.plan.interleaved};
             w = settle_codes(lo, w, s, g, y + 8 * k, by > 0.f ? &half : nullptr);
         }
-        *reinterpret_cast<uint32_t *>(row + at / 2 + 4 * k) = scale < 0.f ? w ^ 0x88888888u : w;
+        *reinterpret_cast<uint32_t *>(row + at / 2 + 4 * k) = stored_codes(w, scale);
     }
     row[a.d / 2 + at / 16] = (char)byte;
 }

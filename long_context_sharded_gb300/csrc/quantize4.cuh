@@ -195,4 +195,13 @@ __device__ __forceinline__ void code_ends(const float (&y)[8], float off, float 
     hi = pack_e2m1(h);
 }
 
+// Codes with signs as they are stored: all signs turned for a negative head
+// scale, and a zero without one (which sign a zero's would be hangs on how 32
+// bits round).
+__device__ __forceinline__ uint32_t stored_codes(uint32_t w, float scale)
+{
+    const uint32_t magnitudes = w & 0x77777777u, some = (magnitudes + 0x77777777u) & 0x88888888u;
+    return magnitudes | ((scale < 0.f ? ~w : w) & some);
+}
+
 }  // namespace mercury

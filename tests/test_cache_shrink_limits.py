@@ -65,3 +65,31 @@ def test_4_bit_append_of_halves_far_apart(gm, aligned, scale, d, rot, base, inte
         assert torch.equal(mine & 7, codes)
         some = codes > 0
         assert torch.equal((mine >> 3)[some].bool(), ((ref < 0) != (scale < 0))[some])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.01, -0.01, 3.0, -3.0])
+@pytest.mark.parametrize("d,rot,interleaved", [(128, 128, False), (64, 64, True), (128, 24, False), (64, 0, False)])
+def test_4_bit_append_gives_the_same_bytes_both_ways(gm, scale, d, rot, interleaved):
+    """Zeros of both signs, blocks whose scale is zero, rotated halves that are: a zero's code has no sign, and the bytes
+    are the formula's, whichever way they are made."""
+    gen = torch.Generator("cuda").manual_seed(rot + d)
+    B, Hkv, S = 4, 2, 40
+    k = torch.randn(B, Hkv, S, d, generator=gen, device="cuda")
+    k *= torch.exp2(torch.randint(-20, 3, (B, Hkv, S, d // 16, 1), generator=gen, device="cuda").float()).expand(-1, -1, -1, -1, 16).flatten(-2)
+    k[torch.rand(k.shape, generator=gen, device="cuda") < 0.2] = -0.0
+    k[:, :, ::5] = -0.0
+    k[:, :, 1::5, :d // 2] = -0.0
+    k[:, :, 2::5, d // 2:] = 0.0
+    k = k.to(BF16)
+    past = torch.tensor([0, 3, 8, 1000], dtype=torch.int32, device="cuda")
+    sc = torch.full((Hkv,), scale, device="cuda")
+    rope = (rot, 1e4) if rot else None
+    rows, other = (append4(gm, k, k, past, sc, rope, interleaved, aligned) for aligned in (True, False))
+    pos = past[:, None].long() + torch.arange(S, device="cuda")
+    rk = rotate(k, pos, frequencies(rot), interleaved) if rot else k.double()
+    for got, same, ref in zip(rows, other, (rk, k.double())):
+        assert torch.equal(got, same)
+        codes, sbytes = quantize(ref, sc[:, None])
+        codes += 8 * ((codes > 0) & ((ref < 0) != (scale < 0)))
+        assert torch.equal(got, torch.cat((codes[..., ::2] + 16 * codes[..., 1::2], sbytes), -1).to(torch.uint8))
