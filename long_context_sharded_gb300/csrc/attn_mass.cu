@@ -481,9 +481,13 @@ __global__ void __launch_bounds__(kMassThreads, blocks_of(D)) attn_mass_kernel(c
 // with the other's exponentials.  What a row costs there is its constants, read
 // from shared memory by every warp: so there is only one (of four rows at a
 // time), the exponent's summand; the factor is one for all rows, since their
-// queries are scaled by one power of two (of a row far below the largest
-// elements are lost that are 2^-38 of it, and scores enter by their absolute
-// error), and what rounding the summand leaves out, 2^-24 of lse, is left out.
+// queries are scaled by one power of two, and what rounding the summand leaves
+// out, 2^-24 of lse, is left out.  Such a scale rounds elements to 2^-40 of the
+// largest of all rows.  So it is taken where no eight elements that lie together
+// have a largest one 2^kApart below that one, but for zeros: they are rounded to
+// 2^-27 of their own largest, far below what the sum of the products in 32 bits
+// costs.  Else each row has a scale of its own and its factor is read too, so
+// that no row's weights hang on another's queries.
 template <int ELEM, int D>
 struct Raw {  // half of a key's row
     static constexpr int kWords = ELEM == MERCURY_ELEM_BF16 ? D / 4 : ELEM == MERCURY_ELEM_E4M3 ? D / 8 : D / 16 + 1;
@@ -554,7 +558,42 @@ __device__ __forceinline__ int operand_at(int row, int c, int rows)
 
 constexpr int wide_smem(int D, int N)
 {
-    return 128 * D * 2 + N * D * 2 + N * 8 + 128 * 4 + 32;
+    return 128 * D * 2 + N * D * 2 + N * 12 + 128 * 4 + 48;
+}
+
+constexpr int kApart = 12;
+
+// Magnitudes of bf16 elements, as 16-bit integers, whose order is theirs: two's,
+// infinite and NaN ones as zero.
+__device__ __forceinline__ uint32_t magnitude(uint32_t w)
+{
+    w &= 0x7fff7fffu;
+    return w & ~__vcmpgeu2(w, 0x7f807f80u);
+}
+
+// The largest of eight, in both halves.
+__device__ __forceinline__ uint32_t top_of_eight(const uint4 &x)
+{
+    const uint32_t w = __vmaxu2(__vmaxu2(magnitude(x.x), magnitude(x.y)), __vmaxu2(magnitude(x.z), magnitude(x.w)));
+    return __vmaxu2(w, __byte_perm(w, 0, 0x1032));
+}
+
+// The largest element of each of a head's rows of a launch that counts, a row a thread.
+template <int D>
+__device__ __forceinline__ void row_tops(const MassArgs &a, int b, int h, int n_new, float *tops)
+{
+    const PagedArgs &p = a.p;
+    const int n = threadIdx.x, r = a.r0 + n, head = r / p.Sq, i = r - head * p.Sq;
+    if (n >= a.wide)
+        return;
+    uint32_t top = 0;
+    if (n < a.rows && i < n_new && fabsf(a.lse[((long long)b * p.Hkv + h) * p.R + r]) != INFINITY) {
+        const uint4 *const src = reinterpret_cast<const uint4 *>(p.q + b * p.qs.b + (h * p.G + head) * p.qs.h + i * p.qs.s);
+#pragma unroll 1
+        for (int k = 0; k < D / 8; ++k)
+            top = __vmaxu2(top, top_of_eight(src[k]));
+    }
+    tops[n] = __uint_as_float(top << 16);
 }
 
 template <int ELEM, int D>
@@ -567,10 +606,13 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
     char *const keys_at = smem, *const queries_at = smem + 128 * D * 2;
     float *const summands = reinterpret_cast<float *>(queries_at + N * D * 2);  // -inf: the row counts nothing
     int *const steps = reinterpret_cast<int *>(summands + N);                   // of the new tokens
-    float *const halves = reinterpret_cast<float *>(steps + N);
+    float *const factors = reinterpret_cast<float *>(steps + N);                // from products to log2 units
+    float *const halves = factors + N;
     uint64_t *const done = reinterpret_cast<uint64_t *>(halves + 128);
     uint32_t *const slot = reinterpret_cast<uint32_t *>(done + 1);
-    int *const largest = reinterpret_cast<int *>(slot + 1);  // magnitude of the job's queries (bits)
+    // Each warp's of a job's queries (bf16's bits): the largest magnitude; in the upper
+    // half the smallest of eight elements' largest, but for zeros, taken from infinity.
+    uint32_t *const extremes = slot + 2;
     const PagedArgs &p = a.p;
     const PagedView &c = p.cache;
     chain_wait();
@@ -580,7 +622,6 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
     if (!find_share(a, lane, now, at, end))
         return;
     if (tid == 0) {
-        *largest = 0;
         mbar_init(done, 1);
         fence_mbar_init();
     }
@@ -650,12 +691,8 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
             const int ch = tid % LPR;
             const __nv_bfloat16 *const head_q = p.q + now.b * p.qs.b + now.h * p.G * p.qs.h;
             const float *const head_lse = a.lse + (long long)this_job * p.R;
-            // (as 16-bit integers, whose order is theirs)
-            auto magnitude = [](uint32_t w) {
-                w &= 0x7fff7fffu;
-                return w & ~__vcmpgeu2(w, 0x7f807f80u);
-            };
             float mul_lo = a.mul_lo, to = 1.f;
+            bool apart = false;
             mul = a.mul;
             uint4 x[U];
             // Rows' elements; their lse and new tokens go where the rows' constants
@@ -688,18 +725,37 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                 }
             };
             if constexpr (kF16) {
-                uint32_t top = 0;
+                uint32_t most = 0, few = 0xffffffffu;
                 for (int n0 = tid / LPR; n0 < N; n0 += U * EACH) {
                     load_rows(n0);
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(magnitude(x[u].x), magnitude(x[u].y)), __vmaxu2(magnitude(x[u].z), magnitude(x[u].w))));
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t top = top_of_eight(x[u]);
+                        most = __vmaxu2(most, top);
+                        few = __vminu2(few, __vsub2(top, 0x00010001u));  // (zero above all)
+                    }
                 }
-                atomicMax(largest, __reduce_max_sync(0xffffffffu, (int)max(top << 16, top & 0xffff0000u)));  // (their bits are in order)
+                constexpr uint32_t kInf = 0x7f80;
+                most = __reduce_max_sync(0xffffffffu, most & 0xffffu);
+                few = kInf - min(__reduce_min_sync(0xffffffffu, few & 0xffffu) + 1, kInf);
+                if (lane == 0)
+                    extremes[warp] = most | few << 16;
                 __syncthreads();
+                {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(extremes), z = *reinterpret_cast<const uint4 *>(extremes + 4);
+                    most = __vmaxu2(__vmaxu2(__vmaxu2(y.x, y.y), __vmaxu2(y.z, y.w)), __vmaxu2(__vmaxu2(z.x, z.y), __vmaxu2(z.z, z.w)));
+                }
+                few = most >> 16;
+                apart = few != 0 && (int)((most & 0xffffu) >> 7) - (int)((kInf - few) >> 7) > kApart;
+                if (apart) {
+                    row_tops<D>(a, now.b, now.h, n_new, factors);
+                    __syncthreads();
+                }
                 float back;
-                scale_of(__int_as_float(*largest), to, back);
+                scale_of(__uint_as_float(most << 16), to, back);
                 const float ks = c.k_scale[now.h], hi = a.mul * ks;
+                if (apart)
+                    back = 1.f;
                 mul_lo = (fmaf(a.mul, ks, -hi) + a.mul_lo * ks) * back;
                 mul = hi * back;
             }
@@ -711,17 +767,26 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                     const int n = n0 + u * EACH;
                     if (n >= N)
                         break;
+                    float back = 1.f;
+                    if (kF16 && apart) {
+                        scale_of(factors[n], to, back);
+                        __syncwarp();  // (the row's lanes have read it)
+                    }
                     if (kF16)
                         x[u] = make_uint4(pack_f16(bf16_lo(x[u].x) * to, bf16_hi(x[u].x) * to), pack_f16(bf16_lo(x[u].y) * to, bf16_hi(x[u].y) * to),
                                           pack_f16(bf16_lo(x[u].z) * to, bf16_hi(x[u].z) * to), pack_f16(bf16_lo(x[u].w) * to, bf16_hi(x[u].w) * to));
                     *reinterpret_cast<uint4 *>(queries_at + operand_at(n, ch, N)) = x[u];
                     if (ch == 0) {
                         // (of mul and lse in log2 units, as in row_of)
+                        factors[n] = mul * back;
                         const float off = mul == 0.f ? 0.f : mul_lo / mul, l = summands[n];
                         summands[n] = fabsf(l) < INFINITY || l != l ? fmaf(-l, kLog2e, l * kLog2e * off) : -INFINITY;
                     }
                 }
             }
+            // (the short way's sums are not finite then, and made again by the rows' factors)
+            if (apart)
+                mul = __int_as_float(0x7fffffff);
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -734,8 +799,6 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
-        if (tid == 0)
-            *largest = 0;  // (the next job's comes behind another barrier)
         if (warp == 0) {
             tc_fence_after();
             const uint32_t leader = elect_lane();
@@ -780,7 +843,7 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                     const float nl[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float w = ex2_approx(fmaf(__uint_as_float(x[k + e]), mul, nl[e]));
+                        const float w = ex2_approx(fmaf(__uint_as_float(x[k + e]), kF16 && decltype(masked)::value ? factors[n + k + e] : mul, nl[e]));
                         if constexpr (decltype(masked)::value) {
                             if (nl[e] != -INFINITY && key < (p.causal ? seen_by_all + steps[n + k + e] : tile.keys))
                                 sum += w;
@@ -792,7 +855,8 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
             }
         };
         // (An infinite or NaN key gives NaN in rows that count nothing, too: such
-        // sums are made again, row by row.)
+        // sums are made again, row by row; so are all where the rows have scales of
+        // their own.)
         bool all = k0 + kMassTile > seen_by_all;
         if (!all) {
             add_rows(Masked<false>());

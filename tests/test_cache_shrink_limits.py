@@ -1,5 +1,6 @@
 """The 4-bit cache, weights of cached keys and eviction where they are hardest:
-rotated blocks far smaller than what they were turned from.
+rotated blocks far smaller than what they were turned from, rows of queries far
+apart.
 
 Bounds as in test_cache_shrink.py.
 """
@@ -7,8 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache_shrink import quantize
-from tests.test_paged import BF16, frequencies, gm, m, rotate  # noqa: F401
+from tests.test_cache_shrink import E2M1, quantize, run4, weights
+from tests.test_paged import BF16, E4M3, assert_within, frequencies, gm, m, rotate  # noqa: F401
 
 
 # ---------------------------------------------------------------------------------- append
@@ -93,3 +94,30 @@ def test_4_bit_append_gives_the_same_bytes_both_ways(gm, scale, d, rot, interlea
         codes, sbytes = quantize(ref, sc[:, None])
         codes += 8 * ((codes > 0) & ((ref < 0) != (scale < 0)))
         assert torch.equal(got, torch.cat((codes[..., ::2] + 16 * codes[..., 1::2], sbytes), -1).to(torch.uint8))
+
+
+# ------------------------------------------------------------------------------------ weights
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("d,Sq,up", [(128, 8, 60), (128, 24, 7), (128, 24, 13), (128, 24, 20), (64, 24, 45), (128, 64, 40), (64, 64, 100)])
+def test_mass_does_not_hang_on_other_rows(gm, elem, d, Sq, up):
+    """Rows whose queries are 2^up times the others', in elements that all keys are zero in: neither their own weights
+    nor the others' lose anything."""
+    lens = [300, 1100]
+
+    def spoil(k, v, table):
+        k[..., :16 if elem is not E2M1 else 8] = 0  # (codes of zero)
+
+    r = run4(gm, 2, 5, 1, Sq, d, 16, lens, spoil=spoil, seed=25 + up, elem=elem)
+    assert (r["q"][..., :16] != 0).any()
+    for b, head, i in ((0, 1, 3), (1, 0, 0), (1, 4, Sq - 1)):
+        r["q"][b, head, i, 16:] = 0
+        r["q"][b, head, i, :16] *= 2.0 ** up
+    _, lse = gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    got = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse)
+    gm.mercury_sync_status()
+    assert torch.isfinite(lse).all()
+    ref, bound = weights(r, lse, lens, None, True, torch.zeros(2, 1, got.shape[2], device="cuda"), got.shape[2])
+    for b, n in enumerate(lens):
+        assert_within(got[b, :, :n], ref[b, :, :n], bound[b, :, :n], "sequence %d" % b)
