@@ -54,7 +54,8 @@ struct MassArgs {
     int r0, rows;       // this launch's rows of each head
     int wide;           // rows of the tensor unit's product, or 0
     float mul, mul_lo;  // log2(e) / sqrt(d), and what its rounding leaves out
-    unsigned long long per_sq;  // 2^40 / Sq, rounded up
+    int head0, step0;   // r0's head and new token
+    int per_sq;         // 2^16 / Sq, rounded up
 };
 
 // A row of queries: a weight is 2^(score * mul + nl) * rest.  nl, lse in log2
@@ -689,12 +690,14 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
             // next tile takes more registers: with 8 they spill, 128 rows 213 us)
             constexpr int LPR = D / 8, EACH = kMassThreads / LPR, U = kF16 ? 8 : 4;
             const int ch = tid % LPR;
-            const __nv_bfloat16 *const head_q = p.q + now.b * p.qs.b + now.h * p.G * p.qs.h;
+            const __nv_bfloat16 *const head_q = p.q + now.b * p.qs.b + (now.h * p.G + a.head0) * p.qs.h;
             const float *const head_lse = a.lse + (long long)this_job * p.R;
             float mul_lo = a.mul_lo, to = 1.f;
             bool apart = false;
             mul = a.mul;
             uint4 x[U];
+            // (n + step0 is below 384: exact)
+            auto head_of = [&](int n) { return (n + a.step0) * a.per_sq >> 16; };
             // Rows' elements; their lse and new tokens go where the rows' constants
             // do.  Where all rows share a scale, one that counts nothing is taken as
             // zeros: the scale may not hang on what it holds (nor on an infinity).
@@ -702,25 +705,25 @@ __global__ void __launch_bounds__(kMassThreads, 2) attn_mass_wide_kernel(const _
                 float l[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int n = n0 + u * EACH, r = a.r0 + n, head = (int)(r * a.per_sq >> 40), i = r - head * p.Sq;
+                    const int n = n0 + u * EACH, r = a.r0 + n, up = head_of(n), i = n + a.step0 - up * p.Sq;
                     x[u] = make_uint4(0, 0, 0, 0);
                     l[u] = INFINITY;
                     if (n < a.rows && i < n_new) {
-                        x[u] = *reinterpret_cast<const uint4 *>(head_q + head * p.qs.h + i * p.qs.s + ch * 8);
+                        x[u] = *reinterpret_cast<const uint4 *>(head_q + up * p.qs.h + i * p.qs.s + ch * 8);
                         if (kF16 || ch == 0)
                             l[u] = head_lse[r];
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int n = n0 + u * EACH, r = a.r0 + n;
+                    const int n = n0 + u * EACH;
                     if (kF16) {
                         const uint32_t keep = fabsf(l[u]) == INFINITY ? 0u : 0xffffffffu;
                         x[u].x &= keep, x[u].y &= keep, x[u].z &= keep, x[u].w &= keep;
                     }
                     if (ch == 0 && n < N) {
                         summands[n] = l[u];
-                        steps[n] = r - (int)(r * a.per_sq >> 40) * p.Sq;
+                        steps[n] = n + a.step0 - head_of(n) * p.Sq;
                     }
                 }
             };
@@ -921,7 +924,10 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     const bool narrow_keys = D == 64 || ELEM == MERCURY_ELEM_E2M1;
     const bool wide = a.p.R > kMassRows || (a.p.R > 48 && narrow_keys && most >= 24LL * ki.sms);
     const int each = wide ? kWideRows : kMassRows;
-    for (a.r0 = 0; a.r0 < a.p.R; a.r0 += each) {
+    for (long long r0 = 0; r0 < a.p.R; r0 += each) {
+        a.r0 = (int)r0;
+        a.head0 = a.r0 / a.p.Sq;
+        a.step0 = a.r0 % a.p.Sq;
         a.rows = a.p.R - a.r0 < each ? a.p.R - a.r0 : each;
         a.wide = !wide ? 0 : a.rows <= 64 ? 64 : a.rows <= 128 ? 128 : 256;
         const int smem = wide ? wide_smem(D, a.wide) : (a.rows + 7) / 8 * 8 * kRowSmem;
@@ -958,7 +964,7 @@ int launch_attn_mass(const void *q, const Strides &qs, const mercury_paged_cache
     a.mass = mass;
     a.out = out;
     a.width = width;
-    a.per_sq = ((1ULL << 40) + Sq - 1) / Sq;  // (Sq <= 64: exact for every row below 2^34)
+    a.per_sq = ((1 << 16) + Sq - 1) / Sq;
     const double mul = 1.4426950408889634074 / sqrt((double)cache.d);
     a.mul = (float)mul;
     a.mul_lo = (float)(mul - (double)a.mul);

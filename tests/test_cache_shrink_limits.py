@@ -121,3 +121,23 @@ def test_mass_does_not_hang_on_other_rows(gm, elem, d, Sq, up):
     ref, bound = weights(r, lse, lens, None, True, torch.zeros(2, 1, got.shape[2], device="cuda"), got.shape[2])
     for b, n in enumerate(lens):
         assert_within(got[b, :, :n], ref[b, :, :n], bound[b, :, :n], "sequence %d" % b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3])
+@pytest.mark.parametrize("heads,Sq", [(2 ** 24 + 64, 1), (2 ** 23 + 40, 3)])
+def test_mass_of_more_heads_than_24_bits_count(gm, elem, heads, Sq):
+    """The last query heads of many (whose queries overlap in memory), the only ones that count."""
+    n, d, last = 40, 64, 30
+    r = run4(gm, 1, 1, 1, 1, d, 16, [n], seed=27, elem=elem)
+    gen = torch.Generator("cuda").manual_seed(3)
+    flat = torch.randn(8 * heads + 64 * Sq, generator=gen, device="cuda").to(BF16)
+    q = flat.as_strided((1, heads, Sq, d), (flat.numel(), 8, 64, 1))
+    lse = torch.full((1, heads, Sq), torch.inf, device="cuda")
+    lse[:, -last:] = 5.0
+    out = torch.full((1, 1, n), 9.0, device="cuda")
+    gm.mercury_attn_paged_mass(q, r["cache"], r["lens"], lse, out=out)
+    gm.mercury_sync_status()
+    few = dict(r, q=q[:, -last:])
+    ref, bound = weights(few, lse[:, -last:], [n], None, True, torch.zeros(1, 1, n, device="cuda"), n)
+    assert_within(out, ref, bound, "weights")
