@@ -276,7 +276,8 @@ MERCURY_API int mercury_attn_split_noalloc(const void *q, const void *k, const v
  * error words of this process's kernels.  Returns MERCURY_OK,
  * MERCURY_ETIMEOUT (a bounded device wait ran out in some earlier kernel),
  * MERCURY_EBOUNDS (a paged-cache kernel met a page, position or length out
- * of range and skipped the access; or, only in the checked build,
+ * of range and skipped the access, or mercury_kv_evict two caches of other head
+ * scales; or, only in the checked build,
  * libmercury_attn.so built with -DMERCURY_CHECK, a kernel found an
  * out-of-range TMA coordinate or output index and skipped that access) or
  * MERCURY_ECUDA (the synchronise itself failed).
@@ -769,7 +770,8 @@ MERCURY_API int mercury_attn_paged_mass(const void *q, const long long *q_stride
  * arrays); the same elem, Hkv, d, B and head scales.
  * A seq_lens outside the block table or above width is taken to the nearer end,
  * a page outside cache counts as rows of zeros, a row whose page lies outside
- * into is not stored; each is reported as MERCURY_EBOUNDS.
+ * into is not stored; each is reported as MERCURY_EBOUNDS, and so are head scales
+ * of into that are not cache's (the rows are moved all the same).
  * Requirements: the caches as in mercury_kv_append; 1 <= keep <= what into's
  * table holds; first + last <= keep; out_width >= keep; out_lens and out_mass
  * are not seq_lens and mass; into's table and arrays are not both cache's.  The

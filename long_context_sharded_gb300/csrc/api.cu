@@ -157,6 +157,9 @@ int collect_device_errors(cudaStream_t stream)
         rc = read_and_clear_evict_error(&w[7], &site[7], g_msg, sizeof g_msg);
     if (rc != MERCURY_OK)
         return rc;
+    if ((w[7] & 2u) && site[7] == 0xa04u)
+        return fail(MERCURY_EBOUNDS, "cache eviction: the two caches' head scales differ, the rows moved mean "
+                    "something else (site 0x%x)", site[7]);
     for (int i = 3; i < n; ++i)
         if (w[i] & 2u)
             return fail(MERCURY_EBOUNDS, "paged cache: a length, position or page out of range was found and its "

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache_shrink import E2M1, quantize, run4, weights
+from tests.test_cache_shrink import E2M1, make_any, quantize, run4, weights
 from tests.test_paged import BF16, E4M3, assert_within, frequencies, gm, m, rotate  # noqa: F401
 
 
@@ -141,3 +141,30 @@ def test_mass_of_more_heads_than_24_bits_count(gm, elem, heads, Sq):
     few = dict(r, q=q[:, -last:])
     ref, bound = weights(few, lse[:, -last:], [n], None, True, torch.zeros(1, 1, n, device="cuda"), n)
     assert_within(out, ref, bound, "weights")
+
+
+# ----------------------------------------------------------------------------------- eviction
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [E4M3, E2M1])
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_eviction_into_a_cache_of_other_scales_is_reported(gm, elem, which):
+    """Rows are moved as they are, so other head scales would give them other values; the same ones in tensors of their
+    own are fine, and so is a cache of which nothing is kept."""
+    r = run4(gm, 2, 4, 2, 1, 128, 16, [0, 90], seed=55, elem=elem)
+    gen = torch.Generator("cuda").manual_seed(6)
+    k2, v2, table2, _ = make_any(2, 2, 128, 16, 3, elem, gen)
+    scales = dict(k_scale=r["ks"].clone(), v_scale=r["vs"].clone())
+    into = gm.PagedCache(k2, v2, table2, **scales)
+    mass = torch.rand(2, 2, 96, device="cuda")
+    lens = r["lens"]
+    gm.mercury_kv_evict(r["cache"], into, mass, lens, 48)
+    gm.mercury_sync_status()
+    scales[which][1] *= 1.0 + 2.0 ** -20
+    gm.mercury_kv_evict(r["cache"], into, mass, lens, 48)
+    with pytest.raises(gm.MercuryError, match="head scales") as e:
+        gm.mercury_sync_status()
+    assert e.value.status == gm.MERCURY_EBOUNDS
+    gm.mercury_sync_status()
+    gm.mercury_kv_evict(r["cache"], into, mass, torch.zeros_like(lens), 48)
+    gm.mercury_sync_status()
