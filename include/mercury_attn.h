@@ -628,7 +628,8 @@ typedef struct mercury_paged_cache {
  * its 32-bit rounding: the products that decide are made exactly, or for a
  * rotated key to 2^-48.  (Head scales are finite and of magnitudes 2^-60 to
  * 2^60; other ones give codes that nothing is said about.)  A NaN makes the
- * scale of its 16 elements NaN; an infinity alone is held as +-6 * 448.
+ * scale of its 16 elements NaN; an infinity alone is held as +-6 * 448 (and what
+ * lies beside a rotated one is rounded from 32 bits).
  * q [B, Hq, S, d] bf16 (optional): the queries of the same tokens, rotated
  * likewise into q_out (which may be q itself, with its strides); q NULL means
  * q_out is not touched.
@@ -761,9 +762,12 @@ MERCURY_API int mercury_attn_paged_mass(const void *q, const long long *q_stride
  * mass.  out_lens[b] = m.  Everything else of into, kept [B, Hkv, keep] and
  * out_mass [B, Hkv, out_width] is left as it was.
  * The heads of a sequence keep different tokens, so a token's place is no
- * longer its position: queries and keys are rotated by positions that the
- * caller counts on (a key's was stored with it), and of the shorter cache's
- * tokens mercury_attn_paged's causal order holds, since it is kept.
+ * longer its position (a key was stored rotated by its own), and of the shorter
+ * cache's tokens mercury_attn_paged's causal order holds, since it is kept.
+ * Further tokens go behind them at place out_lens[b], which mercury_kv_append
+ * with a plan would rotate by; so their queries and keys are rotated by
+ * mercury_rope with the positions that the caller counts on, and appended with a
+ * plan of NULL.  (A key is then rounded to bf16 before it is to the cache's type.)
  * mass [B, Hkv, width] fp32, contiguous, as mercury_attn_paged_mass gives it.
  * into: pages of its own for each sequence, of any page size, none of them
  * among cache's pages of any sequence (the two structs may name the same

@@ -956,7 +956,10 @@ def mercury_kv_evict(cache: PagedCache, into: PagedCache, mass, seq_lens, keep: 
     order; mass [B,Hkv,width] fp32.  Returns (out_lens [B] int32, kept
     [B,Hkv,keep] int32: the token that each kept one was), made where they are
     not given (kept: -1 behind out_lens[b]); out_mass [B,Hkv,>=keep] fp32, where
-    given, gets the kept tokens' mass."""
+    given, gets the kept tokens' mass.  A token's place is no longer its
+    position then: further queries and keys are rotated by mercury_rope with
+    positions that the caller counts on, and appended without a plan.  Both
+    caches have the same head scales (others are reported by mercury_sync_status)."""
     if out_lens is not None and kept is not None and stream is None and isinstance(cache, PagedCache) and \
             isinstance(into, PagedCache) and into.device_index == cache.device_index:
         rc = _fast.evict(cache.address, into.address, cache.device_index, mass, seq_lens, keep, first, last, out_lens, kept,

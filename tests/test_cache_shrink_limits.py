@@ -1,6 +1,6 @@
 """The 4-bit cache, weights of cached keys and eviction where they are hardest:
 rotated blocks far smaller than what they were turned from, rows of queries far
-apart.
+apart, tokens behind an evicted cache, many rows on the tensor unit.
 
 Bounds as in test_cache_shrink.py.
 """
@@ -8,8 +8,9 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache_shrink import E2M1, make_any, quantize, run4, weights
-from tests.test_paged import BF16, E4M3, assert_within, frequencies, gm, m, rotate  # noqa: F401
+from tests.test_cache_shrink import E2M1, make_any, quantize, rows_of, run4, states, weights
+from tests.test_paged import (  # noqa: F401
+    BF16, E4M3, assert_within, attention, frequencies, gm, half_step, m, rotate, rotation_bound)
 
 
 # ---------------------------------------------------------------------------------- append
@@ -167,4 +168,196 @@ def test_eviction_into_a_cache_of_other_scales_is_reported(gm, elem, which):
     assert e.value.status == gm.MERCURY_EBOUNDS
     gm.mercury_sync_status()
     gm.mercury_kv_evict(r["cache"], into, mass, torch.zeros_like(lens), 48)
+    gm.mercury_sync_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tokens_behind_an_evicted_cache(gm, elem, d):
+    """After an eviction a token's place is no longer its position: queries and keys are rotated by mercury_rope at the
+    positions that the caller counts on and appended without a plan.  Attention and weights are those over the kept tokens
+    and the new ones."""
+    gen = torch.Generator("cuda").manual_seed(d)
+    B, Hq, Hkv, page, S, keep, more = 2, 6, 2, 16, 200, 64, 5
+    plan = gm.mercury_rope_init(d)
+
+    def new_cache(pages):
+        k, v, _, scales = make_any(B, Hkv, d, page, pages, elem, gen)
+        table = torch.randperm(B * pages, generator=gen, device="cuda").to(torch.int32).view(B, pages)
+        if scales[0] is not None:
+            scales = [torch.full((Hkv,), 0.01, device="cuda") for _ in range(2)]
+        return gm.PagedCache(k, v, table, k_scale=scales[0], v_scale=scales[1])
+
+    def token(b):
+        return [torch.randn(B, h, b, d, generator=gen, device="cuda").to(BF16) for h in (Hq, Hkv, Hkv)]
+
+    cache, into = new_cache(14), new_cache(6)
+    lens = torch.tensor([S, 150], dtype=torch.int32, device="cuda")
+    q, k, v = token(S)
+    q = gm.mercury_kv_append(cache, k, v, torch.zeros_like(lens), new_lens=lens, rope=plan, q=q)
+    mass = torch.rand(B, Hkv, S, generator=gen, device="cuda")
+    at, kept = gm.mercury_kv_evict(cache, into, mass, lens, keep, first=4, last=16)
+    gm.mercury_sync_status()
+    assert at.tolist() == [keep, keep]
+    short = [torch.stack([states(c, s, into.block_table[b], keep, d) for b in range(B)])
+             for c, s in ((into.k_cache, into.k_scale), (into.v_cache, into.v_scale))]
+    for c, s, got in ((cache.k_cache, cache.k_scale, short[0]), (cache.v_cache, cache.v_scale, short[1])):
+        for b in range(B):  # the tokens that were kept, each rotated at its own position
+            rows = states(c, s, cache.block_table[b], int(lens[b]), d)
+            assert torch.equal(got[b], rows.gather(1, kept[b].long()[..., None].expand(-1, -1, d)))
+    for step in range(more):
+        q, k, v = token(1)
+        pos = (lens + step)[:, None].contiguous()
+        q, rk = (gm.mercury_rope(x, plan, positions=pos) for x in (q, k))
+        gm.mercury_kv_append(into, rk, v, at + step)
+        out, lse = gm.mercury_attn_paged(q, into, at + step + 1)
+        w = gm.mercury_attn_paged_mass(q, into, at + step + 1, lse)
+        gm.mercury_sync_status()
+        n = keep + step + 1
+        ref = rotate(k, pos.long(), frequencies(d), False)
+        # rotated in 32 bits (6e-7 of a pair) and rounded to bf16
+        assert_within(rk, ref, half_step(ref, BF16) + rotation_bound(k, d // 2, False), "key")
+        for x, c, s, got in ((rk, into.k_cache, into.k_scale, short[0]), (v, into.v_cache, into.v_scale, short[1])):
+            for b in range(B):
+                rows = states(c, s, into.block_table[b], n, d)
+                assert torch.equal(rows[:, :keep], got[b])
+                if elem is BF16:
+                    assert torch.equal(rows[:, n - 1], x[b, :, 0].double())
+                elif elem is E2M1:
+                    codes, sbytes = quantize(x[b, :, 0].double(), s)
+                    new = rows_of(c, into.block_table[b], n)[:, n - 1]
+                    assert torch.equal(codes_of(new, d) & 7, codes) and torch.equal(new[:, d // 2:].long(), sbytes)
+        r = dict(q=q, k=into.k_cache, ks=into.k_scale, table=into.block_table)
+        for b in range(B):
+            kk, vv = (states(c, s, into.block_table[b], n, d) for c, s in ((into.k_cache, into.k_scale), (into.v_cache, into.v_scale)))
+            o, l, eo, el = attention(q[b], kk, vv, [n])
+            assert_within(out[b], o, eo, "O")
+            assert_within(lse[b], l, el, "LSE")
+        wide = w.shape[2]
+        ref, bound = weights(r, lse, [n, n], None, True, torch.zeros(B, Hkv, wide, device="cuda"), wide)
+        assert_within(w, ref, bound, "weights")
+
+
+# ------------------------------------------------- weights of many rows, where few were tested
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("d,Hq,Sq", [(128, 4, 50), (64, 6, 24), (128, 10, 64), (64, 8, 9)])
+def test_mass_of_many_rows_and_keys_that_some_see(gm, elem, d, Hq, Sq):
+    """NaN keys behind the last one and infinite or NaN ones that only rows without weight see, with pages whose tail is
+    not in the table."""
+    lens, page = [131, 500, Sq], 16
+
+    def spoil(k, v, table):
+        for b, n in enumerate(lens):
+            for at in list(range(n, (n + page - 1) // page * page)) + [n - 1]:
+                if elem is BF16:
+                    k[table[b, at // page].long(), :, at % page] = float("inf") if at % 2 else float("nan")
+                else:
+                    k.view(torch.uint8)[table[b, at // page].long(), :, at % page] = 0x7f
+
+    r = run4(gm, 3, Hq, 2, Sq, d, page, lens, spoil=spoil, seed=31, elem=elem)
+    lse = r["lse"].clone()
+    lse[:, :, Sq - 1] = torch.inf  # the row that sees the bad key
+    out = torch.full((3, 2, 512), 9.0, device="cuda")
+    gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse, out=out)
+    gm.mercury_sync_status()
+    clean = r["k"].clone()
+    for b, n in enumerate(lens):
+        clean.view(torch.uint8)[r["table"][b, (n - 1) // page].long(), :, (n - 1) % page] = 0
+    ref, bound = weights(dict(r, k=clean), lse, lens, None, True, torch.zeros(3, 2, 512, device="cuda"), 512)
+    for b, n in enumerate(lens):
+        assert_within(out[b, :, :n], ref[b, :, :n], bound[b, :, :n], "sequence %d" % b)
+        assert (out[b, :, n - 1] == 0).all() and (out[b, :, n:] == 9.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Sq", [8, 40])
+def test_mass_of_many_rows_and_infinite_keys(gm, Sq):
+    """An infinite key in a full tile, whose weight is 0 in all rows: they all score -inf."""
+    r = run4(gm, 1, 6, 2, Sq, 128, 16, [1000], seed=22, elem=BF16)
+    r["q"].copy_(r["q"].abs() + 0.1)
+    r["k"][r["table"][0, 20].long(), 1, 5] = -torch.inf  # token 325
+    out, lse = gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    got = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse)
+    gm.mercury_sync_status()
+    assert torch.isfinite(lse).all() and torch.isfinite(got).all() and got[0, 1, 325] == 0
+    assert (got.sum((0, 2)) - 3 * Sq).abs().max() < 1e-4 * Sq
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [E4M3, E2M1])
+@pytest.mark.parametrize("Sq", [1, 12, 30])
+@pytest.mark.parametrize("scale", [-0.7, -1e-3, 2.0 ** -40])
+def test_mass_with_head_scales_of_any_sign(gm, elem, Sq, scale):
+    lens = [700, 33]
+    r = run4(gm, 2, 8, 2, Sq, 128, 16, lens, seed=12, scale=0.1, elem=elem)
+    r["ks"].fill_(scale)
+    _, lse = gm.mercury_attn_paged(r["q"], r["cache"], r["lens"])
+    got = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], lse)
+    gm.mercury_sync_status()
+    wide = got.shape[2]
+    ref, bound = weights(r, lse, lens, None, True, torch.zeros(2, 2, wide, device="cuda"), wide)
+    assert_within(got, ref, bound, "weights")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_mass_of_many_rows_with_pages_and_lengths_out_of_range(gm, elem, d):
+    lens, Sq = [100, 300, 90], 40
+    r = run4(gm, 3, 4, 2, Sq, d, 16, lens, seed=51, elem=elem)
+    first = gm.mercury_attn_paged_mass(r["q"], r["cache"], r["lens"], r["lse"])
+    gm.mercury_sync_status()
+    good = r["table"].clone()
+
+    def expect(lens_t, **kw):
+        got = gm.mercury_attn_paged_mass(r["q"], r["cache"], lens_t, r["lse"], **kw)
+        with pytest.raises(gm.MercuryError) as e:
+            gm.mercury_sync_status()
+        assert e.value.status == gm.MERCURY_EBOUNDS
+        gm.mercury_sync_status()
+        return got
+
+    for entry in (-1, r["k"].shape[0], 2 ** 31 - 1, -2 ** 31):
+        r["table"][1, 5] = entry  # tokens 80 to 95 count as zeros: exp(-lse) of each row that sees them
+        got = expect(r["lens"])
+        want = torch.exp(-r["lse"][1].double()).view(2, 2 * Sq).sum(1)
+        assert (got[1, :, 80:96] / want[:, None] - 1).abs().max() < 1e-5
+        got[1, :, 80:96] = first[1, :, 80:96]
+        assert torch.equal(got, first)
+    r["table"].copy_(good)
+    for n in (-3, 10 ** 6, 2 ** 31 - 1):
+        got = expect(torch.tensor([100, n, 90], dtype=torch.int32, device="cuda"))
+        assert torch.equal(got[0], first[0]) and torch.equal(got[2], first[2])
+    narrow = expect(r["lens"], mass=torch.zeros(3, 2, 256, device="cuda"))
+    assert torch.equal(narrow[0, :, :100], first[0, :, :100])
+    expect(r["lens"], new_lens=torch.tensor([Sq, Sq + 1, -1], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("elem", [BF16, E4M3, E2M1])
+def test_mass_of_many_rows_on_streams_and_in_graphs(gm, elem):
+    r = run4(gm, 3, 8, 2, 64, 128, 16, [3000, 64, 700], seed=41, elem=elem)  # 256 rows
+    other = run4(gm, 1, 3, 1, 30, 128, 16, [900], seed=42, elem=elem)
+    calls = [lambda x=x, s=None: gm.mercury_attn_paged_mass(x["q"], x["cache"], x["lens"], x["lse"], stream=s) for x in (r, other)]
+    first = [f() for f in calls]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):  # at the same time, both holding the tensor unit's memory
+        got = [[f(s=side) for f, side in zip(calls, sides)] for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for pair in got for a, b in zip(pair, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [f() for f in calls + calls]
+    for _ in range(3):
+        for x in held:
+            x.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, first + first))
     gm.mercury_sync_status()
