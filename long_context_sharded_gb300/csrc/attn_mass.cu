@@ -22,10 +22,11 @@
 // Measured on a GB300, of the measured copy bandwidth (6680 GB/s) or the
 // product's rate: one token of 8 sequences of 20K to 32K, 32 query and 8 KV
 // heads of 128: 16-bit keys 69 us, 95 %; e4m3 50 us, 67 %, e2m1 51 us, 37 %:
-// not by bytes, but by a tile's chain of look-up, load, widening and products
-// (16-bit keys take 320 instructions for 16 keys of a warp).  Rows a KV head, 16
-// bits: 16 72 us, 32 86, 64 122, 128 157, 256 219 (505 TFLOP/s); e2m1 57, 74,
-// 87, 109, 154; heads of 64, one token: 41, 36 and 40 us.
+// not by bytes, but since each warp looks up, loads and widens its own next tile,
+// one ahead (attention over 4 bits, whose copying warps fill a ring, reads twice the
+// bytes in that time; 16-bit keys take 320 instructions for 16 keys of a warp).  Rows a KV head, 16
+// bits: 16 73 us, 32 86, 64 122, 128 157, 256 221 (501 TFLOP/s); e2m1 57, 74,
+// 86, 106, 153; e4m3 55, 72, 105, 106, 157; heads of 64, one token: 41, 36 and 40 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -916,11 +917,13 @@ int launch(MassArgs &a, cudaStream_t stream, char *msg, size_t msg_len)
     // On the tensor unit a tile takes the same time up to 64 rows; there it pays
     // from some 50 on where keys are narrow and each block has many tiles (8 x 8
     // heads, 32K, 64 rows by warps and on the tensor unit: d 64 16 bits 101 us and
-    // 82, e4m3 88 and 76; d 128 e2m1 130 and 104, but e4m3 128 and 133, 16 bits 149
-    // and 169; 48 rows: d 64 16 bits 87 and 82, e4m3 75 and 76, d 128 e2m1 110 and
-    // 104; 2K tiles, d 64 e4m3, 64 rows: 15.9 and 16.5; one sequence of 4K, d 128:
-    // 6.3 and 9.5).  128 rows, d 128, 8 x 20K to 32K:
-    // 16 bits 190 us and 157, 4 bits 178 and 109.
+    // 82, e4m3 87 and 78, e2m1 95 and 82; d 128 e2m1 130 and 103, 16 bits 149 and
+    // 170, and e4m3 128 and 110, which goes by warps yet; 48 rows: d 64 16 bits 87
+    // and 82, e4m3 75 and 78, d 128 e2m1 110 and 103; 2K tiles, d 64 e4m3, 64 rows:
+    // 16.8 and 19.4; one sequence of 4K, d 128, 64 rows: 6.7 and 9.0).  More rows are
+    // two launches by warps: one sequence of 4K, d 128, 68 rows 11.4 us and 10.2,
+    // 128 rows 13.4 and 10.7, in 4 bits 10.9 and 10.8, 12.7 and 11.1; 128 rows of 8
+    // x 20K to 32K 246 and 157, in 4 bits 215 and 107.
     const bool narrow_keys = D == 64 || ELEM == MERCURY_ELEM_E2M1;
     const bool wide = a.p.R > kMassRows || (a.p.R > 48 && narrow_keys && most >= 24LL * ki.sms);
     const int each = wide ? kWideRows : kMassRows;

@@ -22,9 +22,13 @@
 // bandwidth; one token of 32 sequences: 3.0 us; 6 x 1000 padded tokens of 24
 // heads of 64 into an 8-bit cache: 8.2 us, bound by the latency of short
 // threads (3 us of bytes).  Into a 4-bit cache: 8K tokens of 32 query and 8 + 8
-// key and value heads of 128: 45 us (26 us of bytes), its keys and values alone 26
-// us; with the quantisation's work taken out it would be 2 us less.  6 x 1000
-// padded tokens of 24 heads of 64 10.6 us, one token of 32 sequences 4.1 us.
+// key and value heads of 128: 48 us (26 us of bytes), its keys and values alone 28
+// us (6 us of bytes; 16 bits 35 and 10 us): not by the quantisation's work (2 us
+// of it) but by the little that a thread has on the way, one head, where the
+// other caches' have two to four and the next ones.  6 x 1000 padded tokens of 24 heads of 64
+// 10.6 us, one token of 32 sequences 3.5 to 4.2 us.  Element by element (other rotated
+// parts and alignments): the 8K tokens with 24 elements rotated 87 us, their
+// keys and values alone 57; all 128 rotated, heads that begin at odd elements, 122.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>

@@ -12,10 +12,11 @@
 // of steps that each wait for the one before.
 //
 // Measured on a GB300: one sequence of 32K, 8 KV heads of 128, to 4K, 16 bits: 17
-// us (5 us of bytes); 16 sequences of 500 to 16K to 2K, 8 bits: 35 us (20 us of
-// bytes).  Each kernel alone and cold: selection 14 and 15 us, rows 10 and 23;
+// us (5 us of bytes), 4 bits 14 (2); 16 sequences of 500 to 16K to 2K, 16 bits 53 us
+// (40 us of bytes), 8 bits 35 (20), 4 bits 32 (12).  Each kernel alone and cold: selection 14 and 15 us, rows 10 and 23;
 // with one block a head the first selection took 30 us.  32K tokens of a 4-bit
-// cache read back: 29 us, 89 % of the measured copy bandwidth.
+// cache read back: 29 us, 89 % of the measured copy bandwidth (8 bits 32 us, 95 %; 16
+// bits 41, 98 %).
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
